@@ -24,6 +24,7 @@ MK_HEAD_DIM = 128
 MK_MAX_SEGMENTS = 4
 MK_MAX_SPLITS = 64
 MK_PAGES_PACKED, MK_PAGES_DENSE, MK_PAGES_BITMAP = 0, 1, 2
+MK_KV_BF16, MK_KV_E4M3 = 0, 1
 STATUS = {0: "MK_OK", 1: "MK_EINVAL", 2: "MK_ENOMEM", 3: "MK_ESTATE", 4: "MK_ECUDA",
           5: "MK_EDEVICE", 6: "MK_ETIMEOUT", 7: "MK_ENOTSUP"}
 c_i32, c_i64, c_size, c_vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
@@ -65,6 +66,20 @@ class MkLayoutInfo(ctypes.Structure):
                 ("cmeta", c_i64), ("cmeta_row", c_i32), ("meta_channels", c_i32)]
 
 
+class MkPagedConfig(ctypes.Structure):
+    _fields_ = [("head_dim", c_i32), ("n_q_heads", c_i32), ("n_kv_heads", c_i32), ("n_layers", c_i32),
+                ("page", c_i32), ("n_pages", c_i32), ("max_seqs", c_i32), ("kv_type", c_i32)]
+
+
+class MkPagedBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", c_i32), ("n_tokens", c_i32), ("max_new", c_i32), ("table_stride", c_i32),
+                ("cu_new", c_vp), ("kv_len", c_vp), ("page_table", c_vp)]
+
+
+class MkRope(ctypes.Structure):
+    _fields_ = [("cos_sin", c_vp), ("n_pos", c_i32), ("rot_dim", c_i32), ("interleaved", c_i32), ("positions", c_vp)]
+
+
 _SIGS = {
     "mk_arena_bytes": [ctypes.POINTER(MkConfig), ctypes.POINTER(c_size)],
     "mk_workspace_bytes": [ctypes.POINTER(MkConfig), ctypes.POINTER(c_size)],
@@ -96,6 +111,18 @@ _SIGS = {
                             c_vp, c_vp, c_vp],
     "mk_swap_segment": [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp],
 }
+
+_SIGS.update({
+    "mk_paged_sizes": [ctypes.POINTER(MkPagedConfig), ctypes.POINTER(c_size), ctypes.POINTER(c_size),
+                       ctypes.POINTER(c_size)],
+    "mk_paged_create": [ctypes.POINTER(MkPagedConfig), c_vp, c_vp, c_vp, c_vp, c_vp, c_size, ctypes.POINTER(c_vp)],
+    "mk_paged_destroy": [c_vp],
+    "mk_paged_append": [c_vp, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp],
+    "mk_paged_decode_attn": [c_vp, c_i32, c_vp, c_vp, c_i64, ctypes.c_float, c_vp, c_i64, c_vp, c_vp],
+    "mk_paged_prefill_attn": [c_vp, c_i32, c_vp, c_i32, c_vp, c_i64, ctypes.c_float, c_vp, c_i64, c_vp, c_vp],
+    "mk_paged_poll_error": [c_vp, ctypes.POINTER(c_i32)],
+    "mk_paged_clear_error": [c_vp],
+})
 
 _lib = None
 
@@ -314,6 +341,201 @@ class MosaicKV:
                       if L["meta_channels"] else None),
             "layout": L,
         }
+
+
+# ---- the paged cache (bf16, or e4m3 with a scale per page and head) -----------
+
+def make_paged_config(n_q_heads, n_kv_heads, n_layers, page, n_pages, max_seqs, kv_type=MK_KV_E4M3) -> MkPagedConfig:
+    return MkPagedConfig(MK_HEAD_DIM, n_q_heads, n_kv_heads, n_layers, page, n_pages, max_seqs, kv_type)
+
+
+def paged_sizes(cfg: MkPagedConfig):
+    """(bytes of each pool, bytes of each scale array, workspace bytes)."""
+    p, s, w = c_size(), c_size(), c_size()
+    _check("mk_paged_sizes", load().mk_paged_sizes(ctypes.byref(cfg), ctypes.byref(p), ctypes.byref(s), ctypes.byref(w)))
+    return p.value, s.value, w.value
+
+
+def rope_table(n_pos, rot_dim, base=10000.0, scale=1.0, device="cuda"):
+    """cos | sin of (position * scale) * base^(-2 i / rot_dim), fp32 [n_pos, rot_dim].  The angles are formed in 64
+    bits and rounded once: in 32 bits a far position's angle is off by more than a whole step of the table."""
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * scale * f[None, :]
+    return torch.cat([a.cos(), a.sin()], dim=1).to(torch.float32).contiguous()
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dev_i32(t, name, device=None):
+    _need(t.dtype == torch.int32 and t.is_cuda and t.is_contiguous(), f"{name} must be a contiguous int32 CUDA tensor")
+    _need(device is None or t.device == device, f"{name} is on another device")
+
+
+class Rope:
+    """The rotation of an append: table [n_pos, rot_dim] fp32 (rope_table), optional int32 positions per row."""
+
+    def __init__(self, table, rot_dim, interleaved=False, positions=None):
+        _need(table.dtype == torch.float32 and table.is_cuda and table.is_contiguous() and table.dim() == 2
+              and table.shape[1] == rot_dim, "the table must be contiguous fp32 [n_pos, rot_dim] on the GPU")
+        if positions is not None:
+            _dev_i32(positions, "positions", table.device)
+        self.table, self.positions, self.device = table, positions, table.device
+        self.c = MkRope(table.data_ptr(), table.shape[0], rot_dim, int(interleaved),
+                        positions.data_ptr() if positions is not None else None)
+        self.ref = ctypes.byref(self.c)
+
+
+class PagedBatch:
+    """The sequences of a call: kv_len int32 [n] (new tokens included), page_table int32 [n, columns], cu_new int32
+    [n + 1] (None: one new token per sequence, row i of sequence i), max_new, and n_tokens, the rows of k, v, q and
+    out (default: n without cu_new).  The tensors are read when the kernels run, so their values may be changed
+    between calls and between replays of a captured graph."""
+
+    def __init__(self, kv_len, page_table, cu_new=None, max_new=1, n_tokens=None):
+        _dev_i32(kv_len, "kv_len")
+        n = kv_len.shape[0]
+        _dev_i32(page_table, "page_table", kv_len.device)
+        _need(page_table.dim() == 2 and page_table.shape[0] >= n, "page_table must be [n, columns]")
+        if cu_new is not None:
+            _dev_i32(cu_new, "cu_new", kv_len.device)
+            _need(cu_new.shape[0] == n + 1 and n_tokens is not None, "cu_new must be [n + 1], with n_tokens given")
+        if n_tokens is None:
+            n_tokens = n
+        self.device, self.n_tokens, self.n_seqs = kv_len.device, int(n_tokens), n
+        self.kv_len, self.page_table, self.cu_new = kv_len, page_table, cu_new
+        self.c = MkPagedBatch(n, self.n_tokens, int(max_new), page_table.shape[1],
+                              cu_new.data_ptr() if cu_new is not None else None, kv_len.data_ptr(), page_table.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+
+class PagedKV:
+    """A paged KV cache (all layers) on one GPU: pools [n_layers, n_pages, n_kv_heads, page, 128] in bf16 or e4m3,
+    for e4m3 scales [n_layers, n_pages, n_kv_heads] fp32.  The pools are allocated here unless given."""
+
+    def __init__(self, cfg: MkPagedConfig, device="cuda", k_pool=None, v_pool=None, k_scale=None, v_scale=None):
+        self.lib = load()
+        self.cfg = cfg
+        dev = torch.device(device)
+        self.device = dev if dev.index is not None else torch.device(dev.type, torch.cuda.current_device())
+        pool_bytes, scale_bytes, ws_bytes = paged_sizes(cfg)
+        e4m3 = cfg.kv_type == MK_KV_E4M3
+        self.dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+        shape = (cfg.n_layers, cfg.n_pages, cfg.n_kv_heads, cfg.page, MK_HEAD_DIM)
+
+        def own(t, name, dtype, shape):
+            if t is None:
+                return torch.zeros(shape, dtype=dtype, device=self.device)
+            _need(tuple(t.shape) == tuple(shape) and t.dtype == dtype and t.is_contiguous() and t.device == self.device,
+                  f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}")
+            return t
+
+        self.k_pool, self.v_pool = own(k_pool, "k_pool", self.dtype, shape), own(v_pool, "v_pool", self.dtype, shape)
+        _need(e4m3 or (k_scale is None and v_scale is None), "a bf16 cache has no scales")
+        self.k_scale = own(k_scale, "k_scale", torch.float32, shape[:3]) if e4m3 else None
+        self.v_scale = own(v_scale, "v_scale", torch.float32, shape[:3]) if e4m3 else None
+        self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
+        self.q_row, self.kv_row = cfg.n_q_heads * MK_HEAD_DIM, cfg.n_kv_heads * MK_HEAD_DIM
+        self.h = None
+        h = c_vp()
+        with torch.cuda.device(self.device):
+            _check("mk_paged_create", self.lib.mk_paged_create(
+                ctypes.byref(cfg), _ptr(self.k_pool), _ptr(self.v_pool), _ptr(self.k_scale), _ptr(self.v_scale),
+                _ptr(self.workspace), ws_bytes, ctypes.byref(h)))
+        self.h = h
+
+    def close(self):
+        if getattr(self, "h", None):
+            self.lib.mk_paged_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _rows(self, t, name, batch, heads):
+        """Row stride of a bf16 [rows, heads, 128] (or [rows, heads * 128]) tensor whose rows are contiguous."""
+        if t.dim() == 3:
+            ok = t.shape[1] == heads and t.shape[2] == MK_HEAD_DIM and t.stride(2) == 1 and (
+                heads == 1 or t.stride(1) == MK_HEAD_DIM)
+        else:
+            ok = t.dim() == 2 and t.shape[1] == heads * MK_HEAD_DIM and t.stride(1) == 1
+        _need(ok and t.dtype == torch.bfloat16 and t.shape[0] >= batch.n_tokens and t.device == self.device,
+              f"{name} must be bf16 [{batch.n_tokens}, {heads}, 128] on {self.device} with contiguous rows")
+        return t.stride(0) if t.shape[0] > 1 else heads * MK_HEAD_DIM
+
+    def _stream(self, stream, *tensors):
+        cur = torch.cuda.current_stream(self.device)
+        if stream is None or stream == cur:
+            return cur.cuda_stream
+        for t in tensors:       # the allocator must not reuse them before that stream is done
+            if t is not None:
+                t.record_stream(stream)
+        return stream.cuda_stream
+
+    def append(self, layer, batch, k, v, rope=None, q=None, q_out=None, stream=None):
+        """Stores the batch's new tokens (k, v: bf16 [n_tokens, n_kv_heads, 128], rows may be strided), keys turned by
+        `rope`; q, if given, is turned too, into q_out (default: a new tensor), which is returned."""
+        _need(batch.device == self.device and (rope is None or rope.device == self.device), "the batch is on another device")
+        ks, vs = self._rows(k, "k", batch, self.cfg.n_kv_heads), self._rows(v, "v", batch, self.cfg.n_kv_heads)
+        qs = os_ = 0
+        if q is not None:
+            qs = self._rows(q, "q", batch, self.cfg.n_q_heads)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            os_ = self._rows(q_out, "q_out", batch, self.cfg.n_q_heads)
+        else:
+            _need(q_out is None, "q_out needs q")
+        st = self.lib.mk_paged_append(
+            self.h, layer, batch.ref, rope.ref if rope is not None else None, k.data_ptr(), ks, v.data_ptr(), vs,
+            q.data_ptr() if q is not None else None, qs, q_out.data_ptr() if q is not None else None, os_,
+            self._stream(stream, k, v, q, q_out))
+        if st:
+            raise MosaicKVError("mk_paged_append", st)
+        return q_out
+
+    def _attn(self, batch, q, scale, out, lse, stream):
+        _need(batch.device == self.device, "the batch is on another device")
+        qs = self._rows(q, "q", batch, self.cfg.n_q_heads)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        os_ = self._rows(out, "out", batch, self.cfg.n_q_heads)
+        if lse is True:
+            lse = torch.empty(q.shape[0], self.cfg.n_q_heads, dtype=torch.float32, device=q.device)
+        if lse is not None:
+            _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == self.device
+                  and lse.numel() >= batch.n_tokens * self.cfg.n_q_heads, "lse must be contiguous fp32 [n_tokens, n_q_heads]")
+        return (q.data_ptr(), qs, MK_HEAD_DIM ** -0.5 if scale is None else scale, out.data_ptr(), os_,
+                lse.data_ptr() if lse is not None else None, self._stream(stream, q, out, lse)), out, lse
+
+    def decode_attn(self, layer, batch, q, scale=None, out=None, lse=None, stream=None):
+        """Attention of one query token per sequence (bf16 [n_tokens, n_q_heads, 128]); scale: default 1/sqrt(128).
+        lse: an fp32 [n_tokens, n_q_heads] tensor to fill, or True for a new one; then (out, lse) is returned."""
+        args, out, lse = self._attn(batch, q, scale, out, lse, stream)
+        st = self.lib.mk_paged_decode_attn(self.h, layer, batch.ref, *args)
+        if st:
+            raise MosaicKVError("mk_paged_decode_attn", st)
+        return out if lse is None else (out, lse)
+
+    def prefill_attn(self, layer, batch, q, causal=True, scale=None, out=None, lse=None, stream=None):
+        """Attention of several query tokens per sequence: a prompt's chunk (causal), or cross attention (not)."""
+        args, out, lse = self._attn(batch, q, scale, out, lse, stream)
+        st = self.lib.mk_paged_prefill_attn(self.h, layer, batch.ref, int(bool(causal)), *args)
+        if st:
+            raise MosaicKVError("mk_paged_prefill_attn", st)
+        return out if lse is None else (out, lse)
+
+    def poll_error(self):
+        d = c_i32()
+        st = self.lib.mk_paged_poll_error(self.h, ctypes.byref(d))
+        return st, d.value
+
+    def clear_error(self):
+        _check("mk_paged_clear_error", self.lib.mk_paged_clear_error(self.h))
 
 
 def dense_attn_noalloc(n_q_heads, n_kv_heads, T, q, K, V, out, stream=None):

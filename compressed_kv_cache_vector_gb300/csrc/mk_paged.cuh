@@ -1,0 +1,63 @@
+// Declarations shared by the paged cache's kernels and their host side.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "mk_internal.cuh"
+
+namespace mk {
+
+// One layer of the pools and what every paged kernel needs besides.
+struct PagedLayer {
+  uint8_t* k;                   // [n_pages][n_kv][P][128] bf16 or e4m3
+  uint8_t* v;
+  float* k_scale;               // [n_pages][n_kv] (e4m3)
+  float* v_scale;
+  int32_t* err;                 // [0] status, [1] detail, [2] sequence, [3] aux
+  int32_t n_pages, n_kv, G, P, p_log2, e4m3;
+};
+
+// Device error codes of the paged calls (detail word), after DevErr's.
+enum PagedErr : int32_t {
+  ERR_PAGED_BATCH = 16,     // cu_new not ascending or past n_tokens, more new tokens than max_new, a length out of range
+  ERR_PAGED_PAGE = 17,      // a page id outside [0, n_pages)
+  ERR_PAGED_POSITION = 18,  // a rotary position outside [0, n_pos)
+  ERR_PAGED_WAIT = 19,      // a copy or a matrix instruction did not complete within the wait bound (MK_ETIMEOUT)
+};
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void paged_error(const PagedLayer& L, int32_t detail, int32_t seq, int32_t aux,
+                                            int32_t status = (int32_t)MK_EDEVICE) {
+  if (atomicCAS(&L.err[0], 0, status) == 0) {
+    L.err[1] = detail;
+    L.err[2] = seq;
+    L.err[3] = aux;
+  }
+}
+__device__ __forceinline__ bool paged_has_error(const PagedLayer& L) { return *(volatile int32_t*)L.err != 0; }
+
+// Sequence i of a batch: its first row, new tokens and length.  ok is false
+// (and the error word set by the callers) when they contradict the batch.
+struct PagedSeq {
+  int row0, n_new, len;
+  bool ok;
+};
+__device__ __forceinline__ PagedSeq paged_seq(const mk_paged_batch& b, int P, int i, bool new_in_len) {
+  PagedSeq s;
+  s.row0 = b.cu_new ? b.cu_new[i] : i;
+  s.n_new = (b.cu_new ? b.cu_new[i + 1] : i + 1) - s.row0;
+  s.len = b.kv_len[i];
+  s.ok = s.row0 >= 0 && s.n_new >= 0 && s.n_new <= b.max_new && (int64_t)s.row0 + s.n_new <= b.n_tokens && s.len >= 0 &&
+         s.len <= (int64_t)b.table_stride * P && (!new_in_len || s.len >= s.n_new);
+  return s;
+}
+#endif
+
+cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, const mk_rope& rope, const uint16_t* k,
+                                int64_t k_stride, const uint16_t* v, int64_t v_stride, const uint16_t* q,
+                                int64_t q_stride, uint16_t* q_out, int64_t q_out_stride, cudaStream_t s);
+cudaError_t launch_paged_attn_simple(const PagedLayer& L, const mk_paged_batch& b, bool causal, const uint16_t* q,
+                                     int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, float* lse,
+                                     cudaStream_t s);
+
+}  // namespace mk

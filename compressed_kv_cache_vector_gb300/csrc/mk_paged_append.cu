@@ -1,0 +1,313 @@
+// Appending keys and values to the paged cache, rotated on the way.
+//
+// Mathematics.  A token at position p of its sequence has its key's (and
+// query's) first R channels turned in R / 2 planes by the angles of p:
+// (x1, x2) -> (x1 c - x2 s, x2 c + x1 s), products and sum rounded in fp32.
+// A bf16 pool stores the result rounded once.  An e4m3 pool holds code =
+// rn(y / s) under one scale s per (page, kv head), the smallest power of two
+// with amax <= 448 s over the page's tokens (at least 2^-64).  A power of two
+// costs an e4m3 code no precision, only up to one binade of its 18, and makes
+// raising a page's scale exact: the codes held before are multiplied by
+// s_old / s_new, which rounds only those that become subnormal.
+//
+// Work split: a page of one kv head of one tensor per CTA of 128 threads, 16
+// threads a row (8 channels each), so that the page's maximum is a reduction
+// inside the CTA and a row's rotation partner is in the same 16 lanes.  The
+// values stay in registers between the maximum and the rounding: one pass.
+#include "mk_paged.cuh"
+
+namespace mk {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kQRows = 32;  // rows (token, query head) of a query CTA
+
+struct AppendArgs {
+  mk_paged_batch b;
+  mk_rope rope;
+  const uint16_t *k, *v, *q;
+  uint16_t* q_out;
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+  int32_t n_units;  // page slots x kv heads x 2
+};
+
+// Eight channels (16-lane group: chunk j of the row) turned by the angles of
+// row `pos` of the table.  x holds this thread's channels; every lane of the
+// 16-lane group must call.
+__device__ __forceinline__ void rotate8(const mk_rope& r, int pos, int j, int lane, const uint4 raw, float (&y)[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[2 * e] = __uint_as_float(w[e] << 16);
+    y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+  }
+  if (r.rot_dim == 0) return;
+  const int half = r.rot_dim >> 1, c0 = j * 8;
+  const float* row = r.cos_sin + (int64_t)pos * r.rot_dim;
+  if (r.interleaved) {
+    if (c0 < r.rot_dim) {
+      const float4 c = *reinterpret_cast<const float4*>(row + c0 / 2);
+      const float4 s = *reinterpret_cast<const float4*>(row + half + c0 / 2);
+      const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = y[2 * e], b = y[2 * e + 1];
+        y[2 * e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
+        y[2 * e + 1] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
+      }
+    }
+    return;
+  }
+  // Half split: the partner chunk is half / 8 lanes away in the same group.
+  const bool second = c0 >= half;
+  const int partner = (lane & 16) | ((second ? j - half / 8 : j + half / 8) & 15);
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(FULL, w[e], partner);
+  if (c0 < r.rot_dim) {
+    const int i = second ? c0 - half : c0;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * v);
+      const float4 s = *reinterpret_cast<const float4*>(row + half + i + 4 * v);
+      const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int n = 4 * v + e;
+        const float other = (n & 1) ? __uint_as_float(o[n >> 1] & 0xffff0000u) : __uint_as_float(o[n >> 1] << 16);
+        const float p = __fmul_rn(y[n], cs[e]), t = __fmul_rn(other, sn[e]);
+        y[n] = second ? __fadd_rn(p, t) : __fsub_rn(p, t);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ uint4 pack_bf16(const float (&y)[8]) {
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    o[e] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y[2 * e])) |
+           ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y[2 * e + 1])) << 16);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// Eight e4m3 codes of y * inv (infinities saturate to +-448, NaN stays NaN).
+__device__ __forceinline__ uint2 pack_e4m3(const float (&y)[8], float inv) {
+  uint32_t o[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e] * inv, y[4 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi =
+        __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e + 2] * inv, y[4 * e + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    o[e] = lo | (hi << 16);
+  }
+  return make_uint2(o[0], o[1]);
+}
+__device__ __forceinline__ void unpack_e4m3(uint2 c, float (&y)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t w = e < 2 ? c.x : c.y;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (e & 1))), __NV_E4M3);
+    y[2 * e] = __half2float(__half(__half_raw{h.x}));
+    y[2 * e + 1] = __half2float(__half(__half_raw{h.y}));
+  }
+}
+// Smallest 2^e, e >= -64, with amax <= 448 * 2^e (448 = 1.75 * 2^8).
+__device__ __forceinline__ float scale_of(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  if (b < 0x800000u || e < -64) e = -64;
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ int clamp_position(const PagedLayer& L, const mk_rope& r, int pos, int seq) {
+  if (r.rot_dim && (pos < 0 || pos >= r.n_pos)) {
+    paged_error(L, ERR_PAGED_POSITION, seq, pos);
+    return 0;
+  }
+  return pos;
+}
+
+template <int P, bool E4M3>
+__global__ void __launch_bounds__(kThreads) k_paged_append(PagedLayer L, AppendArgs a) {
+  __shared__ int s_pre[MK_MAX_CALL_SEQS + 1], s_wsum[kThreads / 32], s_seq, s_idx;
+  __shared__ float s_max[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = tid & 15, rr = tid >> 4;
+  pdl_wait();
+  pdl_trigger();
+  if (paged_has_error(L)) return;
+
+  if ((int)blockIdx.x >= a.n_units) {  // a query CTA: kQRows rows (token, query head)
+    const int n_q = L.n_kv * L.G;
+    const int64_t rows = (int64_t)a.b.n_tokens * n_q;
+    const int64_t r0 = (int64_t)((int)blockIdx.x - a.n_units) * kQRows;
+#pragma unroll
+    for (int p = 0; p < kQRows / (kThreads / 16); ++p) {
+      const int64_t r = r0 + p * (kThreads / 16) + rr;
+      const bool live = r < rows;
+      const int t = live ? (int)(r / n_q) : 0, h = live ? (int)(r - (int64_t)t * n_q) : 0;
+      int lo = 0, pos = 0;
+      bool in = live;
+      if (live) {
+        if (a.b.cu_new) {
+          int hi = a.b.n_seqs - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.b.cu_new[mid] <= t) lo = mid; else hi = mid - 1;
+          }
+        } else {
+          lo = t;
+        }
+        const PagedSeq s = paged_seq(a.b, P, lo, true);
+        in = s.ok && t >= s.row0 && t < s.row0 + s.n_new;  // rows behind the last sequence stay as they were
+        if (a.rope.positions)
+          pos = a.rope.positions[t];
+        else
+          pos = s.len - s.n_new + (t - s.row0);
+        if (in) pos = clamp_position(L, a.rope, pos, lo); else pos = 0;
+      }
+      const uint4 raw = in ? *reinterpret_cast<const uint4*>(a.q + (int64_t)t * a.q_stride + h * D + j * 8)
+                           : make_uint4(0, 0, 0, 0);
+      float y[8];
+      rotate8(a.rope, pos, j, lane, raw, y);
+      if (in) *reinterpret_cast<uint4*>(a.q_out + (int64_t)t * a.q_out_stride + h * D + j * 8) = pack_bf16(y);
+    }
+    return;
+  }
+
+  const int is_v = (int)blockIdx.x & 1;
+  const int head = ((int)blockIdx.x >> 1) % L.n_kv;
+  const int slot = ((int)blockIdx.x >> 1) / L.n_kv;
+  int seq, idx;  // the sequence and which of its touched pages
+  if (a.b.max_new == 1) {
+    seq = slot;
+    idx = 0;
+  } else {  // the slot-th touched page over all sequences
+    if (tid == 0) s_seq = -1;
+    int base = 0;
+    for (int i0 = 0; i0 < a.b.n_seqs; i0 += kThreads) {
+      const int i = i0 + tid;
+      int cnt = 0;
+      if (i < a.b.n_seqs) {
+        const PagedSeq s = paged_seq(a.b, P, i, true);
+        if (!s.ok) paged_error(L, ERR_PAGED_BATCH, i, s.len);
+        if (s.ok && s.n_new > 0) cnt = (s.len - 1) / P - (s.len - s.n_new) / P + 1;
+      }
+      const int ex = warp_excl_scan(cnt, lane);
+      if (lane == 31) s_wsum[warp] = ex + cnt;
+      __syncthreads();
+      int off = base;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) off += s_wsum[w];
+        base += s_wsum[w];
+      }
+      if (slot >= off + ex && slot < off + ex + cnt) {
+        s_seq = i;
+        s_idx = slot - off - ex;
+      }
+      __syncthreads();
+      if (base > slot) break;
+    }
+    seq = s_seq;
+    idx = s_idx;
+    if (seq < 0) return;
+  }
+  (void)s_pre;
+  const PagedSeq sq = paged_seq(a.b, P, seq, true);
+  if (!sq.ok) {
+    if (tid == 0) paged_error(L, ERR_PAGED_BATCH, seq, sq.len);
+    return;
+  }
+  if (sq.n_new == 0) return;
+  const int start = sq.len - sq.n_new;
+  const int pg = start / P + idx;
+  const int s0 = max(start - pg * P, 0), s1 = min(sq.len - pg * P, P);  // new tokens' slots of this page
+  const int page = a.b.page_table[(int64_t)seq * a.b.table_stride + pg];
+  if (page < 0 || page >= L.n_pages) {
+    if (tid == 0) paged_error(L, ERR_PAGED_PAGE, seq, page);
+    return;
+  }
+  const int64_t unit = (int64_t)page * L.n_kv + head;
+  const uint16_t* src = is_v ? a.v : a.k;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  mk_rope rope = a.rope;
+  if (is_v) rope.rot_dim = 0;
+  constexpr int NP = P / (kThreads / 16);  // rows of a thread
+  float y[NP][8];
+  float amax = 0.0f;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int sl = p * (kThreads / 16) + rr;
+    const bool in = sl >= s0 && sl < s1;
+    const int64_t t = sq.row0 + (int64_t)pg * P + sl - start;
+    int pos = 0;
+    if (in && !is_v) pos = clamp_position(L, rope, rope.positions ? rope.positions[t] : pg * P + sl, seq);
+    const uint4 raw = in ? *reinterpret_cast<const uint4*>(src + t * stride + head * D + j * 8) : make_uint4(0, 0, 0, 0);
+    rotate8(rope, pos, j, lane, raw, y[p]);
+    if (E4M3) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float m = fabsf(y[p][e]);
+        if (m <= 3.402823466e38f) amax = fmaxf(amax, m);  // infinities and NaN do not set the scale
+      }
+    } else if (in) {
+      *reinterpret_cast<uint4*>((is_v ? L.v : L.k) + ((unit * P + sl) * D + j * 8) * 2) = pack_bf16(y[p]);
+    }
+  }
+  if (!E4M3) return;
+  amax = warp_max(amax);
+  if (lane == 0) s_max[warp] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
+  float scale = scale_of(amax);
+  uint8_t* dst = (is_v ? L.v : L.k) + unit * P * D;
+  float* sc = (is_v ? L.v_scale : L.k_scale) + unit;
+  if (s0 > 0) {  // tokens of earlier calls in this page
+    const float was = *sc;
+    scale = fmaxf(scale, was);
+    if (scale > was) {
+      const float ratio = __fdiv_rn(was, scale);
+      for (int sl = rr; sl < s0; sl += kThreads / 16) {
+        uint2* c = reinterpret_cast<uint2*>(dst + sl * D + j * 8);
+        float h[8];
+        unpack_e4m3(*c, h);
+        *c = pack_e4m3(h, ratio);
+      }
+    }
+  }
+  const float inv = __frcp_rn(scale);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int sl = p * (kThreads / 16) + rr;
+    if (sl >= s0 && sl < s1) *reinterpret_cast<uint2*>(dst + sl * D + j * 8) = pack_e4m3(y[p], inv);
+  }
+  __syncthreads();  // every thread has read the page's earlier scale
+  if (tid == 0) *sc = scale;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, const mk_rope& rope, const uint16_t* k,
+                                int64_t k_stride, const uint16_t* v, int64_t v_stride, const uint16_t* q,
+                                int64_t q_stride, uint16_t* q_out, int64_t q_out_stride, cudaStream_t s) {
+  // Touched pages: at most 2 + (n - 2) / P of a sequence with n >= 2 new
+  // tokens, 1 of one with a single one.
+  int64_t slots = b.max_new == 1 ? b.n_seqs : (int64_t)b.n_tokens / L.P + 2 * (int64_t)b.n_seqs;
+  if (slots > b.n_tokens && b.max_new != 1) slots = b.n_tokens;
+  const int64_t units = slots * L.n_kv * 2;
+  const int64_t qb = q ? ((int64_t)b.n_tokens * L.n_kv * L.G + kQRows - 1) / kQRows : 0;
+  if (units + qb == 0) return cudaSuccess;
+  if (units + qb > 0x7fffffff) return cudaErrorInvalidValue;
+  AppendArgs a{b, rope, k, v, q, q_out, k_stride, v_stride, q_stride, q_out_stride, (int32_t)units};
+  const dim3 grid((unsigned)(units + qb)), block(kThreads);
+#define MK_LAUNCH_APPEND(PP)                                                                \
+  return L.e4m3 ? launch_pdl(k_paged_append<PP, true>, grid, block, 0, s, 0, L, a)          \
+                : launch_pdl(k_paged_append<PP, false>, grid, block, 0, s, 0, L, a)
+  if (L.P == 16) MK_LAUNCH_APPEND(16);
+  if (L.P == 32) MK_LAUNCH_APPEND(32);
+  MK_LAUNCH_APPEND(64);
+#undef MK_LAUNCH_APPEND
+}
+
+}  // namespace mk

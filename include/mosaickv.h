@@ -436,6 +436,124 @@ mk_status mk_swap_segment(mk_ctx* ctx, int32_t layer, int32_t seq, int32_t kv_he
                           int32_t keep_channels, const float* R_k, const float* R_v, const void* pages,
                           const void* meta, const void* cmeta, mk_stream stream);
 
+/* ---- Paged KV cache, uncompressed or in 8 bits ----
+ * The cache a serving runtime keeps next to the compressed one (or before it:
+ * the prompt's own attention): pools of pages that sequences share, a page
+ * table per batch, and the attention that reads the pages.  A pool holds
+ * bf16, or e4m3 codes under one fp32 scale per (layer, page, kv head) and
+ * tensor.  No channel is dropped; the 8-bit pool is the quantising comparator
+ * of the packed pages.
+ *
+ * Layouts (device memory, all owned by the caller):
+ *   k_pool, v_pool    [n_layers][n_pages][n_kv_heads][page][128]
+ *   k_scale, v_scale  [n_layers][n_pages][n_kv_heads] fp32 (e4m3 only); a
+ *                     stored code c stands for the value c * scale
+ * Token p of a sequence is in slot p mod page of the sequence's (p / page)-th
+ * page, named by its page table row.  Slots past a sequence's length are never
+ * read as values: they may hold anything.
+ *
+ * The calls follow the conventions above (host checks first, a sticky device
+ * error word read with mk_paged_poll_error, one host thread and one device
+ * order per handle: calls that may overlap on the GPU need handles with
+ * workspaces of their own).  They run on the device that was current at
+ * mk_paged_create, whichever is current at the call.  Lengths, new-token
+ * offsets and page tables are read on the device, so a captured CUDA graph
+ * may be replayed with new ones. */
+#define MK_KV_BF16 0
+#define MK_KV_E4M3 1
+
+typedef struct mk_paged mk_paged;
+
+typedef struct mk_paged_config {
+  int32_t head_dim;   /* must be 128 */
+  int32_t n_q_heads;  /* query heads per layer */
+  int32_t n_kv_heads; /* kv heads per layer; n_q_heads/n_kv_heads 1, 2, 4 or 8 */
+  int32_t n_layers;
+  int32_t page;       /* tokens per page: 16, 32 or 64 */
+  int32_t n_pages;    /* pages per layer */
+  int32_t max_seqs;   /* sequences per call, <= MK_MAX_CALL_SEQS */
+  int32_t kv_type;    /* MK_KV_BF16 or MK_KV_E4M3 */
+} mk_paged_config;
+
+/* The sequences of a call.  One batch serves every layer and call of a step.
+ * The arrays are device memory, read when the kernels run. */
+typedef struct mk_paged_batch {
+  int32_t n_seqs;            /* 0..max_seqs */
+  int32_t n_tokens;          /* rows of k, v, q and out in the call */
+  int32_t max_new;           /* no sequence has more new tokens than this */
+  int32_t table_stride;      /* entries per page table row */
+  const int32_t* cu_new;     /* [n_seqs + 1]: sequence i's new tokens are rows cu_new[i] .. cu_new[i+1] - 1.
+                                Rows past cu_new[n_seqs] (a padded batch) are not touched.  NULL with
+                                max_new = 1 and n_tokens >= n_seqs: row i is sequence i's one token. */
+  const int32_t* kv_len;     /* [n_seqs]: tokens held, the call's new ones included */
+  const int32_t* page_table; /* [n_seqs][table_stride]: page ids; entries past a length are not read */
+} mk_paged_batch;
+
+/* The position rotation of mk_paged_append.  rot_dim = 0: none. */
+typedef struct mk_rope {
+  const float* cos_sin;      /* device fp32 [n_pos][rot_dim]: rot_dim/2 cosines, then rot_dim/2 sines of the
+                                position's angles (16-byte aligned) */
+  int32_t n_pos;
+  int32_t rot_dim;           /* rotated channels, the first ones: 0..128, a multiple of 16 */
+  int32_t interleaved;       /* 0: channel i turns with i + rot_dim/2; 1: channel 2i with 2i + 1 */
+  const int32_t* positions;  /* device [n_tokens]: row of cos_sin per row; NULL: the token's position in its sequence */
+} mk_rope;
+
+/* Bytes of each pool, of each scale array (0 for bf16) and of the workspace. */
+mk_status mk_paged_sizes(const mk_paged_config* cfg, size_t* pool_bytes, size_t* scale_bytes, size_t* workspace_bytes);
+/* Creates a handle over the caller's buffers (pools and workspace 256-byte
+ * aligned; scales NULL for bf16) on the current device.  Clears the
+ * workspace's counters and synchronises the device once; reads and writes no
+ * pool.  The buffers must outlive the handle. */
+mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                          void* workspace, size_t workspace_bytes, mk_paged** out);
+mk_status mk_paged_destroy(mk_paged* h);
+
+/* Stores the batch's new tokens: sequence i's last n_new[i] positions.  Keys
+ * are turned by `rope` first (NULL: not), in fp32 with every operation
+ * rounded, and so is the optional q into q_out (q_out may be q).
+ * k, v: bf16 rows of n_kv_heads x 128, row t at k + t * k_stride elements; q,
+ * q_out: bf16 rows of n_q_heads x 128 (all 16-byte aligned, strides multiples
+ * of 8, so that slices of one fused projection can be given).
+ * bf16 pools: rounded once, to nearest even.  e4m3 pools: a page's scale is
+ * the smallest power of two >= 2^-64 with max |y| <= 448 scale over the
+ * page's tokens (infinities and NaN left out; an infinity is stored as +-448
+ * codes, a NaN as NaN), and a code is y / scale rounded to nearest even.  When
+ * new tokens raise the scale of a page that holds older ones, those codes are
+ * rewritten as code * old / new, rounded again where that is subnormal.  A
+ * page whose slot 0 is written by the call starts afresh, whatever it held.
+ * A page that the call writes may be in one row and place of the table only.
+ * Errors: MK_EINVAL (null or misaligned pointers, strides, sizes); on the
+ * device, for a bad offset, length, page id or position: that sequence or
+ * page is skipped (a bad position reads row 0) and the error word set. */
+mk_status mk_paged_append(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const mk_rope* rope, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                          void* q_out, int64_t q_out_stride, mk_stream stream);
+
+/* Attention of one query token per sequence over its kv_len tokens:
+ * out = softmax(scale q K^T) V per query head.  q, out: bf16 rows of
+ * n_q_heads x 128 (16-byte aligned, strides multiples of 8); batch->max_new
+ * must be 1 and a sequence without new tokens has no row.  lse (optional):
+ * fp32 [n_tokens][n_q_heads], the natural logarithm of the row's sum of
+ * exponentials.  A sequence of length 0 gives out = 0, lse = -infinity.
+ * The work is split over the tokens of all sequences by their lengths, read
+ * on the device.  On the device, a sequence with a bad length or page id sets
+ * the error word; its rows are then undefined. */
+mk_status mk_paged_decode_attn(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const void* q, int64_t q_stride,
+                               float scale, void* out, int64_t out_stride, float* lse, mk_stream stream);
+
+/* The same for several query tokens per sequence (a prompt's chunk,
+ * verification of drafted tokens, cross attention).  causal = 1: query j of
+ * n_new sees the first kv_len - n_new + j + 1 keys (none where that is <= 0:
+ * out = 0, lse = -infinity); causal = 0: every query sees all kv_len keys. */
+mk_status mk_paged_prefill_attn(mk_paged* h, int32_t layer, const mk_paged_batch* batch, int32_t causal, const void* q,
+                                int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
+                                mk_stream stream);
+
+/* As mk_poll_error and mk_clear_error, for a paged handle. */
+mk_status mk_paged_poll_error(mk_paged* h, int32_t* detail);
+mk_status mk_paged_clear_error(mk_paged* h);
+
 /* Waits for the device and reads the sticky error word: MK_OK, MK_EDEVICE or
  * MK_ETIMEOUT; *detail (optional) receives the kernel's detail code. */
 mk_status mk_poll_error(mk_ctx* ctx, int32_t* detail);
