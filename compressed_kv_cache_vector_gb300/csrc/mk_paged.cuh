@@ -1,6 +1,7 @@
 // Declarations shared by the paged cache's kernels and their host side.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_fp8.h>
 
 #include "mk_internal.cuh"
@@ -23,6 +24,21 @@ enum PagedErr : int32_t {
   ERR_PAGED_PAGE = 17,      // a page id outside [0, n_pages)
   ERR_PAGED_POSITION = 18,  // a rotary position outside [0, n_pos)
   ERR_PAGED_WAIT = 19,      // a copy or a matrix instruction did not complete within the wait bound (MK_ETIMEOUT)
+};
+
+constexpr int kPagedMaxCtas = 160;  // CTAs of a persistent attention kernel (GB300: 152 SMs)
+
+// Tensor maps of the pools, 128-byte swizzle, dimensions {128 channels,
+// kv head x page slot, layer x page}; a box is one 128-byte run of channels
+// (all of them in e4m3, half in bf16) by 16 or 32 tokens.
+struct PagedMaps {
+  CUtensorMap k, v;
+};
+// The workspace's parts that the attention kernels use.
+struct PagedScratch {
+  float* part_acc;
+  float* part_ml;
+  int32_t* counters;  // [max_seqs][n_kv], zero between calls
 };
 
 #ifdef __CUDACC__
@@ -56,6 +72,9 @@ __device__ __forceinline__ PagedSeq paged_seq(const mk_paged_batch& b, int P, in
 cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, const mk_rope& rope, const uint16_t* k,
                                 int64_t k_stride, const uint16_t* v, int64_t v_stride, const uint16_t* q,
                                 int64_t q_stride, uint16_t* q_out, int64_t q_out_stride, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale, uint16_t* out,
+                                int64_t out_stride, float* lse, cudaStream_t s);
 cudaError_t launch_paged_attn_simple(const PagedLayer& L, const mk_paged_batch& b, bool causal, const uint16_t* q,
                                      int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, float* lse,
                                      cudaStream_t s);

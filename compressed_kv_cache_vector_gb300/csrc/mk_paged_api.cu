@@ -14,6 +14,8 @@ struct mk_paged {
   char* ws;
   int64_t ws_clear;   // leading bytes of the workspace that must start at zero
   int64_t pool_layer, scale_layer;
+  mk::PagedMaps dec;        // boxes of the decode kernel
+  mk::PagedScratch scratch;
   int device;
 };
 
@@ -31,6 +33,7 @@ mk_status check(const mk_paged_config* c) {
   if (c->max_seqs < 1 || c->max_seqs > MK_MAX_CALL_SEQS) return MK_EINVAL;
   if (c->page != 16 && c->page != 32 && c->page != 64) return MK_EINVAL;
   if (c->kv_type != MK_KV_BF16 && c->kv_type != MK_KV_E4M3) return MK_EINVAL;
+  if ((int64_t)c->n_layers * c->n_pages > 0x7fffffff) return MK_EINVAL;  // a copy's coordinate
   return MK_OK;
 }
 inline int64_t elem(const mk_paged_config* c) { return c->kv_type == MK_KV_E4M3 ? 1 : 2; }
@@ -40,7 +43,39 @@ inline int64_t pool_layer_bytes(const mk_paged_config* c) {
 inline int64_t scale_layer_count(const mk_paged_config* c) {
   return c->kv_type == MK_KV_E4M3 ? (int64_t)c->n_pages * c->n_kv_heads : 0;
 }
-inline int64_t clear_bytes(const mk_paged_config*) { return kAlign; }
+// Workspace: [error word][counters, zero between calls][split-token parts].
+inline int64_t clear_bytes(const mk_paged_config* c) {
+  return align_up(kAlign + (int64_t)c->max_seqs * c->n_kv_heads * 4);
+}
+inline int64_t part_acc_bytes(const mk_paged_config* c) {
+  return align_up((int64_t)2 * mk::kPagedMaxCtas * (c->n_q_heads / c->n_kv_heads) * MK_HEAD_DIM * 4);
+}
+inline int64_t part_ml_bytes(const mk_paged_config* c) {
+  return align_up((int64_t)2 * mk::kPagedMaxCtas * (c->n_q_heads / c->n_kv_heads) * 2 * 4);
+}
+
+// The driver's tensor-map encoder, looked up through the runtime (the library
+// links no driver stub).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<EncodeFn>(fn);
+}
+bool pool_map(EncodeFn enc, const mk_paged_config* c, void* pool, int rows, CUtensorMap* m) {
+  const int64_t es = elem(c), row = MK_HEAD_DIM * es;
+  const cuuint64_t dim[3] = {MK_HEAD_DIM, (cuuint64_t)c->n_kv_heads * c->page, (cuuint64_t)c->n_layers * c->n_pages};
+  const cuuint64_t stride[2] = {(cuuint64_t)row, (cuuint64_t)(row * c->n_kv_heads * c->page)};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)rows, 1}, one[3] = {1, 1, 1};
+  return enc(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pool, dim, stride, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // Makes the handle's device current for the call and restores the caller's.
 struct DeviceGuard {
@@ -109,7 +144,7 @@ mk_status mk_paged_sizes(const mk_paged_config* cfg, size_t* pool_bytes, size_t*
   if (st != MK_OK) return st;
   if (pool_bytes) *pool_bytes = (size_t)(pool_layer_bytes(cfg) * cfg->n_layers);
   if (scale_bytes) *scale_bytes = (size_t)(scale_layer_count(cfg) * cfg->n_layers * 4);
-  if (workspace_bytes) *workspace_bytes = (size_t)align_up(clear_bytes(cfg));
+  if (workspace_bytes) *workspace_bytes = (size_t)(clear_bytes(cfg) + part_acc_bytes(cfg) + part_ml_bytes(cfg));
   return MK_OK;
 }
 
@@ -136,7 +171,16 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
   h->ws_clear = clear_bytes(cfg);
   h->pool_layer = pool_layer_bytes(cfg);
   h->scale_layer = scale_layer_count(cfg);
+  h->scratch.counters = reinterpret_cast<int32_t*>(h->ws + kAlign);
+  h->scratch.part_acc = reinterpret_cast<float*>(h->ws + h->ws_clear);
+  h->scratch.part_ml = reinterpret_cast<float*>(h->ws + h->ws_clear + part_acc_bytes(cfg));
   cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) {
+    const EncodeFn enc = encoder();
+    const int rows = e4m3 && cfg->page >= 32 ? 32 : 16;
+    if (!enc || !pool_map(enc, cfg, k_pool, rows, &h->dec.k) || !pool_map(enc, cfg, v_pool, rows, &h->dec.v))
+      e = cudaErrorInvalidValue;
+  }
   if (e == cudaSuccess) e = cudaMemset(workspace, 0, (size_t)h->ws_clear);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
@@ -183,8 +227,8 @@ mk_status mk_paged_decode_attn(mk_paged* h, int32_t layer, const mk_paged_batch*
   DeviceGuard dev(h->device);
   if (!dev.ok) return MK_ECUDA;
   const cudaError_t e =
-      mk::launch_paged_attn_simple(layer_of(h, layer), *batch, true, static_cast<const uint16_t*>(q), q_stride, scale,
-                                   static_cast<uint16_t*>(out), out_stride, lse, (cudaStream_t)stream);
+      mk::launch_paged_decode(layer_of(h, layer), h->dec, h->scratch, layer, *batch, static_cast<const uint16_t*>(q),
+                              q_stride, scale, static_cast<uint16_t*>(out), out_stride, lse, (cudaStream_t)stream);
   return e == cudaSuccess ? MK_OK : MK_ECUDA;
 }
 

@@ -130,12 +130,12 @@ __device__ __forceinline__ int clamp_position(const PagedLayer& L, const mk_rope
 
 template <int P, bool E4M3>
 __global__ void __launch_bounds__(kThreads) k_paged_append(PagedLayer L, AppendArgs a) {
-  __shared__ int s_pre[MK_MAX_CALL_SEQS + 1], s_wsum[kThreads / 32], s_seq, s_idx;
+  __shared__ int s_wsum[kThreads / 32], s_seq, s_idx;
   __shared__ float s_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = tid & 15, rr = tid >> 4;
   pdl_wait();
   pdl_trigger();
-  if (paged_has_error(L)) return;
+  if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;  // one thread's reading for the CTA
 
   if ((int)blockIdx.x >= a.n_units) {  // a query CTA: kQRows rows (token, query head)
     const int n_q = L.n_kv * L.G;
@@ -212,7 +212,6 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(PagedLayer L, AppendA
     idx = s_idx;
     if (seq < 0) return;
   }
-  (void)s_pre;
   const PagedSeq sq = paged_seq(a.b, P, seq, true);
   if (!sq.ok) {
     if (tid == 0) paged_error(L, ERR_PAGED_BATCH, seq, sq.len);

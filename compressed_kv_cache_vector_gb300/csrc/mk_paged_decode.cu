@@ -1,0 +1,627 @@
+// Attention of single tokens over the paged cache (bf16, or e4m3 with a scale
+// per page and head).
+//
+// Mathematics.  With z_t = scale q.k_t, out = sum_t e^(z_t) v_t / sum_t e^(z_t),
+// kept as a running maximum, sum and accumulator in fp32, base 2.  In e4m3,
+// k_t = a_p K_t and v_t = b_p V_t with one a_p, b_p per page: a_p multiplies
+// the logit, and b_p is added to it as log2 b_p, so that the weight that
+// multiplies the codes is 2^(z_t + log2 b_p - m); the sum of the plain weights
+// takes it back with 1 / b_p.  The maximum m is over z_t + log2 b_p: the
+// weights that reach the value product are relative to the largest
+// contribution, whatever the pages' scales.
+//
+// What bounds it: HBM, each page is read once for all query heads that share
+// it (4 flops a byte and head).  The layout therefore follows the loads:
+//  * Work split on the device, from the lengths: the tokens of all (sequence,
+//    kv head) units are cut into chunks (32 tokens in e4m3, 16 in bf16: 8 KB of
+//    keys and values), and every CTA takes an equal run of the flat list of
+//    chunks, so a batch of uneven lengths and a single long context load the
+//    SMs alike and no length is needed on the host.
+//  * Each warp has its own ring of stages, filled by tensor copies with a
+//    128-byte swizzle (no barrier between warps while a unit lasts); page ids
+//    are read one chunk ahead of the copy that needs them.
+//  * e4m3 codes become fp16 (exact) and q, scaled by a power of two per head
+//    so that it fits, fp16 too; products on mma.sync m16n8k16.  Few rows: the
+//    tensor cores idle either way, and this form needs no shared-memory
+//    round trip for the weights.  S = Q K^T puts a head's weights in the lanes
+//    that hold them as the B operand of O^T = V^T P.  V's transpose is taken
+//    in registers: a lane loads 16 channels of 4 tokens and pairs bytes of two
+//    tokens, one permute and two conversions for four elements.
+//  * The weights are rounded to fp16 after a factor 2^14 (smallest step
+//    2^-38 of the largest weight: a long flat tail under one dominant token
+//    is not lost); for bf16 values they are two bf16 parts (16 bits).
+//  * A unit that lies in several CTAs is joined by the last of them to arrive
+//    (counter, no waiting), in the order of the parts: the same result in
+//    every run.
+#include "mk_paged.cuh"
+
+namespace mk {
+
+namespace {
+
+constexpr int kStageBytes = 8192;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct DecodeArgs {
+  mk_paged_batch b;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  int64_t q_stride, out_stride;
+  float scale;          // times log2 e
+  int32_t layer_page0;  // first page of the layer in the maps
+  int32_t min_chunks;   // fewest chunks of a CTA
+  float* part_acc;      // [2 grid][G][128]
+  float* part_ml;       // [2 grid][G][2]
+  int32_t* counters;    // [max_seqs][n_kv]
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes (low 16 bits) as two halves.
+__device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
+  uint32_t r;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A place in the flat list of chunks: chunk ch of (sequence seq, kv head).
+struct Cursor {
+  int seq, head, ch;
+};
+
+template <bool E4M3, int NW, int NS>
+struct DecodeSmem {
+  static constexpr int CH = E4M3 ? 32 : 16;  // tokens of a chunk
+  static constexpr int ring = NW * NS * kStageBytes;
+  static int bytes(int G) { return 1024 + ring + NW * G * D * 4; }
+};
+
+template <bool E4M3, int NW, int NS>
+__global__ void __launch_bounds__(NW * 32, 1)
+    k_paged_decode(PagedLayer L, DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap) {
+  constexpr int CH = DecodeSmem<E4M3, NW, NS>::CH, NT = CH / 8, NTHR = NW * 32;
+  constexpr float kShift = E4M3 ? 14.0f : 0.0f;  // weights times 2^kShift before their rounding
+  extern __shared__ unsigned char dyn[];
+  __shared__ int64_t s_pre[MK_MAX_CALL_SEQS + 1];
+  __shared__ int s_len[MK_MAX_CALL_SEQS], s_row[MK_MAX_CALL_SEQS];
+  __shared__ int64_t s_wsum[NW];
+  __shared__ __align__(8) uint64_t s_bar[NW][NS];
+  __shared__ __align__(16) float s_sc[NW][NS][4];  // k scale of box 0, 1; v scale of box 0, 1
+  __shared__ float s_ml[NW][MK_MAX_GROUP][2];
+  __shared__ float s_M[MK_MAX_GROUP], s_L[MK_MAX_GROUP];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  unsigned char* ring = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023);
+  float* s_acc = reinterpret_cast<float*>(ring + DecodeSmem<E4M3, NW, NS>::ring);
+  const int n_kv = L.n_kv, G = L.G, n_seqs = a.b.n_seqs;
+
+  if (lane == 0)
+    for (int i = 0; i < NS; ++i) mbar_init(&s_bar[warp][i], E4M3 ? 5 : 1);
+  mbar_init_fence();
+  pdl_wait();
+  pdl_trigger();
+  if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;  // one thread's reading for the CTA
+
+  // The list of chunks: exclusive prefix over the sequences, in chunks of all heads.
+  int64_t base = 0;
+  for (int i0 = 0; i0 < n_seqs; i0 += NTHR) {
+    const int i = i0 + tid;
+    int64_t mine = 0;
+    if (i < n_seqs) {
+      const PagedSeq s = paged_seq(a.b, L.P, i, false);
+      if (!s.ok) paged_error(L, ERR_PAGED_BATCH, i, s.len);
+      const bool live = s.ok && s.n_new == 1;
+      s_len[i] = live ? s.len : 0;
+      s_row[i] = live ? s.row0 : -1;
+      mine = live ? (int64_t)((s.len + CH - 1) / CH) * n_kv : 0;
+    }
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(FULL, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_wsum[warp] = x;
+    __syncthreads();
+    int64_t off = base;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) off += s_wsum[w];
+      base += s_wsum[w];
+    }
+    if (i < n_seqs) s_pre[i] = off + x - mine;
+    __syncthreads();
+  }
+  if (tid == 0) s_pre[n_seqs] = base;
+  __syncthreads();
+  const int64_t total = base;
+
+  // Rows of empty sequences.
+  for (int i = blockIdx.x; i < n_seqs; i += gridDim.x)
+    if (s_row[i] >= 0 && s_len[i] == 0) {
+      for (int e = tid; e < n_kv * G * D / 8; e += NTHR)
+        *reinterpret_cast<uint4*>(a.out + (int64_t)s_row[i] * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int e = tid; e < n_kv * G; e += NTHR) a.lse[(int64_t)s_row[i] * n_kv * G + e] = -INFINITY;
+    }
+
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < a.min_chunks) per = a.min_chunks;
+  const int64_t c0 = (int64_t)blockIdx.x * per;
+  const int64_t c1 = c0 + per < total ? c0 + per : total;
+  if (c0 >= c1) return;
+  const int n_flat = (int)(c1 - c0);
+
+  auto n_chunks = [&](int seq) { return (s_len[seq] + CH - 1) / CH; };
+  Cursor first;
+  {
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {  // the last sequence whose prefix is <= c0 and that has chunks
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_pre[mid] <= c0) lo = mid; else hi = mid - 1;
+    }
+    const int64_t rem = c0 - s_pre[lo];
+    const int n = n_chunks(lo);
+    first.seq = lo;
+    first.head = (int)(rem / n);
+    first.ch = (int)(rem - (int64_t)first.head * n);
+  }
+  auto advance = [&](Cursor& k, int by) {
+    k.ch += by;
+    while (k.seq < n_seqs) {
+      const int n = n_chunks(k.seq);
+      if (k.ch < n) break;
+      k.ch -= n;
+      if (n == 0 || ++k.head == n_kv) {
+        k.head = 0;
+        ++k.seq;
+      }
+    }
+  };
+
+  // ---- the warp's copies ----
+  const int box = E4M3 ? (L.P < 32 ? L.P : 32) : 16;  // tokens of one copy
+  const int n_box = CH / box;
+  Cursor ic = first;
+  int issued = warp;  // flat index of the next chunk to copy
+  advance(ic, warp);
+  int pid = 0;
+  auto fetch_pid = [&]() {
+    if (issued < n_flat && lane < n_box) {
+      const int p = (ic.ch * CH + lane * box) >> L.p_log2;
+      if (ic.ch * CH + lane * box < s_len[ic.seq]) pid = a.b.page_table[(int64_t)ic.seq * a.b.table_stride + p];
+    }
+  };
+  auto issue = [&](int stage) {
+    if (issued >= n_flat) return;
+    const int valid = s_len[ic.seq] - ic.ch * CH;  // tokens from the chunk's start
+    if (lane < n_box && lane * box < valid && (pid < 0 || pid >= L.n_pages)) {
+      paged_error(L, ERR_PAGED_PAGE, ic.seq, pid);
+      pid = 0;
+    }
+    const int boxes = valid >= CH ? n_box : (valid + box - 1) / box;
+    unsigned char* st = ring + (warp * NS + stage) * kStageBytes;
+    uint64_t* bar = &s_bar[warp][stage];
+    fence_proxy_async();  // this warp's earlier accesses to the stage come before the copies
+    const int p0 = __shfl_sync(FULL, pid, 0), p1 = __shfl_sync(FULL, pid, 1);
+    if (lane == 0) {
+      mbar_expect_tx(bar, boxes * box * (E4M3 ? 2 * D : 4 * D));
+      const int y = ic.head * L.P + ((ic.ch * CH) & (L.P - 1));
+      for (int i = 0; i < boxes; ++i) {
+        const int z = a.layer_page0 + (i ? p1 : p0);
+        if (E4M3) {
+          tma3(smem_u32(st) + i * box * D, &kmap, 0, y, z, bar);
+          tma3(smem_u32(st) + 4096 + i * box * D, &vmap, 0, y, z, bar);
+        } else {
+          tma3(smem_u32(st), &kmap, 0, y, z, bar);
+          tma3(smem_u32(st) + 2048, &kmap, 64, y, z, bar);
+          tma3(smem_u32(st) + 4096, &vmap, 0, y, z, bar);
+          tma3(smem_u32(st) + 6144, &vmap, 64, y, z, bar);
+        }
+      }
+    }
+    if (E4M3 && lane < 4) {
+      float* to = &s_sc[warp][stage][lane];
+      const int i = lane & 1;
+      if (i < boxes) {
+        const float* from = (lane < 2 ? L.k_scale : L.v_scale) + (int64_t)(i ? p1 : p0) * n_kv + ic.head;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+      } else {
+        *to = 1.0f;
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    }
+    issued += NW;
+    if (issued < n_flat) advance(ic, NW);
+    fetch_pid();
+  };
+
+  fetch_pid();
+#pragma unroll
+  for (int i = 0; i < NS; ++i) issue(i);
+  __syncwarp();
+
+  // ---- the units ----
+  const uint32_t kRow = (uint32_t)(lane & 7) * 128u, kXor = (uint32_t)(lane & 7);
+  int flat = warp, fs = 0, stage = 0;  // the warp's next chunk; the unit's first flat index; ring place
+  unsigned phase = 0;
+  bool dead = false;
+  Cursor u = first;
+  while (fs < n_flat) {
+    const int len = s_len[u.seq], nch = n_chunks(u.seq);
+    const int fe = min(n_flat, fs + nch - u.ch);  // the unit's chunks of this CTA: flat [fs, fe)
+    const int row = s_row[u.seq];
+
+    // The unit's queries as A fragments: row g = head g.  e4m3: fp16 after a
+    // power of two per head, in the channel order that the codes' pairs have.
+    uint32_t qa[8], qb[8];
+    float zf = a.scale;
+    {
+      const uint16_t* qp = a.q + (int64_t)row * a.q_stride + (u.head * G + (g < G ? g : 0)) * D;
+      if (E4M3) {
+        uint2 w[8];
+        float top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          w[s] = g < G ? *reinterpret_cast<const uint2*>(qp + 16 * s + 4 * c) : make_uint2(0, 0);
+          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf2f(w[s].x & 0xffff)), fabsf(bf2f(w[s].x >> 16))),
+                                 fmaxf(fabsf(bf2f(w[s].y & 0xffff)), fabsf(bf2f(w[s].y >> 16)))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        e = max(-100, min(e, 120));
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        zf *= __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          qa[s] = pack_h2(bf2f(w[s].x & 0xffff) * down, bf2f(w[s].x >> 16) * down);
+          qb[s] = pack_h2(bf2f(w[s].y & 0xffff) * down, bf2f(w[s].y >> 16) * down);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          qa[s] = g < G ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * c) : 0u;
+          qb[s] = g < G ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 8 + 2 * c) : 0u;
+        }
+      }
+    }
+    float m = -INFINITY, l = 0.0f;
+    float o[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+
+    for (; flat < fe; flat += NW) {
+      const int tok0 = (u.ch + flat - fs) * CH;
+      const int valid = min(CH, len - tok0);
+      unsigned char* st = ring + (warp * NS + stage) * kStageBytes;
+      // After a wait that ran out nothing more is copied; what is in flight is
+      // still waited for (with the same limit) before the kernel ends.
+      if (flat < issued && !mbar_wait_warp(&s_bar[warp][stage], phase)) {
+        dead = true;
+        if (lane == 0) paged_error(L, ERR_PAGED_WAIT, u.seq, flat, (int32_t)MK_ETIMEOUT);
+      }
+      if (!dead) {
+        const uint32_t kb = smem_u32(st), vb = kb + 4096;
+        if (valid < CH) {  // slots past the length hold anything: their values must not reach 0 * value
+          for (int r = valid + (lane >> 3); r < CH; r += 4) {
+            const uint32_t at = vb + r * 128 + (lane & 7) * 16;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at), "r"(0) : "memory");
+            if (!E4M3) asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(at + 2048), "r"(0) : "memory");
+          }
+          __syncwarp();
+        }
+        // logits: rows = heads, columns = tokens 8 nt + 2 c (+ 1)
+        float z[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (E4M3) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[4];
+              ldsm4(r, kb + nt * 1024 + kRow + (((uint32_t)(4 * h + (lane >> 3)) ^ kXor) << 4));
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                mma16<true>(acc, qa[4 * h + s], 0u, qb[4 * h + s], 0u, e4m3_h2(r[s]), e4m3_h2(r[s] >> 16));
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              uint32_t r[4];
+              ldsm4(r, kb + (h >> 1) * 2048 + nt * 1024 + kRow + (((uint32_t)(4 * (h & 1) + (lane >> 3)) ^ kXor) << 4));
+              mma16<false>(acc, qa[2 * h], 0u, qb[2 * h], 0u, r[0], r[1]);
+              mma16<false>(acc, qa[2 * h + 1], 0u, qb[2 * h + 1], 0u, r[2], r[3]);
+            }
+          }
+          z[nt][0] = acc[0];
+          z[nt][1] = acc[1];
+        }
+        float inv[2] = {1.0f, 1.0f};
+        if (E4M3) {
+          const float4 sc = *reinterpret_cast<const float4*>(&s_sc[warp][stage][0]);
+          const bool two = box < 32;
+          const float k0 = zf * sc.x, k1 = two ? zf * sc.y : k0, v1 = two ? sc.w : sc.z;
+          const float b0 = __log2f(sc.z), b1 = __log2f(v1);
+          inv[0] = __frcp_rn(sc.z);
+          inv[1] = __frcp_rn(v1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) z[nt][e] = fmaf(z[nt][e], nt < 2 ? k0 : k1, nt < 2 ? b0 : b1);
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) z[nt][e] *= zf;
+        }
+        if (valid < CH) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (8 * nt + 2 * c + e >= valid) z[nt][e] = -INFINITY;
+        }
+        float mx = z[0][0];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(z[nt][0], z[nt][1]));
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+        if (__any_sync(FULL, mx > m)) {
+          const float mn = fmaxf(m, mx);
+          const float cr = m == -INFINITY ? 0.0f : ex2(m - mn);
+          m = mn;
+          l *= cr;
+          const float c0f = __shfl_sync(FULL, cr, 8 * c), c1f = __shfl_sync(FULL, cr, 8 * c + 4);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            o[n][0] *= c0f;
+            o[n][1] *= c1f;
+            o[n][2] *= c0f;
+            o[n][3] *= c1f;
+          }
+        }
+        const float ms = (m == -INFINITY ? 0.0f : m) - kShift;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          z[nt][0] = ex2(z[nt][0] - ms);
+          z[nt][1] = ex2(z[nt][1] - ms);
+          l = E4M3 ? fmaf(z[nt][0] + z[nt][1], inv[nt >> 1], l) : l + (z[nt][0] + z[nt][1]);
+        }
+        // values: rows = channels, columns = heads
+        if (E4M3) {
+#pragma unroll
+          for (int t = 0; t < CH / 16; ++t) {
+            const uint32_t p0 = pack_h2(z[2 * t][0], z[2 * t][1]), p1 = pack_h2(z[2 * t + 1][0], z[2 * t + 1][1]);
+            const uint32_t r0 = vb + (16 * t + 2 * c) * 128;
+            const uint32_t x0 = ((uint32_t)g ^ (uint32_t)(2 * c)) << 4, x1 = ((uint32_t)g ^ (uint32_t)(2 * c + 1)) << 4;
+            const uint4 w0 = lds128(r0 + x0), w1 = lds128(r0 + 128 + x1), w2 = lds128(r0 + 1024 + x0),
+                        w3 = lds128(r0 + 1152 + x1);
+            const uint32_t a0[4] = {w0.x, w0.y, w0.z, w0.w}, a1[4] = {w1.x, w1.y, w1.z, w1.w},
+                           a2[4] = {w2.x, w2.y, w2.z, w2.w}, a3[4] = {w3.x, w3.y, w3.z, w3.w};
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const uint32_t x = __byte_perm(a0[n >> 1], a1[n >> 1], n & 1 ? 0x7362 : 0x5140);
+              const uint32_t y = __byte_perm(a2[n >> 1], a3[n >> 1], n & 1 ? 0x7362 : 0x5140);
+              mma16<true>(o[n], e4m3_h2(x), e4m3_h2(x >> 16), e4m3_h2(y), e4m3_h2(y >> 16), p0, p1);
+            }
+          }
+        } else {
+          const uint32_t p0 = pack_b2(z[0][0], z[0][1]), p1 = pack_b2(z[1][0], z[1][1]);
+          const uint32_t q0 = pack_b2(z[0][0] - bf2f(p0 & 0xffff), z[0][1] - bf2f(p0 >> 16));
+          const uint32_t q1 = pack_b2(z[1][0] - bf2f(p1 & 0xffff), z[1][1] - bf2f(p1 >> 16));
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            uint32_t r[4];
+            const int tr = ((lane >> 4) & 1) * 8 + (lane & 7), ck = 2 * n + ((lane >> 3) & 1);
+            ldsm4_t(r, vb + (ck >> 3) * 2048 + tr * 128 + (((uint32_t)(ck & 7) ^ kXor) << 4));
+            mma16<false>(o[n], r[0], r[1], r[2], r[3], p0, p1);
+            mma16<false>(o[n], r[0], r[1], r[2], r[3], q0, q1);
+          }
+        }
+      }
+      __syncwarp();
+      if (!dead) issue(stage);
+      if (++stage == NS) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+
+    // ---- join the warps ----
+    l += __shfl_xor_sync(FULL, l, 1);
+    l += __shfl_xor_sync(FULL, l, 2);
+    if (c == 0) {
+      s_ml[warp][g][0] = m;
+      s_ml[warp][g][1] = l;
+    }
+    __syncthreads();
+    if (warp == 0 && c == 0) {
+      float M = -INFINITY, S = 0.0f;
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][g][0]);
+      for (int w = 0; w < NW; ++w)
+        if (s_ml[w][g][0] != -INFINITY) S += s_ml[w][g][1] * ex2(s_ml[w][g][0] - M);
+      s_M[g] = M;
+      s_L[g] = S;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int h = 2 * c + e;
+      if (h < G) {
+        float M = -INFINITY;
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][h][0]);
+        const float f = s_ml[warp][h][0] == -INFINITY ? 0.0f : ex2(s_ml[warp][h][0] - M);
+        float* to = s_acc + (warp * G + h) * D;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          if (E4M3) {
+            *reinterpret_cast<float2*>(to + 16 * g + 2 * n) = make_float2(o[n][e] * f, o[n][2 + e] * f);
+          } else {
+            to[16 * n + g] = o[n][e] * f;
+            to[16 * n + 8 + g] = o[n][2 + e] * f;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = u.ch == 0 && fe - fs == nch;
+    const int64_t part = 2 * (int64_t)blockIdx.x + (u.ch == 0 ? 1 : 0);
+    const int64_t orow = (int64_t)row * a.out_stride + (int64_t)u.head * G * D;
+    for (int e = tid; e < G * D / 2; e += NTHR) {
+      float x = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(s_acc + w * G * D + 2 * e);
+        x += v.x;
+        y += v.y;
+      }
+      if (whole) {
+        const float r = 1.0f / s_L[e >> 6];
+        *reinterpret_cast<uint32_t*>(a.out + orow + 2 * e) = pack_b2(x * r, y * r);
+      } else {
+        *reinterpret_cast<float2*>(a.part_acc + part * G * D + 2 * e) = make_float2(x, y);
+      }
+    }
+    if (tid < G) {
+      if (whole) {
+        if (a.lse)
+          a.lse[(int64_t)row * n_kv * G + u.head * G + tid] =
+              (log2f(s_L[tid]) + (s_M[tid] - kShift)) * 0.6931471805599453f;
+      } else {
+        a.part_ml[(part * G + tid) * 2] = s_M[tid];
+        a.part_ml[(part * G + tid) * 2 + 1] = s_L[tid];
+      }
+    }
+    if (!whole) {
+      // CTAs that hold a part of this unit: b_lo .. b_hi; the last to arrive joins them.
+      const int64_t u0 = s_pre[u.seq] + (int64_t)u.head * nch;
+      const int b_lo = (int)(u0 / per), b_hi = (int)((u0 + nch - 1) / per), parts = b_hi - b_lo + 1;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        int32_t* ctr = a.counters + (int64_t)u.seq * n_kv + u.head;
+        const int old = atomicAdd(ctr, 1);
+        s_last = old == parts - 1;
+        if (s_last) *ctr = 0;
+      }
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        auto slot = [&](int i) { return 2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0); };
+        for (int h = warp; h < G; h += NW) {  // a warp per head: the joined maximum and sum
+          float M = -INFINITY, S = 0.0f;
+          for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(a.part_ml + (slot(i) * G + h) * 2));
+          M = warp_max(M);
+          for (int i = lane; i < parts; i += 32)
+            S += __ldcg(a.part_ml + (slot(i) * G + h) * 2 + 1) * ex2(__ldcg(a.part_ml + (slot(i) * G + h) * 2) - M);
+          S = warp_sum(S);
+          if (lane == 0) {
+            s_M[h] = M;
+            s_L[h] = S;
+          }
+        }
+        __syncthreads();
+        for (int e = tid; e < G * D / 2; e += NTHR) {
+          const int h = e >> 6;
+          const float M = s_M[h], r = 1.0f / s_L[h];
+          float x = 0.0f, y = 0.0f;
+#pragma unroll 8
+          for (int i = 0; i < parts; ++i) {
+            const float f = ex2(__ldcg(a.part_ml + (slot(i) * G + h) * 2) - M);
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_acc + slot(i) * G * D + 2 * e));
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+          }
+          *reinterpret_cast<uint32_t*>(a.out + orow + 2 * e) = pack_b2(x * r, y * r);
+        }
+        if (a.lse && tid < G)
+          a.lse[(int64_t)row * n_kv * G + u.head * G + tid] =
+              (log2f(s_L[tid]) + (s_M[tid] - kShift)) * 0.6931471805599453f;
+      }
+    }
+    __syncthreads();  // s_ml, s_acc, s_M, s_L are free again
+    fs = fe;
+    u.ch = 0;
+    if (++u.head == n_kv) {
+      u.head = 0;
+      ++u.seq;
+    }
+    while (u.seq < n_seqs && n_chunks(u.seq) == 0) ++u.seq;
+  }
+}
+
+template <bool E4M3, int NW, int NS>
+cudaError_t launch(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, cudaStream_t s) {
+  const int bytes = DecodeSmem<E4M3, NW, NS>::bytes(L.G);
+  int sms = 0;
+  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, NS>, bytes, NW * 32, nullptr, &sms);
+  if (e != cudaSuccess) return e;
+  const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
+  a.min_chunks = NW;
+  return launch_pdl(k_paged_decode<E4M3, NW, NS>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale, uint16_t* out,
+                                int64_t out_stride, float* lse, cudaStream_t s) {
+  DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 1, w.part_acc, w.part_ml, w.counters};
+  // Eight heads' joining buffer (32 KB) leaves room for two stages a warp.
+  if (L.G == 8) return L.e4m3 ? launch<true, 8, 2>(L, maps, a, s) : launch<false, 8, 2>(L, maps, a, s);
+  return L.e4m3 ? launch<true, 8, 3>(L, maps, a, s) : launch<false, 8, 3>(L, maps, a, s);
+}
+
+}  // namespace mk
