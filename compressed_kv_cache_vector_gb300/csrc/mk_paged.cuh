@@ -38,8 +38,11 @@ struct PagedMaps {
 struct PagedScratch {
   float* part_acc;
   float* part_ml;
-  int32_t* counters;  // [max_seqs][n_kv], zero between calls
+  int32_t* counters;          // [max_seqs][n_kv], zero between calls
+  int32_t* prefill_counters;  // [kPagedMaxCtas], zero between calls
+  float* prefill_part;        // paged_prefill_part_floats()
 };
+int64_t paged_prefill_part_floats();
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void paged_error(const PagedLayer& L, int32_t detail, int32_t seq, int32_t aux,
@@ -75,8 +78,8 @@ cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, co
 cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale, uint16_t* out,
                                 int64_t out_stride, float* lse, cudaStream_t s);
-cudaError_t launch_paged_attn_simple(const PagedLayer& L, const mk_paged_batch& b, bool causal, const uint16_t* q,
-                                     int64_t q_stride, float scale, uint16_t* out, int64_t out_stride, float* lse,
-                                     cudaStream_t s);
+cudaError_t launch_paged_prefill(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, bool causal,
+                                 const uint16_t* q, int64_t q_stride, float scale, uint16_t* out, int64_t out_stride,
+                                 float* lse, cudaStream_t s);
 
 }  // namespace mk

@@ -45,7 +45,7 @@ inline int64_t scale_layer_count(const mk_paged_config* c) {
 }
 // Workspace: [error word][counters, zero between calls][split-token parts].
 inline int64_t clear_bytes(const mk_paged_config* c) {
-  return align_up(kAlign + (int64_t)c->max_seqs * c->n_kv_heads * 4);
+  return align_up(kAlign + ((int64_t)c->max_seqs * c->n_kv_heads + mk::kPagedMaxCtas) * 4);
 }
 inline int64_t part_acc_bytes(const mk_paged_config* c) {
   return align_up((int64_t)2 * mk::kPagedMaxCtas * (c->n_q_heads / c->n_kv_heads) * MK_HEAD_DIM * 4);
@@ -53,6 +53,8 @@ inline int64_t part_acc_bytes(const mk_paged_config* c) {
 inline int64_t part_ml_bytes(const mk_paged_config* c) {
   return align_up((int64_t)2 * mk::kPagedMaxCtas * (c->n_q_heads / c->n_kv_heads) * 2 * 4);
 }
+
+inline int64_t prefill_part_bytes() { return align_up(mk::paged_prefill_part_floats() * 4); }
 
 // The driver's tensor-map encoder, looked up through the runtime (the library
 // links no driver stub).
@@ -144,7 +146,7 @@ mk_status mk_paged_sizes(const mk_paged_config* cfg, size_t* pool_bytes, size_t*
   if (st != MK_OK) return st;
   if (pool_bytes) *pool_bytes = (size_t)(pool_layer_bytes(cfg) * cfg->n_layers);
   if (scale_bytes) *scale_bytes = (size_t)(scale_layer_count(cfg) * cfg->n_layers * 4);
-  if (workspace_bytes) *workspace_bytes = (size_t)(clear_bytes(cfg) + part_acc_bytes(cfg) + part_ml_bytes(cfg));
+  if (workspace_bytes) *workspace_bytes = (size_t)(clear_bytes(cfg) + part_acc_bytes(cfg) + part_ml_bytes(cfg) + prefill_part_bytes());
   return MK_OK;
 }
 
@@ -172,8 +174,10 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
   h->pool_layer = pool_layer_bytes(cfg);
   h->scale_layer = scale_layer_count(cfg);
   h->scratch.counters = reinterpret_cast<int32_t*>(h->ws + kAlign);
+  h->scratch.prefill_counters = h->scratch.counters + (int64_t)cfg->max_seqs * cfg->n_kv_heads;
   h->scratch.part_acc = reinterpret_cast<float*>(h->ws + h->ws_clear);
   h->scratch.part_ml = reinterpret_cast<float*>(h->ws + h->ws_clear + part_acc_bytes(cfg));
+  h->scratch.prefill_part = reinterpret_cast<float*>(h->ws + h->ws_clear + part_acc_bytes(cfg) + part_ml_bytes(cfg));
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) {
     const EncodeFn enc = encoder();
@@ -241,9 +245,9 @@ mk_status mk_paged_prefill_attn(mk_paged* h, int32_t layer, const mk_paged_batch
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return MK_OK;
   DeviceGuard dev(h->device);
   if (!dev.ok) return MK_ECUDA;
-  const cudaError_t e = mk::launch_paged_attn_simple(
-      layer_of(h, layer), *batch, causal != 0, static_cast<const uint16_t*>(q), q_stride, scale,
-      static_cast<uint16_t*>(out), out_stride, lse, (cudaStream_t)stream);
+  const cudaError_t e = mk::launch_paged_prefill(layer_of(h, layer), h->scratch, *batch, causal != 0,
+                                                 static_cast<const uint16_t*>(q), q_stride, scale,
+                                                 static_cast<uint16_t*>(out), out_stride, lse, (cudaStream_t)stream);
   return e == cudaSuccess ? MK_OK : MK_ECUDA;
 }
 

@@ -1,0 +1,791 @@
+// Attention of several query tokens per sequence over the paged cache: prompt
+// chunks, verification of drafted tokens, cross attention.
+//
+// Mathematics as in mk_paged_decode.cu; one row per (query token, query head
+// of the kv head's group), so the heads of a group share every key and value
+// tile.  A tile of 256 rows is two accumulators of 128 rows.
+//
+// What bounds it: the tensor cores (4 x 128 flops a pair) and, at the same
+// order, the exponentials.  Hence the 5th-generation tensor cores with every
+// accumulator in tensor memory, and two row tiles in turn: while one tile's
+// weights are formed, the products of the other run.  One CTA per SM:
+//  * warps 0-3 and 4-7: the softmax of row tile 0 and 1, one row a thread;
+//  * warps 8-11: keys and values into shared memory (e4m3 codes to fp16 on the
+//    way, exact; rows past the length as zeros), two stages each;
+//  * warp 12: issues the products.  S = Q K^T into tensor memory; the weights
+//    replace S there in 16 bits and are the A operand of O += P V.
+// The order of issue, S(0)0 S(1)0 | P(0)V S(0) P(1)V S(1) | ..., makes the
+// completion of a tile's S also that of its previous value product, so one
+// barrier covers both.
+//  * The running maximum is raised only when a row's logits pass it by 2^4
+//    (fp16 weights) or 2^8 (bf16): only then is the accumulator rescaled.
+//    e4m3: weights in fp16 after a factor 2^10 (at most 2^14, smallest step
+//    2^-34 of the maximum's); bf16: weights in bf16 (2^-9 each).
+//  * When there are fewer row tiles than SMs, the keys of a row tile are
+//    split over several CTAs by their count; the last CTA of a tile to arrive
+//    joins the parts in their order.
+#include "mk_paged.cuh"
+
+namespace mk {
+
+namespace {
+
+constexpr int kRows = 256;                 // rows of a work item: two tiles of 128
+constexpr int kKeys = 128;                 // keys of a step
+constexpr int kTile = kKeys * D * 2;       // 32 KB: a 16-bit tile
+constexpr int kHalf = kTile / 2;           // its channels 0-63, then 64-127
+constexpr int kThreads = 416;              // 8 softmax warps, 4 loading warps, 1 issuing warp
+constexpr int kSmem = 1024 + 2 * kTile + 4 * kTile;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct PrefillArgs {
+  mk_paged_batch b;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  int64_t q_stride, out_stride;
+  float scale;        // |scale| log2 e
+  uint32_t q_sign;    // 0x80008000 when the scale is negative
+  int32_t causal;
+  float* part;        // [2 x kPagedMaxCtas][128 / 4][kRows] float4, then [..][2][kRows]: see part_of
+  int32_t* counters;  // [kPagedMaxCtas]
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
+  uint32_t r;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(two));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Descriptor of a 128-byte-swizzled operand: rows of 128 bytes, groups of 8
+// rows 1024 bytes apart.  Along the rows' direction (K-major: Q, K) `lbo` has
+// no use; for an operand whose rows run along the products' K (V), it is the
+// distance between its two 64-channel halves.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t lbo) {
+  uint64_t d = (uint64_t)((addr >> 4) & 0x3fffu);
+  d |= (uint64_t)((lbo >> 4) & 0x3fffu) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// D (128 x 128, fp32): fp16 (0) or bf16 (1) operands; B along N when b_mn.
+__host__ __device__ constexpr uint32_t idesc(int bf16, int b_mn) {
+  return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)b_mn << 16) | ((uint32_t)(128 >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int acc) {
+  umma_bf16(d, a, b, id, acc);  // kind::f16; the descriptor names the type
+}
+// A from tensor memory.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, int acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
+}
+// Values loaded by earlier tmem_ld32_async may be used after this: they pass
+// through it so that no use is moved before the wait.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                 "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])::"memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
+      "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(
+          v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// One work item: a row tile of one (sequence, kv head) against keys
+// [j0, j1) x 128, part `part` of `parts`.
+struct Item {
+  int seq, head, q0, row0, n_new, len, see_max, j0, j1, parts, slot, ctr;
+};
+
+struct Shared {
+  int pre[MK_MAX_CALL_SEQS + 1];       // row tiles x kv heads before each sequence
+  int row0[MK_MAX_CALL_SEQS], n_new[MK_MAX_CALL_SEQS], len[MK_MAX_CALL_SEQS];
+  int epre[kPagedMaxCtas + 1];         // split: entries before each row tile of the batch
+  int eparts[kPagedMaxCtas];
+  int wsum[16];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], k_full[2], k_free[2], v_full[2], v_free[2];
+  float kf[4][8], lsv[4][8], inv[4][8];  // e4m3: per 16 keys of a step, ring of 4 steps
+  uint32_t tmem;
+  int last;
+  volatile int dead;
+};
+
+template <bool E4M3>
+__global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, PrefillArgs a) {
+  constexpr float kShift = E4M3 ? 10.0f : 0.0f;   // weights times 2^kShift before their rounding
+  constexpr float kLazy = E4M3 ? 4.0f : 8.0f;     // how far logits may pass the running maximum
+  extern __shared__ unsigned char dyn[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t sq = base, sk = base + 2 * kTile, sv = base + 4 * kTile;
+  const int G = L.G, n_kv = L.n_kv, n_seqs = a.b.n_seqs;
+  const int q_tile = kRows / G;                    // query tokens of a work item
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 128);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.o_full[i], 1);
+      mbar_init(&sh.k_full[i], 128);
+      mbar_init(&sh.k_free[i], 1);
+      mbar_init(&sh.v_full[i], 128);
+      mbar_init(&sh.v_free[i], 1);
+    }
+    sh.dead = 0;
+  }
+  mbar_init_fence();
+  pdl_wait();
+  pdl_trigger();
+  if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;
+
+  // ---- the list of work items (every CTA forms the same one) ----
+  int total = 0;
+  for (int i0 = 0; i0 < n_seqs; i0 += kThreads) {
+    const int i = i0 + tid;
+    int mine = 0;
+    if (i < n_seqs) {
+      PagedSeq s = paged_seq(a.b, L.P, i, false);
+      if (!s.ok) {
+        paged_error(L, ERR_PAGED_BATCH, i, s.len);
+        s.n_new = 0;
+      }
+      sh.row0[i] = s.row0;
+      sh.n_new[i] = s.n_new;
+      sh.len[i] = s.len;
+      mine = (s.n_new + q_tile - 1) / q_tile * n_kv;
+    }
+    const int ex = warp_excl_scan(mine, lane);
+    if (lane == 31) sh.wsum[warp] = ex + mine;
+    __syncthreads();
+    int off = total;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) off += sh.wsum[w];
+      total += sh.wsum[w];
+    }
+    if (i < n_seqs) sh.pre[i] = off + ex;
+    __syncthreads();
+  }
+  if (tid == 0) sh.pre[n_seqs] = total;
+  __syncthreads();
+
+  // Row tile t (without its head) of the batch: sequence and first query.
+  // Within a sequence the last queries come first: with a causal mask they
+  // see the most keys, and the long items start early.
+  auto find = [&](int t, Item& it) {
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sh.pre[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    it.seq = lo;
+    it.row0 = sh.row0[lo];
+    it.n_new = sh.n_new[lo];
+    it.len = sh.len[lo];
+    const int r = t - sh.pre[lo], tiles = (it.n_new + q_tile - 1) / q_tile;
+    it.head = r % n_kv;
+    it.q0 = (tiles - 1 - r / n_kv) * q_tile;
+    const int q1 = min(it.q0 + q_tile, it.n_new) - 1;
+    it.see_max = a.causal ? max(0, min(it.len, it.len - it.n_new + q1 + 1)) : it.len;
+  };
+  const bool split = total < (int)gridDim.x;
+  int entries = total;
+  if (split) {
+    const int n_pairs = total / n_kv;
+    int n = 0;
+    if (tid < n_pairs) {
+      Item it;
+      find(tid * n_kv, it);
+      n = (it.see_max + kKeys - 1) / kKeys;
+    }
+    int x = n;  // the sum of n over the row tiles
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+    if (lane == 0) sh.wsum[warp] = x;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) all += sh.wsum[w];
+    __syncthreads();
+    int per = (int)(((int64_t)all * n_kv + gridDim.x - 1) / gridDim.x);
+    if (per < 2) per = 2;
+    const int parts = tid < n_pairs ? max(1, (n + per - 1) / per) : 0;
+    const int ex = warp_excl_scan(parts, lane);
+    if (lane == 31) sh.wsum[warp] = ex + parts;
+    __syncthreads();
+    int off = 0, sum = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) off += sh.wsum[w];
+      sum += sh.wsum[w];
+    }
+    if (tid < n_pairs) {
+      sh.epre[tid] = (off + ex) * n_kv;
+      sh.eparts[tid] = parts;
+    }
+    entries = sum * n_kv;
+    __syncthreads();
+  }
+  auto item_of = [&](int e) {
+    Item it;
+    if (!split) {
+      find(e, it);
+      it.j0 = 0;
+      it.j1 = (it.see_max + kKeys - 1) / kKeys;
+      it.parts = 1;
+      it.slot = it.ctr = 0;
+      return it;
+    }
+    int lo = 0, hi = total / n_kv - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sh.epre[mid] <= e) lo = mid; else hi = mid - 1;
+    }
+    find(lo * n_kv, it);
+    const int r = e - sh.epre[lo], n = (it.see_max + kKeys - 1) / kKeys;
+    it.parts = sh.eparts[lo];
+    it.head = r / it.parts;
+    const int p = r - it.head * it.parts;
+    it.j0 = (int)((int64_t)n * p / it.parts);
+    it.j1 = (int)((int64_t)n * (p + 1) / it.parts);
+    it.slot = e;
+    it.ctr = lo * n_kv + it.head;
+    return it;
+  };
+
+  if (warp == 12) tmem_alloc(&sh.tmem, 512);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+
+  auto wait = [&](uint64_t* bar, unsigned parity) {
+    if (sh.dead) return false;
+    if (mbar_wait(bar, parity)) return true;
+    sh.dead = 1;
+    paged_error(L, ERR_PAGED_WAIT, blockIdx.x, warp, (int32_t)MK_ETIMEOUT);
+    return false;
+  };
+
+  if (warp == 12) {
+    // ---- issues the products ----
+    if (lane == 0) {
+      unsigned kc = 0, vc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+      bool ok = true;
+      auto s_mma = [&](int t, unsigned stage) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
+          umma_ss(tmem + t * 128, sw128_desc(sq + t * kTile + o, 16), sw128_desc(sk + stage * kTile + o, 16),
+                  idesc(!E4M3, 0), k > 0);
+        }
+        umma_commit(&sh.s_full[t]);
+      };
+      for (int e = blockIdx.x; e < entries && ok; e += gridDim.x) {
+        const Item it = item_of(e);
+        const int n = it.j1 - it.j0;
+        const int nt = min(it.n_new - it.q0, q_tile) * G > 128 ? 2 : 1;
+        if (n == 0) continue;
+        for (int t = 0; t < nt; ++t) ok = ok && wait(&sh.q_full[t], qc[t]++ & 1);
+        ok = ok && wait(&sh.k_full[kc & 1], (kc >> 1) & 1);
+        if (!ok) break;
+        tmem_fence_after_sync();
+        for (int t = 0; t < nt; ++t) s_mma(t, kc & 1);
+        umma_commit(&sh.k_free[kc & 1]);
+        ++kc;
+        for (int j = 0; j < n && ok; ++j) {
+          ok = wait(&sh.v_full[vc & 1], (vc >> 1) & 1);
+          for (int t = 0; t < nt && ok; ++t) {
+            ok = wait(&sh.p_full[t], pc[t]++ & 1);
+            if (!ok) break;
+            tmem_fence_after_sync();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, sw128_desc(sv + (vc & 1) * kTile + k * 2048, kHalf),
+                      idesc(!E4M3, 1), j > 0 || k > 0);
+            if (t == nt - 1) umma_commit(&sh.v_free[vc & 1]);
+            if (j == n - 1) {
+              umma_commit(&sh.o_full[t]);
+            } else {
+              if (t == 0) ok = wait(&sh.k_full[kc & 1], (kc >> 1) & 1);
+              if (!ok) break;
+              tmem_fence_after_sync();
+              s_mma(t, kc & 1);
+              if (t == nt - 1) umma_commit(&sh.k_free[kc & 1]);
+            }
+          }
+          ++vc;
+          if (j < n - 1) ++kc;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 8) {
+    // ---- keys and values into shared memory ----
+    const int lt = tid - 256;
+    unsigned c = 0;  // steps so far
+    bool ok = true;
+    for (int e = blockIdx.x; e < entries && ok; e += gridDim.x) {
+      const Item it = item_of(e);
+      const int32_t* table = a.b.page_table + (int64_t)it.seq * a.b.table_stride;
+      // Page of 16-key group g of step j; a bad id is recorded and page 0 read.
+      auto page_of = [&](int j, int g) {
+        const int tok = j * kKeys + g * 16;
+        if (tok >= it.len) return -1;
+        const int p = table[tok >> L.p_log2];
+        if (p < 0 || p >= L.n_pages) {
+          paged_error(L, ERR_PAGED_PAGE, it.seq, p);
+          return 0;
+        }
+        return p;
+      };
+      if (E4M3) {
+        const int ck = lt & 7, r = lt >> 3;  // 16 codes ck of rows r + 16 i
+        uint4 kr[8], vr[8];
+        int pg[8];
+        auto load = [&](int j, const uint8_t* pool, uint4 (&x)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int tok = j * kKeys + 16 * i + r;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (tok < it.len)
+              x[i] = *reinterpret_cast<const uint4*>(
+                  pool + (((int64_t)pg[i] * n_kv + it.head) * L.P + (tok & (L.P - 1))) * D + ck * 16);
+          }
+        };
+        auto store = [&](uint32_t to, const uint4 (&x)[8]) {
+          const uint32_t half = to + (ck >> 2) * kHalf;
+          const int c0 = (2 * ck) & 7, first = ck >> 2;  // the two halves of a row take turns: no bank conflicts
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              h[2 * k] = e4m3_h2(w[k]);
+              h[2 * k + 1] = e4m3_h2(w[k] >> 16);
+            }
+            const int row = 16 * i + r;
+            const uint32_t at = half + row * 128;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int s = z ^ first;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (uint32_t)(((c0 + s) ^ (row & 7)) << 4)),
+                           "r"(s ? h[4] : h[0]), "r"(s ? h[5] : h[1]), "r"(s ? h[6] : h[2]), "r"(s ? h[7] : h[3])
+                           : "memory");
+            }
+          }
+        };
+        auto pages = [&](int j) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pg[i] = page_of(j, i);
+        };
+        if (it.j0 < it.j1) {
+          pages(it.j0);
+          load(it.j0, L.k, kr);
+        }
+        for (int j = it.j0; j < it.j1 && ok; ++j, ++c) {
+          load(j, L.v, vr);
+          float ks = 1.0f, vs = 1.0f;
+          if (lt < 8) {
+            const int p = page_of(j, lt);
+            if (p >= 0) {
+              ks = L.k_scale[(int64_t)p * n_kv + it.head];
+              vs = L.v_scale[(int64_t)p * n_kv + it.head];
+            }
+          }
+          ok = c < 2 || wait(&sh.k_free[c & 1], ((c >> 1) - 1) & 1);
+          if (!ok) break;
+          if (lt < 8) {
+            sh.kf[c & 3][lt] = ks;
+            sh.lsv[c & 3][lt] = __log2f(vs);
+            sh.inv[c & 3][lt] = __frcp_rn(vs);
+          }
+          store(sk + (c & 1) * kTile, kr);
+          fence_proxy_async();
+          mbar_arrive(&sh.k_full[c & 1]);
+          if (j + 1 < it.j1) {
+            pages(j + 1);
+            load(j + 1, L.k, kr);
+          }
+          ok = c < 2 || wait(&sh.v_free[c & 1], ((c >> 1) - 1) & 1);
+          if (!ok) break;
+          store(sv + (c & 1) * kTile, vr);
+          fence_proxy_async();
+          mbar_arrive(&sh.v_full[c & 1]);
+        }
+      } else {
+        const int ck = lt & 15, r = lt >> 4;  // 8 channels ck of rows r + 8 i
+        auto load = [&](int j, const uint8_t* pool, uint32_t to) {
+          const uint32_t half = to + (ck >> 3) * kHalf;
+          int p = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int row = 8 * i + r, tok = j * kKeys + row;
+            if ((i & 1) == 0) p = page_of(j, i >> 1);
+            const bool in = tok < it.len;
+            const uint8_t* from =
+                pool + ((((int64_t)(in ? p : 0) * n_kv + it.head) * L.P + (tok & (L.P - 1))) * D + ck * 8) * 2;
+            cp_async16_z(half + row * 128 + (((ck & 7) ^ (row & 7)) << 4), from, in);
+          }
+          cp_async_commit();
+        };
+        uint64_t* pending = nullptr;
+        auto signal = [&](bool last) {
+          if (!pending) return;
+          if (last)
+            asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+          else
+            asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+          fence_proxy_async();
+          mbar_arrive(pending);
+        };
+        for (int j = it.j0; j < it.j1 && ok; ++j, ++c) {
+          ok = c < 2 || wait(&sh.k_free[c & 1], ((c >> 1) - 1) & 1);
+          if (!ok) break;
+          load(j, L.k, sk + (c & 1) * kTile);
+          signal(false);
+          pending = &sh.k_full[c & 1];
+          ok = c < 2 || wait(&sh.v_free[c & 1], ((c >> 1) - 1) & 1);
+          if (!ok) break;
+          load(j, L.v, sv + (c & 1) * kTile);
+          signal(false);
+          pending = &sh.v_full[c & 1];
+        }
+        if (ok) signal(true);
+        asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+      }
+    }
+  } else {
+    // ---- softmax: one row a thread ----
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t ts = trow + t * 128, to = trow + 256 + t * 128;
+    unsigned sc = 0, oc = 0, c = 0;  // phases of s_full, o_full; steps so far (the scales' ring)
+    bool ok = true;
+    for (int e = blockIdx.x; e < entries; e += gridDim.x) {
+      const Item it = item_of(e);
+      const int n = it.j1 - it.j0;
+      const int nt = min(it.n_new - it.q0, q_tile) * G > 128 ? 2 : 1;
+      const int row = t * 128 + r, tok = it.q0 + row / G, head = it.head * G + row % G;
+      const bool live = tok < it.n_new && row < kRows;
+      const int64_t out_row = (int64_t)it.row0 + tok;
+      const int see = !live ? 0 : a.causal ? max(0, min(it.len, it.len - it.n_new + tok + 1)) : it.len;
+      float m = -INFINITY, l = 0.0f, zf = a.scale;
+      if (t < nt && n > 0 && ok) {
+        // The row's query into the operand tile.
+        const uint16_t* qp = a.q + out_row * a.q_stride + head * D;
+        const uint32_t dst = sq + t * kTile + r * 128;
+        if (E4M3) {
+          float top = 0.0f;
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint4 x = *reinterpret_cast<const uint4*>(qp + i * 8);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+            }
+          }
+          int ex = (int)(__float_as_uint(top) >> 23) - 127;  // a power of two that brings the row into fp16
+          ex = max(-100, min(ex, 120));
+          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+          zf *= __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live) x = *reinterpret_cast<const uint4*>(qp + i * 8);
+            const uint32_t w[4] = {x.x ^ a.q_sign, x.y ^ a.q_sign, x.z ^ a.q_sign, x.w ^ a.q_sign};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (i >> 3) * kHalf +
+                                                                       (uint32_t)(((i & 7) ^ (r & 7)) << 4)),
+                         "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                         : "memory");
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live) x = *reinterpret_cast<const uint4*>(qp + i * 8);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (i >> 3) * kHalf +
+                                                                       (uint32_t)(((i & 7) ^ (r & 7)) << 4)),
+                         "r"(x.x ^ a.q_sign), "r"(x.y ^ a.q_sign), "r"(x.z ^ a.q_sign), "r"(x.w ^ a.q_sign)
+                         : "memory");
+          }
+        }
+        fence_proxy_async();
+        mbar_arrive(&sh.q_full[t]);
+
+        for (int j = 0; j < n; ++j, ++c) {
+          ok = __all_sync(FULL, wait(&sh.s_full[t], sc++ & 1));
+          if (!ok) break;
+          tmem_fence_after_sync();
+          const int lim = see - (it.j0 + j) * kKeys;  // columns from here on are hidden
+          const bool cut = __any_sync(FULL, lim < kKeys);
+          float kf[8], bs[8];
+          if (E4M3) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              kf[i] = zf * sh.kf[c & 3][i];
+              bs[i] = sh.lsv[c & 3][i];
+            }
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t v[32];
+            tmem_ld32_async(ts + h * 32, v);
+            tmem_ld_wait(v);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              float x = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float y = __uint_as_float(v[16 * s + i]);
+                if (cut && 32 * h + 16 * s + i >= lim) y = -INFINITY;
+                x = fmaxf(x, y);
+              }
+              if (x != -INFINITY) mx = fmaxf(mx, E4M3 ? fmaf(x, kf[2 * h + s], bs[2 * h + s]) : x * zf);
+            }
+          }
+          const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
+          if (__any_sync(FULL, raise)) {
+            const float mn = raise ? mx : m;
+            const float f = m == -INFINITY ? 0.0f : ex2(m - mn);  // rows that stay: 2^0
+            l *= f;
+            m = mn;
+            if (j > 0) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                uint32_t v[32];
+                tmem_ld32_async(to + h * 32, v);
+                tmem_ld_wait(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                tmem_st32(to + h * 32, v);
+              }
+            }
+          }
+          const float ms = (m == -INFINITY ? 0.0f : m) - kShift;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t v[32], p[16];
+            tmem_ld32_async(ts + h * 32, v);
+            tmem_ld_wait(v);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const float k = E4M3 ? kf[2 * h + s] : zf, b = E4M3 ? bs[2 * h + s] - ms : -ms;
+              float add = 0.0f;
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                float x = ex2(fmaf(__uint_as_float(v[16 * s + i]), k, b));
+                float y = ex2(fmaf(__uint_as_float(v[16 * s + i + 1]), k, b));
+                if (cut) {
+                  if (32 * h + 16 * s + i >= lim) x = 0.0f;
+                  if (32 * h + 16 * s + i + 1 >= lim) y = 0.0f;
+                }
+                add += x + y;
+                p[8 * s + i / 2] = pack2<E4M3>(x, y);
+              }
+              l = E4M3 ? fmaf(add, sh.inv[c & 3][2 * h + s], l) : l + add;
+            }
+            tmem_st16(ts + h * 16, p);
+          }
+          tmem_wait_st();
+          tmem_fence_before_sync();
+          mbar_arrive(&sh.p_full[t]);
+        }
+        if (ok) {
+          ok = __all_sync(FULL, wait(&sh.o_full[t], oc++ & 1));
+          tmem_fence_after_sync();
+        }
+      } else {
+        c += n;
+      }
+      // ---- the row's result ----
+      if (it.parts == 1) {
+        if (t < nt) {
+          const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t v[32];
+            if (n > 0 && ok) {
+              tmem_ld32_async(to + h * 32, v);
+              tmem_ld_wait(v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0;
+            }
+            if (see == 0)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0;
+            if (live && ok) {
+              uint4* op = reinterpret_cast<uint4*>(a.out + out_row * a.out_stride + head * D + h * 32);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = pack2<false>(__uint_as_float(v[8 * i + 2 * k]) * f, __uint_as_float(v[8 * i + 2 * k + 1]) * f);
+                op[i] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+          if (live && ok && a.lse)
+            a.lse[out_row * (n_kv * G) + head] = see > 0 ? (log2f(l) + (m - kShift)) * kLn2 : -INFINITY;
+          tmem_fence_before_sync();
+        }
+        continue;
+      }
+      // A part of a split row tile: [32 column groups][256 rows] float4, then
+      // the rows' maxima and sums.
+      constexpr int64_t kPartFloats = (int64_t)kRows * (D + 2);
+      auto part_of = [&](int slot) { return a.part + slot * kPartFloats; };
+      if (t < nt) {
+        float4* op = reinterpret_cast<float4*>(part_of(it.slot));
+        float* ml = part_of(it.slot) + (int64_t)kRows * D;
+        ml[row] = m;
+        ml[kRows + row] = l;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t v[32];
+          if (n > 0 && ok) {
+            tmem_ld32_async(to + h * 32, v);
+            tmem_ld_wait(v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            op[(8 * h + i) * kRows + row] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                        __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+        }
+        tmem_fence_before_sync();
+      }
+      __threadfence();
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the eight softmax warps
+      if (tid == 0) {
+        const int old = atomicAdd(&a.counters[it.ctr], 1);
+        sh.last = old == it.parts - 1;
+        if (sh.last) a.counters[it.ctr] = 0;
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (sh.last) {
+        __threadfence();
+        // The parts of this (row tile, head) have neighbouring slots.
+        const int s0 = sh.epre[it.ctr / n_kv] + it.head * it.parts;
+        if (live && t < nt) {
+          float M = -INFINITY, S = 0.0f;
+          for (int i = 0; i < it.parts; ++i) M = fmaxf(M, __ldcg(part_of(s0 + i) + (int64_t)kRows * D + row));
+          for (int i = 0; i < it.parts; ++i) {
+            const float mi = __ldcg(part_of(s0 + i) + (int64_t)kRows * D + row);
+            if (mi != -INFINITY) S = fmaf(__ldcg(part_of(s0 + i) + (int64_t)kRows * (D + 1) + row), ex2(mi - M), S);
+          }
+          const float f = S > 0.0f || S != S ? 1.0f / S : 0.0f;
+          for (int h = 0; h < 16; ++h) {  // eight columns at a time
+            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int i = 0; i < it.parts; ++i) {
+              const float mi = __ldcg(part_of(s0 + i) + (int64_t)kRows * D + row);
+              if (mi == -INFINITY) continue;
+              const float w = ex2(mi - M);
+              const float4* op = reinterpret_cast<const float4*>(part_of(s0 + i));
+              const float4 u = __ldcg(op + (2 * h) * kRows + row), v = __ldcg(op + (2 * h + 1) * kRows + row);
+              x[0] = fmaf(u.x, w, x[0]); x[1] = fmaf(u.y, w, x[1]); x[2] = fmaf(u.z, w, x[2]); x[3] = fmaf(u.w, w, x[3]);
+              x[4] = fmaf(v.x, w, x[4]); x[5] = fmaf(v.y, w, x[5]); x[6] = fmaf(v.z, w, x[6]); x[7] = fmaf(v.w, w, x[7]);
+            }
+            uint4 o;
+            o.x = pack2<false>(x[0] * f, x[1] * f);
+            o.y = pack2<false>(x[2] * f, x[3] * f);
+            o.z = pack2<false>(x[4] * f, x[5] * f);
+            o.w = pack2<false>(x[6] * f, x[7] * f);
+            *reinterpret_cast<uint4*>(a.out + out_row * a.out_stride + head * D + h * 8) = o;
+          }
+          if (a.lse) a.lse[out_row * (n_kv * G) + head] = see > 0 ? (log2f(S) + (M - kShift)) * kLn2 : -INFINITY;
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // sh.last is free again
+    }
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+int64_t paged_prefill_part_floats() { return (int64_t)2 * kPagedMaxCtas * kRows * (D + 2); }
+
+cudaError_t launch_paged_prefill(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, bool causal,
+                                 const uint16_t* q, int64_t q_stride, float scale, uint16_t* out, int64_t out_stride,
+                                 float* lse, cudaStream_t s) {
+  const void* fn = L.e4m3 ? (const void*)k_paged_prefill<true> : (const void*)k_paged_prefill<false>;
+  int sms = 0;
+  const cudaError_t e = kernel_smem_attr(fn, kSmem, kThreads, nullptr, &sms);
+  if (e != cudaSuccess) return e;
+  const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
+  const PrefillArgs a{b,   q,      out,
+                      lse, q_stride, out_stride,
+                      (scale < 0.0f ? -scale : scale) * kLog2e,
+                      scale < 0.0f ? 0x80008000u : 0u, causal ? 1 : 0, w.prefill_part, w.prefill_counters};
+  return L.e4m3 ? launch_pdl(k_paged_prefill<true>, dim3(grid), dim3(kThreads), (size_t)kSmem, s, 0, L, a)
+                : launch_pdl(k_paged_prefill<false>, dim3(grid), dim3(kThreads), (size_t)kSmem, s, 0, L, a);
+}
+
+}  // namespace mk
