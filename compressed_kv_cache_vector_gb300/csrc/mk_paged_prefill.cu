@@ -34,8 +34,15 @@ constexpr int kRows = 256;                 // rows of a work item: two tiles of 
 constexpr int kKeys = 128;                 // keys of a step
 constexpr int kTile = kKeys * D * 2;       // 32 KB: a 16-bit tile
 constexpr int kHalf = kTile / 2;           // its channels 0-63, then 64-127
-constexpr int kThreads = 416;              // 8 softmax warps, 4 loading warps, 1 issuing warp
+constexpr int kThreads = 512;              // 8 softmax warps, 4 loading warps, 1 issuing warp (and 3 without work)
+// Registers of a thread of each group of four warps; the launch gives 128 each
+// (512 x 128 = 65,536), and the shares add up to that.
+constexpr int kRegsSoftmax = 176, kRegsLoad = 104, kRegsIssue = 56;
+static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue == 4 * 128, "register shares");
 constexpr int kSmem = 1024 + 2 * kTile + 4 * kTile;
+// Logit factors are at least this, so that a hidden key's -infinity stays one
+// (a row of zeros or a scale of 0 would make it NaN).
+constexpr float kTiny = 1.17549435e-38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct PrefillArgs {
@@ -117,15 +124,19 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[32]) {
                  "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
                  "+r"(v[30]), "+r"(v[31])::"memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(v[0]),
-      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]),
-      "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-      "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n" ::"r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -134,6 +145,38 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
       : "memory");
+}
+// A row's 128 columns.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&v)[4][32]) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) tmem_ld32_async(taddr + h * 32, v[h]);
+#pragma unroll
+  for (int h = 0; h < 4; ++h) tmem_ld_wait(v[h]);
+}
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <int R>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -318,9 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     return false;
   };
 
-  if (warp == 12) {
+  if (warp >= 12) {
     // ---- issues the products ----
-    if (lane == 0) {
+    fewer_registers<kRegsIssue>();
+    if (warp == 12 && lane == 0) {
       unsigned kc = 0, vc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
       bool ok = true;
       auto s_mma = [&](int t, unsigned stage) {
@@ -373,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     __syncwarp();
   } else if (warp >= 8) {
     // ---- keys and values into shared memory ----
+    fewer_registers<kRegsLoad>();
     const int lt = tid - 256;
     unsigned c = 0;  // steps so far
     bool ok = true;
@@ -509,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     }
   } else {
     // ---- softmax: one row a thread ----
+    more_registers<kRegsSoftmax>();
     const int t = warp >> 2, r = tid & 127;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = trow + t * 128, to = trow + 256 + t * 128;
@@ -577,32 +623,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           tmem_fence_after_sync();
           const int lim = see - (it.j0 + j) * kKeys;  // columns from here on are hidden
           const bool cut = __any_sync(FULL, lim < kKeys);
-          float kf[8], bs[8];
-          if (E4M3) {
+          uint32_t v[4][32];
+          tmem_ld128(ts, v);
+          if (cut) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              kf[i] = zf * sh.kf[c & 3][i];
-              bs[i] = sh.lsv[c & 3][i];
-            }
+            for (int i = 0; i < 128; ++i)
+              if (i >= lim) v[i >> 5][i & 31] = 0xff800000u;
           }
           float mx = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t v[32];
-            tmem_ld32_async(ts + h * 32, v);
-            tmem_ld_wait(v);
+          for (int h = 0; h < 8; ++h) {  // 16 keys: one scale
+            float x = __uint_as_float(v[h >> 1][16 * (h & 1)]), y = __uint_as_float(v[h >> 1][16 * (h & 1) + 1]);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              float x = -INFINITY;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float y = __uint_as_float(v[16 * s + i]);
-                if (cut && 32 * h + 16 * s + i >= lim) y = -INFINITY;
-                x = fmaxf(x, y);
-              }
-              if (x != -INFINITY) mx = fmaxf(mx, E4M3 ? fmaf(x, kf[2 * h + s], bs[2 * h + s]) : x * zf);
+            for (int i = 2; i < 16; i += 2) {
+              x = fmaxf(x, __uint_as_float(v[h >> 1][16 * (h & 1) + i]));
+              y = fmaxf(y, __uint_as_float(v[h >> 1][16 * (h & 1) + i + 1]));
             }
+            x = fmaxf(x, y);
+            if (E4M3) x = x == -INFINITY ? x : fmaf(x, zf * sh.kf[c & 3][h], sh.lsv[c & 3][h]);
+            mx = fmaxf(mx, x);
           }
+          if (!E4M3) mx = mx == -INFINITY ? mx : mx * zf;
           const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
           if (__any_sync(FULL, raise)) {
             const float mn = raise ? mx : m;
@@ -611,40 +652,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             m = mn;
             if (j > 0) {
 #pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                uint32_t v[32];
-                tmem_ld32_async(to + h * 32, v);
-                tmem_ld_wait(v);
+              for (int h = 0; h < 8; ++h) {
+                uint32_t w[16];
+                tmem_ld16(to + h * 16, w);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                tmem_st32(to + h * 32, v);
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+                tmem_st16(to + h * 16, w);
               }
             }
           }
           const float ms = (m == -INFINITY ? 0.0f : m) - kShift;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t v[32], p[16];
-            tmem_ld32_async(ts + h * 32, v);
-            tmem_ld_wait(v);
+          for (int h = 0; h < 8; ++h) {
+            const float k = fmaxf(E4M3 ? zf * sh.kf[c & 3][h] : zf, kTiny), bb = E4M3 ? sh.lsv[c & 3][h] - ms : -ms;
+            const uint64_t k2 = pair(k, k), b2 = pair(bb, bb);
+            uint64_t add = 0;
+            uint32_t p[8];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const float k = E4M3 ? kf[2 * h + s] : zf, b = E4M3 ? bs[2 * h + s] - ms : -ms;
-              float add = 0.0f;
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                float x = ex2(fmaf(__uint_as_float(v[16 * s + i]), k, b));
-                float y = ex2(fmaf(__uint_as_float(v[16 * s + i + 1]), k, b));
-                if (cut) {
-                  if (32 * h + 16 * s + i >= lim) x = 0.0f;
-                  if (32 * h + 16 * s + i + 1 >= lim) y = 0.0f;
-                }
-                add += x + y;
-                p[8 * s + i / 2] = pack2<E4M3>(x, y);
-              }
-              l = E4M3 ? fmaf(add, sh.inv[c & 3][2 * h + s], l) : l + add;
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t* z = &v[h >> 1][16 * (h & 1) + 2 * i];
+              float x, y;
+              unpair(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), k2, b2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              add = add2(add, pair(x, y));
+              p[i] = pack2<E4M3>(x, y);
             }
-            tmem_st16(ts + h * 16, p);
+            float x, y;
+            unpair(add, x, y);
+            l = E4M3 ? fmaf(x + y, sh.inv[c & 3][h], l) : l + (x + y);
+            tmem_st8(ts + h * 8, p);
           }
           tmem_wait_st();
           tmem_fence_before_sync();

@@ -603,3 +603,30 @@ def test_the_handle_keeps_its_device_and_two_handles_run_side_by_side():
     torch.cuda.synchronize()
     for x, y in outs:
         assert torch.equal(x.view(torch.int16), wa.view(torch.int16)) and torch.equal(y.view(torch.int16), wb.view(torch.int16))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attention_of_zero_rows_zero_pages_and_zero_or_negative_scale(kv):
+    made = Made(kv, 16, 2, 2, [150, 33], 11)
+    c, rows = made.c, made.rows
+    for p in rows[0][:4]:
+        c.k_pool[0, p].view(torch.uint8).zero_()
+        if kv == "e4m3":
+            c.k_scale[0, p] = 2.0 ** -64
+    for p in rows[0][2:7]:
+        c.v_pool[0, p].view(torch.uint8).zero_()
+        if kv == "e4m3":
+            c.v_scale[0, p] = 2.0 ** -64
+    q = torch.randn(60, 4, 128, generator=_gen(8), device=DEV).to(torch.bfloat16)
+    q[3:7] = 0
+    q[50:52, 1] = 0
+    b = K.PagedBatch(made.kv_len, made.table, _i32([0, 40, 60]), 40, 60)
+    one = K.PagedBatch(made.kv_len, made.table)
+    for scale in (0.0, -0.1, 128 ** -0.5):
+        for causal in (True, False):
+            out, lse = c.prefill_attn(0, b, q, causal=causal, scale=scale, lse=True)
+            _check_attention(made, q, out, lse, scale, [40, 20], causal, 2.0 ** -8 if kv == "bf16" else 2.0 ** -11)
+        qq = q[2:4].contiguous()
+        out, lse = c.decode_attn(0, one, qq, scale=scale, lse=True)
+        _check_attention(made, qq, out, lse, scale, [1, 1], True, 2.0 ** -11)
+    assert c.poll_error() == (0, 0)
