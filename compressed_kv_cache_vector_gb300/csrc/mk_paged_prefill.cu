@@ -170,6 +170,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// One lane of a converged warp (the tensor-core instructions take their
+// operands from uniform registers: a branch that only the lane's number
+// decides would make each of them a loop over the lanes).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 template <int R>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -364,57 +372,64 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   if (warp >= 12) {
     // ---- issues the products ----
     fewer_registers<kRegsIssue>();
-    if (warp == 12 && lane == 0) {
+    if (warp == 12) {
       unsigned kc = 0, vc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
       bool ok = true;
-      auto s_mma = [&](int t, unsigned stage) {
+      const uint64_t dq = sw128_desc(sq, 16), dk = sw128_desc(sk, 16), dv = sw128_desc(sv, kHalf);
+      auto wait_all = [&](uint64_t* bar, unsigned parity) { return __all_sync(FULL, wait(bar, parity)) != 0; };
+      // The whole warp walks the list; one lane issues.
+      auto s_mma = [&](int t, unsigned stage, bool last) {
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
-          umma_ss(tmem + t * 128, sw128_desc(sq + t * kTile + o, 16), sw128_desc(sk + stage * kTile + o, 16),
-                  idesc(!E4M3, 0), k > 0);
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+            umma_ss(tmem + t * 128, dq + (uint64_t)(t * (kTile >> 4) + o), dk + (uint64_t)(stage * (kTile >> 4) + o),
+                    idesc(!E4M3, 0), k > 0);
+          }
+          umma_commit(&sh.s_full[t]);
+          if (last) umma_commit(&sh.k_free[stage]);
         }
-        umma_commit(&sh.s_full[t]);
+        __syncwarp();
       };
       for (int e = blockIdx.x; e < entries && ok; e += gridDim.x) {
         const Item it = item_of(e);
         const int n = it.j1 - it.j0;
         const int nt = min(it.n_new - it.q0, q_tile) * G > 128 ? 2 : 1;
         if (n == 0) continue;
-        for (int t = 0; t < nt; ++t) ok = ok && wait(&sh.q_full[t], qc[t]++ & 1);
-        ok = ok && wait(&sh.k_full[kc & 1], (kc >> 1) & 1);
+        for (int t = 0; t < nt; ++t) ok = ok && wait_all(&sh.q_full[t], qc[t]++ & 1);
+        ok = ok && wait_all(&sh.k_full[kc & 1], (kc >> 1) & 1);
         if (!ok) break;
         tmem_fence_after_sync();
-        for (int t = 0; t < nt; ++t) s_mma(t, kc & 1);
-        umma_commit(&sh.k_free[kc & 1]);
+        for (int t = 0; t < nt; ++t) s_mma(t, kc & 1, t == nt - 1);
         ++kc;
         for (int j = 0; j < n && ok; ++j) {
-          ok = wait(&sh.v_full[vc & 1], (vc >> 1) & 1);
+          const bool end = j == n - 1;
+          ok = wait_all(&sh.v_full[vc & 1], (vc >> 1) & 1);
           for (int t = 0; t < nt && ok; ++t) {
-            ok = wait(&sh.p_full[t], pc[t]++ & 1);
+            ok = wait_all(&sh.p_full[t], pc[t]++ & 1);
             if (!ok) break;
             tmem_fence_after_sync();
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, sw128_desc(sv + (vc & 1) * kTile + k * 2048, kHalf),
-                      idesc(!E4M3, 1), j > 0 || k > 0);
-            if (t == nt - 1) umma_commit(&sh.v_free[vc & 1]);
-            if (j == n - 1) {
-              umma_commit(&sh.o_full[t]);
-            } else {
-              if (t == 0) ok = wait(&sh.k_full[kc & 1], (kc >> 1) & 1);
+              for (int k = 0; k < 8; ++k)
+                umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, dv + (uint64_t)((vc & 1) * (kTile >> 4) + k * (2048 >> 4)),
+                        idesc(!E4M3, 1), j > 0 || k > 0);
+              if (t == nt - 1) umma_commit(&sh.v_free[vc & 1]);
+              if (end) umma_commit(&sh.o_full[t]);
+            }
+            __syncwarp();
+            if (!end) {
+              if (t == 0) ok = wait_all(&sh.k_full[kc & 1], (kc >> 1) & 1);
               if (!ok) break;
               tmem_fence_after_sync();
-              s_mma(t, kc & 1);
-              if (t == nt - 1) umma_commit(&sh.k_free[kc & 1]);
+              s_mma(t, kc & 1, t == nt - 1);
             }
           }
           ++vc;
-          if (j < n - 1) ++kc;
+          if (!end) ++kc;
         }
       }
     }
-    __syncwarp();
   } else if (warp >= 8) {
     // ---- keys and values into shared memory ----
     fewer_registers<kRegsLoad>();
