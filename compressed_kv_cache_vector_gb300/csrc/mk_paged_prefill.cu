@@ -37,7 +37,7 @@ constexpr int kHalf = kTile / 2;           // its channels 0-63, then 64-127
 constexpr int kThreads = 512;              // 8 softmax warps, 4 loading warps, 1 issuing warp (and 3 without work)
 // Registers of a thread of each group of four warps; the launch gives 128 each
 // (512 x 128 = 65,536), and the shares add up to that.
-constexpr int kRegsSoftmax = 176, kRegsLoad = 104, kRegsIssue = 56;
+constexpr int kRegsSoftmax = 184, kRegsLoad = 96, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue == 4 * 128, "register shares");
 constexpr int kSmem = 1024 + 2 * kTile + 4 * kTile;
 // Logit factors are at least this, so that a hidden key's -infinity stays one
@@ -178,6 +178,11 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p != 0;
 }
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return r;
+}
 template <int R>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -207,7 +212,9 @@ struct Shared {
   int eparts[kPagedMaxCtas];
   int wsum[16];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], k_full[2], k_free[2], v_full[2], v_free[2];
-  float kf[4][8], lsv[4][8], inv[4][8];  // e4m3: per 16 keys of a step, ring of 4 steps
+  // e4m3, per 16 keys of a step, ring of 4 steps: {k scale, log2 v scale}, 1 / v scale
+  __align__(16) float2 kb[4][8];
+  float inv[4][8];
   uint32_t tmem;
   int last;
   volatile int dead;
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       // The whole warp walks the list; one lane issues.
       auto s_mma = [&](int t, unsigned stage, bool last) {
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
           for (int k = 0; k < 8; ++k) {
             const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
             umma_ss(tmem + t * 128, dq + (uint64_t)(t * (kTile >> 4) + o), dk + (uint64_t)(stage * (kTile >> 4) + o),
@@ -410,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             if (!ok) break;
             tmem_fence_after_sync();
             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
               for (int k = 0; k < 8; ++k)
                 umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, dv + (uint64_t)((vc & 1) * (kTile >> 4) + k * (2048 >> 4)),
                         idesc(!E4M3, 1), j > 0 || k > 0);
@@ -439,87 +446,85 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     for (int e = blockIdx.x; e < entries && ok; e += gridDim.x) {
       const Item it = item_of(e);
       const int32_t* table = a.b.page_table + (int64_t)it.seq * a.b.table_stride;
-      // Page of 16-key group g of step j; a bad id is recorded and page 0 read.
-      auto page_of = [&](int j, int g) {
-        const int tok = j * kKeys + g * 16;
-        if (tok >= it.len) return -1;
-        const int p = table[tok >> L.p_log2];
-        if (p < 0 || p >= L.n_pages) {
-          paged_error(L, ERR_PAGED_PAGE, it.seq, p);
-          return 0;
-        }
-        return p;
+      // Lane g < 8 of each warp: the page of 16-key group g of step j, read two
+      // steps ahead of its use; a bad id is recorded and page 0 read.
+      auto fetch = [&](int j) {
+        const int tok = j * kKeys + lane * 16;
+        return lane < 8 && j < it.j1 && tok < it.len ? table[tok >> L.p_log2] : 0;
       };
+      auto checked = [&](int p) {
+        if (p >= 0 && p < L.n_pages) return p;
+        paged_error(L, ERR_PAGED_PAGE, it.seq, p);
+        return 0;
+      };
+      int pg = checked(fetch(it.j0)), pg_next = fetch(it.j0 + 1);
       if (E4M3) {
-        const int ck = lt & 7, r = lt >> 3;  // 16 codes ck of rows r + 16 i
+        // 16 codes ck of rows r + 16 i.  Eight neighbouring lanes are four
+        // chunks of one half by two rows of different parity: their 16-byte
+        // stores meet in no bank.
+        const int ck = (lane & 3) | (lane >> 1 & 4), r = (lane >> 2 & 1) | (lane >> 3 & 2) | (warp & 3) << 2;
+        const uint32_t put = (ck >> 2) * kHalf + r * 128 + ((((2 * ck) & 7) ^ (r & 7)) << 4);
+        const int64_t page_stride = (int64_t)n_kv * L.P * D;
+        const int64_t at = (int64_t)it.head * L.P * D + ck * 16;
         uint4 kr[8], vr[8];
-        int pg[8];
         auto load = [&](int j, const uint8_t* pool, uint4 (&x)[8]) {
+          const uint8_t* from = pool + at;
+          const int left = it.len - j * kKeys - r;  // row 16 i + r is held where 16 i < left
+          const int slot = (j * kKeys + r) & (L.P - 1), mask = L.P - 1;
+          if (__all_sync(FULL, left > 112)) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int tok = j * kKeys + 16 * i + r;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (tok < it.len)
-              x[i] = *reinterpret_cast<const uint4*>(
-                  pool + (((int64_t)pg[i] * n_kv + it.head) * L.P + (tok & (L.P - 1))) * D + ck * 16);
+            for (int i = 0; i < 8; ++i)
+              x[i] = *reinterpret_cast<const uint4*>(from + __shfl_sync(FULL, pg, i) * page_stride + ((slot + 16 * i) & mask) * D);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t p = __shfl_sync(FULL, pg, i);
+              x[i] = make_uint4(0, 0, 0, 0);
+              if (16 * i < left) x[i] = *reinterpret_cast<const uint4*>(from + p * page_stride + ((slot + 16 * i) & mask) * D);
+            }
           }
         };
         auto store = [&](uint32_t to, const uint4 (&x)[8]) {
-          const uint32_t half = to + (ck >> 2) * kHalf;
-          const int c0 = (2 * ck) & 7, first = ck >> 2;  // the two halves of a row take turns: no bank conflicts
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t h[8];
+            const uint32_t a0 = to + put + i * 2048;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              h[2 * k] = e4m3_h2(w[k]);
-              h[2 * k + 1] = e4m3_h2(w[k] >> 16);
-            }
-            const int row = 16 * i + r;
-            const uint32_t at = half + row * 128;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int s = z ^ first;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + (uint32_t)(((c0 + s) ^ (row & 7)) << 4)),
-                           "r"(s ? h[4] : h[0]), "r"(s ? h[5] : h[1]), "r"(s ? h[6] : h[2]), "r"(s ? h[7] : h[3])
+            for (int k = 0; k < 2; ++k)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a0 ^ (k * 16)), "r"(e4m3_h2(w[2 * k])),
+                           "r"(e4m3_h2(w[2 * k] >> 16)), "r"(e4m3_h2(w[2 * k + 1])), "r"(e4m3_h2(w[2 * k + 1] >> 16))
                            : "memory");
-            }
           }
         };
-        auto pages = [&](int j) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) pg[i] = page_of(j, i);
+        float ks = 1.0f, vs = 1.0f;  // lanes < 8 of the first warp: the groups' scales of the step that pg belongs to
+        auto scales = [&](int j) {
+          ks = vs = 1.0f;
+          if (lt < 8 && j < it.j1 && j * kKeys + lt * 16 < it.len) {
+            ks = L.k_scale[(int64_t)pg * n_kv + it.head];
+            vs = L.v_scale[(int64_t)pg * n_kv + it.head];
+          }
         };
         if (it.j0 < it.j1) {
-          pages(it.j0);
           load(it.j0, L.k, kr);
+          scales(it.j0);
         }
-        for (int j = it.j0; j < it.j1 && ok; ++j, ++c) {
+        for (int j = it.j0; j < it.j1; ++j, ++c) {
           load(j, L.v, vr);
-          float ks = 1.0f, vs = 1.0f;
-          if (lt < 8) {
-            const int p = page_of(j, lt);
-            if (p >= 0) {
-              ks = L.k_scale[(int64_t)p * n_kv + it.head];
-              vs = L.v_scale[(int64_t)p * n_kv + it.head];
-            }
-          }
-          ok = c < 2 || wait(&sh.k_free[c & 1], ((c >> 1) - 1) & 1);
+          const float ks0 = ks, vs0 = vs;
+          pg = checked(pg_next);
+          pg_next = fetch(j + 2);
+          scales(j + 1);
+          ok = c < 2 || __all_sync(FULL, wait(&sh.k_free[c & 1], ((c >> 1) - 1) & 1));
           if (!ok) break;
           if (lt < 8) {
-            sh.kf[c & 3][lt] = ks;
-            sh.lsv[c & 3][lt] = __log2f(vs);
-            sh.inv[c & 3][lt] = __frcp_rn(vs);
+            sh.kb[c & 3][lt] = make_float2(ks0, __log2f(vs0));
+            sh.inv[c & 3][lt] = __frcp_rn(vs0);
           }
           store(sk + (c & 1) * kTile, kr);
           fence_proxy_async();
           mbar_arrive(&sh.k_full[c & 1]);
-          if (j + 1 < it.j1) {
-            pages(j + 1);
-            load(j + 1, L.k, kr);
-          }
-          ok = c < 2 || wait(&sh.v_free[c & 1], ((c >> 1) - 1) & 1);
+          if (j + 1 < it.j1) load(j + 1, L.k, kr);
+          ok = c < 2 || __all_sync(FULL, wait(&sh.v_free[c & 1], ((c >> 1) - 1) & 1));
           if (!ok) break;
           store(sv + (c & 1) * kTile, vr);
           fence_proxy_async();
@@ -527,17 +532,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
         }
       } else {
         const int ck = lt & 15, r = lt >> 4;  // 8 channels ck of rows r + 8 i
+        const uint32_t put = (ck >> 3) * kHalf + r * 128 + (((ck & 7) ^ r) << 4);
+        const int64_t page_stride = (int64_t)n_kv * L.P * D * 2;
+        const int64_t at = ((int64_t)it.head * L.P * D + ck * 8) * 2;
         auto load = [&](int j, const uint8_t* pool, uint32_t to) {
-          const uint32_t half = to + (ck >> 3) * kHalf;
-          int p = 0;
+          const uint8_t* from = pool + at;
+          const int left = it.len - j * kKeys - r;  // row 8 i + r is held where 8 i < left
+          const int slot = (j * kKeys + r) & (L.P - 1), mask = L.P - 1;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int row = 8 * i + r, tok = j * kKeys + row;
-            if ((i & 1) == 0) p = page_of(j, i >> 1);
-            const bool in = tok < it.len;
-            const uint8_t* from =
-                pool + ((((int64_t)(in ? p : 0) * n_kv + it.head) * L.P + (tok & (L.P - 1))) * D + ck * 8) * 2;
-            cp_async16_z(half + row * 128 + (((ck & 7) ^ (row & 7)) << 4), from, in);
+            const int64_t p = __shfl_sync(FULL, pg, i >> 1);
+            cp_async16_z(to + put + i * 1024, from + p * page_stride + ((slot + 8 * i) & mask) * (D * 2), 8 * i < left);
           }
           cp_async_commit();
         };
@@ -551,17 +556,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           fence_proxy_async();
           mbar_arrive(pending);
         };
-        for (int j = it.j0; j < it.j1 && ok; ++j, ++c) {
-          ok = c < 2 || wait(&sh.k_free[c & 1], ((c >> 1) - 1) & 1);
+        for (int j = it.j0; j < it.j1; ++j, ++c) {
+          ok = c < 2 || __all_sync(FULL, wait(&sh.k_free[c & 1], ((c >> 1) - 1) & 1));
           if (!ok) break;
           load(j, L.k, sk + (c & 1) * kTile);
           signal(false);
           pending = &sh.k_full[c & 1];
-          ok = c < 2 || wait(&sh.v_free[c & 1], ((c >> 1) - 1) & 1);
+          ok = c < 2 || __all_sync(FULL, wait(&sh.v_free[c & 1], ((c >> 1) - 1) & 1));
           if (!ok) break;
           load(j, L.v, sv + (c & 1) * kTile);
           signal(false);
           pending = &sh.v_full[c & 1];
+          pg = checked(pg_next);
+          pg_next = fetch(j + 2);
         }
         if (ok) signal(true);
         asm volatile("cp.async.wait_group 0;\n" ::: "memory");
@@ -575,18 +582,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     const uint32_t ts = trow + t * 128, to = trow + 256 + t * 128;
     unsigned sc = 0, oc = 0, c = 0;  // phases of s_full, o_full; steps so far (the scales' ring)
     bool ok = true;
+    // A row's place, from its item.
+    struct Row {
+      int row, tok, head, see, nt;
+      bool live;
+      int64_t out_row;
+    };
+    auto row_of = [&](const Item& it) {
+      Row x;
+      x.row = t * 128 + r;
+      x.tok = it.q0 + x.row / G;
+      x.head = it.head * G + x.row % G;
+      x.live = x.tok < it.n_new;
+      x.out_row = (int64_t)it.row0 + x.tok;
+      x.see = !x.live ? 0 : a.causal ? max(0, min(it.len, it.len - it.n_new + x.tok + 1)) : it.len;
+      x.nt = min(it.n_new - it.q0, q_tile) * G > 128 ? 2 : 1;
+      return x;
+    };
     for (int e = blockIdx.x; e < entries; e += gridDim.x) {
-      const Item it = item_of(e);
-      const int n = it.j1 - it.j0;
-      const int nt = min(it.n_new - it.q0, q_tile) * G > 128 ? 2 : 1;
-      const int row = t * 128 + r, tok = it.q0 + row / G, head = it.head * G + row % G;
-      const bool live = tok < it.n_new && row < kRows;
-      const int64_t out_row = (int64_t)it.row0 + tok;
-      const int see = !live ? 0 : a.causal ? max(0, min(it.len, it.len - it.n_new + tok + 1)) : it.len;
-      float m = -INFINITY, l = 0.0f, zf = a.scale;
-      if (t < nt && n > 0 && ok) {
+      // The item is formed anew after the steps: in them, the registers are
+      // for the row's logits.
+      int n, lim0, nt;
+      float m = -INFINITY, l = 0.0f, zf = fmaxf(a.scale, kTiny);
+      {
+        const Item it = item_of(e);
+        const Row x = row_of(it);
+        n = it.j1 - it.j0;
+        nt = x.nt;
+        lim0 = x.see - it.j0 * kKeys;
+        if (t < nt && n > 0 && ok) {
+          const bool live = x.live;
+          const uint16_t* qp = a.q + x.out_row * a.q_stride + x.head * D;
+
         // The row's query into the operand tile.
-        const uint16_t* qp = a.q + out_row * a.q_stride + head * D;
         const uint32_t dst = sq + t * kTile + r * 128;
         if (E4M3) {
           float top = 0.0f;
@@ -631,16 +659,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
         }
         fence_proxy_async();
         mbar_arrive(&sh.q_full[t]);
-
+        }
+      }
+      if (t < nt && n > 0 && ok) {
         for (int j = 0; j < n; ++j, ++c) {
           ok = __all_sync(FULL, wait(&sh.s_full[t], sc++ & 1));
           if (!ok) break;
           tmem_fence_after_sync();
-          const int lim = see - (it.j0 + j) * kKeys;  // columns from here on are hidden
+          const int lim = lim0 - j * kKeys;  // columns from here on are hidden
           const bool cut = __any_sync(FULL, lim < kKeys);
           uint32_t v[4][32];
           tmem_ld128(ts, v);
           if (cut) {
+            asm volatile("");  // a branch, not 128 selections in every step
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               if (i >= lim) v[i >> 5][i & 31] = 0xff800000u;
@@ -648,17 +679,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           float mx = -INFINITY;
 #pragma unroll
           for (int h = 0; h < 8; ++h) {  // 16 keys: one scale
-            float x = __uint_as_float(v[h >> 1][16 * (h & 1)]), y = __uint_as_float(v[h >> 1][16 * (h & 1) + 1]);
-#pragma unroll
-            for (int i = 2; i < 16; i += 2) {
-              x = fmaxf(x, __uint_as_float(v[h >> 1][16 * (h & 1) + i]));
-              y = fmaxf(y, __uint_as_float(v[h >> 1][16 * (h & 1) + i + 1]));
+            const uint32_t* z = &v[h >> 1][16 * (h & 1)];
+            float x = max3(z[0], z[1], z[2]);
+            float y = max3(z[3], z[4], z[5]);
+            x = max3(__float_as_uint(x), z[6], z[7]);
+            y = max3(__float_as_uint(y), z[8], z[9]);
+            x = max3(__float_as_uint(x), z[10], z[11]);
+            y = max3(__float_as_uint(y), z[12], z[13]);
+            x = fmaxf(max3(__float_as_uint(x), z[14], z[15]), y);
+            if (E4M3) {
+              const float2 kb = sh.kb[c & 3][h];
+              x = fmaf(x, fmaxf(zf * kb.x, kTiny), kb.y);
             }
-            x = fmaxf(x, y);
-            if (E4M3) x = x == -INFINITY ? x : fmaf(x, zf * sh.kf[c & 3][h], sh.lsv[c & 3][h]);
             mx = fmaxf(mx, x);
           }
-          if (!E4M3) mx = mx == -INFINITY ? mx : mx * zf;
+          if (!E4M3) mx *= zf;
           const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
           if (__any_sync(FULL, raise)) {
             const float mn = raise ? mx : m;
@@ -679,7 +714,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           const float ms = (m == -INFINITY ? 0.0f : m) - kShift;
 #pragma unroll
           for (int h = 0; h < 8; ++h) {
-            const float k = fmaxf(E4M3 ? zf * sh.kf[c & 3][h] : zf, kTiny), bb = E4M3 ? sh.lsv[c & 3][h] - ms : -ms;
+            float k = zf, bb = -ms;
+            if (E4M3) {
+              const float2 kb = sh.kb[c & 3][h];
+              k = fmaxf(zf * kb.x, kTiny);
+              bb = kb.y - ms;
+            }
             const uint64_t k2 = pair(k, k), b2 = pair(bb, bb);
             uint64_t add = 0;
             uint32_t p[8];
@@ -710,6 +750,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
         c += n;
       }
       // ---- the row's result ----
+      int e2 = e;
+      asm volatile("" : "+r"(e2));
+      const Item it = item_of(e2);
+      const Row x = row_of(it);
+      const int row = x.row, head = x.head, see = x.see;
+      const bool live = x.live;
+      const int64_t out_row = x.out_row;
       if (it.parts == 1) {
         if (t < nt) {
           const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
