@@ -21,9 +21,11 @@
 //    (fp16 weights) or 2^8 (bf16): only then is the accumulator rescaled.
 //    e4m3: weights in fp16 after a factor 2^10 (at most 2^14, smallest step
 //    2^-34 of the maximum's); bf16: weights in bf16 (2^-9 each).
-//  * When there are fewer row tiles than SMs, the keys of a row tile are
-//    split over several CTAs by their count; the last CTA of a tile to arrive
-//    joins the parts in their order.
+//  * Work split on the device, from the lengths: all row tiles' steps of 128
+//    keys in a row, cut into equal runs, one a CTA, so that uneven batches,
+//    causal masks and a few rows against a long context load the SMs alike.  A
+//    row tile that lies in several runs is joined by the last CTA of it to
+//    arrive, in the order of the parts.
 #include "mk_paged.cuh"
 
 namespace mk {
@@ -39,6 +41,8 @@ constexpr int kThreads = 512;              // 8 softmax warps, 4 loading warps, 
 // (512 x 128 = 65,536), and the shares add up to that.
 constexpr int kRegsSoftmax = 184, kRegsLoad = 96, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue == 4 * 128, "register shares");
+constexpr int kItems = 4;                  // items that the list may run ahead of the slowest group
+constexpr int kMinRun = 4;                 // shortest run of a CTA, in steps
 constexpr int kSmem = 1024 + 2 * kTile + 4 * kTile;
 // Logit factors are at least this, so that a hidden key's -infinity stays one
 // (a row of zeros or a scale of 0 would make it NaN).
@@ -199,18 +203,28 @@ __device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, bool
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-// One work item: a row tile of one (sequence, kv head) against keys
-// [j0, j1) x 128, part `part` of `parts`.
+// One work item of a CTA: a row tile of one (sequence, kv head) against its
+// keys [j0, j1) x 128 (of n steps in all).
 struct Item {
-  int seq, head, q0, row0, n_new, len, see_max, j0, j1, parts, slot, ctr;
+  int seq, head, q0, row0, n_new, len, n, j0, j1;
+  int b_lo, parts;  // the CTAs b_lo .. b_lo + parts - 1 have a part of it
+  int end;          // 1: no item, the list is at its end
+};
+// A place in the list of all items: its sequence, row tile (the last queries
+// first: with a causal mask they see the most keys), head, and where it begins
+// in the CTA's run (negative: in an earlier CTA's).
+struct Cursor {
+  int seq, tile, head, rel;
 };
 
 struct Shared {
-  int pre[MK_MAX_CALL_SEQS + 1];       // row tiles x kv heads before each sequence
+  int64_t pre[MK_MAX_CALL_SEQS + 1];   // cost of the sequences before each
   int row0[MK_MAX_CALL_SEQS], n_new[MK_MAX_CALL_SEQS], len[MK_MAX_CALL_SEQS];
-  int epre[kPagedMaxCtas + 1];         // split: entries before each row tile of the batch
-  int eparts[kPagedMaxCtas];
-  int wsum[16];
+  Cursor start;
+  int64_t f0, per;                     // the CTA's run: its begin and the length of all runs
+  int span;                            // its length
+  Item ring[kItems];                   // items on their way to the groups of warps
+  uint64_t item_full[kItems], item_free[kItems], met, done;
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], k_full[2], k_free[2], v_full[2], v_free[2];
   // e4m3, per 16 keys of a step, ring of 4 steps: {k scale, log2 v scale}, 1 / v scale
   __align__(16) float2 kb[4][8];
@@ -243,6 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       mbar_init(&sh.v_full[i], 128);
       mbar_init(&sh.v_free[i], 1);
     }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&sh.item_full[i], 1);
+      mbar_init(&sh.item_free[i], 13);  // one arrival of each softmax, loading and issuing warp
+    }
+    mbar_init(&sh.met, 256);
+    mbar_init(&sh.done, 1);
     sh.dead = 0;
   }
   mbar_init_fence();
@@ -250,118 +270,92 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   pdl_trigger();
   if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;
 
-  // ---- the list of work items (every CTA forms the same one) ----
-  int total = 0;
-  for (int i0 = 0; i0 < n_seqs; i0 += kThreads) {
-    const int i = i0 + tid;
-    int mine = 0;
-    if (i < n_seqs) {
-      PagedSeq s = paged_seq(a.b, L.P, i, false);
-      if (!s.ok) {
-        paged_error(L, ERR_PAGED_BATCH, i, s.len);
-        s.n_new = 0;
-      }
+  // ---- the CTA's run of the list of work items ----
+  // All items in a row, each as long as its steps and one more (its queries
+  // and its result), are cut into equal runs, one a CTA: an item may lie in
+  // several.  Its step j is at its place plus j.
+  auto tiles_of = [&](int seq) { return (sh.n_new[seq] + q_tile - 1) / q_tile; };
+  auto steps_of = [&](int seq, int tile) {  // 128-key steps that the tile's last query needs
+    const int n_new = sh.n_new[seq], len = sh.len[seq];
+    const int q1 = min((tiles_of(seq) - tile) * q_tile, n_new);
+    const int see = a.causal ? max(0, min(len, len - n_new + q1)) : len;
+    return (see + kKeys - 1) / kKeys;
+  };
+  for (int i = warp; i < n_seqs; i += kThreads / 32) {
+    PagedSeq s = paged_seq(a.b, L.P, i, false);
+    if (!s.ok) {
+      if (lane == 0) paged_error(L, ERR_PAGED_BATCH, i, s.len);
+      s.n_new = 0;
+    }
+    if (lane == 0) {
       sh.row0[i] = s.row0;
       sh.n_new[i] = s.n_new;
       sh.len[i] = s.len;
-      mine = (s.n_new + q_tile - 1) / q_tile * n_kv;
     }
-    const int ex = warp_excl_scan(mine, lane);
-    if (lane == 31) sh.wsum[warp] = ex + mine;
-    __syncthreads();
-    int off = total;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) off += sh.wsum[w];
-      total += sh.wsum[w];
-    }
-    if (i < n_seqs) sh.pre[i] = off + ex;
-    __syncthreads();
-  }
-  if (tid == 0) sh.pre[n_seqs] = total;
-  __syncthreads();
-
-  // Row tile t (without its head) of the batch: sequence and first query.
-  // Within a sequence the last queries come first: with a causal mask they
-  // see the most keys, and the long items start early.
-  auto find = [&](int t, Item& it) {
-    int lo = 0, hi = n_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (sh.pre[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    it.seq = lo;
-    it.row0 = sh.row0[lo];
-    it.n_new = sh.n_new[lo];
-    it.len = sh.len[lo];
-    const int r = t - sh.pre[lo], tiles = (it.n_new + q_tile - 1) / q_tile;
-    it.head = r % n_kv;
-    it.q0 = (tiles - 1 - r / n_kv) * q_tile;
-    const int q1 = min(it.q0 + q_tile, it.n_new) - 1;
-    it.see_max = a.causal ? max(0, min(it.len, it.len - it.n_new + q1 + 1)) : it.len;
-  };
-  const bool split = total < (int)gridDim.x;
-  int entries = total;
-  if (split) {
-    const int n_pairs = total / n_kv;
-    int n = 0;
-    if (tid < n_pairs) {
-      Item it;
-      find(tid * n_kv, it);
-      n = (it.see_max + kKeys - 1) / kKeys;
-    }
-    int x = n;  // the sum of n over the row tiles
+    __syncwarp();
+    int64_t x = 0;
+    for (int t = lane, nt = tiles_of(i); t < nt; t += 32) x += max(steps_of(i, t), 1) + 1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
-    if (lane == 0) sh.wsum[warp] = x;
-    __syncthreads();
-    int all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) all += sh.wsum[w];
-    __syncthreads();
-    int per = (int)(((int64_t)all * n_kv + gridDim.x - 1) / gridDim.x);
-    if (per < 2) per = 2;
-    const int parts = tid < n_pairs ? max(1, (n + per - 1) / per) : 0;
-    const int ex = warp_excl_scan(parts, lane);
-    if (lane == 31) sh.wsum[warp] = ex + parts;
-    __syncthreads();
-    int off = 0, sum = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) off += sh.wsum[w];
-      sum += sh.wsum[w];
-    }
-    if (tid < n_pairs) {
-      sh.epre[tid] = (off + ex) * n_kv;
-      sh.eparts[tid] = parts;
-    }
-    entries = sum * n_kv;
-    __syncthreads();
+    if (lane == 0) sh.pre[i] = x * n_kv;
   }
-  auto item_of = [&](int e) {
-    Item it;
-    if (!split) {
-      find(e, it);
-      it.j0 = 0;
-      it.j1 = (it.see_max + kKeys - 1) / kKeys;
-      it.parts = 1;
-      it.slot = it.ctr = 0;
-      return it;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t base = 0;
+    for (int i0 = 0; i0 < n_seqs; i0 += 32) {
+      const int i = i0 + lane;
+      const int64_t mine = i < n_seqs ? sh.pre[i] : 0;
+      int64_t x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+      }
+      if (i < n_seqs) sh.pre[i] = base + x - mine;
+      base += __shfl_sync(FULL, x, 31);
     }
-    int lo = 0, hi = total / n_kv - 1;
-    while (lo < hi) {
+    if (lane == 0) sh.pre[n_seqs] = base;
+  }
+  __syncthreads();
+  const int64_t total = sh.pre[n_seqs];
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kMinRun) per = kMinRun;
+  const int64_t f0 = (int64_t)blockIdx.x * per;
+  if (f0 >= total) return;
+  if (tid == 0) {
+    sh.f0 = f0;
+    sh.per = per;
+    sh.span = (int)(total - f0 < per ? total - f0 : per);
+  }
+  if (warp == 0) {
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {  // the last sequence that begins at or before f0 (one without queries begins where the next does)
       const int mid = (lo + hi + 1) >> 1;
-      if (sh.epre[mid] <= e) lo = mid; else hi = mid - 1;
+      if (sh.pre[mid] <= f0) lo = mid; else hi = mid - 1;
     }
-    find(lo * n_kv, it);
-    const int r = e - sh.epre[lo], n = (it.see_max + kKeys - 1) / kKeys;
-    it.parts = sh.eparts[lo];
-    it.head = r / it.parts;
-    const int p = r - it.head * it.parts;
-    it.j0 = (int)((int64_t)n * p / it.parts);
-    it.j1 = (int)((int64_t)n * (p + 1) / it.parts);
-    it.slot = e;
-    it.ctr = lo * n_kv + it.head;
-    return it;
-  };
-
+    int64_t at = sh.pre[lo];
+    for (int t0 = 0, nt = tiles_of(lo); t0 < nt; t0 += 32) {
+      const int t = t0 + lane;
+      const int cost = t < nt ? max(steps_of(lo, t), 1) + 1 : 0;
+      int64_t x = (int64_t)cost * n_kv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned past = __ballot_sync(FULL, at + x > f0);
+      if (past) {
+        if (lane == __ffs(past) - 1) {
+          const int64_t begin = at + x - (int64_t)cost * n_kv;
+          const int head = (int)((f0 - begin) / cost);
+          sh.start = Cursor{lo, t, head, (int)(begin + (int64_t)head * cost - f0)};
+        }
+        break;
+      }
+      at += __shfl_sync(FULL, x, 31);
+    }
+  }
+  __syncthreads();
   if (warp == 12) tmem_alloc(&sh.tmem, 512);
   tmem_fence_before_sync();
   __syncthreads();
@@ -376,9 +370,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     return false;
   };
 
+  // Items last longer than a single wait's limit: a hundred of them.
+  auto wait_long = [&](uint64_t* bar, unsigned parity) {
+    for (int i = 0; i < 100; ++i) {
+      if (sh.dead) return false;
+      if (mbar_wait(bar, parity)) return true;
+    }
+    return wait(bar, parity);
+  };
+  // The next item of the list for a group of warps; nullptr at its end.
+  auto take = [&](unsigned c) -> const Item* {
+    if (!__all_sync(FULL, wait_long(&sh.item_full[c % kItems], (c / kItems) & 1))) return nullptr;
+    const Item* it = &sh.ring[c % kItems];
+    return it->end ? nullptr : it;
+  };
+  auto give_back = [&](unsigned c) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.item_free[c % kItems]);
+  };
+
   if (warp >= 12) {
-    // ---- issues the products ----
     fewer_registers<kRegsIssue>();
+    if (warp == 13 && lane == 0) {
+      // ---- lists the items ----
+      Cursor k = sh.start;
+      unsigned c = 0;
+      auto put = [&](const Item& it) {
+        if (c >= kItems && !wait_long(&sh.item_free[c % kItems], (c / kItems - 1) & 1)) return false;
+        sh.ring[c % kItems] = it;
+        mbar_arrive(&sh.item_full[c % kItems]);
+        ++c;
+        return true;
+      };
+      Item it;
+      it.end = 0;
+      bool ok = true;
+      while (ok && k.rel < sh.span) {
+        it.n = steps_of(k.seq, k.tile);
+        it.j0 = max(0, -k.rel);
+        it.j1 = min(it.n, sh.span - k.rel);
+        if (it.n == 0 ? k.rel >= 0 : it.j0 < it.j1) {
+          it.seq = k.seq;
+          it.head = k.head;
+          it.row0 = sh.row0[k.seq];
+          it.n_new = sh.n_new[k.seq];
+          it.len = sh.len[k.seq];
+          it.q0 = (tiles_of(k.seq) - 1 - k.tile) * q_tile;
+          const int64_t place = sh.f0 + k.rel;
+          it.b_lo = (int)(place / sh.per);
+          it.parts = it.n == 0 ? 1 : (int)((place + it.n - 1) / sh.per) - it.b_lo + 1;
+          ok = put(it);
+        }
+        k.rel += max(it.n, 1) + 1;
+        if (++k.head == n_kv) {
+          k.head = 0;
+          if (++k.tile == tiles_of(k.seq)) {
+            k.tile = 0;
+            do ++k.seq;
+            while (k.seq < n_seqs && sh.n_new[k.seq] == 0);
+          }
+        }
+      }
+      it.end = 1;
+      if (ok) put(it);
+    }
+    // ---- issues the products ----
     if (warp == 12) {
       unsigned kc = 0, vc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
       bool ok = true;
@@ -398,10 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
         }
         __syncwarp();
       };
-      for (int e = blockIdx.x; e < entries && ok; e += gridDim.x) {
-        const Item it = item_of(e);
-        const int n = it.j1 - it.j0;
-        const int nt = min(it.n_new - it.q0, q_tile) * G > 128 ? 2 : 1;
+      const Item* it;
+      for (unsigned ic = 0; ok && (it = take(ic)); ++ic) {
+        const int n = it->j1 - it->j0;
+        const int nt = min(it->n_new - it->q0, q_tile) * G > 128 ? 2 : 1;
+        give_back(ic);
         if (n == 0) continue;
         for (int t = 0; t < nt; ++t) ok = ok && wait_all(&sh.q_full[t], qc[t]++ & 1);
         ok = ok && wait_all(&sh.k_full[kc & 1], (kc >> 1) & 1);
@@ -436,6 +493,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           if (!end) ++kc;
         }
       }
+      // Nothing is in flight when the tensor memory is freed, also after a
+      // wait that ran out.
+      if (elect_one()) umma_commit(&sh.done);
+      __syncwarp();
+      (void)mbar_wait_warp(&sh.done, 0);
     }
   } else if (warp >= 8) {
     // ---- keys and values into shared memory ----
@@ -443,8 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     const int lt = tid - 256;
     unsigned c = 0;  // steps so far
     bool ok = true;
-    for (int e = blockIdx.x; e < entries && ok; e += gridDim.x) {
-      const Item it = item_of(e);
+    const Item* item;
+    for (unsigned ic = 0; ok && (item = take(ic)); ++ic) {
+      const Item it = *item;
+      give_back(ic);
       const int32_t* table = a.b.page_table + (int64_t)it.seq * a.b.table_stride;
       // Lane g < 8 of each warp: the page of 16-key group g of step j, read two
       // steps ahead of its use; a bad id is recorded and page 0 read.
@@ -580,8 +644,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     const int t = warp >> 2, r = tid & 127;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = trow + t * 128, to = trow + 256 + t * 128;
-    unsigned sc = 0, oc = 0, c = 0;  // phases of s_full, o_full; steps so far (the scales' ring)
     bool ok = true;
+    // One register: phases of s_full (bit 0), o_full (1) and met (2); place in
+    // the scales' ring (bits 4, 5); items so far (from bit 8).
+    unsigned st = 0;
+    auto step_ring = [&](unsigned by) { st = (st & ~0x30u) | ((st + (by << 4)) & 0x30u); };
+    // The eight softmax warps meet (an mbarrier: with the limit that every wait has).
+    auto meet = [&]() {
+      mbar_arrive(&sh.met);
+      st ^= 4u;
+      return __all_sync(FULL, wait(&sh.met, (~st >> 2) & 1)) != 0;
+    };
     // A row's place, from its item.
     struct Row {
       int row, tok, head, see, nt;
@@ -599,17 +672,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       x.nt = min(it.n_new - it.q0, q_tile) * G > 128 ? 2 : 1;
       return x;
     };
-    for (int e = blockIdx.x; e < entries; e += gridDim.x) {
+    const Item* it;
+    for (; (it = take(st >> 8)); st += 0x100u) {
       // The item is formed anew after the steps: in them, the registers are
       // for the row's logits.
       int n, lim0, nt;
       float m = -INFINITY, l = 0.0f, zf = fmaxf(a.scale, kTiny);
       {
-        const Item it = item_of(e);
-        const Row x = row_of(it);
-        n = it.j1 - it.j0;
+        const Row x = row_of(*it);
+        n = it->j1 - it->j0;
         nt = x.nt;
-        lim0 = x.see - it.j0 * kKeys;
+        lim0 = x.see - it->j0 * kKeys;
         if (t < nt && n > 0 && ok) {
           const bool live = x.live;
           const uint16_t* qp = a.q + x.out_row * a.q_stride + x.head * D;
@@ -662,8 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
         }
       }
       if (t < nt && n > 0 && ok) {
-        for (int j = 0; j < n; ++j, ++c) {
-          ok = __all_sync(FULL, wait(&sh.s_full[t], sc++ & 1));
+        for (int j = 0; j < n; ++j, step_ring(1)) {
+          ok = __all_sync(FULL, wait(&sh.s_full[t], st & 1));
+          st ^= 1u;
           if (!ok) break;
           tmem_fence_after_sync();
           const int lim = lim0 - j * kKeys;  // columns from here on are hidden
@@ -688,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             y = max3(__float_as_uint(y), z[12], z[13]);
             x = fmaxf(max3(__float_as_uint(x), z[14], z[15]), y);
             if (E4M3) {
-              const float2 kb = sh.kb[c & 3][h];
+              const float2 kb = sh.kb[(st >> 4) & 3][h];
               x = fmaf(x, fmaxf(zf * kb.x, kTiny), kb.y);
             }
             mx = fmaxf(mx, x);
@@ -716,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           for (int h = 0; h < 8; ++h) {
             float k = zf, bb = -ms;
             if (E4M3) {
-              const float2 kb = sh.kb[c & 3][h];
+              const float2 kb = sh.kb[(st >> 4) & 3][h];
               k = fmaxf(zf * kb.x, kTiny);
               bb = kb.y - ms;
             }
@@ -735,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             }
             float x, y;
             unpair(add, x, y);
-            l = E4M3 ? fmaf(x + y, sh.inv[c & 3][h], l) : l + (x + y);
+            l = E4M3 ? fmaf(x + y, sh.inv[(st >> 4) & 3][h], l) : l + (x + y);
             tmem_st8(ts + h * 8, p);
           }
           tmem_wait_st();
@@ -743,21 +817,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           mbar_arrive(&sh.p_full[t]);
         }
         if (ok) {
-          ok = __all_sync(FULL, wait(&sh.o_full[t], oc++ & 1));
+          ok = __all_sync(FULL, wait(&sh.o_full[t], (st >> 1) & 1));
+          st ^= 2u;
           tmem_fence_after_sync();
         }
       } else {
-        c += n;
+        step_ring((unsigned)n);
       }
       // ---- the row's result ----
-      int e2 = e;
-      asm volatile("" : "+r"(e2));
-      const Item it = item_of(e2);
-      const Row x = row_of(it);
+      asm volatile("" ::: "memory");  // formed anew, as above
+      const Row x = row_of(*it);
       const int row = x.row, head = x.head, see = x.see;
       const bool live = x.live;
       const int64_t out_row = x.out_row;
-      if (it.parts == 1) {
+      const int parts = it->parts, b_lo = it->b_lo, j0 = it->j0;
+      give_back(st >> 8);
+      if (parts == 1) {
         if (t < nt) {
           const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll
@@ -794,10 +869,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       // A part of a split row tile: [32 column groups][256 rows] float4, then
       // the rows' maxima and sums.
       constexpr int64_t kPartFloats = (int64_t)kRows * (D + 2);
-      auto part_of = [&](int slot) { return a.part + slot * kPartFloats; };
+      auto part_of = [&](int64_t slot) { return a.part + slot * kPartFloats; };
+      // A CTA can hold the beginning of one item and the rest of another.
+      const int64_t mine = 2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0);
+      auto slot = [&](int i) { return 2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0); };
       if (t < nt) {
-        float4* op = reinterpret_cast<float4*>(part_of(it.slot));
-        float* ml = part_of(it.slot) + (int64_t)kRows * D;
+        float4* op = reinterpret_cast<float4*>(part_of(mine));
+        float* ml = part_of(mine) + (int64_t)kRows * D;
         ml[row] = m;
         ml[kRows + row] = l;
 #pragma unroll
@@ -818,47 +896,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
         tmem_fence_before_sync();
       }
       __threadfence();
-      asm volatile("bar.sync 1, 256;" ::: "memory");  // the eight softmax warps
+      if (!meet()) break;
       if (tid == 0) {
-        const int old = atomicAdd(&a.counters[it.ctr], 1);
-        sh.last = old == it.parts - 1;
-        if (sh.last) a.counters[it.ctr] = 0;
+        const int old = atomicAdd(&a.counters[b_lo], 1);  // one item at most begins in b_lo and ends after it
+        sh.last = old == parts - 1;
+        if (sh.last) a.counters[b_lo] = 0;
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (!meet()) break;
       if (sh.last) {
         __threadfence();
-        // The parts of this (row tile, head) have neighbouring slots.
-        const int s0 = sh.epre[it.ctr / n_kv] + it.head * it.parts;
         if (live && t < nt) {
           float M = -INFINITY, S = 0.0f;
-          for (int i = 0; i < it.parts; ++i) M = fmaxf(M, __ldcg(part_of(s0 + i) + (int64_t)kRows * D + row));
-          for (int i = 0; i < it.parts; ++i) {
-            const float mi = __ldcg(part_of(s0 + i) + (int64_t)kRows * D + row);
-            if (mi != -INFINITY) S = fmaf(__ldcg(part_of(s0 + i) + (int64_t)kRows * (D + 1) + row), ex2(mi - M), S);
+          for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(part_of(slot(i)) + (int64_t)kRows * D + row));
+          for (int i = 0; i < parts; ++i) {
+            const float mi = __ldcg(part_of(slot(i)) + (int64_t)kRows * D + row);
+            if (mi != -INFINITY) S = fmaf(__ldcg(part_of(slot(i)) + (int64_t)kRows * (D + 1) + row), ex2(mi - M), S);
           }
           const float f = S > 0.0f || S != S ? 1.0f / S : 0.0f;
-          for (int h = 0; h < 16; ++h) {  // eight columns at a time
-            float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            for (int i = 0; i < it.parts; ++i) {
-              const float mi = __ldcg(part_of(s0 + i) + (int64_t)kRows * D + row);
-              if (mi == -INFINITY) continue;
-              const float w = ex2(mi - M);
-              const float4* op = reinterpret_cast<const float4*>(part_of(s0 + i));
-              const float4 u = __ldcg(op + (2 * h) * kRows + row), v = __ldcg(op + (2 * h + 1) * kRows + row);
-              x[0] = fmaf(u.x, w, x[0]); x[1] = fmaf(u.y, w, x[1]); x[2] = fmaf(u.z, w, x[2]); x[3] = fmaf(u.w, w, x[3]);
-              x[4] = fmaf(v.x, w, x[4]); x[5] = fmaf(v.y, w, x[5]); x[6] = fmaf(v.z, w, x[6]); x[7] = fmaf(v.w, w, x[7]);
+          for (int h = 0; h < 2; ++h) {  // 64 columns at a time: 16 loads in flight
+            float4 o[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int i = 0; i < parts; ++i) {
+              const float mi = __ldcg(part_of(slot(i)) + (int64_t)kRows * D + row);
+              const float w = mi == -INFINITY ? 0.0f : ex2(mi - M);
+              const float4* op = reinterpret_cast<const float4*>(part_of(slot(i))) + 16 * h * kRows + row;
+              float4 u[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) u[k] = __ldcg(op + k * kRows);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                o[k].x = fmaf(u[k].x, w, o[k].x);
+                o[k].y = fmaf(u[k].y, w, o[k].y);
+                o[k].z = fmaf(u[k].z, w, o[k].z);
+                o[k].w = fmaf(u[k].w, w, o[k].w);
+              }
             }
-            uint4 o;
-            o.x = pack2<false>(x[0] * f, x[1] * f);
-            o.y = pack2<false>(x[2] * f, x[3] * f);
-            o.z = pack2<false>(x[4] * f, x[5] * f);
-            o.w = pack2<false>(x[6] * f, x[7] * f);
-            *reinterpret_cast<uint4*>(a.out + out_row * a.out_stride + head * D + h * 8) = o;
+            uint4* to = reinterpret_cast<uint4*>(a.out + out_row * a.out_stride + head * D + h * 64);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              to[k] = make_uint4(pack2<false>(o[2 * k].x * f, o[2 * k].y * f), pack2<false>(o[2 * k].z * f, o[2 * k].w * f),
+                                 pack2<false>(o[2 * k + 1].x * f, o[2 * k + 1].y * f),
+                                 pack2<false>(o[2 * k + 1].z * f, o[2 * k + 1].w * f));
           }
           if (a.lse) a.lse[out_row * (n_kv * G) + head] = see > 0 ? (log2f(S) + (M - kShift)) * kLn2 : -INFINITY;
         }
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");  // sh.last is free again
+      if (!meet()) break;  // sh.last is free again
     }
   }
   tmem_fence_before_sync();
