@@ -39,8 +39,9 @@ constexpr int kHalf = kTile / 2;           // its channels 0-63, then 64-127
 constexpr int kThreads = 512;              // 8 softmax warps, 4 loading warps, 1 issuing warp (and 3 without work)
 // Registers of a thread of each group of four warps; the launch gives 128 each
 // (512 x 128 = 65,536), and the shares add up to that.
-constexpr int kRegsSoftmax = 184, kRegsLoad = 96, kRegsIssue = 48;
+constexpr int kRegsSoftmax = 144, kRegsLoad = 128, kRegsIssue = 96;
 static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue == 4 * 128, "register shares");
+constexpr int kItemCost = 3;               // an item's queries and result take as long as this many steps
 constexpr int kItems = 4;                  // items that the list may run ahead of the slowest group
 constexpr int kMinRun = 4;                 // shortest run of a CTA, in steps
 constexpr int kSmem = 1024 + 2 * kTile + 4 * kTile;
@@ -137,11 +138,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n" ::"r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(taddr)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(
@@ -149,13 +145,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
       : "memory");
-}
-// A row's 128 columns.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, uint32_t (&v)[4][32]) {
-#pragma unroll
-  for (int h = 0; h < 4; ++h) tmem_ld32_async(taddr + h * 32, v[h]);
-#pragma unroll
-  for (int h = 0; h < 4; ++h) tmem_ld_wait(v[h]);
 }
 // Two fp32 operations at once.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
@@ -271,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;
 
   // ---- the CTA's run of the list of work items ----
-  // All items in a row, each as long as its steps and one more (its queries
+  // All items in a row, each as long as its steps and kItemCost (its queries
   // and its result), are cut into equal runs, one a CTA: an item may lie in
   // several.  Its step j is at its place plus j.
   auto tiles_of = [&](int seq) { return (sh.n_new[seq] + q_tile - 1) / q_tile; };
@@ -294,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     }
     __syncwarp();
     int64_t x = 0;
-    for (int t = lane, nt = tiles_of(i); t < nt; t += 32) x += max(steps_of(i, t), 1) + 1;
+    for (int t = lane, nt = tiles_of(i); t < nt; t += 32) x += max(steps_of(i, t), 1) + kItemCost;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
     if (lane == 0) sh.pre[i] = x * n_kv;
@@ -336,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     int64_t at = sh.pre[lo];
     for (int t0 = 0, nt = tiles_of(lo); t0 < nt; t0 += 32) {
       const int t = t0 + lane;
-      const int cost = t < nt ? max(steps_of(lo, t), 1) + 1 : 0;
+      const int cost = t < nt ? max(steps_of(lo, t), 1) + kItemCost : 0;
       int64_t x = (int64_t)cost * n_kv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -421,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           it.parts = it.n == 0 ? 1 : (int)((place + it.n - 1) / sh.per) - it.b_lo + 1;
           ok = put(it);
         }
-        k.rel += max(it.n, 1) + 1;
+        k.rel += max(it.n, 1) + kItemCost;
         if (++k.head == n_kv) {
           k.head = 0;
           if (++k.tile == tiles_of(k.seq)) {
@@ -641,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   } else {
     // ---- softmax: one row a thread ----
     more_registers<kRegsSoftmax>();
-    const int t = warp >> 2, r = tid & 127;
+    const int t = warp >> 2;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = trow + t * 128, to = trow + 256 + t * 128;
     bool ok = true;
@@ -655,22 +644,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       st ^= 4u;
       return __all_sync(FULL, wait(&sh.met, (~st >> 2) & 1)) != 0;
     };
-    // A row's place, from its item.
-    struct Row {
-      int row, tok, head, see, nt;
+    // Row x of the warp's 32, from its item.
+    struct Place {
+      int tok, head;
       bool live;
       int64_t out_row;
     };
-    auto row_of = [&](const Item& it) {
-      Row x;
-      x.row = t * 128 + r;
-      x.tok = it.q0 + x.row / G;
-      x.head = it.head * G + x.row % G;
-      x.live = x.tok < it.n_new;
-      x.out_row = (int64_t)it.row0 + x.tok;
-      x.see = !x.live ? 0 : a.causal ? max(0, min(it.len, it.len - it.n_new + x.tok + 1)) : it.len;
-      x.nt = min(it.n_new - it.q0, q_tile) * G > 128 ? 2 : 1;
-      return x;
+    const int g_log2 = __ffs(G) - 1, wrow = t * 128 + (warp & 3) * 32;
+    auto place_of = [&](const Item& it, int x) {
+      Place y;
+      y.tok = it.q0 + ((wrow + x) >> g_log2);
+      y.head = it.head * G + ((wrow + x) & (G - 1));
+      y.live = y.tok < it.n_new;
+      y.out_row = (int64_t)it.row0 + y.tok;
+      return y;
+    };
+    auto see_of = [&](const Item& it, const Place& y) {  // keys that the row sees
+      return !y.live ? 0 : a.causal ? max(0, min(it.len, it.len - it.n_new + y.tok + 1)) : it.len;
+    };
+    // 16 bytes (8 channels) of row x of the warp in the query tile, where its
+    // results are staged too once its products are done: rows move to and from
+    // global memory 256 bytes at a time.
+    auto stage_at = [&](int x, int chunk) {
+      const int y = (warp & 3) * 32 + x;
+      return sq + t * kTile + (chunk >> 3) * kHalf + y * 128 + (((chunk & 7) ^ (y & 7)) << 4);
+    };
+    auto stage_out = [&](int chunk, uint32_t h0, uint32_t h1, uint32_t h2, uint32_t h3) {
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stage_at(lane, chunk)), "r"(h0), "r"(h1), "r"(h2), "r"(h3)
+                   : "memory");
+    };
+    auto write_out = [&](const Item& it) {
+      __syncwarp();
+#pragma unroll 8
+      for (int i = 0; i < 16; ++i) {
+        const int x = 2 * i + (lane >> 4);
+        const Place y = place_of(it, x);
+        uint4 w;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(stage_at(x, lane & 15)));
+        if (y.live) *reinterpret_cast<uint4*>(a.out + y.out_row * a.out_stride + y.head * D + (lane & 15) * 8) = w;
+      }
+      __syncwarp();
     };
     const Item* it;
     for (; (it = take(st >> 8)); st += 0x100u) {
@@ -679,59 +692,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       int n, lim0, nt;
       float m = -INFINITY, l = 0.0f, zf = fmaxf(a.scale, kTiny);
       {
-        const Row x = row_of(*it);
         n = it->j1 - it->j0;
-        nt = x.nt;
-        lim0 = x.see - it->j0 * kKeys;
+        nt = min(it->n_new - it->q0, q_tile) * G > 128 ? 2 : 1;
+        lim0 = see_of(*it, place_of(*it, lane)) - it->j0 * kKeys;
         if (t < nt && n > 0 && ok) {
-          const bool live = x.live;
-          const uint16_t* qp = a.q + x.out_row * a.q_stride + x.head * D;
-
-        // The row's query into the operand tile.
-        const uint32_t dst = sq + t * kTile + r * 128;
-        if (E4M3) {
-          float top = 0.0f;
-          if (live) {
+          // The warp's 32 queries into the operand tile: 16 lanes a row.
+          uint4 w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint4 x = *reinterpret_cast<const uint4*>(qp + i * 8);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          for (int i = 0; i < 16; ++i) {
+            const Place y = place_of(*it, 2 * i + (lane >> 4));
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (y.live) w[i] = *reinterpret_cast<const uint4*>(a.q + y.out_row * a.q_stride + y.head * D + (lane & 15) * 8);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            uint32_t h[4] = {w[i].x ^ a.q_sign, w[i].y ^ a.q_sign, w[i].z ^ a.q_sign, w[i].w ^ a.q_sign};
+            if (E4M3) {  // fp16, after a power of two that brings the row into its range
+              float top = 0.0f;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(h[k] << 16)), fabsf(__uint_as_float(h[k] & 0xffff0000u))));
+#pragma unroll
+              for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+              int ex = (int)(__float_as_uint(top) >> 23) - 127;
+              ex = max(-100, min(ex, 120));
+              const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                h[k] = pack2<true>(__uint_as_float(h[k] << 16) * down, __uint_as_float(h[k] & 0xffff0000u) * down);
+              const int own = __shfl_sync(FULL, ex, (lane & 1) << 4);  // row 2 i + (lane & 1)
+              if (lane >> 1 == i) zf *= __uint_as_float((uint32_t)(127 + own) << 23);
             }
-          }
-          int ex = (int)(__float_as_uint(top) >> 23) - 127;  // a power of two that brings the row into fp16
-          ex = max(-100, min(ex, 120));
-          const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-          zf *= __uint_as_float((uint32_t)(127 + ex) << 23);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live) x = *reinterpret_cast<const uint4*>(qp + i * 8);
-            const uint32_t w[4] = {x.x ^ a.q_sign, x.y ^ a.q_sign, x.z ^ a.q_sign, x.w ^ a.q_sign};
-            uint32_t h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              h[k] = pack2<true>(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (i >> 3) * kHalf +
-                                                                       (uint32_t)(((i & 7) ^ (r & 7)) << 4)),
-                         "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stage_at(2 * i + (lane >> 4), lane & 15)), "r"(h[0]),
+                         "r"(h[1]), "r"(h[2]), "r"(h[3])
                          : "memory");
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (live) x = *reinterpret_cast<const uint4*>(qp + i * 8);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (i >> 3) * kHalf +
-                                                                       (uint32_t)(((i & 7) ^ (r & 7)) << 4)),
-                         "r"(x.x ^ a.q_sign), "r"(x.y ^ a.q_sign), "r"(x.z ^ a.q_sign), "r"(x.w ^ a.q_sign)
-                         : "memory");
-          }
-        }
-        fence_proxy_async();
-        mbar_arrive(&sh.q_full[t]);
+          fence_proxy_async();
+          mbar_arrive(&sh.q_full[t]);
         }
       }
       if (t < nt && n > 0 && ok) {
@@ -742,31 +739,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           tmem_fence_after_sync();
           const int lim = lim0 - j * kKeys;  // columns from here on are hidden
           const bool cut = __any_sync(FULL, lim < kKeys);
-          uint32_t v[4][32];
-          tmem_ld128(ts, v);
-          if (cut) {
-            asm volatile("");  // a branch, not 128 selections in every step
+          // The logits are read twice from tensor memory, 32 columns at a time,
+          // the next ones on their way: holding all 128 in registers spilled.
+          uint32_t v[2][32];
+          auto arrive = [&](int h) {  // columns 32 h .. are there, the next are asked for
+            tmem_ld_wait(v[h & 1]);
+            if (h < 3) tmem_ld32_async(ts + (h + 1) * 32, v[(h + 1) & 1]);
+            if (cut) {
+              asm volatile("");  // a branch, not 32 selections in every step
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i >= lim) v[i >> 5][i & 31] = 0xff800000u;
-          }
+              for (int i = 0; i < 32; ++i)
+                if (32 * h + i >= lim) v[h & 1][i] = 0xff800000u;
+            }
+          };
+          tmem_ld32_async(ts, v[0]);
           float mx = -INFINITY;
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {  // 16 keys: one scale
-            const uint32_t* z = &v[h >> 1][16 * (h & 1)];
-            float x = max3(z[0], z[1], z[2]);
-            float y = max3(z[3], z[4], z[5]);
-            x = max3(__float_as_uint(x), z[6], z[7]);
-            y = max3(__float_as_uint(y), z[8], z[9]);
-            x = max3(__float_as_uint(x), z[10], z[11]);
-            y = max3(__float_as_uint(y), z[12], z[13]);
-            x = fmaxf(max3(__float_as_uint(x), z[14], z[15]), y);
-            if (E4M3) {
-              const float2 kb = sh.kb[(st >> 4) & 3][h];
-              x = fmaf(x, fmaxf(zf * kb.x, kTiny), kb.y);
+          for (int h = 0; h < 4; ++h) {
+            arrive(h);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {  // 16 keys: one scale
+              const uint32_t* z = &v[h & 1][16 * s];
+              float x = max3(z[0], z[1], z[2]);
+              float y = max3(z[3], z[4], z[5]);
+              x = max3(__float_as_uint(x), z[6], z[7]);
+              y = max3(__float_as_uint(y), z[8], z[9]);
+              x = max3(__float_as_uint(x), z[10], z[11]);
+              y = max3(__float_as_uint(y), z[12], z[13]);
+              x = fmaxf(max3(__float_as_uint(x), z[14], z[15]), y);
+              if (E4M3) {
+                const float2 kb = sh.kb[(st >> 4) & 3][2 * h + s];
+                x = fmaf(x, fmaxf(zf * kb.x, kTiny), kb.y);
+              }
+              mx = fmaxf(mx, x);
             }
-            mx = fmaxf(mx, x);
           }
+          tmem_ld32_async(ts, v[0]);
           if (!E4M3) mx *= zf;
           const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
           if (__any_sync(FULL, raise)) {
@@ -787,30 +795,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           }
           const float ms = (m == -INFINITY ? 0.0f : m) - kShift;
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            float k = zf, bb = -ms;
-            if (E4M3) {
-              const float2 kb = sh.kb[(st >> 4) & 3][h];
-              k = fmaxf(zf * kb.x, kTiny);
-              bb = kb.y - ms;
-            }
-            const uint64_t k2 = pair(k, k), b2 = pair(bb, bb);
-            uint64_t add = 0;
-            uint32_t p[8];
+          for (int h = 0; h < 4; ++h) {
+            arrive(h);
+            uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t* z = &v[h >> 1][16 * (h & 1) + 2 * i];
+            for (int s = 0; s < 2; ++s) {
+              float k = zf, bb = -ms;
+              if (E4M3) {
+                const float2 kb = sh.kb[(st >> 4) & 3][2 * h + s];
+                k = fmaxf(zf * kb.x, kTiny);
+                bb = kb.y - ms;
+              }
+              const uint64_t k2 = pair(k, k), b2 = pair(bb, bb);
+              uint64_t add = 0;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t* z = &v[h & 1][16 * s + 2 * i];
+                float x, y;
+                unpair(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), k2, b2), x, y);
+                x = ex2(x);
+                y = ex2(y);
+                add = add2(add, pair(x, y));
+                p[8 * s + i] = pack2<E4M3>(x, y);
+              }
               float x, y;
-              unpair(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), k2, b2), x, y);
-              x = ex2(x);
-              y = ex2(y);
-              add = add2(add, pair(x, y));
-              p[i] = pack2<E4M3>(x, y);
+              unpair(add, x, y);
+              l = E4M3 ? fmaf(x + y, sh.inv[(st >> 4) & 3][2 * h + s], l) : l + (x + y);
             }
-            float x, y;
-            unpair(add, x, y);
-            l = E4M3 ? fmaf(x + y, sh.inv[(st >> 4) & 3][h], l) : l + (x + y);
-            tmem_st8(ts + h * 8, p);
+            tmem_st16(ts + h * 16, p);
           }
           tmem_wait_st();
           tmem_fence_before_sync();
@@ -826,42 +838,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       }
       // ---- the row's result ----
       asm volatile("" ::: "memory");  // formed anew, as above
-      const Row x = row_of(*it);
-      const int row = x.row, head = x.head, see = x.see;
-      const bool live = x.live;
-      const int64_t out_row = x.out_row;
-      const int parts = it->parts, b_lo = it->b_lo, j0 = it->j0;
+      const Item item = *it;
       give_back(st >> 8);
+      const Place x = place_of(item, lane);
+      const int row = wrow + lane, see = see_of(item, x), parts = item.parts, b_lo = item.b_lo;
       if (parts == 1) {
-        if (t < nt) {
+        if (t < nt && ok) {
           const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             uint32_t v[32];
-            if (n > 0 && ok) {
+            if (n > 0) {
               tmem_ld32_async(to + h * 32, v);
               tmem_ld_wait(v);
-            } else {
+            }
+            if (n == 0 || see == 0) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = 0;
             }
-            if (see == 0)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0;
-            if (live && ok) {
-              uint4* op = reinterpret_cast<uint4*>(a.out + out_row * a.out_stride + head * D + h * 32);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  w[k] = pack2<false>(__uint_as_float(v[8 * i + 2 * k]) * f, __uint_as_float(v[8 * i + 2 * k + 1]) * f);
-                op[i] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2<false>(__uint_as_float(v[8 * i + 2 * k]) * f, __uint_as_float(v[8 * i + 2 * k + 1]) * f);
+              stage_out(4 * h + i, w[0], w[1], w[2], w[3]);
             }
           }
-          if (live && ok && a.lse)
-            a.lse[out_row * (n_kv * G) + head] = see > 0 ? (log2f(l) + (m - kShift)) * kLn2 : -INFINITY;
+          write_out(item);
+          if (x.live && a.lse)
+            a.lse[x.out_row * (n_kv * G) + x.head] = see > 0 ? (log2f(l) + (m - kShift)) * kLn2 : -INFINITY;
           tmem_fence_before_sync();
         }
         continue;
@@ -871,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       constexpr int64_t kPartFloats = (int64_t)kRows * (D + 2);
       auto part_of = [&](int64_t slot) { return a.part + slot * kPartFloats; };
       // A CTA can hold the beginning of one item and the rest of another.
-      const int64_t mine = 2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0);
+      const int64_t mine = 2 * (int64_t)blockIdx.x + (item.j0 == 0 ? 1 : 0);
       auto slot = [&](int i) { return 2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0); };
       if (t < nt) {
         float4* op = reinterpret_cast<float4*>(part_of(mine));
@@ -905,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       if (!meet()) break;
       if (sh.last) {
         __threadfence();
-        if (live && t < nt) {
+        if (t < nt) {
           float M = -INFINITY, S = 0.0f;
           for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(part_of(slot(i)) + (int64_t)kRows * D + row));
           for (int i = 0; i < parts; ++i) {
@@ -932,14 +938,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
                 o[k].w = fmaf(u[k].w, w, o[k].w);
               }
             }
-            uint4* to = reinterpret_cast<uint4*>(a.out + out_row * a.out_stride + head * D + h * 64);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              to[k] = make_uint4(pack2<false>(o[2 * k].x * f, o[2 * k].y * f), pack2<false>(o[2 * k].z * f, o[2 * k].w * f),
-                                 pack2<false>(o[2 * k + 1].x * f, o[2 * k + 1].y * f),
-                                 pack2<false>(o[2 * k + 1].z * f, o[2 * k + 1].w * f));
+              stage_out(8 * h + k, pack2<false>(o[2 * k].x * f, o[2 * k].y * f), pack2<false>(o[2 * k].z * f, o[2 * k].w * f),
+                        pack2<false>(o[2 * k + 1].x * f, o[2 * k + 1].y * f),
+                        pack2<false>(o[2 * k + 1].z * f, o[2 * k + 1].w * f));
           }
-          if (a.lse) a.lse[out_row * (n_kv * G) + head] = see > 0 ? (log2f(S) + (M - kShift)) * kLn2 : -INFINITY;
+          write_out(item);
+          if (x.live && a.lse)
+            a.lse[x.out_row * (n_kv * G) + x.head] = see > 0 ? (log2f(S) + (M - kShift)) * kLn2 : -INFINITY;
         }
       }
       if (!meet()) break;  // sh.last is free again
