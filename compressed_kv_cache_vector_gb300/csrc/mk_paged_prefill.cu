@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     };
     auto write_out = [&](const Item& it) {
       __syncwarp();
-#pragma unroll 8
+#pragma unroll 4
       for (int i = 0; i < 16; ++i) {
         const int x = 2 * i + (lane >> 4);
         const Place y = place_of(it, x);
@@ -697,35 +697,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
         lim0 = see_of(*it, place_of(*it, lane)) - it->j0 * kKeys;
         if (t < nt && n > 0 && ok) {
           // The warp's 32 queries into the operand tile: 16 lanes a row.
-          uint4 w[16];
+          // Loops kept short here and at the result: this code runs once an
+          // item, and what it does not fetch anew each time it runs faster.
+#pragma unroll 1
+          for (int i0 = 0; i0 < 16; i0 += 8) {
+            uint4 w[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const Place y = place_of(*it, 2 * i + (lane >> 4));
-            w[i] = make_uint4(0, 0, 0, 0);
-            if (y.live) w[i] = *reinterpret_cast<const uint4*>(a.q + y.out_row * a.q_stride + y.head * D + (lane & 15) * 8);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint32_t h[4] = {w[i].x ^ a.q_sign, w[i].y ^ a.q_sign, w[i].z ^ a.q_sign, w[i].w ^ a.q_sign};
-            if (E4M3) {  // fp16, after a power of two that brings the row into its range
-              float top = 0.0f;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(h[k] << 16)), fabsf(__uint_as_float(h[k] & 0xffff0000u))));
-#pragma unroll
-              for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-              int ex = (int)(__float_as_uint(top) >> 23) - 127;
-              ex = max(-100, min(ex, 120));
-              const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                h[k] = pack2<true>(__uint_as_float(h[k] << 16) * down, __uint_as_float(h[k] & 0xffff0000u) * down);
-              const int own = __shfl_sync(FULL, ex, (lane & 1) << 4);  // row 2 i + (lane & 1)
-              if (lane >> 1 == i) zf *= __uint_as_float((uint32_t)(127 + own) << 23);
+            for (int i = 0; i < 8; ++i) {
+              const Place y = place_of(*it, 2 * (i0 + i) + (lane >> 4));
+              w[i] = make_uint4(0, 0, 0, 0);
+              if (y.live) w[i] = *reinterpret_cast<const uint4*>(a.q + y.out_row * a.q_stride + y.head * D + (lane & 15) * 8);
             }
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stage_at(2 * i + (lane >> 4), lane & 15)), "r"(h[0]),
-                         "r"(h[1]), "r"(h[2]), "r"(h[3])
-                         : "memory");
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t h[4] = {w[i].x ^ a.q_sign, w[i].y ^ a.q_sign, w[i].z ^ a.q_sign, w[i].w ^ a.q_sign};
+              if (E4M3) {  // fp16, after a power of two that brings the row into its range
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  top = fmaxf(top, fmaxf(fabsf(__uint_as_float(h[k] << 16)), fabsf(__uint_as_float(h[k] & 0xffff0000u))));
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+                int ex = (int)(__float_as_uint(top) >> 23) - 127;
+                ex = max(-100, min(ex, 120));
+                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  h[k] = pack2<true>(__uint_as_float(h[k] << 16) * down, __uint_as_float(h[k] & 0xffff0000u) * down);
+                const int own = __shfl_sync(FULL, ex, (lane & 1) << 4);  // row 2 i + (lane & 1)
+                if (lane >> 1 == i0 + i) zf *= __uint_as_float((uint32_t)(127 + own) << 23);
+              }
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stage_at(2 * (i0 + i) + (lane >> 4), lane & 15)),
+                           "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                           : "memory");
+            }
           }
           fence_proxy_async();
           mbar_arrive(&sh.q_full[t]);
@@ -783,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             l *= f;
             m = mn;
             if (j > 0) {
-#pragma unroll
+#pragma unroll 2
               for (int h = 0; h < 8; ++h) {
                 uint32_t w[16];
                 tmem_ld16(to + h * 16, w);
@@ -845,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       if (parts == 1) {
         if (t < nt && ok) {
           const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 4; ++h) {
             uint32_t v[32];
             if (n > 0) {
@@ -884,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
         float* ml = part_of(mine) + (int64_t)kRows * D;
         ml[row] = m;
         ml[kRows + row] = l;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 4; ++h) {
           uint32_t v[32];
           if (n > 0 && ok) {
@@ -919,6 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             if (mi != -INFINITY) S = fmaf(__ldcg(part_of(slot(i)) + (int64_t)kRows * (D + 1) + row), ex2(mi - M), S);
           }
           const float f = S > 0.0f || S != S ? 1.0f / S : 0.0f;
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {  // 64 columns at a time: 16 loads in flight
             float4 o[16];
 #pragma unroll
