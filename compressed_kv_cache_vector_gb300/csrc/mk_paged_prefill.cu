@@ -39,7 +39,7 @@ constexpr int kHalf = kTile / 2;           // its channels 0-63, then 64-127
 constexpr int kThreads = 512;              // 8 softmax warps, 4 loading warps, 1 issuing warp (and 3 without work)
 // Registers of a thread of each group of four warps; the launch gives 128 each
 // (512 x 128 = 65,536), and the shares add up to that.
-constexpr int kRegsSoftmax = 144, kRegsLoad = 128, kRegsIssue = 96;
+constexpr int kRegsSoftmax = 160, kRegsLoad = 128, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue == 4 * 128, "register shares");
 constexpr int kItemCost = 3;               // an item's queries and result take as long as this many steps
 constexpr int kItems = 4;                  // items that the list may run ahead of the slowest group
@@ -214,7 +214,7 @@ struct Shared {
   int span;                            // its length
   Item ring[kItems];                   // items on their way to the groups of warps
   uint64_t item_full[kItems], item_free[kItems], met, done;
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], k_full[2], k_free[2], v_full[2], v_free[2];
+  uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], k_full[2], k_free[2], v_full[2], v_free[2];
   // e4m3, per 16 keys of a step, ring of 4 steps: {k scale, log2 v scale}, 1 / v scale
   __align__(16) float2 kb[4][8];
   float inv[4][8];
@@ -222,6 +222,22 @@ struct Shared {
   int last;
   volatile int dead;
 };
+
+// The rest of a wait that has not ended at once, up to `times` times its limit.
+
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, unsigned parity, int times, volatile int* dead, int32_t* err) {
+  for (int i = 0; i < times; ++i) {
+    if (*dead) return false;
+    if (mbar_wait(bar, parity)) return true;
+  }
+  *dead = 1;
+  if (atomicCAS(&err[0], 0, (int32_t)MK_ETIMEOUT) == 0) {
+    err[1] = ERR_PAGED_WAIT;
+    err[2] = blockIdx.x;
+    err[3] = threadIdx.x >> 5;
+  }
+  return false;
+}
 
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, PrefillArgs a) {
@@ -239,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 128);
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_half[i], 128);
       mbar_init(&sh.p_full[i], 128);
       mbar_init(&sh.o_full[i], 1);
       mbar_init(&sh.k_full[i], 128);
@@ -352,20 +369,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   const uint32_t tmem = sh.tmem;
 
   auto wait = [&](uint64_t* bar, unsigned parity) {
-    if (sh.dead) return false;
-    if (mbar_wait(bar, parity)) return true;
-    sh.dead = 1;
-    paged_error(L, ERR_PAGED_WAIT, blockIdx.x, warp, (int32_t)MK_ETIMEOUT);
-    return false;
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, 1, &sh.dead, L.err);
   };
-
   // Items last longer than a single wait's limit: a hundred of them.
   auto wait_long = [&](uint64_t* bar, unsigned parity) {
-    for (int i = 0; i < 100; ++i) {
-      if (sh.dead) return false;
-      if (mbar_wait(bar, parity)) return true;
-    }
-    return wait(bar, parity);
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, 100, &sh.dead, L.err);
   };
   // The next item of the list for a group of warps; nullptr at its end.
   auto take = [&](unsigned c) -> const Item* {
@@ -459,14 +467,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           const bool end = j == n - 1;
           ok = wait_all(&sh.v_full[vc & 1], (vc >> 1) & 1);
           for (int t = 0; t < nt && ok; ++t) {
-            ok = wait_all(&sh.p_full[t], pc[t]++ & 1);
+            // The value product, 64 keys at a time as their weights come.
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              ok = wait_all(half ? &sh.p_full[t] : &sh.p_half[t], pc[t] & 1);
+              if (!ok) break;
+              tmem_fence_after_sync();
+              if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int k = 4 * half + i;
+                  umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
+                          dv + (uint64_t)((vc & 1) * (kTile >> 4) + k * (2048 >> 4)), idesc(!E4M3, 1), j > 0 || k > 0);
+                }
+              }
+              __syncwarp();
+            }
             if (!ok) break;
-            tmem_fence_after_sync();
+            ++pc[t];
             if (elect_one()) {
-#pragma unroll 2
-              for (int k = 0; k < 8; ++k)
-                umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, dv + (uint64_t)((vc & 1) * (kTile >> 4) + k * (2048 >> 4)),
-                        idesc(!E4M3, 1), j > 0 || k > 0);
               if (t == nt - 1) umma_commit(&sh.v_free[vc & 1]);
               if (end) umma_commit(&sh.o_full[t]);
             }
@@ -747,24 +766,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           // The logits are read twice from tensor memory, 32 columns at a time,
           // the next ones on their way: holding all 128 in registers spilled.
           uint32_t v[2][32];
-          auto arrive = [&](int h) {  // columns 32 h .. are there, the next are asked for
-            tmem_ld_wait(v[h & 1]);
-            if (h < 3) tmem_ld32_async(ts + (h + 1) * 32, v[(h + 1) & 1]);
+          auto arrive = [&](int h, int hh) {  // columns 32 h .. are in v[hh], the next are asked for
+            tmem_ld_wait(v[hh]);
+            if (h < 3) tmem_ld32_async(ts + (h + 1) * 32, v[hh ^ 1]);
             if (cut) {
               asm volatile("");  // a branch, not 32 selections in every step
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (32 * h + i >= lim) v[h & 1][i] = 0xff800000u;
+                if (i >= lim - 32 * h) v[hh][i] = 0xff800000u;
             }
           };
           tmem_ld32_async(ts, v[0]);
           float mx = -INFINITY;
+#pragma unroll 1
+          for (int h0 = 0; h0 < 4; h0 += 2)
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            arrive(h);
+          for (int hh = 0; hh < 2; ++hh) {
+            const int h = h0 + hh;
+            arrive(h, hh);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {  // 16 keys: one scale
-              const uint32_t* z = &v[h & 1][16 * s];
+              const uint32_t* z = &v[hh][16 * s];
               float x = max3(z[0], z[1], z[2]);
               float y = max3(z[3], z[4], z[5]);
               x = max3(__float_as_uint(x), z[6], z[7]);
@@ -799,9 +821,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             }
           }
           const float ms = (m == -INFINITY ? 0.0f : m) - kShift;
+#pragma unroll 1
+          for (int h0 = 0; h0 < 4; h0 += 2) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            arrive(h);
+          for (int hh = 0; hh < 2; ++hh) {
+            const int h = h0 + hh;
+            arrive(h, hh);
             uint32_t p[16];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -815,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
               uint64_t add = 0;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const uint32_t* z = &v[h & 1][16 * s + 2 * i];
+                const uint32_t* z = &v[hh][16 * s + 2 * i];
                 float x, y;
                 unpair(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), k2, b2), x, y);
                 x = ex2(x);
@@ -829,9 +854,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             }
             tmem_st16(ts + h * 16, p);
           }
+          // Half of the weights are enough to begin the value product.
           tmem_wait_st();
           tmem_fence_before_sync();
-          mbar_arrive(&sh.p_full[t]);
+          mbar_arrive(h0 == 0 ? &sh.p_half[t] : &sh.p_full[t]);
+          }
         }
         if (ok) {
           ok = __all_sync(FULL, wait(&sh.o_full[t], (st >> 1) & 1));
