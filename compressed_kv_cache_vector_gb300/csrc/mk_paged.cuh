@@ -55,6 +55,21 @@ __device__ __forceinline__ void paged_error(const PagedLayer& L, int32_t detail,
 }
 __device__ __forceinline__ bool paged_has_error(const PagedLayer& L) { return *(volatile int32_t*)L.err != 0; }
 
+// Bounded wait for the phase with the given parity, as mbar_wait, with the
+// limit (about 20 ms) counted in clocks: reading the global timer between two
+// tries costs several hundred cycles of every wait that does not end at once.
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, unsigned parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > 40000000ll) return false;
+  return true;
+}
+// The same for a full warp: if any lane gave up, all report failure.
+__device__ __forceinline__ bool paged_wait_warp(uint64_t* bar, unsigned parity) {
+  return __all_sync(FULL, paged_wait(bar, parity)) != 0;
+}
+
 // Sequence i of a batch: its first row, new tokens and length.  ok is false
 // (and the error word set by the callers) when they contradict the batch.
 struct PagedSeq {

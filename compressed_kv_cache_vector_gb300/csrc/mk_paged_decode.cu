@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       unsigned char* st = ring + (warp * NS + stage) * kStageBytes;
       // After a wait that ran out nothing more is copied; what is in flight is
       // still waited for (with the same limit) before the kernel ends.
-      if (flat < issued && !mbar_wait_warp(&s_bar[warp][stage], phase)) {
+      if (flat < issued && !paged_wait_warp(&s_bar[warp][stage], phase)) {
         dead = true;
         if (lane == 0) paged_error(L, ERR_PAGED_WAIT, u.seq, flat, (int32_t)MK_ETIMEOUT);
       }

@@ -12,11 +12,10 @@
 //  * warps 0-3 and 4-7: the softmax of row tile 0 and 1, one row a thread;
 //  * warps 8-11: keys and values into shared memory (e4m3 codes to fp16 on the
 //    way, exact; rows past the length as zeros), two stages each;
-//  * warp 12: issues the products.  S = Q K^T into tensor memory; the weights
+//  * warps 12 and 14: issue the products, one of them for each row tile.  S = Q K^T into tensor memory; the weights
 //    replace S there in 16 bits and are the A operand of O += P V.
-// The order of issue, S(0)0 S(1)0 | P(0)V S(0) P(1)V S(1) | ..., makes the
-// completion of a tile's S also that of its previous value product, so one
-// barrier covers both.
+// A tile's products are issued by one lane in order, so that the completion of
+// its S is also that of its previous value product.
 //  * The running maximum is raised only when a row's logits pass it by 2^4
 //    (fp16 weights) or 2^8 (bf16): only then is the accumulator rescaled.
 //    e4m3: weights in fp16 after a factor 2^10 (at most 2^14, smallest step
@@ -188,6 +187,12 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// One arrival for a warp whose lanes have all done their part (and fenced it):
+// 32 arrivals at one barrier are 32 operations in a row on its word.
+__device__ __forceinline__ void mbar_arrive_warp(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
 __device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
@@ -228,7 +233,7 @@ struct Shared {
 __device__ __forceinline__ bool wait_slow(uint64_t* bar, unsigned parity, int times, volatile int* dead, int32_t* err) {
   for (int i = 0; i < times; ++i) {
     if (*dead) return false;
-    if (mbar_wait(bar, parity)) return true;
+    if (paged_wait(bar, parity)) return true;
   }
   *dead = 1;
   if (atomicCAS(&err[0], 0, (int32_t)MK_ETIMEOUT) == 0) {
@@ -253,22 +258,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 128);
+      mbar_init(&sh.q_full[i], 4);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_half[i], 128);
-      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.p_half[i], 4);
+      mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_full[i], 1);
-      mbar_init(&sh.k_full[i], 128);
-      mbar_init(&sh.k_free[i], 1);
-      mbar_init(&sh.v_full[i], 128);
-      mbar_init(&sh.v_free[i], 1);
+      mbar_init(&sh.k_full[i], 4);
+      mbar_init(&sh.k_free[i], 2);
+      mbar_init(&sh.v_full[i], 4);
+      mbar_init(&sh.v_free[i], 2);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      mbar_init(&sh.item_free[i], 13);  // one arrival of each softmax, loading and issuing warp
+      mbar_init(&sh.item_free[i], 14);  // one arrival of each softmax, loading and issuing warp
     }
-    mbar_init(&sh.met, 256);
-    mbar_init(&sh.done, 1);
+    mbar_init(&sh.met, 8);
+    mbar_init(&sh.done, 2);
     sh.dead = 0;
   }
   mbar_init_fence();
@@ -431,81 +436,81 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       it.end = 1;
       if (ok) put(it);
     }
-    // ---- issues the products ----
-    if (warp == 12) {
-      unsigned kc = 0, vc = 0, qc[2] = {0, 0}, pc[2] = {0, 0};
+    // ---- issue the products: warp 12 those of row tile 0, warp 14 of tile 1 ----
+    if (warp == 12 || warp == 14) {
+      const int t = warp == 14;
+      unsigned c = 0, qc = 0, pc = 0;  // steps so far; phases of q_full and of p_half, p_full
       bool ok = true;
-      const uint64_t dq = sw128_desc(sq, 16), dk = sw128_desc(sk, 16), dv = sw128_desc(sv, kHalf);
+      const uint64_t dq = sw128_desc(sq + t * kTile, 16), dk = sw128_desc(sk, 16), dv = sw128_desc(sv, kHalf);
       auto wait_all = [&](uint64_t* bar, unsigned parity) { return __all_sync(FULL, wait(bar, parity)) != 0; };
-      // The whole warp walks the list; one lane issues.
-      auto s_mma = [&](int t, unsigned stage, bool last) {
-        if (elect_one()) {
-#pragma unroll 2
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            umma_ss(tmem + t * 128, dq + (uint64_t)(t * (kTile >> 4) + o), dk + (uint64_t)(stage * (kTile >> 4) + o),
-                    idesc(!E4M3, 0), k > 0);
-          }
-          umma_commit(&sh.s_full[t]);
-          if (last) umma_commit(&sh.k_free[stage]);
-        }
-        __syncwarp();
-      };
       const Item* it;
+      // The whole warp walks the list; one lane issues.
       for (unsigned ic = 0; ok && (it = take(ic)); ++ic) {
         const int n = it->j1 - it->j0;
-        const int nt = min(it->n_new - it->q0, q_tile) * G > 128 ? 2 : 1;
+        const bool alone = min(it->n_new - it->q0, q_tile) * G <= 128;  // the item has no rows in tile 1
         give_back(ic);
         if (n == 0) continue;
-        for (int t = 0; t < nt; ++t) ok = ok && wait_all(&sh.q_full[t], qc[t]++ & 1);
-        ok = ok && wait_all(&sh.k_full[kc & 1], (kc >> 1) & 1);
+        if (t == 1 && alone) {  // no products here: the stages are passed on, step by step
+          for (int j = 0; j < n && ok; ++j, ++c) {
+            ok = wait_all(&sh.k_full[c & 1], (c >> 1) & 1);
+            if (ok && lane == 0) mbar_arrive(&sh.k_free[c & 1]);
+            ok = ok && wait_all(&sh.v_full[c & 1], (c >> 1) & 1);
+            if (ok && lane == 0) mbar_arrive(&sh.v_free[c & 1]);
+          }
+          continue;
+        }
+        auto s_mma = [&](unsigned stage) {
+          if (elect_one()) {
+#pragma unroll 2
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+              umma_ss(tmem + t * 128, dq + o, dk + (uint64_t)(stage * (kTile >> 4) + o), idesc(!E4M3, 0), k > 0);
+            }
+            umma_commit(&sh.s_full[t]);
+            umma_commit(&sh.k_free[stage]);
+          }
+          __syncwarp();
+        };
+        ok = wait_all(&sh.q_full[t], qc++ & 1) && wait_all(&sh.k_full[c & 1], (c >> 1) & 1);
         if (!ok) break;
         tmem_fence_after_sync();
-        for (int t = 0; t < nt; ++t) s_mma(t, kc & 1, t == nt - 1);
-        ++kc;
-        for (int j = 0; j < n && ok; ++j) {
-          const bool end = j == n - 1;
-          ok = wait_all(&sh.v_full[vc & 1], (vc >> 1) & 1);
-          for (int t = 0; t < nt && ok; ++t) {
-            // The value product, 64 keys at a time as their weights come.
+        s_mma(c & 1);
+        for (int j = 0; j < n && ok; ++j, ++c) {
+          ok = wait_all(&sh.v_full[c & 1], (c >> 1) & 1);
+          // The value product, 64 keys at a time as their weights come.
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              ok = wait_all(half ? &sh.p_full[t] : &sh.p_half[t], pc[t] & 1);
-              if (!ok) break;
-              tmem_fence_after_sync();
-              if (elect_one()) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int k = 4 * half + i;
-                  umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
-                          dv + (uint64_t)((vc & 1) * (kTile >> 4) + k * (2048 >> 4)), idesc(!E4M3, 1), j > 0 || k > 0);
-                }
-              }
-              __syncwarp();
-            }
+          for (int half = 0; half < 2 && ok; ++half) {
+            ok = wait_all(half ? &sh.p_full[t] : &sh.p_half[t], pc & 1);
             if (!ok) break;
-            ++pc[t];
+            tmem_fence_after_sync();
             if (elect_one()) {
-              if (t == nt - 1) umma_commit(&sh.v_free[vc & 1]);
-              if (end) umma_commit(&sh.o_full[t]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = 4 * half + i;
+                umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, dv + (uint64_t)((c & 1) * (kTile >> 4) + k * (2048 >> 4)),
+                        idesc(!E4M3, 1), j > 0 || k > 0);
+              }
+              if (half) {
+                umma_commit(&sh.v_free[c & 1]);
+                if (j == n - 1) umma_commit(&sh.o_full[t]);
+              }
             }
             __syncwarp();
-            if (!end) {
-              if (t == 0) ok = wait_all(&sh.k_full[kc & 1], (kc >> 1) & 1);
-              if (!ok) break;
-              tmem_fence_after_sync();
-              s_mma(t, kc & 1, t == nt - 1);
-            }
           }
-          ++vc;
-          if (!end) ++kc;
+          ++pc;
+          if (ok && j < n - 1) {
+            ok = wait_all(&sh.k_full[(c + 1) & 1], ((c + 1) >> 1) & 1);
+            if (!ok) break;
+            tmem_fence_after_sync();
+            s_mma((c + 1) & 1);
+          }
         }
       }
       // Nothing is in flight when the tensor memory is freed, also after a
       // wait that ran out.
       if (elect_one()) umma_commit(&sh.done);
       __syncwarp();
-      (void)mbar_wait_warp(&sh.done, 0);
+      (void)paged_wait_warp(&sh.done, 0);
     }
   } else if (warp >= 8) {
     // ---- keys and values into shared memory ----
@@ -594,13 +599,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           }
           store(sk + (c & 1) * kTile, kr);
           fence_proxy_async();
-          mbar_arrive(&sh.k_full[c & 1]);
+          mbar_arrive_warp(&sh.k_full[c & 1], lane);
           if (j + 1 < it.j1) load(j + 1, L.k, kr);
           ok = c < 2 || __all_sync(FULL, wait(&sh.v_free[c & 1], ((c >> 1) - 1) & 1));
           if (!ok) break;
           store(sv + (c & 1) * kTile, vr);
           fence_proxy_async();
-          mbar_arrive(&sh.v_full[c & 1]);
+          mbar_arrive_warp(&sh.v_full[c & 1], lane);
         }
       } else {
         const int ck = lt & 15, r = lt >> 4;  // 8 channels ck of rows r + 8 i
@@ -626,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           else
             asm volatile("cp.async.wait_group 1;\n" ::: "memory");
           fence_proxy_async();
-          mbar_arrive(pending);
+          mbar_arrive_warp(pending, lane);
         };
         for (int j = it.j0; j < it.j1; ++j, ++c) {
           ok = c < 2 || __all_sync(FULL, wait(&sh.k_free[c & 1], ((c >> 1) - 1) & 1));
@@ -659,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     auto step_ring = [&](unsigned by) { st = (st & ~0x30u) | ((st + (by << 4)) & 0x30u); };
     // The eight softmax warps meet (an mbarrier: with the limit that every wait has).
     auto meet = [&]() {
-      mbar_arrive(&sh.met);
+      mbar_arrive_warp(&sh.met, lane);
       st ^= 4u;
       return __all_sync(FULL, wait(&sh.met, (~st >> 2) & 1)) != 0;
     };
@@ -752,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
             }
           }
           fence_proxy_async();
-          mbar_arrive(&sh.q_full[t]);
+          mbar_arrive_warp(&sh.q_full[t], lane);
         }
       }
       if (t < nt && n > 0 && ok) {
@@ -857,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           // Half of the weights are enough to begin the value product.
           tmem_wait_st();
           tmem_fence_before_sync();
-          mbar_arrive(h0 == 0 ? &sh.p_half[t] : &sh.p_full[t]);
+          mbar_arrive_warp(h0 == 0 ? &sh.p_half[t] : &sh.p_full[t], lane);
           }
         }
         if (ok) {

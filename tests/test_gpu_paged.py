@@ -376,7 +376,7 @@ def test_prefill_ragged(kv, causal, P, n_kv, G):
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("news,lens,G", [([600], [600], 4), ([513], [4100], 4), ([2, 4], [6000, 3333], 4), ([300], [1500], 1),
-                                         ([9], [20000], 8)])
+                                         ([9], [20000], 8), ([40, 900, 33, 500, 3, 1200], [3000, 2500, 4000, 700, 2600, 1200], 4)])
 def test_prefill_longer(kv, news, lens, G):
     made = Made(kv, 32, 2, G, lens, 7)
     rows = sum(news)
