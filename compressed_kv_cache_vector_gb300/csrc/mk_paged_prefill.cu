@@ -38,8 +38,11 @@ constexpr int kHalf = kTile / 2;           // its channels 0-63, then 64-127
 constexpr int kThreads = 512;              // 8 softmax warps, 4 loading warps, 1 issuing warp (and 3 without work)
 // Registers of a thread of each group of four warps; the launch gives 128 each
 // (512 x 128 = 65,536), and the shares add up to that.
-constexpr int kRegsSoftmax = 160, kRegsLoad = 128, kRegsIssue = 64;
-static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue == 4 * 128, "register shares");
+template <bool E4M3>
+struct Regs {
+  static constexpr int softmax = E4M3 ? 160 : 168, load = E4M3 ? 128 : 112, issue = 64;
+  static_assert(2 * softmax + load + issue == 4 * 128, "register shares");
+};
 constexpr int kItemCost = 3;               // an item's queries and result take as long as this many steps
 constexpr int kItems = 4;                  // items that the list may run ahead of the slowest group
 constexpr int kMinRun = 4;                 // shortest run of a CTA, in steps
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   };
 
   if (warp >= 12) {
-    fewer_registers<kRegsIssue>();
+    fewer_registers<Regs<E4M3>::issue>();
     if (warp == 13 && lane == 0) {
       // ---- lists the items ----
       Cursor k = sh.start;
@@ -437,84 +440,78 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       if (ok) put(it);
     }
     // ---- issue the products: warp 12 those of row tile 0, warp 14 of tile 1 ----
+    // One elected lane does it all: between two products every instruction
+    // counts, as they run one after the other.
     if (warp == 12 || warp == 14) {
       const int t = warp == 14;
-      unsigned c = 0, qc = 0, pc = 0;  // steps so far; phases of q_full and of p_half, p_full
-      bool ok = true;
-      const uint64_t dq = sw128_desc(sq + t * kTile, 16), dk = sw128_desc(sk, 16), dv = sw128_desc(sv, kHalf);
-      auto wait_all = [&](uint64_t* bar, unsigned parity) { return __all_sync(FULL, wait(bar, parity)) != 0; };
-      const Item* it;
-      // The whole warp walks the list; one lane issues.
-      for (unsigned ic = 0; ok && (it = take(ic)); ++ic) {
-        const int n = it->j1 - it->j0;
-        const bool alone = min(it->n_new - it->q0, q_tile) * G <= 128;  // the item has no rows in tile 1
-        give_back(ic);
-        if (n == 0) continue;
-        if (t == 1 && alone) {  // no products here: the stages are passed on, step by step
-          for (int j = 0; j < n && ok; ++j, ++c) {
-            ok = wait_all(&sh.k_full[c & 1], (c >> 1) & 1);
-            if (ok && lane == 0) mbar_arrive(&sh.k_free[c & 1]);
-            ok = ok && wait_all(&sh.v_full[c & 1], (c >> 1) & 1);
-            if (ok && lane == 0) mbar_arrive(&sh.v_free[c & 1]);
+      if (elect_one()) {
+        unsigned c = 0, qc = 0, pc = 0;  // steps so far; phases of q_full and of p_half, p_full
+        bool ok = true;
+        const uint64_t dq = sw128_desc(sq + t * kTile, 16), dk = sw128_desc(sk, 16), dv = sw128_desc(sv, kHalf);
+        for (unsigned ic = 0; ok; ++ic) {
+          if (!wait_long(&sh.item_full[ic % kItems], (ic / kItems) & 1)) break;
+          const Item* it = &sh.ring[ic % kItems];
+          if (it->end) break;
+          const int n = it->j1 - it->j0;
+          const bool alone = min(it->n_new - it->q0, q_tile) * G <= 128;  // the item has no rows in tile 1
+          mbar_arrive(&sh.item_free[ic % kItems]);
+          if (n == 0) continue;
+          if (t == 1 && alone) {  // no products here: the stages are passed on, step by step
+            for (int j = 0; j < n && ok; ++j, ++c) {
+              ok = wait(&sh.k_full[c & 1], (c >> 1) & 1);
+              if (ok) mbar_arrive(&sh.k_free[c & 1]);
+              ok = ok && wait(&sh.v_full[c & 1], (c >> 1) & 1);
+              if (ok) mbar_arrive(&sh.v_free[c & 1]);
+            }
+            continue;
           }
-          continue;
-        }
-        auto s_mma = [&](unsigned stage) {
-          if (elect_one()) {
-#pragma unroll 2
+          ok = wait(&sh.q_full[t], qc++ & 1);
+          for (int j = -1; j < n && ok; ++j) {
+            if (j >= 0) {
+              // The value product, 64 keys at a time as their weights come.
+              const uint64_t d = dv + (uint64_t)((c & 1) * (kTile >> 4));
+              ok = wait(&sh.v_full[c & 1], (c >> 1) & 1) && wait(&sh.p_half[t], pc & 1);
+              if (!ok) break;
+              tmem_fence_after_sync();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, d + k * (2048 >> 4), idesc(!E4M3, 1), j > 0 || k > 0);
+              ok = wait(&sh.p_full[t], pc++ & 1);
+              if (!ok) break;
+              tmem_fence_after_sync();
+#pragma unroll
+              for (int k = 4; k < 8; ++k)
+                umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, d + k * (2048 >> 4), idesc(!E4M3, 1), 1);
+              umma_commit(&sh.v_free[c & 1]);
+              ++c;
+              if (j == n - 1) {
+                umma_commit(&sh.o_full[t]);
+                break;
+              }
+            }
+            ok = wait(&sh.k_full[c & 1], (c >> 1) & 1);
+            if (!ok) break;
+            tmem_fence_after_sync();
+            const uint64_t d = dk + (uint64_t)((c & 1) * (kTile >> 4));
+#pragma unroll
             for (int k = 0; k < 8; ++k) {
               const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-              umma_ss(tmem + t * 128, dq + o, dk + (uint64_t)(stage * (kTile >> 4) + o), idesc(!E4M3, 0), k > 0);
+              umma_ss(tmem + t * 128, dq + o, d + o, idesc(!E4M3, 0), k > 0);
             }
             umma_commit(&sh.s_full[t]);
-            umma_commit(&sh.k_free[stage]);
-          }
-          __syncwarp();
-        };
-        ok = wait_all(&sh.q_full[t], qc++ & 1) && wait_all(&sh.k_full[c & 1], (c >> 1) & 1);
-        if (!ok) break;
-        tmem_fence_after_sync();
-        s_mma(c & 1);
-        for (int j = 0; j < n && ok; ++j, ++c) {
-          ok = wait_all(&sh.v_full[c & 1], (c >> 1) & 1);
-          // The value product, 64 keys at a time as their weights come.
-#pragma unroll 1
-          for (int half = 0; half < 2 && ok; ++half) {
-            ok = wait_all(half ? &sh.p_full[t] : &sh.p_half[t], pc & 1);
-            if (!ok) break;
-            tmem_fence_after_sync();
-            if (elect_one()) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int k = 4 * half + i;
-                umma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, dv + (uint64_t)((c & 1) * (kTile >> 4) + k * (2048 >> 4)),
-                        idesc(!E4M3, 1), j > 0 || k > 0);
-              }
-              if (half) {
-                umma_commit(&sh.v_free[c & 1]);
-                if (j == n - 1) umma_commit(&sh.o_full[t]);
-              }
-            }
-            __syncwarp();
-          }
-          ++pc;
-          if (ok && j < n - 1) {
-            ok = wait_all(&sh.k_full[(c + 1) & 1], ((c + 1) >> 1) & 1);
-            if (!ok) break;
-            tmem_fence_after_sync();
-            s_mma((c + 1) & 1);
+            umma_commit(&sh.k_free[c & 1]);
           }
         }
+        umma_commit(&sh.done);
       }
       // Nothing is in flight when the tensor memory is freed, also after a
       // wait that ran out.
-      if (elect_one()) umma_commit(&sh.done);
       __syncwarp();
       (void)paged_wait_warp(&sh.done, 0);
     }
   } else if (warp >= 8) {
     // ---- keys and values into shared memory ----
-    fewer_registers<kRegsLoad>();
+    fewer_registers<Regs<E4M3>::load>();
     const int lt = tid - 256;
     unsigned c = 0;  // steps so far
     bool ok = true;
@@ -653,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     }
   } else {
     // ---- softmax: one row a thread ----
-    more_registers<kRegsSoftmax>();
+    more_registers<Regs<E4M3>::softmax>();
     const int t = warp >> 2;
     const uint32_t trow = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t ts = trow + t * 128, to = trow + 256 + t * 128;
