@@ -459,22 +459,24 @@ class PagedKV:
 
     def _rows(self, t, name, batch, heads):
         """Row stride of a bf16 [rows, heads, 128] (or [rows, heads * 128]) tensor whose rows are contiguous."""
-        if t.dim() == 3:
-            ok = t.shape[1] == heads and t.shape[2] == MK_HEAD_DIM and t.stride(2) == 1 and (
-                heads == 1 or t.stride(1) == MK_HEAD_DIM)
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 3:
+            ok = shape[1] == heads and shape[2] == MK_HEAD_DIM and stride[2] == 1 and (
+                heads == 1 or stride[1] == MK_HEAD_DIM)
         else:
-            ok = t.dim() == 2 and t.shape[1] == heads * MK_HEAD_DIM and t.stride(1) == 1
-        _need(ok and t.dtype == torch.bfloat16 and t.shape[0] >= batch.n_tokens and t.device == self.device,
-              f"{name} must be bf16 [{batch.n_tokens}, {heads}, 128] on {self.device} with contiguous rows")
-        return t.stride(0) if t.shape[0] > 1 else heads * MK_HEAD_DIM
+            ok = len(shape) == 2 and shape[1] == heads * MK_HEAD_DIM and stride[1] == 1
+        _need(ok and t.dtype is torch.bfloat16 and shape[0] >= batch.n_tokens and t.device == self.device,
+              f"{name} must be bf16 [{batch.n_tokens}, {heads}, 128] on {self.device} with contiguous rows"
+              if not ok or t.dtype is not torch.bfloat16 else f"{name} has too few rows or is on another device")
+        return stride[0] if shape[0] > 1 else heads * MK_HEAD_DIM
 
     def _stream(self, stream, *tensors):
-        cur = torch.cuda.current_stream(self.device)
-        if stream is None or stream == cur:
-            return cur.cuda_stream
-        for t in tensors:       # the allocator must not reuse them before that stream is done
-            if t is not None:
-                t.record_stream(stream)
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if stream != torch.cuda.current_stream(self.device):
+            for t in tensors:       # the allocator must not reuse them before that stream is done
+                if t is not None:
+                    t.record_stream(stream)
         return stream.cuda_stream
 
     def append(self, layer, batch, k, v, rope=None, q=None, q_out=None, stream=None):

@@ -10,18 +10,24 @@
 // raising a page's scale exact: the codes held before are multiplied by
 // s_old / s_new, which rounds only those that become subnormal.
 //
-// Work split: a page of one kv head of one tensor per CTA of 128 threads, 16
-// threads a row (8 channels each), so that the page's maximum is a reduction
-// inside the CTA and a row's rotation partner is in the same 16 lanes.  The
-// values stay in registers between the maximum and the rounding: one pass.
+// Work split: a page of one kv head of one tensor per CTA, 16 threads a row (8
+// channels each), so that the page's maximum is a reduction inside the CTA and
+// a row's rotation partner is in the same 16 lanes.  The values stay in
+// registers between the maximum and the rounding: one pass.  A thread has at
+// most four rows of a page (pages of 64 tokens take 256 threads), which keeps
+// enough CTAs on an SM for the loads in flight that HBM wants.  Queries: 16
+// threads a (token, few heads), the angles loaded once for all of its heads
+// (they are four times a head's data).
 #include "mk_paged.cuh"
 
 namespace mk {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kQRows = 32;  // rows (token, query head) of a query CTA
+template <int P>
+struct Shape {
+  static constexpr int threads = P == 64 ? 256 : 128;
+};
 
 struct AppendArgs {
   mk_paged_batch b;
@@ -30,12 +36,32 @@ struct AppendArgs {
   uint16_t* q_out;
   int64_t k_stride, v_stride, q_stride, q_out_stride;
   int32_t n_units;  // page slots x kv heads x 2
+  int32_t q_heads;  // query heads of a (token, heads) item
 };
 
-// Eight channels (16-lane group: chunk j of the row) turned by the angles of
-// row `pos` of the table.  x holds this thread's channels; every lane of the
-// 16-lane group must call.
-__device__ __forceinline__ void rotate8(const mk_rope& r, int pos, int j, int lane, const uint4 raw, float (&y)[8]) {
+// The angles that chunk j (8 channels) of a row at position `pos` needs.
+struct Angles {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void load_angles(const mk_rope& r, int pos, int j, Angles& g) {
+  const int half = r.rot_dim >> 1, c0 = j * 8;
+  if (c0 >= r.rot_dim) return;
+  const float* row = r.cos_sin + (int64_t)pos * r.rot_dim;
+  if (r.interleaved) {
+    *reinterpret_cast<float4*>(g.c) = *reinterpret_cast<const float4*>(row + c0 / 2);
+    *reinterpret_cast<float4*>(g.s) = *reinterpret_cast<const float4*>(row + half + c0 / 2);
+    return;
+  }
+  const int i = c0 >= half ? c0 - half : c0;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    *reinterpret_cast<float4*>(g.c + 4 * v) = *reinterpret_cast<const float4*>(row + i + 4 * v);
+    *reinterpret_cast<float4*>(g.s + 4 * v) = *reinterpret_cast<const float4*>(row + half + i + 4 * v);
+  }
+}
+// Eight channels (16-lane group: chunk j of the row) turned by the row's
+// angles; every lane of the group must call.
+__device__ __forceinline__ void rotate8(const mk_rope& r, const Angles& g, int j, int lane, const uint4 raw, float (&y)[8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -44,17 +70,13 @@ __device__ __forceinline__ void rotate8(const mk_rope& r, int pos, int j, int la
   }
   if (r.rot_dim == 0) return;
   const int half = r.rot_dim >> 1, c0 = j * 8;
-  const float* row = r.cos_sin + (int64_t)pos * r.rot_dim;
   if (r.interleaved) {
     if (c0 < r.rot_dim) {
-      const float4 c = *reinterpret_cast<const float4*>(row + c0 / 2);
-      const float4 s = *reinterpret_cast<const float4*>(row + half + c0 / 2);
-      const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float a = y[2 * e], b = y[2 * e + 1];
-        y[2 * e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(b, sn[e]));
-        y[2 * e + 1] = __fadd_rn(__fmul_rn(b, cs[e]), __fmul_rn(a, sn[e]));
+        y[2 * e] = __fsub_rn(__fmul_rn(a, g.c[e]), __fmul_rn(b, g.s[e]));
+        y[2 * e + 1] = __fadd_rn(__fmul_rn(b, g.c[e]), __fmul_rn(a, g.s[e]));
       }
     }
     return;
@@ -66,19 +88,11 @@ __device__ __forceinline__ void rotate8(const mk_rope& r, int pos, int j, int la
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = __shfl_sync(FULL, w[e], partner);
   if (c0 < r.rot_dim) {
-    const int i = second ? c0 - half : c0;
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * v);
-      const float4 s = *reinterpret_cast<const float4*>(row + half + i + 4 * v);
-      const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int n = 4 * v + e;
-        const float other = (n & 1) ? __uint_as_float(o[n >> 1] & 0xffff0000u) : __uint_as_float(o[n >> 1] << 16);
-        const float p = __fmul_rn(y[n], cs[e]), t = __fmul_rn(other, sn[e]);
-        y[n] = second ? __fadd_rn(p, t) : __fsub_rn(p, t);
-      }
+    for (int n = 0; n < 8; ++n) {
+      const float other = (n & 1) ? __uint_as_float(o[n >> 1] & 0xffff0000u) : __uint_as_float(o[n >> 1] << 16);
+      const float p = __fmul_rn(y[n], g.c[n]), t = __fmul_rn(other, g.s[n]);
+      y[n] = second ? __fadd_rn(p, t) : __fsub_rn(p, t);
     }
   }
 }
@@ -129,7 +143,8 @@ __device__ __forceinline__ int clamp_position(const PagedLayer& L, const mk_rope
 }
 
 template <int P, bool E4M3>
-__global__ void __launch_bounds__(kThreads) k_paged_append(PagedLayer L, AppendArgs a) {
+__global__ void __launch_bounds__(Shape<P>::threads) k_paged_append(PagedLayer L, AppendArgs a) {
+  constexpr int kThreads = Shape<P>::threads;
   __shared__ int s_wsum[kThreads / 32], s_seq, s_idx;
   __shared__ float s_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = tid & 15, rr = tid >> 4;
@@ -137,40 +152,43 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(PagedLayer L, AppendA
   pdl_trigger();
   if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;  // one thread's reading for the CTA
 
-  if ((int)blockIdx.x >= a.n_units) {  // a query CTA: kQRows rows (token, query head)
-    const int n_q = L.n_kv * L.G;
-    const int64_t rows = (int64_t)a.b.n_tokens * n_q;
-    const int64_t r0 = (int64_t)((int)blockIdx.x - a.n_units) * kQRows;
-#pragma unroll
-    for (int p = 0; p < kQRows / (kThreads / 16); ++p) {
-      const int64_t r = r0 + p * (kThreads / 16) + rr;
-      const bool live = r < rows;
-      const int t = live ? (int)(r / n_q) : 0, h = live ? (int)(r - (int64_t)t * n_q) : 0;
-      int lo = 0, pos = 0;
-      bool in = live;
-      if (live) {
-        if (a.b.cu_new) {
-          int hi = a.b.n_seqs - 1;
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.b.cu_new[mid] <= t) lo = mid; else hi = mid - 1;
-          }
-        } else {
-          lo = t;
+  if ((int)blockIdx.x >= a.n_units) {  // a query CTA: 16 threads a (token, q_heads heads)
+    const int n_q = L.n_kv * L.G, groups = (n_q + a.q_heads - 1) / a.q_heads;
+    const int64_t at = (int64_t)((int)blockIdx.x - a.n_units) * (kThreads / 16) + rr;
+    const int t = (int)(at / groups), h0 = (int)(at - (int64_t)t * groups) * a.q_heads;
+    int lo = 0, pos = 0;
+    bool in = t < a.b.n_tokens;
+    if (in) {
+      if (a.b.cu_new) {
+        int hi = a.b.n_seqs - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (a.b.cu_new[mid] <= t) lo = mid; else hi = mid - 1;
         }
-        const PagedSeq s = paged_seq(a.b, P, lo, true);
-        in = s.ok && t >= s.row0 && t < s.row0 + s.n_new;  // rows behind the last sequence stay as they were
-        if (a.rope.positions)
-          pos = a.rope.positions[t];
-        else
-          pos = s.len - s.n_new + (t - s.row0);
-        if (in) pos = clamp_position(L, a.rope, pos, lo); else pos = 0;
+      } else {
+        lo = min(t, a.b.n_seqs - 1);
       }
-      const uint4 raw = in ? *reinterpret_cast<const uint4*>(a.q + (int64_t)t * a.q_stride + h * D + j * 8)
-                           : make_uint4(0, 0, 0, 0);
-      float y[8];
-      rotate8(a.rope, pos, j, lane, raw, y);
-      if (in) *reinterpret_cast<uint4*>(a.q_out + (int64_t)t * a.q_out_stride + h * D + j * 8) = pack_bf16(y);
+      const PagedSeq s = paged_seq(a.b, P, lo, true);
+      in = s.ok && t >= s.row0 && t < s.row0 + s.n_new;  // rows behind the last sequence stay as they were
+      if (in) pos = clamp_position(L, a.rope, a.rope.positions ? a.rope.positions[t] : s.len - s.n_new + (t - s.row0), lo);
+    }
+    Angles g;
+    if (in) load_angles(a.rope, pos, j, g);
+    const uint16_t* from = a.q + (int64_t)t * a.q_stride + h0 * D + j * 8;
+    uint16_t* to = a.q_out + (int64_t)t * a.q_out_stride + h0 * D + j * 8;
+    for (int i0 = 0; i0 < a.q_heads; i0 += 4) {
+      uint4 raw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (in && i0 + i < a.q_heads && h0 + i0 + i < n_q) raw[i] = *reinterpret_cast<const uint4*>(from + (i0 + i) * D);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y[8];
+        rotate8(a.rope, g, j, lane, raw[i], y);
+        if (in && i0 + i < a.q_heads && h0 + i0 + i < n_q) *reinterpret_cast<uint4*>(to + (i0 + i) * D) = pack_bf16(y);
+      }
     }
     return;
   }
@@ -242,7 +260,9 @@ __global__ void __launch_bounds__(kThreads) k_paged_append(PagedLayer L, AppendA
     int pos = 0;
     if (in && !is_v) pos = clamp_position(L, rope, rope.positions ? rope.positions[t] : pg * P + sl, seq);
     const uint4 raw = in ? *reinterpret_cast<const uint4*>(src + t * stride + head * D + j * 8) : make_uint4(0, 0, 0, 0);
-    rotate8(rope, pos, j, lane, raw, y[p]);
+    Angles g;
+    if (in && !is_v) load_angles(rope, pos, j, g);
+    rotate8(rope, g, j, lane, raw, y[p]);
     if (E4M3) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -295,11 +315,18 @@ cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, co
   int64_t slots = b.max_new == 1 ? b.n_seqs : (int64_t)b.n_tokens / L.P + 2 * (int64_t)b.n_seqs;
   if (slots > b.n_tokens && b.max_new != 1) slots = b.n_tokens;
   const int64_t units = slots * L.n_kv * 2;
-  const int64_t qb = q ? ((int64_t)b.n_tokens * L.n_kv * L.G + kQRows - 1) / kQRows : 0;
+  // Heads of a query item: few rows want many items (latency), many rows want
+  // the angles' loads spread over more heads: 64 tokens x 32 heads 1 head,
+  // thousands of tokens 8.
+  const int64_t rows = (int64_t)b.n_tokens * L.n_kv * L.G;
+  const int q_heads = rows >= 32768 ? 8 : rows >= 8192 ? 4 : 1;
+  const int threads = L.P == 64 ? Shape<64>::threads : Shape<16>::threads;
+  const int64_t items = (int64_t)b.n_tokens * ((L.n_kv * L.G + q_heads - 1) / q_heads);
+  const int64_t qb = q ? (items + threads / 16 - 1) / (threads / 16) : 0;
   if (units + qb == 0) return cudaSuccess;
   if (units + qb > 0x7fffffff) return cudaErrorInvalidValue;
-  AppendArgs a{b, rope, k, v, q, q_out, k_stride, v_stride, q_stride, q_out_stride, (int32_t)units};
-  const dim3 grid((unsigned)(units + qb)), block(kThreads);
+  AppendArgs a{b, rope, k, v, q, q_out, k_stride, v_stride, q_stride, q_out_stride, (int32_t)units, q_heads};
+  const dim3 grid((unsigned)(units + qb)), block(threads);
 #define MK_LAUNCH_APPEND(PP)                                                                \
   return L.e4m3 ? launch_pdl(k_paged_append<PP, true>, grid, block, 0, s, 0, L, a)          \
                 : launch_pdl(k_paged_append<PP, false>, grid, block, 0, s, 0, L, a)

@@ -619,9 +619,12 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
                                 const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale, uint16_t* out,
                                 int64_t out_stride, float* lse, cudaStream_t s) {
   DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 1, w.part_acc, w.part_ml, w.counters};
-  // Eight heads' joining buffer (32 KB) leaves room for two stages a warp.
-  if (L.G == 8) return L.e4m3 ? launch<true, 8, 2>(L, maps, a, s) : launch<false, 8, 2>(L, maps, a, s);
-  return L.e4m3 ? launch<true, 8, 3>(L, maps, a, s) : launch<false, 8, 3>(L, maps, a, s);
+  // 12 warps of two 8 KB stages: the conversion of a chunk takes a warp about
+  // 3 000 clocks, so eight were bound by it (64 ragged sequences 228 us, 12
+  // warps 203); 16 with one stage wait for their copies (221).  Eight heads'
+  // joining buffer (10 x 4 KB) leaves room for ten.
+  if (L.G == 8) return L.e4m3 ? launch<true, 10, 2>(L, maps, a, s) : launch<false, 10, 2>(L, maps, a, s);
+  return L.e4m3 ? launch<true, 12, 2>(L, maps, a, s) : launch<false, 12, 2>(L, maps, a, s);
 }
 
 }  // namespace mk
