@@ -484,6 +484,8 @@ class PagedKV:
         `rope`; q, if given, is turned too, into q_out (default: a new tensor), which is returned."""
         _need(batch.device == self.device and (rope is None or rope.device == self.device), "the batch is on another device")
         ks, vs = self._rows(k, "k", batch, self.cfg.n_kv_heads), self._rows(v, "v", batch, self.cfg.n_kv_heads)
+        _need(rope is None or rope.positions is None or rope.positions.numel() >= batch.n_tokens,
+              "rope.positions must name a position for every row")
         qs = os_ = 0
         if q is not None:
             qs = self._rows(q, "q", batch, self.cfg.n_q_heads)

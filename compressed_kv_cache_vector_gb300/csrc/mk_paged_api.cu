@@ -119,7 +119,7 @@ mk_status check_call(const mk_paged* h, int32_t layer, const mk_paged_batch* b) 
   if (b->n_seqs < 0 || b->n_seqs > h->cfg.max_seqs || b->n_tokens < 0 || b->max_new < 1) return MK_EINVAL;
   if (b->n_seqs == 0 || b->n_tokens == 0) return MK_OK;  // nothing to do, nothing read
   if (!b->kv_len || !b->page_table || b->table_stride < 1) return MK_EINVAL;
-  if ((int64_t)b->table_stride * h->cfg.page > 0x7fffffff) return MK_EINVAL;
+  if ((int64_t)b->table_stride * h->cfg.page > 0x7fffff00) return MK_EINVAL;  // token numbers and a step past them
   if (!b->cu_new && (b->max_new != 1 || b->n_tokens < b->n_seqs)) return MK_EINVAL;
   return MK_OK;
 }

@@ -450,7 +450,8 @@ mk_status mk_swap_segment(mk_ctx* ctx, int32_t layer, int32_t seq, int32_t kv_he
  *                     stored code c stands for the value c * scale
  * Token p of a sequence is in slot p mod page of the sequence's (p / page)-th
  * page, named by its page table row.  Slots past a sequence's length are never
- * read as values: they may hold anything.
+ * read as values: they may hold anything.  The attention takes any scales
+ * from 2^-64 to 2^120, not only the powers of two that the append writes.
  *
  * The calls follow the conventions above (host checks first, a sticky device
  * error word read with mk_paged_poll_error, one host thread and one device
@@ -467,7 +468,7 @@ typedef struct mk_paged mk_paged;
 typedef struct mk_paged_config {
   int32_t head_dim;   /* must be 128 */
   int32_t n_q_heads;  /* query heads per layer */
-  int32_t n_kv_heads; /* kv heads per layer; n_q_heads/n_kv_heads 1, 2, 4 or 8 */
+  int32_t n_kv_heads; /* kv heads per layer, <= 1024; n_q_heads/n_kv_heads 1, 2, 4 or 8 */
   int32_t n_layers;
   int32_t page;       /* tokens per page: 16, 32 or 64 */
   int32_t n_pages;    /* pages per layer */
@@ -481,7 +482,7 @@ typedef struct mk_paged_batch {
   int32_t n_seqs;            /* 0..max_seqs */
   int32_t n_tokens;          /* rows of k, v, q and out in the call */
   int32_t max_new;           /* no sequence has more new tokens than this */
-  int32_t table_stride;      /* entries per page table row */
+  int32_t table_stride;      /* entries per page table row; table_stride * page <= 2^31 - 256 */
   const int32_t* cu_new;     /* [n_seqs + 1]: sequence i's new tokens are rows cu_new[i] .. cu_new[i+1] - 1.
                                 Rows past cu_new[n_seqs] (a padded batch) are not touched.  NULL with
                                 max_new = 1 and n_tokens >= n_seqs: row i is sequence i's one token. */
@@ -545,12 +546,17 @@ mk_status mk_paged_decode_attn(mk_paged* h, int32_t layer, const mk_paged_batch*
 /* The same for several query tokens per sequence (a prompt's chunk,
  * verification of drafted tokens, cross attention).  causal = 1: query j of
  * n_new sees the first kv_len - n_new + j + 1 keys (none where that is <= 0:
- * out = 0, lse = -infinity); causal = 0: every query sees all kv_len keys. */
+ * out = 0, lse = -infinity); causal = 0: every query sees all kv_len keys.
+ * Keys that a query does not see have no influence on it whatever they hold;
+ * values must be finite: 256 rows (256 / group query tokens) are worked on
+ * together, and a NaN or infinity among the values that the last of them sees
+ * reaches them all (0 times it).  mk_paged_decode_attn has no such rows. */
 mk_status mk_paged_prefill_attn(mk_paged* h, int32_t layer, const mk_paged_batch* batch, int32_t causal, const void* q,
                                 int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
                                 mk_stream stream);
 
-/* As mk_poll_error and mk_clear_error, for a paged handle. */
+/* As mk_poll_error and mk_clear_error, for a paged handle: MK_ETIMEOUT after a
+ * bounded device-side wait gave up. */
 mk_status mk_paged_poll_error(mk_paged* h, int32_t* detail);
 mk_status mk_paged_clear_error(mk_paged* h);
 

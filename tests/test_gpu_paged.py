@@ -535,7 +535,8 @@ def test_refusals_before_any_launch():
         with pytest.raises(K.MosaicKVError) as e:
             call()
         assert e.value.status == 1
-    for call in (lambda: c.decode_attn(0, one, q.float()), lambda: c.decode_attn(0, one, q[:1]),
+    short = K.Rope(K.rope_table(64, 128), 128, positions=_i32([0]))
+    for call in (lambda: c.append(0, one, k, k, rope=short), lambda: c.decode_attn(0, one, q.float()), lambda: c.decode_attn(0, one, q[:1]),
                  lambda: c.decode_attn(0, one, q[:, :3]), lambda: c.append(0, one, k, k, q_out=q),
                  lambda: c.append(0, one, k.transpose(1, 2), k), lambda: c.decode_attn(0, one, q.cpu()),
                  lambda: c.prefill_attn(0, many, q, lse=torch.zeros(2, 4, device=DEV)),
@@ -629,4 +630,25 @@ def test_attention_of_zero_rows_zero_pages_and_zero_or_negative_scale(kv):
         qq = q[2:4].contiguous()
         out, lse = c.decode_attn(0, one, qq, scale=scale, lse=True)
         _check_attention(made, qq, out, lse, scale, [1, 1], True, 2.0 ** -11)
+    assert c.poll_error() == (0, 0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_nan_key_reaches_only_the_queries_that_see_it(kv):
+    lens, at = [600], 300
+    made = Made(kv, 16, 2, 4, lens, 12)
+    c = made.c
+    q = torch.randn(600, 8, 128, generator=_gen(4), device=DEV).to(torch.bfloat16)
+    b = K.PagedBatch(made.kv_len, made.table, _i32([0, 600]), 600, 600)
+    want, wl = c.prefill_attn(0, b, q, lse=True)
+    nan = 0x7f if kv == "e4m3" else 0xff
+    c.k_pool[0, made.rows[0][at // 16], 1, at % 16].view(torch.uint8).fill_(nan)        # head 1, token 300
+    out, lse = c.prefill_attn(0, b, q, lse=True)
+    assert torch.equal(out[:at], want[:at]) and torch.equal(lse[:at], wl[:at])
+    assert torch.equal(out[:, :4], want[:, :4]) and torch.equal(lse[:, :4], wl[:, :4])
+    assert bool(torch.isnan(out[at:, 4:]).all()) and bool(torch.isnan(lse[at:, 4:]).all())
+    one = K.PagedBatch(_i32([at]), made.table)
+    assert not bool(torch.isnan(c.decode_attn(0, one, q[:1])).any())
+    one = K.PagedBatch(_i32([at + 1]), made.table)
+    assert bool(torch.isnan(c.decode_attn(0, one, q[:1])[:, 4:]).all())
     assert c.poll_error() == (0, 0)
