@@ -91,8 +91,8 @@ cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, co
                                 int64_t k_stride, const uint16_t* v, int64_t v_stride, const uint16_t* q,
                                 int64_t q_stride, uint16_t* q_out, int64_t q_out_stride, cudaStream_t s);
 cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
-                                const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale, uint16_t* out,
-                                int64_t out_stride, float* lse, cudaStream_t s);
+                                const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
+                                float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s);
 cudaError_t launch_paged_prefill(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, bool causal,
                                  const uint16_t* q, int64_t q_stride, float scale, uint16_t* out, int64_t out_stride,
                                  float* lse, cudaStream_t s);

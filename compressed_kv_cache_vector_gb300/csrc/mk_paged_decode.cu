@@ -55,8 +55,9 @@ struct DecodeArgs {
   float scale;          // times log2 e
   int32_t layer_page0;  // first page of the layer in the maps
   int32_t min_chunks;   // fewest chunks of a CTA
-  float* part_acc;      // [2 grid][G][128]
-  float* part_ml;       // [2 grid][G][2]
+  int32_t causal;       // several tokens a sequence: token j sees the first len - n_new + j + 1 keys
+  float* part_acc;      // [2 grid][rows][128]
+  float* part_ml;       // [2 grid][rows][2]
   int32_t* counters;    // [max_seqs][n_kv]
 };
 
@@ -123,32 +124,37 @@ struct Cursor {
   int seq, head, ch;
 };
 
-template <bool E4M3, int NW, int NS>
+// C = 1: one token a sequence, a unit's rows are the head's G query heads.
+// C = 2: a few tokens a sequence (verification), a unit's rows are up to 16
+// (token, query head) rows: they fill the rows of the A operand that one token
+// leaves empty.
+template <bool E4M3, int NW, int NS, int C>
 struct DecodeSmem {
   static constexpr int CH = E4M3 ? 32 : 16;  // tokens of a chunk
   static constexpr int ring = NW * NS * kStageBytes;
-  static int bytes(int G) { return 1024 + ring + NW * G * D * 4; }
+  static int rows(int G) { return C == 1 ? G : 16; }
+  static int bytes(int G) { return 1024 + ring + NW * rows(G) * D * 4; }
 };
 
-template <bool E4M3, int NW, int NS>
+template <bool E4M3, int NW, int NS, int C>
 __global__ void __launch_bounds__(NW * 32, 1)
     k_paged_decode(PagedLayer L, DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
-  constexpr int CH = DecodeSmem<E4M3, NW, NS>::CH, NT = CH / 8, NTHR = NW * 32;
+  constexpr int CH = DecodeSmem<E4M3, NW, NS, C>::CH, NT = CH / 8, NTHR = NW * 32;
   constexpr float kShift = E4M3 ? 14.0f : 0.0f;  // weights times 2^kShift before their rounding
   extern __shared__ unsigned char dyn[];
   __shared__ int64_t s_pre[MK_MAX_CALL_SEQS + 1];
-  __shared__ int s_len[MK_MAX_CALL_SEQS], s_row[MK_MAX_CALL_SEQS];
+  __shared__ int s_len[MK_MAX_CALL_SEQS], s_row[MK_MAX_CALL_SEQS], s_new[C == 1 ? 1 : MK_MAX_CALL_SEQS];
   __shared__ int64_t s_wsum[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NS];
   __shared__ __align__(16) float s_sc[NW][NS][4];  // k scale of box 0, 1; v scale of box 0, 1
-  __shared__ float s_ml[NW][MK_MAX_GROUP][2];
-  __shared__ float s_M[MK_MAX_GROUP], s_L[MK_MAX_GROUP];
+  __shared__ float s_ml[NW][8 * C][2];
+  __shared__ float s_M[8 * C], s_L[8 * C];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
   unsigned char* ring = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023);
-  float* s_acc = reinterpret_cast<float*>(ring + DecodeSmem<E4M3, NW, NS>::ring);
-  const int n_kv = L.n_kv, G = L.G, n_seqs = a.b.n_seqs;
+  float* s_acc = reinterpret_cast<float*>(ring + DecodeSmem<E4M3, NW, NS, C>::ring);
+  const int n_kv = L.n_kv, G = L.G, n_seqs = a.b.n_seqs, R = C == 1 ? G : 16;
 
   if (lane == 0)
     for (int i = 0; i < NS; ++i) mbar_init(&s_bar[warp][i], E4M3 ? 5 : 1);
@@ -165,9 +171,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (i < n_seqs) {
       const PagedSeq s = paged_seq(a.b, L.P, i, false);
       if (!s.ok) paged_error(L, ERR_PAGED_BATCH, i, s.len);
-      const bool live = s.ok && s.n_new == 1;
+      const bool live = s.ok && (C == 1 ? s.n_new == 1 : s.n_new > 0);  // C = 2: n_new <= max_new <= 16 / G
       s_len[i] = live ? s.len : 0;
       s_row[i] = live ? s.row0 : -1;
+      if (C > 1) s_new[i] = live ? s.n_new : 0;
       mine = live ? (int64_t)((s.len + CH - 1) / CH) * n_kv : 0;
     }
     int64_t x = mine;
@@ -193,10 +200,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
   // Rows of empty sequences.
   for (int i = blockIdx.x; i < n_seqs; i += gridDim.x)
     if (s_row[i] >= 0 && s_len[i] == 0) {
-      for (int e = tid; e < n_kv * G * D / 8; e += NTHR)
-        *reinterpret_cast<uint4*>(a.out + (int64_t)s_row[i] * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
-      if (a.lse)
-        for (int e = tid; e < n_kv * G; e += NTHR) a.lse[(int64_t)s_row[i] * n_kv * G + e] = -INFINITY;
+      for (int t = 0; t < (C == 1 ? 1 : s_new[i]); ++t) {
+        for (int e = tid; e < n_kv * G * D / 8; e += NTHR)
+          *reinterpret_cast<uint4*>(a.out + (int64_t)(s_row[i] + t) * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+          for (int e = tid; e < n_kv * G; e += NTHR) a.lse[(int64_t)(s_row[i] + t) * n_kv * G + e] = -INFINITY;
+      }
     }
 
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
@@ -304,20 +313,30 @@ __global__ void __launch_bounds__(NW * 32, 1)
   while (fs < n_flat) {
     const int len = s_len[u.seq], nch = n_chunks(u.seq);
     const int fe = min(n_flat, fs + nch - u.ch);  // the unit's chunks of this CTA: flat [fs, fe)
-    const int row = s_row[u.seq];
+    const int row = s_row[u.seq], n_new = C == 1 ? 1 : s_new[u.seq];
+    // Row x of the unit: its token, query head and whether there is one.
+    auto tok_of = [&](int x) { return C == 1 ? 0 : x / G; };
+    auto head_of = [&](int x) { return u.head * G + (C == 1 ? x : x % G); };
+    auto live_row = [&](int x) { return C == 1 ? x < G : tok_of(x) < n_new; };
 
-    // The unit's queries as A fragments: row g = head g.  e4m3: fp16 after a
-    // power of two per head, in the channel order that the codes' pairs have.
-    uint32_t qa[8], qb[8];
-    float zf = a.scale;
-    {
-      const uint16_t* qp = a.q + (int64_t)row * a.q_stride + (u.head * G + (g < G ? g : 0)) * D;
+    // The unit's queries as A fragments: rows g and (C = 2) g + 8.  e4m3: fp16
+    // after a power of two per row, in the channel order that the codes' pairs have.
+    uint32_t qa[C][8], qb[C][8];
+    float zf[C];
+    int see[C];  // keys that the row sees
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int x = g + 8 * i;
+      const bool on = live_row(x);
+      const uint16_t* qp = a.q + (int64_t)(row + (on ? tok_of(x) : 0)) * a.q_stride + (on ? head_of(x) : 0) * D;
+      zf[i] = a.scale;
+      see[i] = C > 1 && a.causal && on ? max(0, min(len, len - n_new + tok_of(x) + 1)) : len;
       if (E4M3) {
         uint2 w[8];
         float top = 0.0f;
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          w[s] = g < G ? *reinterpret_cast<const uint2*>(qp + 16 * s + 4 * c) : make_uint2(0, 0);
+          w[s] = on ? *reinterpret_cast<const uint2*>(qp + 16 * s + 4 * c) : make_uint2(0, 0);
           top = fmaxf(top, fmaxf(fmaxf(fabsf(bf2f(w[s].x & 0xffff)), fabsf(bf2f(w[s].x >> 16))),
                                  fmaxf(fabsf(bf2f(w[s].y & 0xffff)), fabsf(bf2f(w[s].y >> 16)))));
         }
@@ -326,26 +345,33 @@ __global__ void __launch_bounds__(NW * 32, 1)
         int e = (int)(__float_as_uint(top) >> 23) - 127;
         e = max(-100, min(e, 120));
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        zf *= __uint_as_float((uint32_t)(127 + e) << 23);
+        zf[i] *= __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          qa[s] = pack_h2(bf2f(w[s].x & 0xffff) * down, bf2f(w[s].x >> 16) * down);
-          qb[s] = pack_h2(bf2f(w[s].y & 0xffff) * down, bf2f(w[s].y >> 16) * down);
+          qa[i][s] = pack_h2(bf2f(w[s].x & 0xffff) * down, bf2f(w[s].x >> 16) * down);
+          qb[i][s] = pack_h2(bf2f(w[s].y & 0xffff) * down, bf2f(w[s].y >> 16) * down);
         }
       } else {
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          qa[s] = g < G ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * c) : 0u;
-          qb[s] = g < G ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 8 + 2 * c) : 0u;
+          qa[i][s] = on ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * c) : 0u;
+          qb[i][s] = on ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 8 + 2 * c) : 0u;
         }
       }
     }
-    float m = -INFINITY, l = 0.0f;
-    float o[8][4];
+    // The first row sees the least: from there on chunks are masked by row.
+    const int see_all = C > 1 && a.causal ? max(0, min(len, len - n_new + tok_of(0) + 1)) : len;
+    float m[C], l[C];
+    float o[C][8][4];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int i = 0; i < C; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.0f;
+    }
 
     for (; flat < fe; flat += NW) {
       const int tok0 = (u.ch + flat - fs) * CH;
@@ -367,8 +393,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
           }
           __syncwarp();
         }
-        // logits: rows = heads, columns = tokens 8 nt + 2 c (+ 1)
-        float z[NT][2];
+        // logits: rows g and g + 8, columns = tokens 8 nt + 2 c (+ 1)
+        float z[C][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -379,76 +405,97 @@ __global__ void __launch_bounds__(NW * 32, 1)
               ldsm4(r, kb + nt * 1024 + kRow + (((uint32_t)(4 * h + (lane >> 3)) ^ kXor) << 4));
 #pragma unroll
               for (int s = 0; s < 4; ++s)
-                mma16<true>(acc, qa[4 * h + s], 0u, qb[4 * h + s], 0u, e4m3_h2(r[s]), e4m3_h2(r[s] >> 16));
+                mma16<true>(acc, qa[0][4 * h + s], C > 1 ? qa[C - 1][4 * h + s] : 0u, qb[0][4 * h + s],
+                            C > 1 ? qb[C - 1][4 * h + s] : 0u, e4m3_h2(r[s]), e4m3_h2(r[s] >> 16));
             }
           } else {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               uint32_t r[4];
               ldsm4(r, kb + (h >> 1) * 2048 + nt * 1024 + kRow + (((uint32_t)(4 * (h & 1) + (lane >> 3)) ^ kXor) << 4));
-              mma16<false>(acc, qa[2 * h], 0u, qb[2 * h], 0u, r[0], r[1]);
-              mma16<false>(acc, qa[2 * h + 1], 0u, qb[2 * h + 1], 0u, r[2], r[3]);
+#pragma unroll
+              for (int s = 0; s < 2; ++s)
+                mma16<false>(acc, qa[0][2 * h + s], C > 1 ? qa[C - 1][2 * h + s] : 0u, qb[0][2 * h + s],
+                             C > 1 ? qb[C - 1][2 * h + s] : 0u, r[2 * s], r[2 * s + 1]);
             }
           }
-          z[nt][0] = acc[0];
-          z[nt][1] = acc[1];
-        }
-        float inv[2] = {1.0f, 1.0f};
-        if (E4M3) {
-          const float4 sc = *reinterpret_cast<const float4*>(&s_sc[warp][stage][0]);
-          const bool two = box < 32;
-          const float k0 = zf * sc.x, k1 = two ? zf * sc.y : k0, v1 = two ? sc.w : sc.z;
-          const float b0 = __log2f(sc.z), b1 = __log2f(v1);
-          inv[0] = __frcp_rn(sc.z);
-          inv[1] = __frcp_rn(v1);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) z[nt][e] = fmaf(z[nt][e], nt < 2 ? k0 : k1, nt < 2 ? b0 : b1);
-        } else {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) z[nt][e] *= zf;
-        }
-        if (valid < CH) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (8 * nt + 2 * c + e >= valid) z[nt][e] = -INFINITY;
-        }
-        float mx = z[0][0];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(z[nt][0], z[nt][1]));
-        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-        if (__any_sync(FULL, mx > m)) {
-          const float mn = fmaxf(m, mx);
-          const float cr = m == -INFINITY ? 0.0f : ex2(m - mn);
-          m = mn;
-          l *= cr;
-          const float c0f = __shfl_sync(FULL, cr, 8 * c), c1f = __shfl_sync(FULL, cr, 8 * c + 4);
-#pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            o[n][0] *= c0f;
-            o[n][1] *= c1f;
-            o[n][2] *= c0f;
-            o[n][3] *= c1f;
+          for (int i = 0; i < C; ++i) {
+            z[i][nt][0] = acc[2 * i];
+            z[i][nt][1] = acc[2 * i + 1];
           }
         }
-        const float ms = (m == -INFINITY ? 0.0f : m) - kShift;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          z[nt][0] = ex2(z[nt][0] - ms);
-          z[nt][1] = ex2(z[nt][1] - ms);
-          l = E4M3 ? fmaf(z[nt][0] + z[nt][1], inv[nt >> 1], l) : l + (z[nt][0] + z[nt][1]);
+        float inv[2] = {1.0f, 1.0f};
+        float4 sc = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+        float b0 = 0.0f, b1 = 0.0f;
+        const bool two = box < 32;
+        if (E4M3) {
+          sc = *reinterpret_cast<const float4*>(&s_sc[warp][stage][0]);
+          const float v1 = two ? sc.w : sc.z;
+          b0 = __log2f(sc.z);
+          b1 = __log2f(v1);
+          inv[0] = __frcp_rn(sc.z);
+          inv[1] = __frcp_rn(v1);
         }
-        // values: rows = channels, columns = heads
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          if (E4M3) {
+            const float k0 = zf[i] * sc.x, k1 = two ? zf[i] * sc.y : k0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) z[i][nt][e] = fmaf(z[i][nt][e], nt < 2 ? k0 : k1, nt < 2 ? b0 : b1);
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) z[i][nt][e] *= zf[i];
+          }
+          if (tok0 + CH > see_all) {
+            const int lim = see[i] - tok0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (8 * nt + 2 * c + e >= lim) z[i][nt][e] = -INFINITY;
+          }
+          float mx = z[i][0][0];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(z[i][nt][0], z[i][nt][1]));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+          if (__any_sync(FULL, mx > m[i])) {
+            const float mn = fmaxf(m[i], mx);
+            const float cr = m[i] == -INFINITY ? 0.0f : ex2(m[i] - mn);
+            m[i] = mn;
+            l[i] *= cr;
+            const float c0f = __shfl_sync(FULL, cr, 8 * c), c1f = __shfl_sync(FULL, cr, 8 * c + 4);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              o[i][n][0] *= c0f;
+              o[i][n][1] *= c1f;
+              o[i][n][2] *= c0f;
+              o[i][n][3] *= c1f;
+            }
+          }
+          const float ms = (m[i] == -INFINITY ? 0.0f : m[i]) - kShift;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            z[i][nt][0] = ex2(z[i][nt][0] - ms);
+            z[i][nt][1] = ex2(z[i][nt][1] - ms);
+            l[i] = E4M3 ? fmaf(z[i][nt][0] + z[i][nt][1], inv[nt >> 1], l[i]) : l[i] + (z[i][nt][0] + z[i][nt][1]);
+          }
+        }
+        // values: rows = channels, columns = the unit's rows, eight at a time
         if (E4M3) {
 #pragma unroll
           for (int t = 0; t < CH / 16; ++t) {
-            const uint32_t p0 = pack_h2(z[2 * t][0], z[2 * t][1]), p1 = pack_h2(z[2 * t + 1][0], z[2 * t + 1][1]);
+            uint32_t p0[C], p1[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+              p0[i] = pack_h2(z[i][2 * t][0], z[i][2 * t][1]);
+              p1[i] = pack_h2(z[i][2 * t + 1][0], z[i][2 * t + 1][1]);
+            }
             const uint32_t r0 = vb + (16 * t + 2 * c) * 128;
             const uint32_t x0 = ((uint32_t)g ^ (uint32_t)(2 * c)) << 4, x1 = ((uint32_t)g ^ (uint32_t)(2 * c + 1)) << 4;
             const uint4 w0 = lds128(r0 + x0), w1 = lds128(r0 + 128 + x1), w2 = lds128(r0 + 1024 + x0),
@@ -459,20 +506,30 @@ __global__ void __launch_bounds__(NW * 32, 1)
             for (int n = 0; n < 8; ++n) {
               const uint32_t x = __byte_perm(a0[n >> 1], a1[n >> 1], n & 1 ? 0x7362 : 0x5140);
               const uint32_t y = __byte_perm(a2[n >> 1], a3[n >> 1], n & 1 ? 0x7362 : 0x5140);
-              mma16<true>(o[n], e4m3_h2(x), e4m3_h2(x >> 16), e4m3_h2(y), e4m3_h2(y >> 16), p0, p1);
+              const uint32_t v0 = e4m3_h2(x), v1 = e4m3_h2(x >> 16), v2 = e4m3_h2(y), v3 = e4m3_h2(y >> 16);
+#pragma unroll
+              for (int i = 0; i < C; ++i) mma16<true>(o[i][n], v0, v1, v2, v3, p0[i], p1[i]);
             }
           }
         } else {
-          const uint32_t p0 = pack_b2(z[0][0], z[0][1]), p1 = pack_b2(z[1][0], z[1][1]);
-          const uint32_t q0 = pack_b2(z[0][0] - bf2f(p0 & 0xffff), z[0][1] - bf2f(p0 >> 16));
-          const uint32_t q1 = pack_b2(z[1][0] - bf2f(p1 & 0xffff), z[1][1] - bf2f(p1 >> 16));
+          uint32_t p0[C], p1[C], q0[C], q1[C];
+#pragma unroll
+          for (int i = 0; i < C; ++i) {
+            p0[i] = pack_b2(z[i][0][0], z[i][0][1]);
+            p1[i] = pack_b2(z[i][1][0], z[i][1][1]);
+            q0[i] = pack_b2(z[i][0][0] - bf2f(p0[i] & 0xffff), z[i][0][1] - bf2f(p0[i] >> 16));
+            q1[i] = pack_b2(z[i][1][0] - bf2f(p1[i] & 0xffff), z[i][1][1] - bf2f(p1[i] >> 16));
+          }
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
             uint32_t r[4];
             const int tr = ((lane >> 4) & 1) * 8 + (lane & 7), ck = 2 * n + ((lane >> 3) & 1);
             ldsm4_t(r, vb + (ck >> 3) * 2048 + tr * 128 + (((uint32_t)(ck & 7) ^ kXor) << 4));
-            mma16<false>(o[n], r[0], r[1], r[2], r[3], p0, p1);
-            mma16<false>(o[n], r[0], r[1], r[2], r[3], q0, q1);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+              mma16<false>(o[i][n], r[0], r[1], r[2], r[3], p0[i], p1[i]);
+              mma16<false>(o[i][n], r[0], r[1], r[2], r[3], q0[i], q1[i]);
+            }
           }
         }
       }
@@ -485,67 +542,80 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
 
     // ---- join the warps ----
-    l += __shfl_xor_sync(FULL, l, 1);
-    l += __shfl_xor_sync(FULL, l, 2);
-    if (c == 0) {
-      s_ml[warp][g][0] = m;
-      s_ml[warp][g][1] = l;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      l[i] += __shfl_xor_sync(FULL, l[i], 1);
+      l[i] += __shfl_xor_sync(FULL, l[i], 2);
+      if (c == 0) {
+        s_ml[warp][8 * i + g][0] = m[i];
+        s_ml[warp][8 * i + g][1] = l[i];
+      }
     }
     __syncthreads();
-    if (warp == 0 && c == 0) {
+    if (tid < 8 * C) {
       float M = -INFINITY, S = 0.0f;
-      for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][g][0]);
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][tid][0]);
       for (int w = 0; w < NW; ++w)
-        if (s_ml[w][g][0] != -INFINITY) S += s_ml[w][g][1] * ex2(s_ml[w][g][0] - M);
-      s_M[g] = M;
-      s_L[g] = S;
+        if (s_ml[w][tid][0] != -INFINITY) S += s_ml[w][tid][1] * ex2(s_ml[w][tid][0] - M);
+      s_M[tid] = M;
+      s_L[tid] = S;
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int h = 2 * c + e;
-      if (h < G) {
-        float M = -INFINITY;
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][h][0]);
-        const float f = s_ml[warp][h][0] == -INFINITY ? 0.0f : ex2(s_ml[warp][h][0] - M);
-        float* to = s_acc + (warp * G + h) * D;
+    for (int i = 0; i < C; ++i)
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          if (E4M3) {
-            *reinterpret_cast<float2*>(to + 16 * g + 2 * n) = make_float2(o[n][e] * f, o[n][2 + e] * f);
-          } else {
-            to[16 * n + g] = o[n][e] * f;
-            to[16 * n + 8 + g] = o[n][2 + e] * f;
+      for (int e = 0; e < 2; ++e) {
+        const int h = 8 * i + 2 * c + e;
+        if (h < R) {
+          float M = -INFINITY;
+          for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][h][0]);
+          const float f = s_ml[warp][h][0] == -INFINITY ? 0.0f : ex2(s_ml[warp][h][0] - M);
+          float* to = s_acc + (warp * R + h) * D;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            if (E4M3) {
+              *reinterpret_cast<float2*>(to + 16 * g + 2 * n) = make_float2(o[i][n][e] * f, o[i][n][2 + e] * f);
+            } else {
+              to[16 * n + g] = o[i][n][e] * f;
+              to[16 * n + 8 + g] = o[i][n][2 + e] * f;
+            }
           }
         }
       }
-    }
     __syncthreads();
+    // Row x of the result (where it has one): its output, and its lse.
+    auto put = [&](int e, float x, float y) {
+      const int r = e >> 6;
+      if (!live_row(r)) return;
+      const float f = s_L[r] > 0.0f || s_L[r] != s_L[r] ? 1.0f / s_L[r] : 0.0f;
+      *reinterpret_cast<uint32_t*>(a.out + (int64_t)(row + tok_of(r)) * a.out_stride + head_of(r) * D + 2 * (e & 63)) =
+          pack_b2(x * f, y * f);
+    };
+    auto put_lse = [&](int r) {
+      if (!a.lse || !live_row(r)) return;
+      a.lse[(int64_t)(row + tok_of(r)) * n_kv * G + head_of(r)] =
+          s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + (s_M[r] - kShift)) * 0.6931471805599453f : -INFINITY;
+    };
     const bool whole = u.ch == 0 && fe - fs == nch;
     const int64_t part = 2 * (int64_t)blockIdx.x + (u.ch == 0 ? 1 : 0);
-    const int64_t orow = (int64_t)row * a.out_stride + (int64_t)u.head * G * D;
-    for (int e = tid; e < G * D / 2; e += NTHR) {
+    for (int e = tid; e < R * D / 2; e += NTHR) {
       float x = 0.0f, y = 0.0f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(s_acc + w * G * D + 2 * e);
+        const float2 v = *reinterpret_cast<const float2*>(s_acc + w * R * D + 2 * e);
         x += v.x;
         y += v.y;
       }
-      if (whole) {
-        const float r = 1.0f / s_L[e >> 6];
-        *reinterpret_cast<uint32_t*>(a.out + orow + 2 * e) = pack_b2(x * r, y * r);
-      } else {
-        *reinterpret_cast<float2*>(a.part_acc + part * G * D + 2 * e) = make_float2(x, y);
-      }
+      if (whole)
+        put(e, x, y);
+      else
+        *reinterpret_cast<float2*>(a.part_acc + part * R * D + 2 * e) = make_float2(x, y);
     }
-    if (tid < G) {
+    if (tid < R) {
       if (whole) {
-        if (a.lse)
-          a.lse[(int64_t)row * n_kv * G + u.head * G + tid] =
-              (log2f(s_L[tid]) + (s_M[tid] - kShift)) * 0.6931471805599453f;
+        put_lse(tid);
       } else {
-        a.part_ml[(part * G + tid) * 2] = s_M[tid];
-        a.part_ml[(part * G + tid) * 2 + 1] = s_L[tid];
+        a.part_ml[(part * R + tid) * 2] = s_M[tid];
+        a.part_ml[(part * R + tid) * 2 + 1] = s_L[tid];
       }
     }
     if (!whole) {
@@ -564,12 +634,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
       if (s_last) {
         __threadfence();
         auto slot = [&](int i) { return 2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0); };
-        for (int h = warp; h < G; h += NW) {  // a warp per head: the joined maximum and sum
+        for (int h = warp; h < R; h += NW) {  // a warp per row: the joined maximum and sum
           float M = -INFINITY, S = 0.0f;
-          for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(a.part_ml + (slot(i) * G + h) * 2));
+          for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(a.part_ml + (slot(i) * R + h) * 2));
           M = warp_max(M);
-          for (int i = lane; i < parts; i += 32)
-            S += __ldcg(a.part_ml + (slot(i) * G + h) * 2 + 1) * ex2(__ldcg(a.part_ml + (slot(i) * G + h) * 2) - M);
+          for (int i = lane; i < parts; i += 32) {
+            const float mi = __ldcg(a.part_ml + (slot(i) * R + h) * 2);
+            if (mi != -INFINITY) S += __ldcg(a.part_ml + (slot(i) * R + h) * 2 + 1) * ex2(mi - M);
+          }
           S = warp_sum(S);
           if (lane == 0) {
             s_M[h] = M;
@@ -577,22 +649,21 @@ __global__ void __launch_bounds__(NW * 32, 1)
           }
         }
         __syncthreads();
-        for (int e = tid; e < G * D / 2; e += NTHR) {
+        for (int e = tid; e < R * D / 2; e += NTHR) {
           const int h = e >> 6;
-          const float M = s_M[h], r = 1.0f / s_L[h];
+          const float M = s_M[h];
           float x = 0.0f, y = 0.0f;
 #pragma unroll 8
           for (int i = 0; i < parts; ++i) {
-            const float f = ex2(__ldcg(a.part_ml + (slot(i) * G + h) * 2) - M);
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_acc + slot(i) * G * D + 2 * e));
+            const float mi = __ldcg(a.part_ml + (slot(i) * R + h) * 2);
+            const float f = mi == -INFINITY ? 0.0f : ex2(mi - M);
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_acc + slot(i) * R * D + 2 * e));
             x = fmaf(v.x, f, x);
             y = fmaf(v.y, f, y);
           }
-          *reinterpret_cast<uint32_t*>(a.out + orow + 2 * e) = pack_b2(x * r, y * r);
+          put(e, x, y);
         }
-        if (a.lse && tid < G)
-          a.lse[(int64_t)row * n_kv * G + u.head * G + tid] =
-              (log2f(s_L[tid]) + (s_M[tid] - kShift)) * 0.6931471805599453f;
+        if (tid < R) put_lse(tid);
       }
     }
     __syncthreads();  // s_ml, s_acc, s_M, s_L are free again
@@ -606,23 +677,26 @@ __global__ void __launch_bounds__(NW * 32, 1)
   }
 }
 
-template <bool E4M3, int NW, int NS>
+template <bool E4M3, int NW, int NS, int C = 1>
 cudaError_t launch(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, cudaStream_t s) {
-  const int bytes = DecodeSmem<E4M3, NW, NS>::bytes(L.G);
+  const int bytes = DecodeSmem<E4M3, NW, NS, C>::bytes(L.G);
   int sms = 0;
-  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, NS>, bytes, NW * 32, nullptr, &sms);
+  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, NS, C>, bytes, NW * 32, nullptr, &sms);
   if (e != cudaSuccess) return e;
   const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
   a.min_chunks = NW;
-  return launch_pdl(k_paged_decode<E4M3, NW, NS>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
+  return launch_pdl(k_paged_decode<E4M3, NW, NS, C>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
-                                const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale, uint16_t* out,
-                                int64_t out_stride, float* lse, cudaStream_t s) {
-  DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 1, w.part_acc, w.part_ml, w.counters};
+                                const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
+                                float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s) {
+  DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 1, causal ? 1 : 0,
+               w.part_acc, w.part_ml, w.counters};
+  // 16 rows: 64 accumulators more a lane, eight warps of 255 registers.
+  if (several) return L.e4m3 ? launch<true, 8, 2, 2>(L, maps, a, s) : launch<false, 8, 2, 2>(L, maps, a, s);
   // 12 warps of two 8 KB stages: the conversion of a chunk takes a warp about
   // 3 000 clocks, so eight were bound by it (64 ragged sequences 228 us, 12
   // warps 203); 16 with one stage wait for their copies (221).  Eight heads'

@@ -652,3 +652,42 @@ def test_a_nan_key_reaches_only_the_queries_that_see_it(kv):
     one = K.PagedBatch(_i32([at + 1]), made.table)
     assert bool(torch.isnan(c.decode_attn(0, one, q[:1])[:, 4:]).all())
     assert c.poll_error() == (0, 0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("P,n_kv,G", [(16, 2, 4), (32, 1, 8), (64, 3, 1), (16, 2, 2)])
+def test_prefill_of_few_tokens(kv, causal, P, n_kv, G):
+    """Up to 16 rows a kv head, partly filled, empty contexts, no tokens, more tokens than keys, contexts that end at
+    and around the borders of pages and chunks, and a long one split over CTAs."""
+    top = 16 // G
+    lens = [0, 1, 2, 15, 16, 17, 31, 33, 64, 130, 700, 5000, 40, top - 1]
+    news = [min(m, top) for m in (1, top, 1, 2, top, 3, 1, top - 1, top, 2, top // 2, top, 0, top)]
+    made = Made(kv, P, n_kv, G, lens, 70 + P + G)
+    rows = sum(news)
+    cu = [0]
+    for m in news:
+        cu.append(cu[-1] + m)
+    q = (1.5 * torch.randn(rows + 3, n_kv * G, 128, generator=_gen(G), device=DEV)).to(torch.bfloat16)
+    out = torch.full_like(q, 4.0)
+    lse = torch.full((rows + 3, n_kv * G), 4.0, device=DEV)
+    b = K.PagedBatch(made.kv_len, made.table, _i32(cu), top, rows + 3)
+    made.c.prefill_attn(0, b, q, causal=causal, out=out, lse=lse)
+    assert made.c.poll_error() == (0, 0)
+    _check_attention(made, q, out, lse, 128 ** -0.5, news, causal, 2.0 ** -11)
+    assert bool((out[rows:] == 4).all()) and bool((lse[rows:] == 4).all())
+    again = made.c.prefill_attn(0, b, q, causal=causal, out=torch.full_like(q, 4.0))
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16))
+
+
+def test_prefill_of_few_and_of_many_tokens_agree():
+    """The two kernels behind prefill_attn on the same tokens: 4 a sequence as a batch of at most 4, and of at most 5."""
+    for kv in ("bf16", "e4m3"):
+        made = Made(kv, 32, 2, 4, [900, 4, 333], 17)
+        q = torch.randn(12, 8, 128, generator=_gen(2), device=DEV).to(torch.bfloat16)
+        cu = _i32([0, 4, 8, 12])
+        few, fl = made.c.prefill_attn(0, K.PagedBatch(made.kv_len, made.table, cu, 4, 12), q, lse=True)
+        many, ml = made.c.prefill_attn(0, K.PagedBatch(made.kv_len, made.table, cu, 5, 12), q, lse=True)
+        assert made.c.poll_error() == (0, 0)
+        for out, lse in ((few, fl), (many, ml)):
+            _check_attention(made, q, out, lse, 128 ** -0.5, [4, 4, 4], True, 2.0 ** -8 if kv == "bf16" else 2.0 ** -11)
