@@ -364,6 +364,12 @@ def rope_table(n_pos, rot_dim, base=10000.0, scale=1.0, device="cuda"):
     return torch.cat([a.cos(), a.sin()], dim=1).to(torch.float32).contiguous()
 
 
+# The current stream's handle without a Stream object around it (a microsecond
+# of every call) where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
@@ -465,14 +471,13 @@ class PagedKV:
                 heads == 1 or stride[1] == MK_HEAD_DIM)
         else:
             ok = len(shape) == 2 and shape[1] == heads * MK_HEAD_DIM and stride[1] == 1
-        _need(ok and t.dtype is torch.bfloat16 and shape[0] >= batch.n_tokens and t.device == self.device,
-              f"{name} must be bf16 [{batch.n_tokens}, {heads}, 128] on {self.device} with contiguous rows"
-              if not ok or t.dtype is not torch.bfloat16 else f"{name} has too few rows or is on another device")
+        if not (ok and t.dtype is torch.bfloat16 and shape[0] >= batch.n_tokens and t.device == self.device):
+            raise ValueError(f"{name} must be bf16 [{batch.n_tokens}, {heads}, 128] on {self.device} with contiguous rows")
         return stride[0] if shape[0] > 1 else heads * MK_HEAD_DIM
 
     def _stream(self, stream, *tensors):
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _raw_stream(self.device.index)
         if stream != torch.cuda.current_stream(self.device):
             for t in tensors:       # the allocator must not reuse them before that stream is done
                 if t is not None:
