@@ -23,7 +23,7 @@
 // page id, row) for single tokens.  32K tokens with 32 query heads into e4m3
 // pages of 64: 162 us, 4.7 TB/s of the 755 MB it has to move (69% of the copy
 // rate; 128 threads and eight rows a thread: 408 us, with four CTAs an SM); 64
-// single tokens 12 us a call.
+// single tokens 6.7 us a call (4.1 in a graph of calls).
 #include "mk_paged.cuh"
 
 namespace mk {

@@ -33,10 +33,10 @@
 //  * A unit that lies in several CTAs is joined by the last of them to arrive
 //    (counter, no waiting), in the order of the parts: the same result in
 //    every run.
-// Measured (GB300, 32 query heads over 8): 1M tokens e4m3 333 us (6.45 TB/s,
-// 95% of the copy rate), 128K 56 us (4.8 TB/s: about 15 us are launch, ramp and
-// joining), 64 ragged sequences 203 us (5.4 TB/s), 4 x 32K bf16 92 us (5.8
-// TB/s).  Reads its algorithmic bytes once (268.9 MB of DRAM reads at 128K).
+// Measured (GB300, 32 query heads over 8): 1M tokens e4m3 331 us (6.5 TB/s,
+// 96% of the copy rate), 128K 57 us (4.7 TB/s: about 15 us are launch, ramp and
+// joining), 4K 12 us, 64 ragged sequences 204 us (5.3 TB/s), 4 x 32K bf16 92 us
+// (5.8 TB/s).  Reads its algorithmic bytes once (268.9 MB of DRAM reads at 128K).
 #include "mk_paged.cuh"
 
 namespace mk {
@@ -54,7 +54,6 @@ struct DecodeArgs {
   int64_t q_stride, out_stride;
   float scale;          // times log2 e
   int32_t layer_page0;  // first page of the layer in the maps
-  int32_t min_chunks;   // fewest chunks of a CTA
   int32_t causal;       // several tokens a sequence: token j sees the first len - n_new + j + 1 keys
   float* part_acc;      // [2 grid][rows][128]
   float* part_ml;       // [2 grid][rows][2]
@@ -163,11 +162,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
   pdl_trigger();
   if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;  // one thread's reading for the CTA
 
-  // The list of chunks: exclusive prefix over the sequences, in chunks of all heads.
-  int64_t base = 0;
+  int units = 0;  // (sequence, kv head) pairs with keys
   for (int i0 = 0; i0 < n_seqs; i0 += NTHR) {
     const int i = i0 + tid;
-    int64_t mine = 0;
+    bool keys = false;
     if (i < n_seqs) {
       const PagedSeq s = paged_seq(a.b, L.P, i, false);
       if (!s.ok) paged_error(L, ERR_PAGED_BATCH, i, s.len);
@@ -175,27 +173,40 @@ __global__ void __launch_bounds__(NW * 32, 1)
       s_len[i] = live ? s.len : 0;
       s_row[i] = live ? s.row0 : -1;
       if (C > 1) s_new[i] = live ? s.n_new : 0;
-      mine = live ? (int64_t)((s.len + CH - 1) / CH) * n_kv : 0;
+      keys = live && s.len > 0;
     }
-    int64_t x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(FULL, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_wsum[warp] = x;
-    __syncthreads();
-    int64_t off = base;
-    for (int w = 0; w < NW; ++w) {
-      if (w < warp) off += s_wsum[w];
-      base += s_wsum[w];
-    }
-    if (i < n_seqs) s_pre[i] = off + x - mine;
-    __syncthreads();
+    units += __syncthreads_count(keys) * n_kv;
   }
-  if (tid == 0) s_pre[n_seqs] = base;
-  __syncthreads();
-  const int64_t total = base;
+  // The list of chunks: exclusive prefix over the sequences, each unit rounded
+  // up to a multiple of `pad` places.
+  auto n_chunks = [&](int seq) { return (s_len[seq] + CH - 1) / CH; };
+  auto places = [&](int seq, int pad) { return (n_chunks(seq) + pad - 1) / pad * pad; };
+  auto list = [&](int pad) {
+    int64_t base = 0;
+    for (int i0 = 0; i0 < n_seqs; i0 += NTHR) {
+      const int i = i0 + tid;
+      const int64_t mine = i < n_seqs ? (int64_t)places(i, pad) * n_kv : 0;
+      int64_t x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) s_wsum[warp] = x;
+      __syncthreads();
+      int64_t off = base;
+      for (int w = 0; w < NW; ++w) {
+        if (w < warp) off += s_wsum[w];
+        base += s_wsum[w];
+      }
+      if (i < n_seqs) s_pre[i] = off + x - mine;
+      __syncthreads();
+    }
+    if (tid == 0) s_pre[n_seqs] = base;
+    __syncthreads();
+    return base;
+  };
+  int64_t total = list(1);
 
   // Rows of empty sequences.
   for (int i = blockIdx.x; i < n_seqs; i += gridDim.x)
@@ -209,13 +220,24 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
 
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < a.min_chunks) per = a.min_chunks;
+  // A run that ends one unit and begins another joins twice, 5 us a time: where
+  // runs are short (up to kAligned chunks) and the CTAs suffice, every unit
+  // begins a run of its own (4K tokens in a graph of calls: 15.0 us without,
+  // 11.5 with).
+  constexpr int kAligned = 64, kShortest = 4;
+  int pad = 1;
+  if (total > 0 && units < (int)gridDim.x) {
+    const int spare = (int)gridDim.x - units;
+    int64_t p = (total + spare - 1) / spare;  // sum of ceil(n / p) <= total / p + units <= CTAs
+    if (p < kShortest) p = kShortest;
+    if (p <= kAligned) {
+      per = pad = (int)p;
+      total = list(pad);
+    }
+  }
   const int64_t c0 = (int64_t)blockIdx.x * per;
-  const int64_t c1 = c0 + per < total ? c0 + per : total;
-  if (c0 >= c1) return;
-  const int n_flat = (int)(c1 - c0);
+  if (c0 >= total) return;
 
-  auto n_chunks = [&](int seq) { return (s_len[seq] + CH - 1) / CH; };
   Cursor first;
   {
     int lo = 0, hi = n_seqs - 1;
@@ -224,11 +246,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
       if (s_pre[mid] <= c0) lo = mid; else hi = mid - 1;
     }
     const int64_t rem = c0 - s_pre[lo];
-    const int n = n_chunks(lo);
+    const int n = places(lo, pad);
     first.seq = lo;
     first.head = (int)(rem / n);
     first.ch = (int)(rem - (int64_t)first.head * n);
   }
+  // The CTA's chunks, from `first` on: of one unit only where units are padded.
+  const int n_flat = pad > 1 ? min(pad, n_chunks(first.seq) - first.ch) : (int)(c0 + per < total ? per : total - c0);
   auto advance = [&](Cursor& k, int by) {
     k.ch += by;
     while (k.seq < n_seqs) {
@@ -620,7 +644,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
     if (!whole) {
       // CTAs that hold a part of this unit: b_lo .. b_hi; the last to arrive joins them.
-      const int64_t u0 = s_pre[u.seq] + (int64_t)u.head * nch;
+      const int64_t u0 = s_pre[u.seq] + (int64_t)u.head * places(u.seq, pad);
       const int b_lo = (int)(u0 / per), b_hi = (int)((u0 + nch - 1) / per), parts = b_hi - b_lo + 1;
       __threadfence();
       __syncthreads();
@@ -684,7 +708,6 @@ cudaError_t launch(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, cud
   const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, NS, C>, bytes, NW * 32, nullptr, &sms);
   if (e != cudaSuccess) return e;
   const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
-  a.min_chunks = NW;
   return launch_pdl(k_paged_decode<E4M3, NW, NS, C>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
 }
 
@@ -693,7 +716,7 @@ cudaError_t launch(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, cud
 cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
                                 float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s) {
-  DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 1, causal ? 1 : 0,
+  DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, causal ? 1 : 0,
                w.part_acc, w.part_ml, w.counters};
   // 16 rows: 64 accumulators more a lane, eight warps of 255 registers.
   if (several) return L.e4m3 ? launch<true, 8, 2, 2>(L, maps, a, s) : launch<false, 8, 2, 2>(L, maps, a, s);
