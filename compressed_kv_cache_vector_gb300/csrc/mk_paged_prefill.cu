@@ -231,6 +231,7 @@ struct Shared {
   Cursor start;
   int64_t f0, per;                     // the CTA's run: its begin and the length of all runs
   int span;                            // its length
+  int patience;                        // limits of a wait that may span several items, in limits of a single one
   Item ring[kItems];                   // items on their way to the groups of warps
   uint64_t item_full[kItems], item_free[kItems], met, done;
   uint64_t q_full[2], s_full[2], p_half[2], p_full[2], o_full[2], k_full[2], k_free[2], v_full[2], v_free[2];
@@ -351,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     sh.f0 = f0;
     sh.per = per;
     sh.span = (int)(total - f0 < per ? total - f0 : per);
+    // 1024 steps take 2 to 3 ms, a limit is about 20.
+    sh.patience = 100 + sh.span / 1024;
   }
   if (warp == 0) {
     int lo = 0, hi = n_seqs - 1;
@@ -390,9 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   auto wait = [&](uint64_t* bar, unsigned parity) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, 1, &sh.dead, L.err);
   };
-  // Items last longer than a single wait's limit: a hundred of them.
+  // A wait that steps of the run can lie between, as many as it has: for an
+  // item, for a slot of the list, and wherever row tile 1's softmax, which has
+  // no part in items of one row tile and runs up to kItems of them ahead, meets
+  // the others again (a single sequence of 1M keys has 8192 steps an item).
   auto wait_long = [&](uint64_t* bar, unsigned parity) {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, 100, &sh.dead, L.err);
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, sh.patience, &sh.dead, L.err);
   };
   // The next item of the list for a group of warps; nullptr at its end.
   auto take = [&](unsigned c) -> const Item* {
@@ -674,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
     auto meet = [&]() {
       mbar_arrive_warp(&sh.met, lane);
       st ^= 4u;
-      return __all_sync(FULL, wait(&sh.met, (~st >> 2) & 1)) != 0;
+      return __all_sync(FULL, wait_long(&sh.met, (~st >> 2) & 1)) != 0;
     };
     // Row x of the warp's 32, from its item.
     struct Place {
@@ -770,7 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       }
       if (t < nt && n > 0 && ok) {
         for (int j = 0; j < n; ++j, step_ring(1)) {
-          ok = __all_sync(FULL, wait(&sh.s_full[t], st & 1));
+          ok = __all_sync(FULL, mbar_try_wait(&sh.s_full[t], st & 1) ||
+                                    wait_slow(&sh.s_full[t], st & 1, j == 0 ? sh.patience : 1, &sh.dead, L.err));
           st ^= 1u;
           if (!ok) break;
           tmem_fence_after_sync();
