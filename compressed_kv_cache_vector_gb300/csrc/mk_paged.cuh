@@ -14,7 +14,8 @@ struct PagedLayer {
   uint8_t* v;
   float* k_scale;               // [n_pages][n_kv] (e4m3)
   float* v_scale;
-  int32_t* err;                 // [0] status, [1] detail, [2] sequence, [3] aux
+  int32_t* err;                 // [0] status, [1] call that set it, [2] detail, [3] sequence, [4] aux
+  uint32_t call;                // number of this call of the handle
   int32_t n_pages, n_kv, G, P, p_log2, e4m3;
 };
 
@@ -26,6 +27,7 @@ enum PagedErr : int32_t {
   ERR_PAGED_WAIT = 19,      // a copy or a matrix instruction did not complete within the wait bound (MK_ETIMEOUT)
 };
 
+constexpr uint32_t kPagedClosed = 0xffffffffu;  // in place of the call's number: no call's
 constexpr int kPagedMaxCtas = 160;  // CTAs of a persistent attention kernel (GB300: 152 SMs)
 
 // Tensor maps of the pools, 128-byte swizzle, dimensions {128 channels,
@@ -47,13 +49,24 @@ int64_t paged_prefill_part_floats();
 #ifdef __CUDACC__
 __device__ __forceinline__ void paged_error(const PagedLayer& L, int32_t detail, int32_t seq, int32_t aux,
                                             int32_t status = (int32_t)MK_EDEVICE) {
-  if (atomicCAS(&L.err[0], 0, status) == 0) {
-    L.err[1] = detail;
-    L.err[2] = seq;
-    L.err[3] = aux;
+  const unsigned long long word = (unsigned long long)L.call << 32 | (uint32_t)status;
+  if (atomicCAS(reinterpret_cast<unsigned long long*>(L.err), 0ull, word) == 0) {
+    L.err[2] = detail;
+    L.err[3] = seq;
+    L.err[4] = aux;
   }
 }
-__device__ __forceinline__ bool paged_has_error(const PagedLayer& L) { return *(volatile int32_t*)L.err != 0; }
+// Whether the error word keeps this call from working.  An error that the same
+// call has set does not: its CTAs do not all start at once, and those behind
+// the one that met a bad page have good ones to do (after a wait that ran out
+// nothing is left to do).  A call that is kept from working closes the error
+// word, so that a replay of the call that set it is kept from working too.
+__device__ __forceinline__ bool paged_stopped(const PagedLayer& L) {
+  const unsigned long long word = *reinterpret_cast<volatile unsigned long long*>(L.err);
+  if (word == 0 || ((uint32_t)(word >> 32) == L.call && (uint32_t)word != (uint32_t)MK_ETIMEOUT)) return false;
+  *reinterpret_cast<volatile uint32_t*>(&L.err[1]) = kPagedClosed;
+  return true;
+}
 
 // Bounded wait for the phase with the given parity, as mbar_wait, with the
 // limit (about 20 ms) counted in clocks: reading the global timer between two

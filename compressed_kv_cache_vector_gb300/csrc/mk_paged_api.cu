@@ -16,6 +16,7 @@ struct mk_paged {
   int64_t pool_layer, scale_layer;
   mk::PagedMaps dec;        // boxes of the decode kernel
   mk::PagedScratch scratch;
+  uint32_t call;            // calls so far, kPagedClosed left out
   int device;
 };
 
@@ -104,13 +105,15 @@ struct DeviceGuard {
   }
 };
 
-mk::PagedLayer layer_of(const mk_paged* h, int layer) {
+mk::PagedLayer layer_of(mk_paged* h, int layer) {
   mk::PagedLayer L{};
   L.k = h->k + layer * h->pool_layer;
   L.v = h->v + layer * h->pool_layer;
   L.k_scale = h->k_scale ? h->k_scale + layer * h->scale_layer : nullptr;
   L.v_scale = h->v_scale ? h->v_scale + layer * h->scale_layer : nullptr;
   L.err = reinterpret_cast<int32_t*>(h->ws);
+  h->call = (h->call + 1) & 0x7fffffffu;
+  L.call = h->call;
   L.n_pages = h->cfg.n_pages;
   L.n_kv = h->cfg.n_kv_heads;
   L.G = h->cfg.n_q_heads / h->cfg.n_kv_heads;
@@ -268,11 +271,13 @@ mk_status mk_paged_prefill_attn(mk_paged* h, int32_t layer, const mk_paged_batch
 mk_status mk_paged_poll_error(mk_paged* h, int32_t* detail) {
   if (!h) return MK_EINVAL;
   DeviceGuard dev(h->device);
-  int32_t w[4] = {0, 0, 0, 0};
+  int32_t w[4] = {0, 0, 0, 0};  // status, call, detail, sequence
   cudaError_t e = dev.ok ? cudaDeviceSynchronize() : cudaErrorInvalidDevice;
   if (e == cudaSuccess) e = cudaMemcpy(w, h->ws, sizeof(w), cudaMemcpyDeviceToHost);
+  // Closed, as paged_stopped does it: a replay of the call does no work either.
+  if (e == cudaSuccess && w[0] != 0) e = cudaMemset(h->ws + 4, 0xff, 4);
   if (e != cudaSuccess) return MK_ECUDA;
-  if (detail) *detail = w[1];
+  if (detail) *detail = w[2];
   return w[0] == 0 ? MK_OK : (mk_status)w[0];
 }
 

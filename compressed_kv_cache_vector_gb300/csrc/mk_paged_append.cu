@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(Shape<P>::threads) k_paged_append(PagedLayer L
   // No early trigger: q_out may be the query of a call whose prologue reads it
   // before its own wait, and a kernel that triggers early may not write that.
   pdl_wait();
-  if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;  // one thread's reading for the CTA
+  if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;  // one thread's reading for the CTA
 
   if ((int)blockIdx.x >= a.n_units) {  // a query CTA: 16 threads a (token, q_heads heads)
     const int n_q = L.n_kv * L.G, groups = (n_q + a.q_heads - 1) / a.q_heads;

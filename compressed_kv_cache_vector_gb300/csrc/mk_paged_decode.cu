@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   mbar_init_fence();
   pdl_wait();
   pdl_trigger();
-  if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;  // one thread's reading for the CTA
+  if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;  // one thread's reading for the CTA
 
   int units = 0;  // (sequence, kv head) pairs with keys
   for (int i0 = 0; i0 < n_seqs; i0 += NTHR) {

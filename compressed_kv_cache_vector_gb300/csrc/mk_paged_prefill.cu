@@ -240,22 +240,17 @@ struct Shared {
   float inv[4][8];
   uint32_t tmem;
   int last;
-  volatile int dead;
+  volatile int dead;  // 0, or 1 + the warp whose wait ran out: recorded when the kernel ends
 };
 
 // The rest of a wait that has not ended at once, up to `times` times its limit.
 
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, unsigned parity, int times, volatile int* dead, int32_t* err) {
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, unsigned parity, int times, volatile int* dead) {
   for (int i = 0; i < times; ++i) {
     if (*dead) return false;
     if (paged_wait(bar, parity)) return true;
   }
-  *dead = 1;
-  if (atomicCAS(&err[0], 0, (int32_t)MK_ETIMEOUT) == 0) {
-    err[1] = ERR_PAGED_WAIT;
-    err[2] = blockIdx.x;
-    err[3] = threadIdx.x >> 5;
-  }
+  *dead = 1 + (int)(threadIdx.x >> 5);
   return false;
 }
 
@@ -294,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   mbar_init_fence();
   pdl_wait();
   pdl_trigger();
-  if (__syncthreads_or(tid == 0 && paged_has_error(L))) return;
+  if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;
 
   // ---- the CTA's run of the list of work items ----
   // All items in a row, each as long as its steps and kItemCost (its queries
@@ -391,14 +386,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   const uint32_t tmem = sh.tmem;
 
   auto wait = [&](uint64_t* bar, unsigned parity) {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, 1, &sh.dead, L.err);
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, 1, &sh.dead);
   };
   // A wait that steps of the run can lie between, as many as it has: for an
   // item, for a slot of the list, and wherever row tile 1's softmax, which has
   // no part in items of one row tile and runs up to kItems of them ahead, meets
   // the others again (a single sequence of 1M keys has 8192 steps an item).
   auto wait_long = [&](uint64_t* bar, unsigned parity) {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, sh.patience, &sh.dead, L.err);
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, sh.patience, &sh.dead);
   };
   // The next item of the list for a group of warps; nullptr at its end.
   auto take = [&](unsigned c) -> const Item* {
@@ -777,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
       if (t < nt && n > 0 && ok) {
         for (int j = 0; j < n; ++j, step_ring(1)) {
           ok = __all_sync(FULL, mbar_try_wait(&sh.s_full[t], st & 1) ||
-                                    wait_slow(&sh.s_full[t], st & 1, j == 0 ? sh.patience : 1, &sh.dead, L.err));
+                                    wait_slow(&sh.s_full[t], st & 1, j == 0 ? sh.patience : 1, &sh.dead));
           st ^= 1u;
           if (!ok) break;
           tmem_fence_after_sync();
@@ -1009,6 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
   __syncthreads();
   tmem_fence_after_sync();
   if (warp == 12) tmem_dealloc(tmem, 512);
+  if (tid == 0 && sh.dead) paged_error(L, ERR_PAGED_WAIT, (int32_t)blockIdx.x, sh.dead - 1, (int32_t)MK_ETIMEOUT);
 }
 
 }  // namespace

@@ -53,3 +53,104 @@ def test_a_chunk_behind_a_million_tokens_whose_last_row_tile_is_narrow(kv):
             tol = (2.0 ** -8 + 2.0 ** -9) * want.abs() + (p_round + 2.0 ** -8 + 2 * d + 2.0 ** -18) * A
             assert bool((out[rows, x].double() - want).abs().le(tol).all()), (h, x)
             assert bool((lse[rows, x].double() - ls).abs().le(d[:, 0] + 2.0 ** -9 + 2.0 ** -23 * ls.abs()).all()), (h, x)
+
+
+# ---- errors of one sequence beside good ones -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("what", ["page", "length"])
+def test_a_bad_sequence_leaves_the_others_of_its_call_complete(kv, what):
+    """An append of many waves of CTAs, whose first ones meet the error, and attention of both kinds behind it."""
+    P, n_kv, G, n, m = 16, 4, 2, 40, 512
+    cfg = K.make_paged_config(n_kv * G, n_kv, 1, P, n * m // P + 2, n, KV[kv])
+    g = _gen(3)
+    table = torch.randperm(n * m // P, generator=g, device=DEV).int().view(n, m // P).contiguous()
+    k, v = (torch.randn(n * m, n_kv, 128, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(n * m, n_kv * G, 128, generator=g, device=DEV).to(torch.bfloat16)
+    lens, cu = [m] * n, [m * i for i in range(n + 1)]
+    rope = K.Rope(K.rope_table(m, 128), 128)
+    good = torch.tensor([i for i in range(n) if i != 1], device=DEV)
+    pages, rows = table[good].flatten().long(), (good[:, None] * m + torch.arange(m, device=DEV)).flatten()
+
+    def run(kv_len, tab):
+        offsets = _i32(cu)
+        c = K.PagedKV(cfg, DEV)
+        b, res, states = K.PagedBatch(kv_len, tab, offsets, m, n * m), [], []
+
+        def done(*outs):
+            states.append(c.poll_error())
+            if states[-1][0]:
+                c.clear_error()
+            res.extend(outs)
+
+        qo = c.append(0, b, k, v, rope=rope, q=q, q_out=torch.zeros_like(q))
+        done(qo[rows], *(getattr(c, x + "_pool")[0].view(torch.uint8)[pages].clone() for x in ("k", "v")),
+             *([c.k_scale[0, pages], c.v_scale[0, pages]] if kv == "e4m3" else []))
+        # The split over CTAs depends on the lengths of all sequences: attention is compared with the oracle.
+        for per, call in ((m, c.prefill_attn), (1, c.decode_attn), (2, c.prefill_attn)):
+            b = K.PagedBatch(kv_len, tab, offsets if per == m else _i32([per * i for i in range(n + 1)]), per, per * n)
+            o, lse = torch.full_like(q[: per * n], float("nan")), torch.full((per * n, n_kv * G), float("nan"), device=DEV)
+            call(0, b, qo[: per * n], out=o, lse=lse)
+            done()
+            fine = torch.isfinite(o.float()).all(dim=2) & torch.isfinite(lse)
+            assert bool(fine.view(n, -1)[good].all())
+            for i in (0, 2, 17, n - 1):
+                for h in range(n_kv):
+                    kk, vv = (p[0, :, h].view(torch.uint8 if kv == "e4m3" else torch.int16)[table[i].long()].view(p.dtype)
+                              .double() for p in (c.k_pool, c.v_pool))
+                    if kv == "e4m3":
+                        kk, vv = (y * s[0, table[i].long(), h].double()[:, None, None]
+                                  for y, s in ((kk, c.k_scale), (vv, c.v_scale)))
+                    see = torch.arange(per, device=DEV) + m - per + 1
+                    for x in range(h * G, (h + 1) * G):
+                        at = slice(i * per, (i + 1) * per)
+                        w, ls, A, big = O.attention(qo[at, x].double(), kk.reshape(-1, 128), vv.reshape(-1, 128), 128 ** -0.5, see)
+                        d = 2.0 ** -17 * big[:, None]
+                        p_round = 2.0 ** -8 if kv == "bf16" and per == m else 2.0 ** -11
+                        tol = 2.0 ** -8 * w.abs() + (p_round + 2 * d + 2.0 ** -18) * A + 1e-30
+                        assert bool((o[at, x].double() - w).abs().le(tol).all()), (per, i, x)
+                        assert bool((lse[at, x].double() - ls).abs().le(d[:, 0] + 2.0 ** -18 + 2.0 ** -23 * ls.abs()).all())
+        return res, states
+
+    want, states = run(_i32(lens), table)
+    assert states == [(0, 0)] * 4
+    if what == "page":
+        table[1, 0] = 10 ** 6
+    else:
+        lens[1] = 16 * table.shape[1] + 1
+    got, states = run(_i32(lens), table)
+    assert states == [(5, 17 if what == "page" else 16)] * 4
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_an_error_keeps_later_calls_and_replays_from_working():
+    P, n_kv, G = 16, 2, 2
+    cfg = K.make_paged_config(n_kv * G, n_kv, 1, P, 8, 2)
+    table, kv_len = _i32([[0, 1], [10 ** 6, 3]]), _i32([5, 5])
+    k = torch.randn(2, n_kv, 128, device=DEV).to(torch.bfloat16)
+    q = torch.randn(2, n_kv * G, 128, device=DEV).to(torch.bfloat16)
+    out = torch.zeros_like(q)
+    for between in ("attention", "poll"):
+        c = K.PagedKV(cfg, DEV)
+        table[1, 0], b = 10 ** 6, K.PagedBatch(kv_len, table)
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            c.append(0, b, k, k)
+            if between == "attention":
+                c.decode_attn(0, b, q, out=out)
+        out.fill_(9.0)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert bool(c.k_pool[0, 0, :, 4].float().any())               # the good sequence's token is stored
+        assert bool((out == 9).all())                                 # the call behind it does nothing
+        if between == "poll":
+            assert c.poll_error() == (5, 17)
+        table[1, 0] = 2
+        c.k_pool.view(torch.uint8).zero_()
+        gr.replay()
+        assert not bool(c.k_pool.float().any()) and c.poll_error() == (5, 17)
+        c.clear_error()
+        gr.replay()
+        assert bool(c.k_pool[0, 0, :, 4].float().any()) and bool(c.k_pool[0, 2, :, 4].float().any())
+        assert c.poll_error() == (0, 0)
