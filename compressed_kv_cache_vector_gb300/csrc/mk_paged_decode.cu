@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (tid < 8 * C) {
       float M = -INFINITY, S = 0.0f;
       for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][tid][0]);
-      for (int w = 0; w < NW; ++w)
-        if (s_ml[w][tid][0] != -INFINITY) S += s_ml[w][tid][1] * ex2(s_ml[w][tid][0] - M);
+      // A part whose maximum is -infinity has no weights, or only NaN: its sum, 0 or NaN, counts as it is.
+      for (int w = 0; w < NW; ++w) S += s_ml[w][tid][1] * (s_ml[w][tid][0] == -INFINITY ? 1.0f : ex2(s_ml[w][tid][0] - M));
       s_M[tid] = M;
       s_L[tid] = S;
     }
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
           M = warp_max(M);
           for (int i = lane; i < parts; i += 32) {
             const float mi = __ldcg(a.part_ml + (slot(i) * R + h) * 2);
-            if (mi != -INFINITY) S += __ldcg(a.part_ml + (slot(i) * R + h) * 2 + 1) * ex2(mi - M);
+            S += __ldcg(a.part_ml + (slot(i) * R + h) * 2 + 1) * (mi == -INFINITY ? 1.0f : ex2(mi - M));
           }
           S = warp_sum(S);
           if (lane == 0) {

@@ -963,7 +963,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
           for (int i = 0; i < parts; ++i) M = fmaxf(M, __ldcg(part_of(slot(i)) + (int64_t)kRows * D + row));
           for (int i = 0; i < parts; ++i) {
             const float mi = __ldcg(part_of(slot(i)) + (int64_t)kRows * D + row);
-            if (mi != -INFINITY) S = fmaf(__ldcg(part_of(slot(i)) + (int64_t)kRows * (D + 1) + row), ex2(mi - M), S);
+            // A part without a maximum has the sum 0, or NaN where its logits were.
+            S = fmaf(__ldcg(part_of(slot(i)) + (int64_t)kRows * (D + 1) + row), mi == -INFINITY ? 1.0f : ex2(mi - M), S);
           }
           const float f = S > 0.0f || S != S ? 1.0f / S : 0.0f;
 #pragma unroll 1

@@ -9,7 +9,7 @@ import torch
 from compressed_kv_cache_vector_gb300 import binding as K
 from compressed_kv_cache_vector_gb300.build import build
 from oracle import paged_oracle as O
-from tests.test_gpu_paged import DEV, KV, _gen, _i32
+from tests.test_gpu_paged import DEV, KV, Made, _gen, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +154,31 @@ def test_an_error_keeps_later_calls_and_replays_from_working():
         gr.replay()
         assert bool(c.k_pool[0, 0, :, 4].float().any()) and bool(c.k_pool[0, 2, :, 4].float().any())
         assert c.poll_error() == (0, 0)
+
+
+# ---- numbers that are not finite, and scales far apart ---------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n_nan", [0, 600, 20000, 50000])
+def test_nan_logits_give_nan_however_the_tokens_are_split(kv, n_nan):
+    """NaN in a query row, or in the keys of one head from the first on, which fill the chunks of whole warps and whole
+    CTAs: out and lse are NaN in exactly the rows that see one, in every form of the attention."""
+    lens, n_kv, G = [700, 50000], 2, 2
+    made = Made(kv, 16, n_kv, G, lens, 12)
+    c = made.c
+    for p in made.rows[1][: n_nan // 16]:
+        c.k_pool[0, p, 1].view(torch.uint8).fill_(0x7f if kv == "e4m3" else 0xff)
+    for form, news in (("decode", [1, 1]), ("few", [3, 8]), ("wide", [150, 40])):
+        rows = sum(news)
+        q = torch.randn(rows, n_kv * G, 128, generator=_gen(4), device=DEV).to(torch.bfloat16)
+        q[0, 0], q[rows - 1, 3, 77] = float("nan"), float("nan")
+        want = torch.zeros(rows, n_kv * G, dtype=torch.bool, device=DEV)
+        want[0, 0] = want[rows - 1, 3] = True
+        want[news[0]:, 2:] |= n_nan > 0
+        b = K.PagedBatch(made.kv_len, made.table, _i32([0, news[0], rows]), max(news), rows)
+        for causal in (True, False):
+            out, lse = c.decode_attn(0, b, q, lse=True) if form == "decode" else c.prefill_attn(0, b, q, causal, lse=True)
+            assert c.poll_error() == (0, 0)
+            assert torch.equal(torch.isnan(lse), want), (form, causal)
+            assert torch.equal(torch.isnan(out), want[..., None].expand_as(out)), (form, causal)
+            assert bool(torch.isfinite(lse[~want]).all())
