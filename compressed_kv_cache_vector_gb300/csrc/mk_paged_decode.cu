@@ -8,7 +8,8 @@
 // multiplies the codes is 2^(z_t + log2 b_p - m); the sum of the plain weights
 // takes it back with 1 / b_p.  The maximum m is over z_t + log2 b_p: the
 // weights that reach the value product are relative to the largest
-// contribution, whatever the pages' scales.
+// contribution, and with scales up to 2^80 apart none that matters to the sum
+// falls below the smallest exponent (2^-126).
 //
 // What bounds it: HBM, each page is read once for all query heads that share
 // it (4 flops a byte and head).  The layout therefore follows the loads:

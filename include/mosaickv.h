@@ -451,7 +451,13 @@ mk_status mk_swap_segment(mk_ctx* ctx, int32_t layer, int32_t seq, int32_t kv_he
  * Token p of a sequence is in slot p mod page of the sequence's (p / page)-th
  * page, named by its page table row.  Slots past a sequence's length are never
  * read as values: they may hold anything.  The attention takes any scales
- * from 2^-64 to 2^120, not only the powers of two that the append writes.
+ * from 2^-64 to 2^120, not only the powers of two that the append writes, if
+ * the V scales that one query head of a sequence meets lie within 2^80 of each
+ * other.  (A weight is formed together with its page's V scale and can vanish
+ * below 2^-126 of the largest such product: within 2^80, what is lost to the
+ * softmax's sum is below 2^-46 of its largest term.  The append goes beyond
+ * that only with values above 448 x 2^16 next to a page of zeros, whose scale
+ * is 2^-64.)
  *
  * The calls follow the conventions above (host checks first, a sticky device
  * error word read with mk_paged_poll_error, one host thread and one device

@@ -182,3 +182,46 @@ def test_nan_logits_give_nan_however_the_tokens_are_split(kv, n_nan):
             assert torch.equal(torch.isnan(lse), want), (form, causal)
             assert torch.equal(torch.isnan(out), want[..., None].expand_as(out)), (form, causal)
             assert bool(torch.isfinite(lse[~want]).all())
+
+
+@pytest.mark.parametrize("low,high", [(-64, 16), (40, 120)])
+@pytest.mark.parametrize("order", ["alternating", "low first", "high first"])
+def test_v_scales_at_the_limit_of_their_distance(low, high, order):
+    """V scales 2^80 apart in pages next to each other, and in halves of the context, so that warps and CTAs differ.
+
+    The bounds of test_gpu_paged.py hold for weights in fp16's normal range.  Below it a weight (times its page's V
+    scale b, and 2^10 or more relative to the row's largest such product M) is off by half of fp16's smallest step,
+    2^-25, so by at most 2^-35 M: with scales this far apart that is all that some tokens have.  Each multiplies its
+    code, so 2^-35 max_i (p_i b_i) sum_i |code_i| comes on top, p_i the normalised weights: what is left in a channel
+    where the tokens of the large scale happen to hold zeros."""
+    lens, n_kv, G = [3000, 40], 2, 2
+    made = Made("e4m3", 16, n_kv, G, lens, 5)
+    for i, row in enumerate(made.rows):
+        n = -(-lens[i] // 16)
+        for j, p in enumerate(row[:n]):
+            up = {"alternating": j % 2, "low first": j >= n // 2, "high first": j < n // 2}[order]
+            made.c.v_scale[0, p] = 2.0 ** (high if up else low)
+            m = min(16, lens[i] - 16 * j)
+            made.c.v_pool[0, p, :, :m] = torch.randn(n_kv, m, 128, generator=_gen(p), device=DEV).to(made.c.v_pool.dtype)
+    for form, news in (("decode", [1, 1]), ("few", [3, 8]), ("wide", [150, 40])):
+        rows = sum(news)
+        q = (2 * torch.randn(rows, n_kv * G, 128, generator=_gen(4), device=DEV)).to(torch.bfloat16)
+        b = K.PagedBatch(made.kv_len, made.table, _i32([0, news[0], rows]), max(news), rows)
+        out, lse = made.c.decode_attn(0, b, q, lse=True) if form == "decode" else made.c.prefill_attn(0, b, q, lse=True)
+        assert made.c.poll_error() == (0, 0)
+        for i, (t, m, r0) in enumerate(zip(lens, news, (0, news[0]))):
+            see = torch.arange(m, device=DEV) + t - m + 1
+            pages = torch.tensor(made.rows[i][: -(-t // 16)], device=DEV)
+            for x in range(n_kv * G):
+                k, v = made.held(i, x // G)
+                qq, got, ls = q[r0:r0 + m, x].double(), out[r0:r0 + m, x].double(), lse[r0:r0 + m, x].double()
+                want, wl, A, big = O.attention(qq, k, v, 128 ** -0.5, see)
+                d = 2.0 ** -17 * big[:, None]
+                b_tok = made.c.v_scale[0, pages, x // G].double().repeat_interleave(16)[:t]
+                hid = torch.arange(t, device=DEV)[None, :] >= see[:, None]
+                p = torch.exp(qq @ k.T * 128 ** -0.5 - wl[:, None]).masked_fill(hid, 0)
+                codes = (~hid).double() @ (v / b_tok[:, None]).abs()
+                tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2 * d + 2.0 ** -18) * A
+                tol += 2.0 ** -35 * (p * b_tok).amax(dim=1, keepdim=True) * codes
+                assert bool((got - want).abs().le(tol).all()), (form, i, x, float(((got - want).abs() / tol).max()))
+                assert bool((ls - wl).abs().le(d[:, 0] + 2.0 ** -18 + 2.0 ** -23 * wl.abs()).all()), (form, i, x)
