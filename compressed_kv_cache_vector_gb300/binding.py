@@ -443,6 +443,7 @@ class PagedKV:
         self.k_scale = own(k_scale, "k_scale", torch.float32, shape[:3]) if e4m3 else None
         self.v_scale = own(v_scale, "v_scale", torch.float32, shape[:3]) if e4m3 else None
         self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
+        self._remember_streams()
         self.q_row, self.kv_row = cfg.n_q_heads * MK_HEAD_DIM, cfg.n_kv_heads * MK_HEAD_DIM
         self.h = None
         h = c_vp()
@@ -475,14 +476,28 @@ class PagedKV:
             raise ValueError(f"{name} must be bf16 [{batch.n_tokens}, {heads}, 128] on {self.device} with contiguous rows")
         return stride[0] if shape[0] > 1 else heads * MK_HEAD_DIM
 
-    def _stream(self, stream, *tensors):
-        if stream is None:
-            return _raw_stream(self.device.index)
-        if stream != torch.cuda.current_stream(self.device):
-            for t in tensors:       # the allocator must not reuse them before that stream is done
+    def _remember_streams(self):
+        """The stream that the cache's own memory belongs to needs no record, any other one."""
+        self._known = {_raw_stream(self.device.index)}
+
+    def _stream(self, stream, batch, rope, *tensors):
+        """The stream's handle; the allocator is told of all memory that the call reads or writes on another stream than
+        its own: it must not reuse it before that stream is done."""
+        raw = _raw_stream(self.device.index)
+        if stream is not None and stream.cuda_stream != raw:
+            raw = stream.cuda_stream
+            tensors += (batch.kv_len, batch.page_table, batch.cu_new)
+            if rope is not None:
+                tensors += (rope.table, rope.positions)
+            for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
-        return stream.cuda_stream
+        if raw not in self._known:
+            self._known.add(raw)
+            for t in (self.k_pool, self.v_pool, self.k_scale, self.v_scale, self.workspace):
+                if t is not None:
+                    t.record_stream(stream if stream is not None else torch.cuda.current_stream(self.device))
+        return raw
 
     def append(self, layer, batch, k, v, rope=None, q=None, q_out=None, stream=None):
         """Stores the batch's new tokens (k, v: bf16 [n_tokens, n_kv_heads, 128], rows may be strided), keys turned by
@@ -502,7 +517,7 @@ class PagedKV:
         st = self.lib.mk_paged_append(
             self.h, layer, batch.ref, rope.ref if rope is not None else None, k.data_ptr(), ks, v.data_ptr(), vs,
             q.data_ptr() if q is not None else None, qs, q_out.data_ptr() if q is not None else None, os_,
-            self._stream(stream, k, v, q, q_out))
+            self._stream(stream, batch, rope, k, v, q, q_out))
         if st:
             raise MosaicKVError("mk_paged_append", st)
         return q_out
@@ -519,7 +534,7 @@ class PagedKV:
             _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == self.device
                   and lse.numel() >= batch.n_tokens * self.cfg.n_q_heads, "lse must be contiguous fp32 [n_tokens, n_q_heads]")
         return (q.data_ptr(), qs, MK_HEAD_DIM ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-                lse.data_ptr() if lse is not None else None, self._stream(stream, q, out, lse)), out, lse
+                lse.data_ptr() if lse is not None else None, self._stream(stream, batch, None, q, out, lse)), out, lse
 
     def decode_attn(self, layer, batch, q, scale=None, out=None, lse=None, stream=None):
         """Attention of one query token per sequence (bf16 [n_tokens, n_q_heads, 128]); scale: default 1/sqrt(128).

@@ -225,3 +225,35 @@ def test_v_scales_at_the_limit_of_their_distance(low, high, order):
                 tol += 2.0 ** -35 * (p * b_tok).amax(dim=1, keepdim=True) * codes
                 assert bool((got - want).abs().le(tol).all()), (form, i, x, float(((got - want).abs() / tol).max()))
                 assert bool((ls - wl).abs().le(d[:, 0] + 2.0 ** -18 + 2.0 ** -23 * wl.abs()).all()), (form, i, x)
+
+
+# ---- other streams ---------------------------------------------------------------------------------------------------
+
+def test_memory_that_a_queued_call_reads_is_not_handed_out_again():
+    """Batch and rotation dropped while the call that reads them waits behind another kernel of its stream."""
+    made = Made("bf16", 16, 2, 2, [50, 90, 33], 6)
+    k, v = (torch.randn(3, 2, 128, generator=_gen(i), device=DEV).to(torch.bfloat16) for i in (1, 2))
+    q = torch.randn(3, 4, 128, generator=_gen(3), device=DEV).to(torch.bfloat16)
+    table = K.rope_table(100, 128)
+    qo = torch.empty_like(q)
+    want = made.c.append(0, K.PagedBatch(made.kv_len, made.table), k, v, rope=K.Rope(table, 128), q=q)
+    o = made.c.decode_attn(0, K.PagedBatch(made.kv_len, made.table), want)
+    out = torch.zeros_like(o)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    made.c.k_pool[0, made.rows[0][3], :, 1] = 0            # the first sequence's token is stored anew
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+    parts = [made.kv_len.clone(), made.table.clone(), table.clone(), _i32([49, 89, 32])]
+    torch.cuda.current_stream().synchronize()
+    spec = [(x.shape, x.dtype, x.data_ptr()) for x in parts]
+    b = K.PagedBatch(parts[0], parts[1])
+    made.c.append(0, b, k, v, rope=K.Rope(parts[2], 128, positions=parts[3]), q=q, q_out=qo, stream=s)
+    made.c.decode_attn(0, b, qo, out=out, stream=s)
+    queued = not s.query()
+    del parts, b
+    new = [torch.zeros(shape, dtype=dtype, device=DEV) for shape, dtype, _ in spec]      # what comes next on this stream
+    assert queued and not {x.data_ptr() for x in new} & {p for _, _, p in spec}
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(qo, want) and torch.equal(out, o) and made.c.poll_error() == (0, 0)
