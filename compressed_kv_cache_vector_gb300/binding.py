@@ -499,6 +499,17 @@ class PagedKV:
                     t.record_stream(stream if stream is not None else torch.cuda.current_stream(self.device))
         return raw
 
+    def _new(self, shape, dtype, stream):
+        """A new output.  For another stream than the current one it is allocated on that stream: a block that this
+        stream has just freed may still be read here when that one writes it."""
+        if stream is None or stream.cuda_stream == _raw_stream(self.device.index):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        here = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(here)
+        return t
+
     def append(self, layer, batch, k, v, rope=None, q=None, q_out=None, stream=None):
         """Stores the batch's new tokens (k, v: bf16 [n_tokens, n_kv_heads, 128], rows may be strided), keys turned by
         `rope`; q, if given, is turned too, into q_out (default: a new tensor), which is returned."""
@@ -510,7 +521,7 @@ class PagedKV:
         if q is not None:
             qs = self._rows(q, "q", batch, self.cfg.n_q_heads)
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                q_out = self._new(q.shape, q.dtype, stream)
             os_ = self._rows(q_out, "q_out", batch, self.cfg.n_q_heads)
         else:
             _need(q_out is None, "q_out needs q")
@@ -526,10 +537,10 @@ class PagedKV:
         _need(batch.device == self.device, "the batch is on another device")
         qs = self._rows(q, "q", batch, self.cfg.n_q_heads)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = self._new(q.shape, q.dtype, stream)
         os_ = self._rows(out, "out", batch, self.cfg.n_q_heads)
         if lse is True:
-            lse = torch.empty(q.shape[0], self.cfg.n_q_heads, dtype=torch.float32, device=q.device)
+            lse = self._new((q.shape[0], self.cfg.n_q_heads), torch.float32, stream)
         if lse is not None:
             _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == self.device
                   and lse.numel() >= batch.n_tokens * self.cfg.n_q_heads, "lse must be contiguous fp32 [n_tokens, n_q_heads]")

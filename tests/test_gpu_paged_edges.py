@@ -257,3 +257,21 @@ def test_memory_that_a_queued_call_reads_is_not_handed_out_again():
     assert queued and not {x.data_ptr() for x in new} & {p for _, _, p in spec}
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(qo, want) and torch.equal(out, o) and made.c.poll_error() == (0, 0)
+
+
+def test_new_outputs_for_another_stream_do_not_reuse_what_this_one_still_reads():
+    made = Made("bf16", 16, 2, 2, [50, 90, 33], 6)
+    q = torch.randn(3, 4, 128, generator=_gen(3), device=DEV).to(torch.bfloat16)
+    b = K.PagedBatch(made.kv_len, made.table)
+    want = made.c.decode_attn(0, b, q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    old = torch.full_like(q, 3.0)
+    torch.cuda._sleep(100_000_000)
+    copy = old.clone()                                     # queued behind the sleep, and then the block is free
+    del old
+    out, lse = made.c.decode_attn(0, b, q, lse=True, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)
+    torch.cuda.current_stream().wait_stream(s)
+    assert bool((copy == 3.0).all()) and made.c.poll_error() == (0, 0)

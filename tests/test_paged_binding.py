@@ -95,3 +95,34 @@ def test_nothing_is_recorded_on_the_current_stream_and_the_cache_once_for_each_o
     for _ in range(3):
         kv.decode_attn(0, b, q, out=out)
     assert all(t.streams == [OTHER] for t in _memory(kv)) and not _kept(q) and not _kept(b.kv_len)
+
+
+def test_new_outputs_belong_to_the_stream_that_writes_them(kv, monkeypatch):
+    made = []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            kv.set_current(self.stream.cuda_stream)
+
+        def __exit__(self, *a):
+            kv.set_current(HERE)
+
+    def empty(*shape, dtype, device):
+        t = torch.zeros(*shape, dtype=dtype, device=device).as_subclass(_Kept)
+        made.append((t, K._raw_stream(None)))
+        return t
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch, "empty", empty)
+    b, q, k = _batch(), _t(2, 4, 128), _t(2, 2, 128)
+    for stream, raw in ((None, HERE), (kv.stream_of(HERE), HERE), (kv.stream_of(OTHER), OTHER)):
+        outs = [kv.append(0, b, k, k, q=q, stream=stream), *kv.decode_attn(0, b, q, lse=True, stream=stream),
+                *kv.prefill_attn(0, b, q, lse=True, stream=stream)]
+        assert [t.data_ptr() for t in outs] == [t.data_ptr() for t, _ in made]
+        assert all(on == raw for _, on in made)
+        if raw == OTHER:
+            assert all(HERE in _kept(t) for t in outs)     # and kept for the caller's stream, which will read them
+        made.clear()
