@@ -123,6 +123,9 @@ mk::PagedLayer layer_of(mk_paged* h, int layer) {
   return L;
 }
 
+// An array of 4-byte words, or none.
+bool words_ok(const void* p) { return ((uintptr_t)p & 3) == 0; }
+
 // Arguments every call has.
 mk_status check_call(const mk_paged* h, int32_t layer, const mk_paged_batch* b) {
   if (!h || !b) return MK_EINVAL;
@@ -130,6 +133,7 @@ mk_status check_call(const mk_paged* h, int32_t layer, const mk_paged_batch* b) 
   if (b->n_seqs < 0 || b->n_seqs > h->cfg.max_seqs || b->n_tokens < 0 || b->max_new < 1) return MK_EINVAL;
   if (b->n_seqs == 0 || b->n_tokens == 0) return MK_OK;  // nothing to do, nothing read
   if (!b->kv_len || !b->page_table || b->table_stride < 1) return MK_EINVAL;
+  if (!words_ok(b->kv_len) || !words_ok(b->page_table) || !words_ok(b->cu_new)) return MK_EINVAL;
   if ((int64_t)b->table_stride * h->cfg.page > 0x7fffff00) return MK_EINVAL;  // token numbers and a step past them
   if (!b->cu_new && (b->max_new != 1 || b->n_tokens < b->n_seqs)) return MK_EINVAL;
   return MK_OK;
@@ -139,12 +143,13 @@ bool rows_ok(const void* p, int64_t stride, int64_t heads) {
 }
 
 mk_status check_attn(const mk_paged* h, int32_t layer, const mk_paged_batch* b, const void* q, int64_t q_stride,
-                     float scale, const void* out, int64_t out_stride) {
+                     float scale, const void* out, int64_t out_stride, const float* lse) {
   mk_status st = check_call(h, layer, b);
   if (st != MK_OK) return st;
   if (!std::isfinite(scale)) return MK_EINVAL;
   if (b->n_seqs == 0 || b->n_tokens == 0) return MK_OK;
   if (!rows_ok(q, q_stride, h->cfg.n_q_heads) || !rows_ok(out, out_stride, h->cfg.n_q_heads)) return MK_EINVAL;
+  if (!words_ok(lse)) return MK_EINVAL;
   return MK_OK;
 }
 
@@ -169,7 +174,7 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
   if (((uintptr_t)k_pool | (uintptr_t)v_pool | (uintptr_t)workspace) % kAlign) return MK_EINVAL;
   const bool e4m3 = cfg->kv_type == MK_KV_E4M3;
   if (e4m3 != (k_scale != nullptr) || e4m3 != (v_scale != nullptr)) return MK_EINVAL;
-  if (((uintptr_t)k_scale | (uintptr_t)v_scale) & 3) return MK_EINVAL;
+  if (!words_ok(k_scale) || !words_ok(v_scale)) return MK_EINVAL;
   size_t need = 0;
   (void)mk_paged_sizes(cfg, nullptr, nullptr, &need);
   if (workspace_bytes < need) return MK_ENOMEM;
@@ -219,7 +224,8 @@ mk_status mk_paged_append(mk_paged* h, int32_t layer, const mk_paged_batch* batc
   mk_rope r{};
   if (rope) r = *rope;
   if (r.rot_dim < 0 || r.rot_dim > MK_HEAD_DIM || r.rot_dim % 16) return MK_EINVAL;
-  if (r.rot_dim && (!r.cos_sin || ((uintptr_t)r.cos_sin & 15) || r.n_pos < 1)) return MK_EINVAL;
+  if (r.rot_dim && (!r.cos_sin || ((uintptr_t)r.cos_sin & 15) || r.n_pos < 1 || !words_ok(r.positions)))
+    return MK_EINVAL;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return MK_OK;
   if (!rows_ok(k, k_stride, h->cfg.n_kv_heads) || !rows_ok(v, v_stride, h->cfg.n_kv_heads)) return MK_EINVAL;
   if ((q == nullptr) != (q_out == nullptr)) return MK_EINVAL;
@@ -235,7 +241,7 @@ mk_status mk_paged_append(mk_paged* h, int32_t layer, const mk_paged_batch* batc
 
 mk_status mk_paged_decode_attn(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const void* q, int64_t q_stride,
                                float scale, void* out, int64_t out_stride, float* lse, mk_stream stream) {
-  mk_status st = check_attn(h, layer, batch, q, q_stride, scale, out, out_stride);
+  mk_status st = check_attn(h, layer, batch, q, q_stride, scale, out, out_stride, lse);
   if (st != MK_OK) return st;
   if (batch->max_new != 1) return MK_EINVAL;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return MK_OK;
@@ -251,7 +257,7 @@ mk_status mk_paged_decode_attn(mk_paged* h, int32_t layer, const mk_paged_batch*
 mk_status mk_paged_prefill_attn(mk_paged* h, int32_t layer, const mk_paged_batch* batch, int32_t causal, const void* q,
                                 int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
                                 mk_stream stream) {
-  mk_status st = check_attn(h, layer, batch, q, q_stride, scale, out, out_stride);
+  mk_status st = check_attn(h, layer, batch, q, q_stride, scale, out, out_stride, lse);
   if (st != MK_OK) return st;
   if (causal != 0 && causal != 1) return MK_EINVAL;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return MK_OK;

@@ -487,7 +487,8 @@ typedef struct mk_paged_config {
 } mk_paged_config;
 
 /* The sequences of a call.  One batch serves every layer and call of a step.
- * The arrays are device memory, read when the kernels run. */
+ * The arrays are device memory (4-byte aligned, as are positions, scales and
+ * lse: MK_EINVAL otherwise), read when the kernels run. */
 typedef struct mk_paged_batch {
   int32_t n_seqs;            /* 0..max_seqs */
   int32_t n_tokens;          /* rows of k, v, q and out in the call */

@@ -275,3 +275,40 @@ def test_new_outputs_for_another_stream_do_not_reuse_what_this_one_still_reads()
     assert torch.equal(out, want)
     torch.cuda.current_stream().wait_stream(s)
     assert bool((copy == 3.0).all()) and made.c.poll_error() == (0, 0)
+
+
+# ---- refusals --------------------------------------------------------------------------------------------------------
+
+def test_word_arrays_off_their_alignment_are_refused_before_any_launch():
+    made = Made("e4m3", 16, 2, 2, [50, 33], 6)
+    c, lib = made.c, K.load()
+    q = torch.randn(2, 4, 128, generator=_gen(3), device=DEV).to(torch.bfloat16)
+    out, cu, lse = torch.full_like(q, 5.0), _i32([0, 1, 2]), torch.full((2, 4), 5.0, device=DEV)
+    table = K.rope_table(64, 128)
+    pos = _i32([1, 2])
+    before = [c.k_pool.view(torch.uint8).clone(), c.k_scale.nan_to_num(-1.0)]
+
+    def batch(*off):
+        return K.MkPagedBatch(2, 2, 1, made.table.shape[1], cu.data_ptr() + off[0], made.kv_len.data_ptr() + off[1],
+                              made.table.data_ptr() + off[2])
+
+    def append(b, at=0):
+        r = K.MkRope(table.data_ptr(), 64, 128, 0, pos.data_ptr() + at)
+        return lib.mk_paged_append(c.h, 0, ref(b), ref(r), p, 512, p, 512, None, 0, None, 0, st)
+
+    def decode(b, at=0):
+        return lib.mk_paged_decode_attn(c.h, 0, ref(b), p, 512, 0.1, out.data_ptr(), 512, lse.data_ptr() + at, st)
+
+    def prefill(b, at=0):
+        return lib.mk_paged_prefill_attn(c.h, 0, ref(b), 1, p, 512, 0.1, out.data_ptr(), 512, lse.data_ptr() + at, st)
+
+    ref, p, st = K.ctypes.byref, q.data_ptr(), K._raw_stream(c.device.index)
+    for call in (append, decode, prefill):
+        for by in (1, 2, 3):
+            for i in range(3):
+                assert call(batch(*(by if j == i else 0 for j in range(3)))) == 1
+            assert call(batch(0, 0, 0), by) == 1               # positions, or lse
+    assert c.poll_error() == (0, 0)
+    assert torch.equal(c.k_pool.view(torch.uint8), before[0]) and torch.equal(c.k_scale.nan_to_num(-1.0), before[1])
+    assert bool((out == 5).all()) and bool((lse == 5).all())
+    assert [call(batch(0, 0, 0)) for call in (append, decode, prefill)] == [0, 0, 0] and c.poll_error() == (0, 0)
