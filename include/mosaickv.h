@@ -534,6 +534,11 @@ mk_status mk_paged_destroy(mk_paged* h);
  * new tokens raise the scale of a page that holds older ones, those codes are
  * rewritten as code * old / new, rounded again where that is subnormal.  A
  * page whose slot 0 is written by the call starts afresh, whatever it held.
+ * Tokens may be taken back (drafts that are rejected) by giving the next call
+ * a smaller kv_len; their slots are written over.  A page that keeps earlier
+ * tokens then keeps its scale too, also where only a token taken back had
+ * called for it: its codes, and the next ones, stay as coarse as that made
+ * them until slot 0 is written again.
  * A page that the call writes may be in one row and place of the table only.
  * Errors: MK_EINVAL (null or misaligned pointers, strides, sizes); on the
  * device, for a bad offset, length, page id or position: that sequence or

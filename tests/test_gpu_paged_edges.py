@@ -9,7 +9,7 @@ import torch
 from compressed_kv_cache_vector_gb300 import binding as K
 from compressed_kv_cache_vector_gb300.build import build
 from oracle import paged_oracle as O
-from tests.test_gpu_paged import DEV, KV, Made, _gen, _i32
+from tests.test_gpu_paged import DEV, KV, Made, _append_oracle, _check_attention, _gen, _i32
 
 pytestmark = pytest.mark.gpu
 
@@ -312,3 +312,62 @@ def test_word_arrays_off_their_alignment_are_refused_before_any_launch():
     assert torch.equal(c.k_pool.view(torch.uint8), before[0]) and torch.equal(c.k_scale.nan_to_num(-1.0), before[1])
     assert bool((out == 5).all()) and bool((lse == 5).all())
     assert [call(batch(0, 0, 0)) for call in (append, decode, prefill)] == [0, 0, 0] and c.poll_error() == (0, 0)
+
+
+# ---- lengths that go back --------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_rejected_drafts_are_written_over_and_leave_the_scale_of_a_page_that_goes_on(kv):
+    """Prompts, drafts of six tokens with much larger values, all but one or none of them taken back: inside a page,
+    to a page's border, and from a new page back into the one before."""
+    P, n_kv, G = 16, 2, 2
+    kept, drafted, left = [5, 16, 29, 12], 6, [6, 16, 30, 16]       # lengths: before, drafted, after the taking back
+    made = Made(kv, P, n_kv, G, [40] * 4, 8)
+    c, g, want, n = made.c, _gen(9), {"k": {}, "v": {}}, 4
+    have = [0] * n
+
+    def append(news, size):
+        rows, at, cu = sum(news), 0, [0]
+        t = {x: (size * torch.randn(rows, n_kv, 128, generator=g, device=DEV)).to(torch.bfloat16) for x in ("k", "v")}
+        for i, m in enumerate(news):
+            for x in ("k", "v"):
+                if m:
+                    _append_oracle(want[x], kv, P, made.rows[i], have[i], t[x][at:at + m].double())
+            at += m
+            have[i] += m
+            cu.append(at)
+        c.append(0, K.PagedBatch(_i32(have), made.table, _i32(cu), max(news), rows), t["k"], t["v"])
+
+    def check():
+        made.lens = list(have)
+        for x in ("k", "v"):
+            for i in range(n):
+                for j in range(-(-have[i] // P)):
+                    for h in range(n_kv):
+                        codes, s = want[x][made.rows[i][j], h]
+                        held = min(P, have[i] - j * P)
+                        assert torch.equal(getattr(c, x + "_pool")[0, made.rows[i][j], h, :held].double(), codes[:held])
+                        if kv == "e4m3":
+                            assert float(getattr(c, x + "_scale")[0, made.rows[i][j], h]) == s
+        for form, m in (("decode", 1), ("few", 3), ("wide", 12)):
+            q = torch.randn(n * m, n_kv * G, 128, generator=g, device=DEV).to(torch.bfloat16)
+            b = K.PagedBatch(_i32(have), made.table, _i32([m * i for i in range(n + 1)]), m, n * m)
+            out, lse = c.decode_attn(0, b, q, lse=True) if form == "decode" else c.prefill_attn(0, b, q, lse=True)
+            p_round = 2.0 ** -8 if kv == "bf16" and form == "wide" else 2.0 ** -11
+            _check_attention(made, q, out, lse, 128 ** -0.5, [m] * n, True, p_round)
+
+    append(kept, 1.0)
+    scales = {} if kv == "bf16" else {x: getattr(c, x + "_scale").clone() for x in ("k", "v")}
+    append([drafted] * n, 60.0)
+    check()
+    have[:] = left
+    check()
+    if kv == "e4m3":          # the page that holds the last token kept has the scale of the drafts
+        page = made.rows[0][0]
+        assert all(bool((getattr(c, x + "_scale")[0, page] >= 16 * scales[x][0, page]).all()) for x in ("k", "v"))
+    append([1, 3, 3, 1], 1.0)
+    check()
+    if kv == "e4m3":          # a page begun anew has its own
+        for i in (1, 3):
+            assert all(bool((getattr(c, x + "_scale")[0, made.rows[i][1]] <= 2.0 ** -6).all()) for x in ("k", "v"))
+    assert c.poll_error() == (0, 0)
