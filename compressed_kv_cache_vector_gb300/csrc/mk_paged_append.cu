@@ -154,8 +154,12 @@ __global__ void __launch_bounds__(Shape<P>::threads) k_paged_append(PagedLayer L
   __shared__ int s_wsum[kThreads / 32], s_seq, s_idx;
   __shared__ float s_max[kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = tid & 15, rr = tid >> 4;
-  // No early trigger: q_out may be the query of a call whose prologue reads it
-  // before its own wait, and a kernel that triggers early may not write that.
+  // No early trigger, since q_out may be the query of mk_block_select, whose
+  // prologue reads it before its own wait: behind a kernel that triggers early
+  // it could start before this one's stores.  Without a trigger it starts when
+  // this one's CTAs have ended, as behind any other producer of a query; that
+  // their stores are seen before the wait is what the older kernels rest on,
+  // not something that the launch order promises.
   pdl_wait();
   if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;  // one thread's reading for the CTA
 

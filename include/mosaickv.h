@@ -563,6 +563,11 @@ mk_status mk_paged_decode_attn(mk_paged* h, int32_t layer, const mk_paged_batch*
  * verification of drafted tokens, cross attention).  causal = 1: query j of
  * n_new sees the first kv_len - n_new + j + 1 keys (none where that is <= 0:
  * out = 0, lse = -infinity); causal = 0: every query sees all kv_len keys.
+ * Logits, softmax statistics and accumulators are fp32.  The weights that
+ * multiply the values are rounded first: to fp16 for an e4m3 cache (2^-11 of
+ * each), and for a bf16 cache to bf16 (2^-8 of each), except in
+ * mk_paged_decode_attn and here for max_new x n_q_heads / n_kv_heads <= 16,
+ * which keep 16 bits of them.
  * Keys that a query does not see have no influence on it whatever they hold;
  * values must be finite: 256 rows (256 / group query tokens) are worked on
  * together, and a NaN or infinity among the values that the last of them sees
