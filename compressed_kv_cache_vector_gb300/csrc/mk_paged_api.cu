@@ -201,6 +201,8 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
     if (!enc || !pool_map(enc, cfg, k_pool, rows, &h->dec.k) || !pool_map(enc, cfg, v_pool, rows, &h->dec.v))
       e = cudaErrorInvalidValue;
   }
+  // Whatever is queued may still write this memory: its last user's work ends first.
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemset(workspace, 0, (size_t)h->ws_clear);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {

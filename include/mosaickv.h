@@ -515,7 +515,8 @@ typedef struct mk_rope {
 mk_status mk_paged_sizes(const mk_paged_config* cfg, size_t* pool_bytes, size_t* scale_bytes, size_t* workspace_bytes);
 /* Creates a handle over the caller's buffers (pools and workspace 256-byte
  * aligned; scales NULL for bf16) on the current device.  Clears the
- * workspace's counters and synchronises the device once; reads and writes no
+ * workspace's counters between two synchronisations of the device (queued
+ * work may still write memory that it was given before); reads and writes no
  * pool.  The buffers must outlive the handle. */
 mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
                           void* workspace, size_t workspace_bytes, mk_paged** out);

@@ -371,3 +371,24 @@ def test_rejected_drafts_are_written_over_and_leave_the_scale_of_a_page_that_goe
         for i in (1, 3):
             assert all(bool((getattr(c, x + "_scale")[0, made.rows[i][1]] <= 2.0 ** -6).all()) for x in ("k", "v"))
     assert c.poll_error() == (0, 0)
+
+
+# ---- making a cache --------------------------------------------------------------------------------------------------
+
+def test_a_cache_made_over_memory_that_queued_work_still_writes_starts_clean():
+    """The workspace comes from a block that the current stream has freed while its last write is still queued."""
+    cfg = K.make_paged_config(4, 2, 1, 16, 8, 4)
+    size = K.paged_sizes(cfg)[2]
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        K.PagedKV(cfg, DEV).close()        # its blocks are the allocator's now: what follows makes no new one
+        torch.cuda.synchronize()
+        old = torch.empty(size, dtype=torch.uint8, device=DEV)
+        at = old.data_ptr()
+        torch.cuda._sleep(100_000_000)
+        old.fill_(1)
+        del old
+        c = K.PagedKV(cfg, DEV)
+        assert c.workspace.data_ptr() == at
+        assert not bool(c.workspace[:1024].any())                  # error word and counters
+        assert c.poll_error() == (0, 0)
