@@ -283,7 +283,10 @@ mk_status mk_paged_poll_error(mk_paged* h, int32_t* detail) {
   cudaError_t e = dev.ok ? cudaDeviceSynchronize() : cudaErrorInvalidDevice;
   if (e == cudaSuccess) e = cudaMemcpy(w, h->ws, sizeof(w), cudaMemcpyDeviceToHost);
   // Closed, as paged_stopped does it: a replay of the call does no work either.
-  if (e == cudaSuccess && w[0] != 0) e = cudaMemset(h->ws + 4, 0xff, 4);
+  if (e == cudaSuccess && w[0] != 0) {
+    e = cudaMemset(h->ws + 4, 0xff, 4);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  }
   if (e != cudaSuccess) return MK_ECUDA;
   if (detail) *detail = w[2];
   return w[0] == 0 ? MK_OK : (mk_status)w[0];
