@@ -392,3 +392,97 @@ def test_a_cache_made_over_memory_that_queued_work_still_writes_starts_clean():
         assert c.workspace.data_ptr() == at
         assert not bool(c.workspace[:1024].any())                  # error word and counters
         assert c.poll_error() == (0, 0)
+
+
+# ---- the largest batch, many heads, captured prompts -----------------------------------------------------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n_kv,G,n", [(1, 4, 256), (1, 8, 33), (48, 1, 5)])
+def test_full_batches_with_empty_sequences_and_many_heads(kv, n_kv, G, n):
+    """Up to 256 sequences (the most of a call), a third of them without tokens or without new ones; 48 kv heads."""
+    P = 16
+    lens = [0 if i % 5 == 3 else 1 + (i * 37) % 211 for i in range(n)]
+    made = Made(kv, P, n_kv, G, lens, 21)
+    c = made.c
+    assert c.cfg.max_seqs == n
+    for form, top in (("few", 16 // G), ("wide", 23)):
+        news = [0 if i % 7 == 2 else 1 + (i * 13) % top for i in range(n)]
+        cu = [0]
+        for m in news:
+            cu.append(cu[-1] + m)
+        q = torch.randn(cu[-1], n_kv * G, 128, generator=_gen(top), device=DEV).to(torch.bfloat16)
+        out, lse = c.prefill_attn(0, K.PagedBatch(made.kv_len, made.table, _i32(cu), top, cu[-1]), q, lse=True)
+        p_round = 2.0 ** -8 if kv == "bf16" and top * G > 16 else 2.0 ** -11
+        _check_attention(made, q, out, lse, 128 ** -0.5, news, True, p_round)
+    q = torch.randn(n, n_kv * G, 128, generator=_gen(5), device=DEV).to(torch.bfloat16)
+    for call in (c.decode_attn, c.prefill_attn):               # prefill without offsets: one token a sequence
+        out, lse = call(0, K.PagedBatch(made.kv_len, made.table), q, lse=True)
+        _check_attention(made, q, out, lse, 128 ** -0.5, [1] * n, True, 2.0 ** -11)
+    # an append over the whole batch: the last tokens of each sequence, stored as they are
+    news = [min(t, (i * 29) % 40) for i, t in enumerate(lens)]
+    cu = [0]
+    for m in news:
+        cu.append(cu[-1] + m)
+    k, v = (torch.randn(cu[-1], n_kv, 128, generator=_gen(i), device=DEV).to(torch.bfloat16) for i in (1, 2))
+    if kv == "e4m3":          # pages that go on: their codes are at most 448, and a large scale stays as it is
+        c.k_scale.fill_(1.0)
+        c.v_scale.fill_(1.0)
+    c.append(0, K.PagedBatch(made.kv_len, made.table, _i32(cu), 39, cu[-1]), k, v)
+    assert c.poll_error() == (0, 0)
+    for i in range(n):
+        for h in range(0, n_kv, 7):
+            for got, want in zip(made.held(i, h), (k, v)):
+                y = want[cu[i]:cu[i + 1], h].double()
+                got = got[lens[i] - news[i]:]
+                # half a step of e4m3 under scales of at most 1, or exact
+                tol = torch.maximum(2.0 ** -4 * y.abs(), torch.full_like(y, 2.0 ** -10)) if kv == "e4m3" else 0 * y
+                assert bool((got - y).abs().le(tol).all()), (i, h)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_captured_prompt_chunks_with_lengths_that_change(kv):
+    """append and both kernels of prefill_attn in one graph, replayed with other lengths, offsets and tables; the same
+    calls eagerly in between."""
+    P, n_kv, G, n, rows = 32, 2, 4, 3, 90
+    plans = [([40, 25, 25], [40, 70, 25]), ([1, 80, 0], [41, 150, 25]), ([30, 30, 30], [71, 180, 55]), ([0, 1, 2], [71, 181, 57])]
+    ends = plans[-1][1]
+    rope = K.Rope(K.rope_table(256, 128), 128)
+    toks = {x: torch.randn(len(plans), rows, h, 128, generator=_gen(i), device=DEV).to(torch.bfloat16)
+            for i, (x, h) in enumerate((("q", n_kv * G), ("k", n_kv), ("v", n_kv)))}
+    results = []
+    for mode in ("eager", "captured"):
+        made = Made(kv, P, n_kv, G, ends, 4)
+        c = made.c
+        kv_len, cu, few = _i32([0] * n), _i32([0] * (n + 1)), _i32([0, 2, 4, 6])
+        x = {name: torch.zeros_like(t[0]) for name, t in toks.items()}
+        b = K.PagedBatch(kv_len, made.table, cu, 80, rows)
+        b_few = K.PagedBatch(kv_len, made.table, few, 2, rows)
+        qo, out, out_few = (torch.zeros_like(x["q"]) for _ in range(3))
+
+        def step():
+            c.append(0, b, x["k"], x["v"], rope=rope, q=x["q"], q_out=qo)
+            c.prefill_attn(0, b, qo, out=out)
+            c.prefill_attn(0, b_few, qo, out=out_few)
+
+        if mode == "captured":
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        for t, (news, lens) in enumerate(plans):
+            kv_len.copy_(_i32(lens))
+            cu.copy_(_i32([0, news[0], news[0] + news[1], sum(news)]))
+            for name in toks:
+                x[name].copy_(toks[name][t])
+            out.zero_()
+            out_few.zero_()
+            graph.replay() if mode == "captured" else step()
+            assert c.poll_error() == (0, 0)
+            results.append((mode, t, qo.clone(), out.clone(), out_few.clone()))
+            if mode == "eager":
+                made.lens = lens
+                _check_attention(made, qo, out, None, 128 ** -0.5, news, True, 2.0 ** -8 if kv == "bf16" else 2.0 ** -11)
+                _check_attention(made, qo, out_few, None, 128 ** -0.5, [2, 2, 2], True, 2.0 ** -11)
+                assert not bool(out[sum(news):].any()) and not bool(out_few[6:].any())
+    for a, b in zip(results[: len(plans)], results[len(plans):]):
+        assert all(torch.equal(p.view(torch.int16), q.view(torch.int16)) for p, q in zip(a[2:], b[2:])), (a[1])
