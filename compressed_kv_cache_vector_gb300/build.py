@@ -17,7 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmosaickv.so")
-# The checked build: every kernel's bounds checks compiled in (MK_CHECKS=1);
+# The checked build: the compressed cache's bounds checks compiled in (MK_CHECKS=1);
 # a failed check sets the error word and skips the access.  For the tests.
 LIB_CHECKS = os.path.join(PKG, "libmosaickv_checks.so")
 BUILD_CHECKS = os.path.join(PKG, "_build_checks")

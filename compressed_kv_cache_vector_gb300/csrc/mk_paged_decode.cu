@@ -34,9 +34,9 @@
 //  * A unit that lies in several CTAs is joined by the last of them to arrive
 //    (counter, no waiting), in the order of the parts: the same result in
 //    every run.
-// Measured (GB300, 32 query heads over 8): 1M tokens e4m3 331 us (6.5 TB/s,
-// 96% of the copy rate), 128K 57 us (4.7 TB/s: about 15 us are launch, ramp and
-// joining), 4K 12 us, 64 ragged sequences 204 us (5.3 TB/s), 4 x 32K bf16 92 us
+// Measured (GB300, 32 query heads over 8): 1M tokens e4m3 330 us (6.5 TB/s,
+// 96% of the copy rate), 128K 56 us (4.7 TB/s: about 15 us are launch, ramp and
+// joining), 4K 12 us, 64 ragged sequences 206 us (5.3 TB/s), 4 x 32K bf16 93 us
 // (5.8 TB/s).  Reads its algorithmic bytes once (268.9 MB of DRAM reads at 128K).
 #include "mk_paged.cuh"
 
@@ -724,7 +724,8 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
   // 12 warps of two 8 KB stages: the conversion of a chunk takes a warp about
   // 3 000 clocks, so eight were bound by it (64 ragged sequences 228 us, 12
   // warps 203); 16 with one stage wait for their copies (221).  Eight heads'
-  // joining buffer (10 x 4 KB) leaves room for ten.
+  // joining buffer (10 x 4 KB) leaves room for ten: the same batch with 64 query
+  // heads 250 us, 344 in bf16 (32 heads: 206, 334).
   if (L.G == 8) return L.e4m3 ? launch<true, 10, 2>(L, maps, a, s) : launch<false, 10, 2>(L, maps, a, s);
   return L.e4m3 ? launch<true, 12, 2>(L, maps, a, s) : launch<false, 12, 2>(L, maps, a, s);
 }

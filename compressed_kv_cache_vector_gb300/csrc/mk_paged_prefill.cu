@@ -31,10 +31,11 @@
 //    causal masks and a few rows against a long context load the SMs alike.  A
 //    row tile that lies in several runs is joined by the last CTA of it to
 //    arrive, in the order of the parts.
-// Measured (GB300, 32 query heads over 8): an 8K prompt e4m3 618 us, 890
-// TFLOP/s of the visible pairs (46% of cuBLAS's burst); six ragged chunks bf16
-// 110 us, 590 TFLOP/s; 16 x 5 tokens against 2K-16K 140 us; cross attention of
-// 8 x 40-300 queries 45 us.  A step of 128 keys for both tiles takes 2.2-2.4
+// Measured (GB300, 32 query heads over 8): an 8K prompt e4m3 615 us, 895
+// TFLOP/s of the visible pairs (47% of cuBLAS's burst), bf16 512; six ragged
+// chunks bf16 108 us, 600 TFLOP/s; 16 x 5 tokens against 2K-16K 140 us; cross
+// attention of 8 x 40-300 queries 45 us.  Equal runs cost whole prompts some
+// 4% (592 us e4m3 in whole items) and halve the few-row cases.  A step of 128 keys for both tiles takes 2.2-2.4
 // us where its products alone would take 1.1: the tensor cores are busy 38% of
 // the time, XU 19%.  The rest is the latency of the chain products -> logits
 // read -> maximum -> exponentials -> weights written -> products, with one

@@ -462,14 +462,18 @@ mk_status mk_swap_segment(mk_ctx* ctx, int32_t layer, int32_t seq, int32_t kv_he
  * The calls follow the conventions above (host checks first, a sticky device
  * error word read with mk_paged_poll_error, one host thread and one device
  * order per handle: calls that may overlap on the GPU need handles with
- * workspaces of their own).  A call that finds the error word set by an
- * earlier one does nothing.  What a call itself finds bad (MK_EDEVICE) leaves
- * its other sequences and pages complete; a captured call that is replayed
- * with no other call of the handle and no mk_paged_poll_error since works on
- * them again.  MK_ETIMEOUT leaves everything the call writes undefined.  They run on the device that was current at
+ * workspaces of their own).  They run on the device that was current at
  * mk_paged_create, whichever is current at the call.  Lengths, new-token
  * offsets and page tables are read on the device, so a captured CUDA graph
- * may be replayed with new ones. */
+ * may be replayed with new ones.  The attention calls trigger early: `out` may
+ * be the query of mk_block_select, which reads it before its wait, only with
+ * another kernel between them.
+ *
+ * A call that finds the error word set by an earlier one does nothing.  What a
+ * call itself finds bad (MK_EDEVICE) leaves its other sequences and pages
+ * complete; a captured call that is replayed with no other call of the handle
+ * and no mk_paged_poll_error since works on them again.  MK_ETIMEOUT leaves
+ * everything that the call writes undefined. */
 #define MK_KV_BF16 0
 #define MK_KV_E4M3 1
 
