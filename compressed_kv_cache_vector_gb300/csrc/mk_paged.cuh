@@ -83,6 +83,29 @@ __device__ __forceinline__ bool paged_wait_warp(uint64_t* bar, unsigned parity) 
   return __all_sync(FULL, paged_wait(bar, parity)) != 0;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two e4m3 codes (low 16 bits) as two halves.
+__device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
+  uint32_t r;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(two));
+  return r;
+}
+// Two numbers rounded to fp16 (F16) or bf16, the first in the low half.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if (F16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Sequence i of a batch: its first row, new tokens and length.  ok is false
 // (and the error word set by the callers) when they contradict the batch.
 struct PagedSeq {

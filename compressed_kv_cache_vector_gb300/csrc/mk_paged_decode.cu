@@ -45,7 +45,6 @@ namespace mk {
 namespace {
 
 constexpr int kStageBytes = 8192;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct DecodeArgs {
   mk_paged_batch b;
@@ -61,11 +60,6 @@ struct DecodeArgs {
   int32_t* counters;    // [max_seqs][n_kv]
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -94,22 +88,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Two e4m3 codes (low 16 bits) as two halves.
-__device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
-  uint32_t r;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(two));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -373,8 +351,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
         zf[i] *= __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
-          qa[i][s] = pack_h2(bf2f(w[s].x & 0xffff) * down, bf2f(w[s].x >> 16) * down);
-          qb[i][s] = pack_h2(bf2f(w[s].y & 0xffff) * down, bf2f(w[s].y >> 16) * down);
+          qa[i][s] = pack2<true>(bf2f(w[s].x & 0xffff) * down, bf2f(w[s].x >> 16) * down);
+          qb[i][s] = pack2<true>(bf2f(w[s].y & 0xffff) * down, bf2f(w[s].y >> 16) * down);
         }
       } else {
 #pragma unroll
@@ -518,8 +496,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
             uint32_t p0[C], p1[C];
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-              p0[i] = pack_h2(z[i][2 * t][0], z[i][2 * t][1]);
-              p1[i] = pack_h2(z[i][2 * t + 1][0], z[i][2 * t + 1][1]);
+              p0[i] = pack2<true>(z[i][2 * t][0], z[i][2 * t][1]);
+              p1[i] = pack2<true>(z[i][2 * t + 1][0], z[i][2 * t + 1][1]);
             }
             const uint32_t r0 = vb + (16 * t + 2 * c) * 128;
             const uint32_t x0 = ((uint32_t)g ^ (uint32_t)(2 * c)) << 4, x1 = ((uint32_t)g ^ (uint32_t)(2 * c + 1)) << 4;
@@ -540,10 +518,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
           uint32_t p0[C], p1[C], q0[C], q1[C];
 #pragma unroll
           for (int i = 0; i < C; ++i) {
-            p0[i] = pack_b2(z[i][0][0], z[i][0][1]);
-            p1[i] = pack_b2(z[i][1][0], z[i][1][1]);
-            q0[i] = pack_b2(z[i][0][0] - bf2f(p0[i] & 0xffff), z[i][0][1] - bf2f(p0[i] >> 16));
-            q1[i] = pack_b2(z[i][1][0] - bf2f(p1[i] & 0xffff), z[i][1][1] - bf2f(p1[i] >> 16));
+            p0[i] = pack2<false>(z[i][0][0], z[i][0][1]);
+            p1[i] = pack2<false>(z[i][1][0], z[i][1][1]);
+            q0[i] = pack2<false>(z[i][0][0] - bf2f(p0[i] & 0xffff), z[i][0][1] - bf2f(p0[i] >> 16));
+            q1[i] = pack2<false>(z[i][1][0] - bf2f(p1[i] & 0xffff), z[i][1][1] - bf2f(p1[i] >> 16));
           }
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
@@ -613,7 +591,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       if (!live_row(r)) return;
       const float f = s_L[r] > 0.0f || s_L[r] != s_L[r] ? 1.0f / s_L[r] : 0.0f;
       *reinterpret_cast<uint32_t*>(a.out + (int64_t)(row + tok_of(r)) * a.out_stride + head_of(r) * D + 2 * (e & 63)) =
-          pack_b2(x * f, y * f);
+          pack2<false>(x * f, y * f);
     };
     auto put_lse = [&](int r) {
       if (!a.lse || !live_row(r)) return;

@@ -67,7 +67,7 @@ constexpr int kSmem = 1024 + 2 * kTile + 4 * kTile;
 // Logit factors are at least this, so that a hidden key's -infinity stays one
 // (a row of zeros or a scale of 0 would make it NaN).
 constexpr float kTiny = 1.17549435e-38f;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct PrefillArgs {
   mk_paged_batch b;
@@ -82,25 +82,6 @@ struct PrefillArgs {
   int32_t* counters;  // [kPagedMaxCtas]
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
-  uint32_t r;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(two));
-  return r;
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  if (F16)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Descriptor of a 128-byte-swizzled operand: rows of 128 bytes, groups of 8
 // rows 1024 bytes apart.  Along the rows' direction (K-major: Q, K) `lbo` has
 // no use; for an operand whose rows run along the products' K (V), it is the
