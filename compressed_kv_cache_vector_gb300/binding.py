@@ -80,6 +80,10 @@ class MkRope(ctypes.Structure):
     _fields_ = [("cos_sin", c_vp), ("n_pos", c_i32), ("rot_dim", c_i32), ("interleaved", c_i32), ("positions", c_vp)]
 
 
+class MkPagedPrefix(ctypes.Structure):
+    _fields_ = [("n_groups", c_i32), ("cu_group", c_vp), ("prefix_len", c_vp)]
+
+
 _SIGS = {
     "mk_arena_bytes": [ctypes.POINTER(MkConfig), ctypes.POINTER(c_size)],
     "mk_workspace_bytes": [ctypes.POINTER(MkConfig), ctypes.POINTER(c_size)],
@@ -120,6 +124,14 @@ _SIGS.update({
     "mk_paged_append": [c_vp, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp],
     "mk_paged_decode_attn": [c_vp, c_i32, c_vp, c_vp, c_i64, ctypes.c_float, c_vp, c_i64, c_vp, c_vp],
     "mk_paged_prefill_attn": [c_vp, c_i32, c_vp, c_i32, c_vp, c_i64, ctypes.c_float, c_vp, c_i64, c_vp, c_vp],
+    "mk_paged_prefix_attn": [c_vp, c_i32, ctypes.POINTER(MkPagedBatch), ctypes.POINTER(MkPagedPrefix), c_vp, c_i64,
+                             ctypes.c_float, c_vp, c_i64, c_vp, c_vp],
+    "mk_paged_mass_sizes": [ctypes.POINTER(MkPagedConfig), ctypes.POINTER(c_size), ctypes.POINTER(c_size)],
+    "mk_paged_decode_attn_mass": [c_vp, c_i32, ctypes.POINTER(MkPagedBatch), c_vp, c_i64, ctypes.c_float, c_vp, c_i64, c_vp,
+                                  c_vp, c_i32, c_vp, c_size, c_vp],
+    "mk_paged_prefill_mass": [c_vp, c_i32, ctypes.POINTER(MkPagedBatch), c_i32, c_vp, c_i64, ctypes.c_float, c_vp, c_vp,
+                              c_i32, c_i32, c_vp],
+    "mk_paged_evict": [c_vp, c_i32, ctypes.POINTER(MkPagedBatch), c_vp, c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp],
     "mk_paged_poll_error": [c_vp, ctypes.POINTER(c_i32)],
     "mk_paged_clear_error": [c_vp],
 })
@@ -417,6 +429,37 @@ class PagedBatch:
         self.ref = ctypes.byref(self.c)
 
 
+class PagedPrefix:
+    """Which sequences of a batch share their first tokens: cu_group int32 [groups + 1] (group g: the sequences
+    cu_group[g] .. cu_group[g + 1] - 1), prefix_len int32 [groups].  Read when the kernels run, like a batch."""
+
+    def __init__(self, cu_group, prefix_len):
+        _dev_i32(prefix_len, "prefix_len")
+        _dev_i32(cu_group, "cu_group", prefix_len.device)
+        n = prefix_len.numel()
+        _need(cu_group.numel() == n + 1, "cu_group must be [groups + 1]")
+        self.cu_group, self.prefix_len, self.device = cu_group, prefix_len, prefix_len.device
+        self.c = MkPagedPrefix(n, cu_group.data_ptr() if n else None, prefix_len.data_ptr() if n else None)
+        self.ref = ctypes.byref(self.c)
+
+
+class PagedMass:
+    """The attention mass of a cache's tokens (fp32 [n_layers, n_pages, n_kv_heads, page], zeros unless given) and the
+    scratch of decode_attn_mass (one layer's logits)."""
+
+    def __init__(self, cache, mass=None):
+        c = cache.cfg
+        shape = (c.n_layers, c.n_pages, c.n_kv_heads, c.page)
+        if mass is None:
+            mass = torch.zeros(shape, dtype=torch.float32, device=cache.device)
+        _need(tuple(mass.shape) == shape and mass.dtype == torch.float32 and mass.is_contiguous()
+              and mass.device == cache.device, f"mass must be a contiguous fp32 tensor of shape {shape} on {cache.device}")
+        need = c_size()
+        _check("mk_paged_mass_sizes", cache.lib.mk_paged_mass_sizes(ctypes.byref(c), None, ctypes.byref(need)))
+        self.mass, self.shape, self.device, self.scratch_bytes = mass, shape, mass.device, need.value
+        self.scratch = torch.empty(need.value, dtype=torch.uint8, device=cache.device)
+
+
 class PagedKV:
     """A paged KV cache (all layers) on one GPU: pools [n_layers, n_pages, n_kv_heads, page, 128] in bf16 or e4m3,
     for e4m3 scales [n_layers, n_pages, n_kv_heads] fp32.  The pools are allocated here unless given."""
@@ -533,7 +576,7 @@ class PagedKV:
             raise MosaicKVError("mk_paged_append", st)
         return q_out
 
-    def _attn(self, batch, q, scale, out, lse, stream):
+    def _attn(self, batch, q, scale, out, lse, stream, *more):
         _need(batch.device == self.device, "the batch is on another device")
         qs = self._rows(q, "q", batch, self.cfg.n_q_heads)
         if out is None:
@@ -545,7 +588,7 @@ class PagedKV:
             _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == self.device
                   and lse.numel() >= batch.n_tokens * self.cfg.n_q_heads, "lse must be contiguous fp32 [n_tokens, n_q_heads]")
         return (q.data_ptr(), qs, MK_HEAD_DIM ** -0.5 if scale is None else scale, out.data_ptr(), os_,
-                lse.data_ptr() if lse is not None else None, self._stream(stream, batch, None, q, out, lse)), out, lse
+                lse.data_ptr() if lse is not None else None, self._stream(stream, batch, None, q, out, lse, *more)), out, lse
 
     def decode_attn(self, layer, batch, q, scale=None, out=None, lse=None, stream=None):
         """Attention of one query token per sequence (bf16 [n_tokens, n_q_heads, 128]); scale: default 1/sqrt(128).
@@ -563,6 +606,70 @@ class PagedKV:
         if st:
             raise MosaicKVError("mk_paged_prefill_attn", st)
         return out if lse is None else (out, lse)
+
+    def prefix_attn(self, layer, batch, prefix, q, scale=None, out=None, lse=None, stream=None):
+        """decode_attn for sequences that share prefixes (a PagedPrefix): shared pages are read once for their group."""
+        _need(prefix.device == self.device, "the prefix is on another device")
+        args, out, lse = self._attn(batch, q, scale, out, lse, stream, prefix.cu_group, prefix.prefix_len)
+        st = self.lib.mk_paged_prefix_attn(self.h, layer, batch.ref, prefix.ref, *args)
+        if st:
+            raise MosaicKVError("mk_paged_prefix_attn", st)
+        return out if lse is None else (out, lse)
+
+    def _mass(self, mass):
+        c = self.cfg
+        _need(mass.shape == (c.n_layers, c.n_pages, c.n_kv_heads, c.page) and mass.device == self.device,
+              "the mass is of another cache's shape or device")
+
+    def decode_attn_mass(self, layer, batch, q, mass, first=0, scale=None, out=None, lse=None, stream=None):
+        """decode_attn that also adds every weight to its token's mass (a PagedMass), from token number `first` on; the
+        new token's mass is set."""
+        self._mass(mass)
+        args, out, lse = self._attn(batch, q, scale, out, lse, stream, mass.mass, mass.scratch)
+        st = self.lib.mk_paged_decode_attn_mass(self.h, layer, batch.ref, *args[:-1], mass.mass.data_ptr(), first,
+                                                mass.scratch.data_ptr(), mass.scratch_bytes, args[-1])
+        if st:
+            raise MosaicKVError("mk_paged_decode_attn_mass", st)
+        return out if lse is None else (out, lse)
+
+    def prefill_mass(self, layer, batch, q, lse, mass, causal=True, first=0, add=True, scale=None, stream=None):
+        """The mass that the batch's queries give, from prefill_attn's q and lse: added to that of the tokens held
+        before the new ones (add=False: it begins anew), from token number `first` on."""
+        _need(batch.device == self.device, "the batch is on another device")
+        self._mass(mass)
+        qs = self._rows(q, "q", batch, self.cfg.n_q_heads)
+        _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == self.device
+              and lse.numel() >= batch.n_tokens * self.cfg.n_q_heads, "lse must be contiguous fp32 [n_tokens, n_q_heads]")
+        st = self.lib.mk_paged_prefill_mass(
+            self.h, layer, batch.ref, int(bool(causal)), q.data_ptr(), qs, MK_HEAD_DIM ** -0.5 if scale is None else scale,
+            lse.data_ptr(), mass.mass.data_ptr(), first, int(bool(add)), self._stream(stream, batch, None, q, lse, mass.mass))
+        if st:
+            raise MosaicKVError("mk_paged_prefill_mass", st)
+
+    def evict(self, layer, batch, mass, keep, first=0, recent=0, kept=None, new_len=None, max_keep=None, stream=None):
+        """Cuts each sequence to keep[i] tokens (int32 on the GPU): the first `first`, the last `recent` and the heaviest
+        between, moved to the front of its pages.  Returns (new_len int32 [n], kept int32 [n, n_kv_heads, columns]: the
+        tokens' numbers from before).  kept is made with max_keep columns (default: what the page table holds)."""
+        _need(batch.device == self.device, "the batch is on another device")
+        self._mass(mass)
+        _dev_i32(keep, "keep", self.device)
+        _need(keep.numel() >= batch.n_seqs, "keep must name a count for every sequence")
+        heads = self.cfg.n_kv_heads
+        if kept is None:
+            columns = batch.page_table.shape[1] * self.cfg.page if max_keep is None else max_keep
+            kept = self._new((batch.n_seqs, heads, columns), torch.int32, stream)
+        if new_len is None:
+            new_len = self._new((batch.n_seqs,), torch.int32, stream)
+        _dev_i32(kept, "kept", self.device)
+        _dev_i32(new_len, "new_len", self.device)
+        _need(kept.dim() == 3 and kept.shape[0] >= batch.n_seqs and kept.shape[1] == heads and new_len.numel() >= batch.n_seqs,
+              "kept must be [n_seqs, n_kv_heads, columns], new_len [n_seqs]")
+        st = self.lib.mk_paged_evict(
+            self.h, layer, batch.ref, mass.mass.data_ptr(), keep.data_ptr(), first, recent, kept.data_ptr(), kept.shape[2],
+            new_len.data_ptr(), self._stream(stream, batch, None, mass.mass, keep, kept, new_len))
+        if st:
+            raise MosaicKVError("mk_paged_evict", st)
+        return new_len, kept
 
     def poll_error(self):
         d = c_i32()

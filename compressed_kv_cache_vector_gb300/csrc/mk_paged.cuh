@@ -43,6 +43,14 @@ struct PagedScratch {
   int32_t* counters;          // [max_seqs][n_kv], zero between calls
   int32_t* prefill_counters;  // [kPagedMaxCtas], zero between calls
   float* prefill_part;        // paged_prefill_part_floats()
+  float* lse2;                // [max_seqs][n_q_heads]: a decode step's sums, as base-2 logarithms
+};
+// The workspace's parts that eviction uses.
+struct PagedEvictScratch {
+  int32_t* ticket;
+  int32_t* plan;    // [max_seqs][2]
+  int32_t* rank0;   // [n_pages][n_kv]
+  int32_t* flag;    // [n_pages][n_kv]
 };
 int64_t paged_prefill_part_floats();
 
@@ -95,6 +103,25 @@ __device__ __forceinline__ uint32_t e4m3_h2(uint32_t two) {
   asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(r) : "r"(two));
   return r;
 }
+// Eight e4m3 codes of y * inv (infinities saturate to +-448, NaN stays NaN).
+__device__ __forceinline__ uint2 pack_e4m3(const float (&y)[8], float inv) {
+  uint32_t o[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e] * inv, y[4 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi =
+        __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e + 2] * inv, y[4 * e + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    o[e] = lo | (hi << 16);
+  }
+  return make_uint2(o[0], o[1]);
+}
+// Smallest 2^e, e >= -64, with amax <= 448 * 2^e (448 = 1.75 * 2^8).
+__device__ __forceinline__ float scale_of(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  if (b < 0x800000u || e < -64) e = -64;
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
 // Two numbers rounded to fp16 (F16) or bf16, the first in the low half.
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -129,6 +156,20 @@ cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, co
 cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
                                 float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s);
+// With mass: the plain logits of layer pages go to scratch ([n_pages][n_kv][G]
+// [P] fp32) and the rows' sums to w.lse2; launch_paged_mass_fold adds their
+// weights to the mass.
+cudaError_t launch_paged_decode_mass(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                     const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
+                                     uint16_t* out, int64_t out_stride, float* lse, float* logits, cudaStream_t s);
+cudaError_t launch_paged_mass_fold(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b,
+                                   const float* logits, float* mass, int32_t first, cudaStream_t s);
+cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, bool causal,
+                                      const uint16_t* q, int64_t q_stride, float scale, const float* lse, float* mass,
+                                      int32_t first, bool add, cudaStream_t s);
+cudaError_t launch_paged_evict(const PagedLayer& L, const PagedEvictScratch& w, const mk_paged_batch& b, float* mass,
+                               const int32_t* keep, int32_t first, int32_t recent, int32_t* kept, int32_t kept_stride,
+                               int32_t* new_len, cudaStream_t s);
 cudaError_t launch_paged_prefill(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, bool causal,
                                  const uint16_t* q, int64_t q_stride, float scale, uint16_t* out, int64_t out_stride,
                                  float* lse, cudaStream_t s);

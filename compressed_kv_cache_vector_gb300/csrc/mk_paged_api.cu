@@ -16,6 +16,7 @@ struct mk_paged {
   int64_t pool_layer, scale_layer;
   mk::PagedMaps dec;        // boxes of the decode kernel
   mk::PagedScratch scratch;
+  mk::PagedEvictScratch evict;
   uint32_t call;            // calls so far, kPagedClosed left out
   int device;
 };
@@ -44,6 +45,10 @@ inline int64_t pool_layer_bytes(const mk_paged_config* c) {
 inline int64_t scale_layer_count(const mk_paged_config* c) {
   return c->kv_type == MK_KV_E4M3 ? (int64_t)c->n_pages * c->n_kv_heads : 0;
 }
+// Attention mass: one word per slot of a layer's pool; the logits of a decode
+// step: one per slot and query head of its kv head.
+inline int64_t mass_layer_count(const mk_paged_config* c) { return (int64_t)c->n_pages * c->n_kv_heads * c->page; }
+inline int64_t logits_bytes(const mk_paged_config* c) { return (int64_t)c->n_pages * c->n_q_heads * c->page * 4; }
 // Workspace: [error word][counters, zero between calls][split-token parts].
 inline int64_t clear_bytes(const mk_paged_config* c) {
   return align_up(kAlign + ((int64_t)c->max_seqs * c->n_kv_heads + mk::kPagedMaxCtas) * 4);
@@ -56,6 +61,10 @@ inline int64_t part_ml_bytes(const mk_paged_config*) {
   return align_up((int64_t)2 * mk::kPagedMaxCtas * 16 * 2 * 4);
 }
 
+inline int64_t lse2_bytes(const mk_paged_config* c) { return align_up((int64_t)c->max_seqs * c->n_q_heads * 4); }
+// Eviction: the counter (a line of its own) and the plan, then two words per page and head.
+inline int64_t plan_bytes(const mk_paged_config* c) { return align_up(kAlign + (int64_t)c->max_seqs * 8); }
+inline int64_t group_words_bytes(const mk_paged_config* c) { return align_up((int64_t)c->n_pages * c->n_kv_heads * 4); }
 inline int64_t prefill_part_bytes() { return align_up(mk::paged_prefill_part_floats() * 4); }
 
 // Rows (query token, query head) of a kv head up to which several query tokens
@@ -162,7 +171,9 @@ mk_status mk_paged_sizes(const mk_paged_config* cfg, size_t* pool_bytes, size_t*
   if (st != MK_OK) return st;
   if (pool_bytes) *pool_bytes = (size_t)(pool_layer_bytes(cfg) * cfg->n_layers);
   if (scale_bytes) *scale_bytes = (size_t)(scale_layer_count(cfg) * cfg->n_layers * 4);
-  if (workspace_bytes) *workspace_bytes = (size_t)(clear_bytes(cfg) + part_acc_bytes(cfg) + part_ml_bytes(cfg) + prefill_part_bytes());
+  if (workspace_bytes)
+    *workspace_bytes = (size_t)(clear_bytes(cfg) + part_acc_bytes(cfg) + part_ml_bytes(cfg) + prefill_part_bytes() +
+                                lse2_bytes(cfg) + plan_bytes(cfg) + 2 * group_words_bytes(cfg));
   return MK_OK;
 }
 
@@ -191,9 +202,21 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
   h->scale_layer = scale_layer_count(cfg);
   h->scratch.counters = reinterpret_cast<int32_t*>(h->ws + kAlign);
   h->scratch.prefill_counters = h->scratch.counters + (int64_t)cfg->max_seqs * cfg->n_kv_heads;
-  h->scratch.part_acc = reinterpret_cast<float*>(h->ws + h->ws_clear);
-  h->scratch.part_ml = reinterpret_cast<float*>(h->ws + h->ws_clear + part_acc_bytes(cfg));
-  h->scratch.prefill_part = reinterpret_cast<float*>(h->ws + h->ws_clear + part_acc_bytes(cfg) + part_ml_bytes(cfg));
+  char* at = h->ws + h->ws_clear;
+  auto take = [&](int64_t bytes) {
+    char* p = at;
+    at += bytes;
+    return p;
+  };
+  h->scratch.part_acc = reinterpret_cast<float*>(take(part_acc_bytes(cfg)));
+  h->scratch.part_ml = reinterpret_cast<float*>(take(part_ml_bytes(cfg)));
+  h->scratch.prefill_part = reinterpret_cast<float*>(take(prefill_part_bytes()));
+  h->scratch.lse2 = reinterpret_cast<float*>(take(lse2_bytes(cfg)));
+  char* plan = take(plan_bytes(cfg));
+  h->evict.ticket = reinterpret_cast<int32_t*>(plan);
+  h->evict.plan = reinterpret_cast<int32_t*>(plan + kAlign);
+  h->evict.rank0 = reinterpret_cast<int32_t*>(take(group_words_bytes(cfg)));
+  h->evict.flag = reinterpret_cast<int32_t*>(take(group_words_bytes(cfg)));
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) {
     const EncodeFn enc = encoder();
@@ -273,6 +296,92 @@ mk_status mk_paged_prefill_attn(mk_paged* h, int32_t layer, const mk_paged_batch
                                                       (cudaStream_t)stream)
                             : mk::launch_paged_prefill(layer_of(h, layer), h->scratch, *batch, causal != 0, qq, q_stride,
                                                        scale, oo, out_stride, lse, (cudaStream_t)stream);
+  return e == cudaSuccess ? MK_OK : MK_ECUDA;
+}
+
+mk_status mk_paged_prefix_attn(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const mk_paged_prefix* prefix,
+                               const void* q, int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
+                               mk_stream stream) {
+  mk_status st = check_attn(h, layer, batch, q, q_stride, scale, out, out_stride, lse);
+  if (st != MK_OK) return st;
+  if (batch->max_new != 1 || !prefix || prefix->n_groups < 0 || prefix->n_groups > batch->n_seqs) return MK_EINVAL;
+  if (prefix->n_groups && (!prefix->cu_group || !prefix->prefix_len)) return MK_EINVAL;
+  if (!words_ok(prefix->cu_group) || !words_ok(prefix->prefix_len)) return MK_EINVAL;
+  if (batch->n_seqs == 0 || batch->n_tokens == 0) return MK_OK;
+  DeviceGuard dev(h->device);
+  if (!dev.ok) return MK_ECUDA;
+  const cudaError_t e =
+      mk::launch_paged_decode(layer_of(h, layer), h->dec, h->scratch, layer, *batch, false, false,
+                              static_cast<const uint16_t*>(q), q_stride, scale, static_cast<uint16_t*>(out), out_stride,
+                              lse, (cudaStream_t)stream);
+  return e == cudaSuccess ? MK_OK : MK_ECUDA;
+}
+
+mk_status mk_paged_mass_sizes(const mk_paged_config* cfg, size_t* mass_bytes, size_t* scratch_bytes) {
+  mk_status st = check(cfg);
+  if (st != MK_OK) return st;
+  if (mass_bytes) *mass_bytes = (size_t)(mass_layer_count(cfg) * cfg->n_layers * 4);
+  if (scratch_bytes) *scratch_bytes = (size_t)logits_bytes(cfg);
+  return MK_OK;
+}
+
+mk_status mk_paged_decode_attn_mass(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const void* q,
+                                    int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
+                                    float* mass, int32_t first, void* scratch, size_t scratch_bytes, mk_stream stream) {
+  mk_status st = check_attn(h, layer, batch, q, q_stride, scale, out, out_stride, lse);
+  if (st != MK_OK) return st;
+  if (batch->max_new != 1 || !mass || !words_ok(mass) || first < 0) return MK_EINVAL;
+  if (!scratch || ((uintptr_t)scratch & 15)) return MK_EINVAL;
+  if (scratch_bytes < (size_t)logits_bytes(&h->cfg)) return MK_ENOMEM;
+  if (batch->n_seqs == 0 || batch->n_tokens == 0) return MK_OK;
+  DeviceGuard dev(h->device);
+  if (!dev.ok) return MK_ECUDA;
+  const mk::PagedLayer L = layer_of(h, layer);
+  float* logits = static_cast<float*>(scratch);
+  cudaError_t e = mk::launch_paged_decode_mass(L, h->dec, h->scratch, layer, *batch, static_cast<const uint16_t*>(q),
+                                               q_stride, scale, static_cast<uint16_t*>(out), out_stride, lse, logits,
+                                               (cudaStream_t)stream);
+  if (e == cudaSuccess)
+    e = mk::launch_paged_mass_fold(L, h->scratch, *batch, logits, mass + layer * mass_layer_count(&h->cfg), first,
+                                   (cudaStream_t)stream);
+  return e == cudaSuccess ? MK_OK : MK_ECUDA;
+}
+
+mk_status mk_paged_prefill_mass(mk_paged* h, int32_t layer, const mk_paged_batch* batch, int32_t causal, const void* q,
+                                int64_t q_stride, float scale, const float* lse, float* mass, int32_t first,
+                                int32_t add, mk_stream stream) {
+  mk_status st = check_call(h, layer, batch);
+  if (st != MK_OK) return st;
+  if (!std::isfinite(scale) || (causal != 0 && causal != 1) || (add != 0 && add != 1) || first < 0) return MK_EINVAL;
+  if (!mass || !words_ok(mass)) return MK_EINVAL;
+  if (batch->n_seqs == 0 || batch->n_tokens == 0) return MK_OK;
+  if (!rows_ok(q, q_stride, h->cfg.n_q_heads) || !lse || !words_ok(lse)) return MK_EINVAL;
+  DeviceGuard dev(h->device);
+  if (!dev.ok) return MK_ECUDA;
+  const cudaError_t e = mk::launch_paged_prefill_mass(
+      layer_of(h, layer), h->scratch, *batch, causal != 0, static_cast<const uint16_t*>(q), q_stride, scale, lse,
+      mass + layer * mass_layer_count(&h->cfg), first, add != 0, (cudaStream_t)stream);
+  return e == cudaSuccess ? MK_OK : MK_ECUDA;
+}
+
+mk_status mk_paged_evict(mk_paged* h, int32_t layer, const mk_paged_batch* batch, float* mass, const int32_t* keep,
+                         int32_t first, int32_t recent, int32_t* kept, int32_t kept_stride, int32_t* new_len,
+                         mk_stream stream) {
+  if (!h || !batch) return MK_EINVAL;
+  if (layer < 0 || layer >= h->cfg.n_layers || batch->n_seqs < 0 || batch->n_seqs > h->cfg.max_seqs) return MK_EINVAL;
+  if (first < 0 || recent < 0 || kept_stride < 0) return MK_EINVAL;
+  if (batch->n_seqs == 0) return MK_OK;
+  if (!batch->kv_len || !batch->page_table || batch->table_stride < 1) return MK_EINVAL;
+  if ((int64_t)batch->table_stride * h->cfg.page > 0x7fffff00) return MK_EINVAL;
+  if (!mass || !keep || !new_len || (kept_stride > 0 && !kept)) return MK_EINVAL;
+  if (!words_ok(batch->kv_len) || !words_ok(batch->page_table) || !words_ok(mass) || !words_ok(keep) ||
+      !words_ok(kept) || !words_ok(new_len) || new_len == batch->kv_len)
+    return MK_EINVAL;
+  DeviceGuard dev(h->device);
+  if (!dev.ok) return MK_ECUDA;
+  const cudaError_t e =
+      mk::launch_paged_evict(layer_of(h, layer), h->evict, *batch, mass + layer * mass_layer_count(&h->cfg), keep, first,
+                             recent, kept, kept_stride, new_len, (cudaStream_t)stream);
   return e == cudaSuccess ? MK_OK : MK_ECUDA;
 }
 

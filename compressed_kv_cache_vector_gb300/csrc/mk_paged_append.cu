@@ -111,18 +111,6 @@ __device__ __forceinline__ uint4 pack_bf16(const float (&y)[8]) {
            ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(y[2 * e + 1])) << 16);
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-// Eight e4m3 codes of y * inv (infinities saturate to +-448, NaN stays NaN).
-__device__ __forceinline__ uint2 pack_e4m3(const float (&y)[8], float inv) {
-  uint32_t o[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e] * inv, y[4 * e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi =
-        __nv_cvt_float2_to_fp8x2(make_float2(y[4 * e + 2] * inv, y[4 * e + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-    o[e] = lo | (hi << 16);
-  }
-  return make_uint2(o[0], o[1]);
-}
 __device__ __forceinline__ void unpack_e4m3(uint2 c, float (&y)[8]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -132,14 +120,6 @@ __device__ __forceinline__ void unpack_e4m3(uint2 c, float (&y)[8]) {
     y[2 * e + 1] = __half2float(__half(__half_raw{h.y}));
   }
 }
-// Smallest 2^e, e >= -64, with amax <= 448 * 2^e (448 = 1.75 * 2^8).
-__device__ __forceinline__ float scale_of(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-  if (b < 0x800000u || e < -64) e = -64;
-  return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-
 __device__ __forceinline__ int clamp_position(const PagedLayer& L, const mk_rope& r, int pos, int seq) {
   if (r.rot_dim && (pos < 0 || pos >= r.n_pos)) {
     paged_error(L, ERR_PAGED_POSITION, seq, pos);

@@ -58,6 +58,8 @@ struct DecodeArgs {
   float* part_acc;      // [2 grid][rows][128]
   float* part_ml;       // [2 grid][rows][2]
   int32_t* counters;    // [max_seqs][n_kv]
+  float* logits;        // MASS: [n_pages][n_kv][G][P], the layer's plain logits in units of log 2
+  float* lse2;          // MASS: [n_seqs][n_kv G], the rows' sums as base-2 logarithms
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -114,7 +116,8 @@ struct DecodeSmem {
   static int bytes(int G) { return 1024 + ring + NW * rows(G) * D * 4; }
 };
 
-template <bool E4M3, int NW, int NS, int C>
+// MASS: the logits and the rows' sums are left for launch_paged_mass_fold.
+template <bool E4M3, int NW, int NS, int C, bool MASS>
 __global__ void __launch_bounds__(NW * 32, 1)
     k_paged_decode(PagedLayer L, DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
@@ -126,6 +129,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   __shared__ int64_t s_wsum[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NS];
   __shared__ __align__(16) float s_sc[NW][NS][4];  // k scale of box 0, 1; v scale of box 0, 1
+  __shared__ int s_pg[MASS ? NW : 1][NS][2];  // pages of box 0, 1
   __shared__ float s_ml[NW][8 * C][2];
   __shared__ float s_M[8 * C], s_L[8 * C];
   __shared__ int s_last;
@@ -286,6 +290,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
       }
     }
+    if (MASS && lane < 2) s_pg[warp][stage][lane] = lane ? p1 : p0;
     if (E4M3 && lane < 4) {
       float* to = &s_sc[warp][stage][lane];
       const int i = lane & 1;
@@ -442,6 +447,16 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
 #pragma unroll
         for (int i = 0; i < C; ++i) {
+          if (MASS && g < G) {
+            const float k0 = E4M3 ? zf[i] * sc.x : zf[i], k1 = E4M3 && two ? zf[i] * sc.y : k0;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int tok = 8 * nt + 2 * c;  // of the chunk; a page begins at an even token
+              const int64_t at = (((int64_t)s_pg[warp][stage][two ? nt >> 1 : 0] * n_kv + u.head) * G + g) * L.P + ((tok0 + tok) & (L.P - 1));
+              const float k = nt < 2 ? k0 : k1;
+              if (tok < valid) *reinterpret_cast<float2*>(a.logits + at) = make_float2(z[i][nt][0] * k, z[i][nt][1] * k);
+            }
+          }
           if (E4M3) {
             const float k0 = zf[i] * sc.x, k1 = two ? zf[i] * sc.y : k0;
 #pragma unroll
@@ -594,6 +609,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
           pack2<false>(x * f, y * f);
     };
     auto put_lse = [&](int r) {
+      if (MASS && live_row(r))  // a row without weights: 2^(z - infinity) = 0
+        a.lse2[(int64_t)u.seq * n_kv * G + head_of(r)] =
+            s_L[r] > 0.0f || s_L[r] != s_L[r] ? log2f(s_L[r]) + (s_M[r] - kShift) : INFINITY;
       if (!a.lse || !live_row(r)) return;
       a.lse[(int64_t)(row + tok_of(r)) * n_kv * G + head_of(r)] =
           s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + (s_M[r] - kShift)) * 0.6931471805599453f : -INFINITY;
@@ -680,14 +698,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
   }
 }
 
-template <bool E4M3, int NW, int NS, int C = 1>
+template <bool E4M3, int NW, int NS, int C = 1, bool MASS = false>
 cudaError_t launch(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, cudaStream_t s) {
   const int bytes = DecodeSmem<E4M3, NW, NS, C>::bytes(L.G);
   int sms = 0;
-  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, NS, C>, bytes, NW * 32, nullptr, &sms);
+  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, NS, C, MASS>, bytes, NW * 32, nullptr, &sms);
   if (e != cudaSuccess) return e;
   const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
-  return launch_pdl(k_paged_decode<E4M3, NW, NS, C>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
+  return launch_pdl(k_paged_decode<E4M3, NW, NS, C, MASS>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
 }
 
 }  // namespace
@@ -696,7 +714,7 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
                                 const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
                                 float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s) {
   DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, causal ? 1 : 0,
-               w.part_acc, w.part_ml, w.counters};
+               w.part_acc, w.part_ml, w.counters, nullptr, nullptr};
   // 16 rows: 64 accumulators more a lane, eight warps of 255 registers.
   if (several) return L.e4m3 ? launch<true, 8, 2, 2>(L, maps, a, s) : launch<false, 8, 2, 2>(L, maps, a, s);
   // 12 warps of two 8 KB stages: the conversion of a chunk takes a warp about
@@ -706,6 +724,15 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
   // heads 250 us, 344 in bf16 (32 heads: 206, 334).
   if (L.G == 8) return L.e4m3 ? launch<true, 10, 2>(L, maps, a, s) : launch<false, 10, 2>(L, maps, a, s);
   return L.e4m3 ? launch<true, 12, 2>(L, maps, a, s) : launch<false, 12, 2>(L, maps, a, s);
+}
+
+cudaError_t launch_paged_decode_mass(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                     const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
+                                     uint16_t* out, int64_t out_stride, float* lse, float* logits, cudaStream_t s) {
+  const DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 0,
+                     w.part_acc, w.part_ml, w.counters, logits, w.lse2};
+  if (L.G == 8) return L.e4m3 ? launch<true, 10, 2, 1, true>(L, maps, a, s) : launch<false, 10, 2, 1, true>(L, maps, a, s);
+  return L.e4m3 ? launch<true, 12, 2, 1, true>(L, maps, a, s) : launch<false, 12, 2, 1, true>(L, maps, a, s);
 }
 
 }  // namespace mk

@@ -581,6 +581,95 @@ mk_status mk_paged_prefill_attn(mk_paged* h, int32_t layer, const mk_paged_batch
                                 int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
                                 mk_stream stream);
 
+/* Sequences of a batch that share their first tokens: the sequences
+ * cu_group[g] .. cu_group[g+1] - 1 share prefix_len[g] tokens, that is, their
+ * page table rows name the same pages for the whole pages of them.  Sequences
+ * outside every group share nothing.  Device memory, 4-byte aligned, read when
+ * the kernels run. */
+typedef struct mk_paged_prefix {
+  int32_t n_groups;          /* 0..n_seqs */
+  const int32_t* cu_group;   /* [n_groups + 1], ascending, 0..n_seqs */
+  const int32_t* prefix_len; /* [n_groups], >= 0 */
+} mk_paged_prefix;
+
+/* mk_paged_decode_attn for sequences that share prefixes: the same result, but
+ * the keys and values of a group's whole shared pages are read once for all of
+ * its sequences (from the page table row of the first one that holds tokens).
+ * What a group shares beyond its last whole page, or beyond what the shortest
+ * of its sequences holds (those without a token in the call or with kv_len 0
+ * do not count), is read for each sequence, as the rest of its tokens is.
+ * The weights of shared tokens are rounded before they multiply the values: to
+ * fp16 for an e4m3 cache (2^-11 of each) and to bf16 for a bf16 cache (2^-8 of
+ * each).  Shared values must be finite: a NaN or infinity among them reaches
+ * every sequence of its group, also where its weight is 0.
+ * MK_EDEVICE: as mk_paged_decode_attn, and cu_group not ascending or out of
+ * range or a negative prefix_len (that group shares nothing; its rows are
+ * right all the same). */
+mk_status mk_paged_prefix_attn(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const mk_paged_prefix* prefix,
+                               const void* q, int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
+                               mk_stream stream);
+
+/* ---- Attention mass, and eviction by it ----
+ * The mass of a held token is the sum of the softmax weights that it got, over
+ * query tokens and over the query heads of its kv head: fp32
+ * [n_layers][n_pages][n_kv_heads][page] next to the pools, owned by the caller.
+ * The calls below write mass only for tokens from number `first` on (>= 0), so
+ * that tokens which are always kept need none.  A page that such a token lies
+ * in may be in one row and place of the batch's table only. */
+
+/* Bytes of the mass array, and of the scratch of mk_paged_decode_attn_mass
+ * (one layer's logits: one fp32 per query head and slot of the pool). */
+mk_status mk_paged_mass_sizes(const mk_paged_config* cfg, size_t* mass_bytes, size_t* scratch_bytes);
+
+/* mk_paged_decode_attn that also counts its weights: adds them to the mass of
+ * the tokens held before, and sets the mass of the sequence's last token (the
+ * new one) to its weight.  out and lse are mk_paged_decode_attn's.  mass: the
+ * array of all layers, 4-byte aligned; scratch: scratch_bytes of
+ * mk_paged_mass_sizes, 16-byte aligned (MK_ENOMEM when smaller), free again
+ * when the call's kernels are done. */
+mk_status mk_paged_decode_attn_mass(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const void* q,
+                                    int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
+                                    float* mass, int32_t first, void* scratch, size_t scratch_bytes, mk_stream stream);
+
+/* The mass that a call's queries give: for each held key of a sequence the sum
+ * over its query tokens and heads of exp(scale q.k - lse), over the queries
+ * that see it (causal as in mk_paged_prefill_attn).  lse: fp32
+ * [n_tokens][n_q_heads] as mk_paged_prefill_attn wrote it for these queries (a
+ * row with lse = -infinity gives nothing).  add = 1: added to the mass of the
+ * tokens held before the call's new ones (the first kv_len - n_new; with
+ * causal = 0 all of them), set for the others; add = 0: set for all.  A
+ * sequence without new tokens is left alone.  Logits, exponentials and sums
+ * are fp32; the order of the sums depends on the lengths alone. */
+mk_status mk_paged_prefill_mass(mk_paged* h, int32_t layer, const mk_paged_batch* batch, int32_t causal, const void* q,
+                                int64_t q_stride, float scale, const float* lse, float* mass, int32_t first,
+                                int32_t add, mk_stream stream);
+
+/* Cuts every sequence of the batch to keep[i] tokens (device int32 [n_seqs]).
+ * A sequence that holds no more is left as it is.  Of any other each kv head
+ * keeps the first `first` tokens, the last `recent`, and of those between the
+ * heaviest (by mass; equal ones: the lower number first; NaN counts as the
+ * least), and moves them, in their order, to the sequence's first keep[i]
+ * slots: keys, values and mass.  kept (device int32
+ * [n_seqs][n_kv_heads][kept_stride]) receives the tokens' numbers from before,
+ * new_len (device int32 [n_seqs], not batch->kv_len: other layers' calls still
+ * read that) min(kv_len, keep).  Pages past the new length are free; what they
+ * and the slots past the new length hold is not defined.  Keys stay turned by
+ * the positions that they had: later appends give mk_rope.positions.
+ * e4m3: a page that got tokens from elsewhere has its scale formed anew over
+ * the values that it now holds, and their codes rounded to it, as
+ * mk_paged_append does; a page whose kept tokens all stay in their slots keeps
+ * codes and scale.  Every other page of the batch may be in one row and place
+ * of its table only: a shared prefix is safe while `first` covers it.
+ * Only n_seqs, table_stride, kv_len and page_table of the batch are read.
+ * MK_EINVAL: null or misaligned arrays, first, recent or kept_stride negative.
+ * MK_EDEVICE: keep[i] negative, below first + recent where the sequence holds
+ * more than keep[i], or min(kv_len, keep) above kept_stride; a bad length or
+ * page id.  That sequence is left as it is, with new_len its kv_len (with a bad
+ * page id, its contents are undefined). */
+mk_status mk_paged_evict(mk_paged* h, int32_t layer, const mk_paged_batch* batch, float* mass, const int32_t* keep,
+                         int32_t first, int32_t recent, int32_t* kept, int32_t kept_stride, int32_t* new_len,
+                         mk_stream stream);
+
 /* As mk_poll_error and mk_clear_error, for a paged handle: MK_ETIMEOUT after a
  * bounded device-side wait gave up. */
 mk_status mk_paged_poll_error(mk_paged* h, int32_t* detail);

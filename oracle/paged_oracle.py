@@ -79,3 +79,31 @@ def attention(q, k, v, scale, n_see):
     lse = torch.where(none, top, top + torch.log(tot))[:, 0]
     big = (q.abs() @ k.abs().T * abs(scale)).masked_fill(hid, 0).amax(dim=1)
     return p @ v, lse, p @ v.abs(), big
+
+
+def mass(q, k, scale, n_see, lse=None):
+    """q: [m, d], k: [T, d] doubles; row j sees the first n_see[j] keys.  (sum over rows of exp(logit - lse) per key,
+    the same with each weight times its row's largest scale sum |q k| plus |lse|: what error bounds are made of.)
+    lse [m]: the rows' (default: their own)."""
+    T = k.shape[0]
+    if T == 0 or q.shape[0] == 0:
+        z = torch.zeros(T, dtype=torch.float64, device=k.device)
+        return z, z
+    hid = torch.arange(T, device=q.device)[None, :] >= n_see[:, None]
+    z = (q @ k.T * scale).masked_fill(hid, -math.inf)
+    if lse is None:
+        lse = torch.logsumexp(z, dim=1)
+    none = torch.isinf(lse) & (lse < 0)
+    w = torch.where(hid | none[:, None], torch.zeros_like(z), torch.exp(z - torch.where(none, torch.zeros_like(lse), lse)[:, None]))
+    big = (q.abs() @ k.abs().T * abs(scale)).masked_fill(hid, 0).amax(dim=1) + torch.where(none, torch.zeros_like(lse), lse).abs()
+    return w.sum(dim=0), (w * big[:, None]).sum(dim=0)
+
+
+def evict_tokens(w, keep, first, recent):
+    """Numbers, ascending, of the tokens of one head that stay; w: the masses of all held tokens (NaN: below all)."""
+    T = len(w)
+    if T <= keep:
+        return list(range(T))
+    mid = range(first, T - recent)
+    best = sorted(mid, key=lambda t: (w[t] != w[t], 0.0 if w[t] != w[t] else -w[t], t))[:keep - first - recent]
+    return list(range(first)) + sorted(best) + list(range(T - recent, T))

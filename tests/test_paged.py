@@ -109,3 +109,32 @@ def test_rope_table_on_the_cpu():
     for i in (0, 7, 31):
         a = 3 * 100.0 ** (-2 * i / 64)
         assert abs(float(t[3, i]) - math.cos(a)) < 1e-7 and abs(float(t[3, 32 + i]) - math.sin(a)) < 1e-7
+
+
+def test_mass_sizes(lib):
+    m, s = ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.mk_paged_mass_sizes(ctypes.byref(_cfg()), ctypes.byref(m), ctypes.byref(s)) == 0
+    assert m.value == 2 * 100 * 8 * 32 * 4 and s.value == 100 * 32 * 32 * 4
+    assert lib.mk_paged_mass_sizes(ctypes.byref(_cfg(page=8)), ctypes.byref(m), ctypes.byref(s)) == 1
+
+
+def test_oracle_mass_and_evicted_tokens_by_hand():
+    q = torch.zeros(2, 128, dtype=torch.float64)
+    q[:, 0] = math.log(3.0)
+    k = torch.zeros(3, 128, dtype=torch.float64)
+    k[1, 0] = 1.0
+    w, _ = O.mass(q, k, 1.0, torch.tensor([2, 3]))
+    assert torch.allclose(w, torch.tensor([1 / 4 + 1 / 5, 3 / 4 + 3 / 5, 1 / 5], dtype=torch.float64))
+    w, _ = O.mass(q, k, 1.0, torch.tensor([3, 3]), torch.tensor([-math.inf, 0.0], dtype=torch.float64))
+    assert torch.allclose(w, torch.tensor([1.0, 3.0, 1.0], dtype=torch.float64))
+    assert O.evict_tokens([9, 1, 1, 5, 1, 0, 7], 4, 1, 1) == [0, 1, 3, 6]
+    assert O.evict_tokens([9, 1, math.nan, -5, 1, 0, 7], 6, 1, 1) == [0, 1, 3, 4, 5, 6]
+    assert O.evict_tokens([1, 2], 2, 0, 0) == [0, 1] and O.evict_tokens([1, 2], 0, 0, 0) == []
+
+
+def test_new_calls_refuse_a_null_handle(lib):
+    good = 1 << 20
+    assert lib.mk_paged_prefix_attn(None, 0, None, None, good, 4096, 1.0, good, 4096, None, None) == 1
+    assert lib.mk_paged_decode_attn_mass(None, 0, None, good, 4096, 1.0, good, 4096, None, good, 0, good, 1 << 30, None) == 1
+    assert lib.mk_paged_prefill_mass(None, 0, None, 1, good, 4096, 1.0, good, good, 0, 1, None) == 1
+    assert lib.mk_paged_evict(None, 0, None, good, good, 0, 0, good, 8, good, None) == 1
