@@ -36,13 +36,20 @@ constexpr int kPagedMaxCtas = 160;  // CTAs of a persistent attention kernel (GB
 struct PagedMaps {
   CUtensorMap k, v;
 };
+// The driver's tensor-map encoder, looked up through the runtime (the library
+// links no driver stub); null where there is none.
+using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TensorMapEncoder tensor_map_encoder();
 // The workspace's parts that the attention kernels use.
 struct PagedScratch {
   float* part_acc;
   float* part_ml;
   int32_t* counters;          // [max_seqs][n_kv], zero between calls
-  int32_t* prefill_counters;  // [kPagedMaxCtas], zero between calls
+  int32_t* prefill_counters;  // [2][kPagedMaxCtas], zero between calls
   float* prefill_part;        // paged_prefill_part_floats()
+  float* mass_part;           // [2 kPagedMaxCtas][256]
   float* lse2;                // [max_seqs][n_q_heads]: a decode step's sums, as base-2 logarithms
 };
 // The workspace's parts that eviction uses.
@@ -89,6 +96,15 @@ __device__ __forceinline__ bool paged_wait(uint64_t* bar, unsigned parity) {
 // The same for a full warp: if any lane gave up, all report failure.
 __device__ __forceinline__ bool paged_wait_warp(uint64_t* bar, unsigned parity) {
   return __all_sync(FULL, paged_wait(bar, parity)) != 0;
+}
+
+// A box of a three-dimensional tensor map into shared memory.
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -164,9 +180,10 @@ cudaError_t launch_paged_decode_mass(const PagedLayer& L, const PagedMaps& maps,
                                      uint16_t* out, int64_t out_stride, float* lse, float* logits, cudaStream_t s);
 cudaError_t launch_paged_mass_fold(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b,
                                    const float* logits, float* mass, int32_t first, cudaStream_t s);
-cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, bool causal,
-                                      const uint16_t* q, int64_t q_stride, float scale, const float* lse, float* mass,
-                                      int32_t first, bool add, cudaStream_t s);
+cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                      const mk_paged_batch& b, bool causal, const uint16_t* q, int64_t q_stride,
+                                      float scale, const float* lse, float* mass, int32_t first, bool add,
+                                      cudaStream_t s);
 cudaError_t launch_paged_evict(const PagedLayer& L, const PagedEvictScratch& w, const mk_paged_batch& b, float* mass,
                                const int32_t* keep, int32_t first, int32_t recent, int32_t* kept, int32_t kept_stride,
                                int32_t* new_len, cudaStream_t s);

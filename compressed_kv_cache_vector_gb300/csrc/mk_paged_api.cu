@@ -21,6 +21,19 @@ struct mk_paged {
   int device;
 };
 
+namespace mk {
+
+TensorMapEncoder tensor_map_encoder() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<TensorMapEncoder>(fn);
+}
+
+}  // namespace mk
+
 namespace {
 
 constexpr int64_t kAlign = 256;
@@ -51,7 +64,7 @@ inline int64_t mass_layer_count(const mk_paged_config* c) { return (int64_t)c->n
 inline int64_t logits_bytes(const mk_paged_config* c) { return (int64_t)c->n_pages * c->n_q_heads * c->page * 4; }
 // Workspace: [error word][counters, zero between calls][split-token parts].
 inline int64_t clear_bytes(const mk_paged_config* c) {
-  return align_up(kAlign + ((int64_t)c->max_seqs * c->n_kv_heads + mk::kPagedMaxCtas) * 4);
+  return align_up(kAlign + ((int64_t)c->max_seqs * c->n_kv_heads + 2 * mk::kPagedMaxCtas) * 4);
 }
 // Rows of a unit of the decode kernel: at most 16 (several tokens a sequence).
 inline int64_t part_acc_bytes(const mk_paged_config*) {
@@ -74,20 +87,7 @@ inline int64_t prefill_part_bytes() { return align_up(mk::paged_prefill_part_flo
 // rows it would take two readings, 142 us against 141.
 constexpr int kFewRows = 16;
 
-// The driver's tensor-map encoder, looked up through the runtime (the library
-// links no driver stub).
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn encoder() {
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult found;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-      found != cudaDriverEntryPointSuccess)
-    return nullptr;
-  return reinterpret_cast<EncodeFn>(fn);
-}
-bool pool_map(EncodeFn enc, const mk_paged_config* c, void* pool, int rows, CUtensorMap* m) {
+bool pool_map(mk::TensorMapEncoder enc, const mk_paged_config* c, void* pool, int rows, CUtensorMap* m) {
   const int64_t es = elem(c), row = MK_HEAD_DIM * es;
   const cuuint64_t dim[3] = {MK_HEAD_DIM, (cuuint64_t)c->n_kv_heads * c->page, (cuuint64_t)c->n_layers * c->n_pages};
   const cuuint64_t stride[2] = {(cuuint64_t)row, (cuuint64_t)(row * c->n_kv_heads * c->page)};
@@ -211,6 +211,7 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
   h->scratch.part_acc = reinterpret_cast<float*>(take(part_acc_bytes(cfg)));
   h->scratch.part_ml = reinterpret_cast<float*>(take(part_ml_bytes(cfg)));
   h->scratch.prefill_part = reinterpret_cast<float*>(take(prefill_part_bytes()));
+  h->scratch.mass_part = h->scratch.prefill_part;  // calls of a handle are ordered
   h->scratch.lse2 = reinterpret_cast<float*>(take(lse2_bytes(cfg)));
   char* plan = take(plan_bytes(cfg));
   h->evict.ticket = reinterpret_cast<int32_t*>(plan);
@@ -219,7 +220,7 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
   h->evict.flag = reinterpret_cast<int32_t*>(take(group_words_bytes(cfg)));
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) {
-    const EncodeFn enc = encoder();
+    const mk::TensorMapEncoder enc = mk::tensor_map_encoder();
     const int rows = e4m3 && cfg->page >= 32 ? 32 : 16;
     if (!enc || !pool_map(enc, cfg, k_pool, rows, &h->dec.k) || !pool_map(enc, cfg, v_pool, rows, &h->dec.v))
       e = cudaErrorInvalidValue;
@@ -359,7 +360,7 @@ mk_status mk_paged_prefill_mass(mk_paged* h, int32_t layer, const mk_paged_batch
   DeviceGuard dev(h->device);
   if (!dev.ok) return MK_ECUDA;
   const cudaError_t e = mk::launch_paged_prefill_mass(
-      layer_of(h, layer), h->scratch, *batch, causal != 0, static_cast<const uint16_t*>(q), q_stride, scale, lse,
+      layer_of(h, layer), h->dec, h->scratch, layer, *batch, causal != 0, static_cast<const uint16_t*>(q), q_stride, scale, lse,
       mass + layer * mass_layer_count(&h->cfg), first, add != 0, (cudaStream_t)stream);
   return e == cudaSuccess ? MK_OK : MK_ECUDA;
 }

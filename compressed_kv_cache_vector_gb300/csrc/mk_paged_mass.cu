@@ -1,8 +1,6 @@
 // Attention mass over the paged cache: what softmax weights each held token
 // got, summed over query tokens and over the query heads of its kv head.
-#include <algorithm>
-
-#include "mk_paged.cuh"
+#include "mk_paged_tc.cuh"
 
 namespace mk {
 
@@ -67,61 +65,465 @@ __global__ void __launch_bounds__(kFoldThreads)
 }
 
 // ---- a prompt's weights ----
-constexpr int kMassThreads = 256;
+// Products on the 5th-generation tensor cores with the keys as rows: S^T = K
+// Q^T, 128 keys by 128 rows (query token, query head).  A thread then has one
+// key: its sum over the rows needs no exchange, a causal mask is a first
+// column, and its page's scale one factor.  A weight is 2^(S k + n) with the
+// key's factor k and the row's n = -lse log2 e from shared memory.
+constexpr int kMassKeys = 256;   // keys of an item: two tiles of 128
+constexpr int kMassRows = 128;   // rows of a step
+constexpr int kMassTile = 128 * D * 2;
+constexpr int kMassThreads = 448;  // 8 warps sum, 4 load keys, 1 loads queries, 1 issues
+constexpr int kMassItemCost = 1;   // an item's begin and end take as long as this many steps
+constexpr int kMassMinRun = 4;
+constexpr int kMassSmem = 1024 + 4 * kMassTile + 2 * kMassTile;
+constexpr int kMeta = 8;           // items whose pages are kept
 
-// A warp a key: lanes hold four channels each.
-__global__ void __launch_bounds__(kMassThreads)
-    k_prefill_mass(PagedLayer L, mk_paged_batch b, int32_t causal, const uint16_t* q, int64_t q_stride, float scale,
-                   const float* lse, float* mass, int32_t first, int32_t add) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_kv = L.n_kv, G = L.G;
-  pdl_wait();
-  if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;
-  const int head = (int)(blockIdx.x % n_kv), seq = (int)(blockIdx.x / n_kv);
-  const PagedSeq s = paged_seq(b, L.P, seq, false);
-  if (!s.ok) {
-    if (tid == 0) paged_error(L, ERR_PAGED_BATCH, seq, s.len);
-    return;
-  }
-  if (s.n_new == 0) return;
-  const int64_t step = (int64_t)gridDim.y * (kMassThreads / 32);
-  for (int64_t t = first + (int64_t)blockIdx.y * (kMassThreads / 32) + warp; t < s.len; t += step) {
-    const int page = b.page_table[(int64_t)seq * b.table_stride + (t >> L.p_log2)];
-    if (page < 0 || page >= L.n_pages) {
-      if (lane == 0) paged_error(L, ERR_PAGED_PAGE, seq, page);
-      continue;
-    }
-    const int64_t unit = (int64_t)page * n_kv + head, row = unit * L.P + (t & (L.P - 1));
-    float k[4];
-    if (L.e4m3) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(L.k + row * D)[lane];
-      const float sc = L.k_scale[unit];
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t h = e4m3_h2(w >> (16 * e));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        k[2 * e] = f.x * sc;
-        k[2 * e + 1] = f.y * sc;
+struct MassArgs {
+  mk_paged_batch b;
+  const float* lse;
+  float* mass;
+  float scale;  // times log2 e
+  int32_t causal, first, add, layer_page0;
+  float* part;        // [2 kPagedMaxCtas][kMassKeys]
+  int32_t* counters;  // [2][kPagedMaxCtas]
+};
+
+// A place in the list of items: 256 keys of a (sequence, kv head), and where
+// it begins in the CTA's run (negative: in an earlier CTA's).
+struct MassCursor {
+  int seq, head, kt, rel;
+};
+
+struct MassShared {
+  int64_t pre[MK_MAX_CALL_SEQS + 1];  // cost of the sequences before each
+  int row0[MK_MAX_CALL_SEQS], n_new[MK_MAX_CALL_SEQS], len[MK_MAX_CALL_SEQS];
+  MassCursor start;
+  int64_t f0, per;
+  int span, patience;
+  uint64_t q_full[2], q_free[2], s_full[2][2], s_free[2][2], k_full[2], k_free[2], met[2], done;
+  // -lse log2 e of a step's rows, -infinity where there is none.  A sum gives its
+  // logits back before it has read the last of these, hence more than four.
+  __align__(16) float nlse[8][kMassRows];
+  int page[kMeta][kMassKeys / 16];         // pages of an item's keys, -1: none
+  float ks[kMeta][kMassKeys / 16];         // their scales (e4m3)
+  uint32_t tmem;
+  int last[2];
+  volatile int dead;
+};
+
+template <bool E4M3>
+__global__ void __launch_bounds__(kMassThreads, 1)
+    k_prefill_mass(PagedLayer L, MassArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
+  extern __shared__ unsigned char dyn[];
+  __shared__ MassShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t sk = base, sq = base + 4 * kMassTile;
+  const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv, n_seqs = a.b.n_seqs;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_free[i], 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&sh.s_full[i][j], 1);
+        mbar_init(&sh.s_free[i][j], 4);
       }
-    } else {
-      const uint2 w = reinterpret_cast<const uint2*>(L.k + row * D * 2)[lane];
-      k[0] = bf2f(w.x & 0xffff);
-      k[1] = bf2f(w.x >> 16);
-      k[2] = bf2f(w.y & 0xffff);
-      k[3] = bf2f(w.y >> 16);
+      mbar_init(&sh.k_full[i], E4M3 ? 4 : 1);
+      mbar_init(&sh.k_free[i], 1);
+      mbar_init(&sh.met[i], 4);
     }
-    // Query j sees the first len - n_new + j + 1 keys.
-    const int64_t j0 = causal ? std::max<int64_t>(0, t - (s.len - s.n_new)) : 0;
-    float sum = 0.0f;
-    for (int64_t r = j0 * G; r < (int64_t)s.n_new * G; ++r) {
-      const int64_t tok = s.row0 + r / G;
-      const int h = head * G + (int)(r % G);
-      const uint2 w = reinterpret_cast<const uint2*>(q + tok * q_stride + h * D)[lane];
-      float z = bf2f(w.x & 0xffff) * k[0] + bf2f(w.x >> 16) * k[1] + bf2f(w.y & 0xffff) * k[2] + bf2f(w.y >> 16) * k[3];
-      z = warp_sum(z);
-      const float ls = lse[tok * n_kv * G + h];
-      if (ls != -INFINITY) sum += ex2(z * scale - ls * kLog2e);
-    }
-    if (lane == 0) mass[row] = add && (!causal || t < s.len - s.n_new) ? mass[row] + sum : sum;
+    mbar_init(&sh.done, 1);
+    sh.dead = 0;
   }
+  mbar_init_fence();
+  pdl_wait();
+  pdl_trigger();
+  if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;
+
+  // ---- the CTA's run of the list of items ----
+  // An item's steps are the row tiles that see its first key; it is as long as
+  // these and kMassItemCost.  The list is cut into equal runs, one a CTA.
+  const int kt0 = a.first / kMassKeys;
+  auto tiles_of = [&](int seq) { return (int)(((int64_t)sh.n_new[seq] * G + kMassRows - 1) / kMassRows); };
+  auto ends_of = [&](int seq) { return (sh.len[seq] + kMassKeys - 1) / kMassKeys; };
+  auto skip_of = [&](int seq, int kt) {  // row tiles before the first that sees the item's first key
+    const int64_t t = (int64_t)kt * kMassKeys - (sh.len[seq] - sh.n_new[seq]);
+    return a.causal && t > 0 ? (int)(t * G / kMassRows) : 0;
+  };
+  auto cost_of = [&](int seq, int kt) { return tiles_of(seq) - skip_of(seq, kt) + kMassItemCost; };
+  for (int i = warp; i < n_seqs; i += kMassThreads / 32) {
+    PagedSeq s = paged_seq(a.b, L.P, i, false);
+    if (!s.ok) {
+      if (lane == 0) paged_error(L, ERR_PAGED_BATCH, i, s.len);
+      s.n_new = 0;
+    }
+    if (s.n_new == 0) s.len = 0;
+    if (lane == 0) {
+      sh.row0[i] = s.row0;
+      sh.n_new[i] = s.n_new;
+      sh.len[i] = s.len;
+    }
+    __syncwarp();
+    int64_t x = 0;
+    for (int kt = kt0 + lane, n = ends_of(i); kt < n; kt += 32) x += cost_of(i, kt);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+    if (lane == 0) sh.pre[i] = x * n_kv;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t at = 0;
+    for (int i0 = 0; i0 < n_seqs; i0 += 32) {
+      const int i = i0 + lane;
+      const int64_t mine = i < n_seqs ? sh.pre[i] : 0;
+      int64_t x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+      }
+      if (i < n_seqs) sh.pre[i] = at + x - mine;
+      at += __shfl_sync(FULL, x, 31);
+    }
+    if (lane == 0) sh.pre[n_seqs] = at;
+  }
+  __syncthreads();
+  const int64_t total = sh.pre[n_seqs];
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kMassMinRun) per = kMassMinRun;
+  const int64_t f0 = (int64_t)blockIdx.x * per;
+  if (f0 >= total) return;
+  if (warp == 0) {
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {  // the last sequence that begins at or before f0
+      const int mid = (lo + hi + 1) >> 1;
+      if (sh.pre[mid] <= f0) lo = mid; else hi = mid - 1;
+    }
+    const int64_t one = (sh.pre[lo + 1] - sh.pre[lo]) / n_kv;  // a kv head's items
+    const int head = (int)((f0 - sh.pre[lo]) / one);
+    int64_t at = sh.pre[lo] + head * one;
+    for (int k0 = kt0, n = ends_of(lo); k0 < n; k0 += 32) {
+      const int kt = k0 + lane;
+      const int64_t cost = kt < n ? cost_of(lo, kt) : 0;
+      int64_t x = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned past = __ballot_sync(FULL, at + x > f0);
+      if (past) {
+        if (lane == __ffs(past) - 1) sh.start = MassCursor{lo, head, kt, (int)(at + x - cost - f0)};
+        break;
+      }
+      at += __shfl_sync(FULL, x, 31);
+    }
+    if (lane == 0) {
+      sh.f0 = f0;
+      sh.per = per;
+      sh.span = (int)(total - f0 < per ? total - f0 : per);
+      sh.patience = 100 + sh.span / 1024;
+    }
+  }
+  __syncthreads();
+  if (warp == 13) tmem_alloc(&sh.tmem, 512);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+
+  auto slow = [&](uint64_t* bar, unsigned parity, int times) {
+    for (int i = 0; i < times; ++i) {
+      if (sh.dead) return false;
+      if (paged_wait(bar, parity)) return true;
+    }
+    sh.dead = 1 + warp;
+    return false;
+  };
+  auto wait = [&](uint64_t* bar, unsigned parity) { return mbar_try_wait(bar, parity) || slow(bar, parity, 1); };
+  // For a wait that an item's steps can lie between.
+  auto wait_long = [&](uint64_t* bar, unsigned parity) { return mbar_try_wait(bar, parity) || slow(bar, parity, sh.patience); };
+  auto next = [&](MassCursor& k) {
+    k.rel += cost_of(k.seq, k.kt);
+    if (++k.kt < ends_of(k.seq)) return;
+    k.kt = kt0;
+    if (++k.head < n_kv) return;
+    k.head = 0;
+    do ++k.seq;
+    while (k.seq < n_seqs && ends_of(k.seq) <= kt0);
+  };
+  // The item's steps in this run are the row tiles [j0, j1) behind the skipped ones.
+  auto steps = [&](const MassCursor& k, int& j0, int& j1) {
+    const int n = cost_of(k.seq, k.kt) - kMassItemCost;
+    j0 = max(0, -k.rel);
+    j1 = min(n, sh.span - k.rel);
+    return n;
+  };
+
+  if (warp == 13) {
+    // ---- issues the products ----
+    if (elect_one()) {
+      unsigned c = 0, ic = 0;
+      bool ok = true;
+      const uint64_t dk = sw128_desc(sk, 16), dq = sw128_desc(sq, 16);
+      int j0, j1;
+      for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
+        steps(k, j0, j1);
+        if (j0 >= j1) continue;
+        ok = wait(&sh.k_full[ic & 1], (ic >> 1) & 1);
+        for (int j = j0; ok && j < j1; ++j, ++c) {
+          ok = wait(&sh.q_full[c & 1], (c >> 1) & 1);
+          for (int w = 0; ok && w < 2; ++w) {
+            ok = c < 2 || wait(&sh.s_free[w][c & 1], ((c >> 1) - 1) & 1);
+            if (!ok) break;
+            tmem_fence_after_sync();
+            const uint64_t da = dk + (uint64_t)((((ic & 1) * 2 + w) * kMassTile) >> 4), db = dq + (uint64_t)(((c & 1) * kMassTile) >> 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t o = ((i >> 2) * (kMassTile / 2) + (i & 3) * 32) >> 4;
+              umma_ss(tmem + (w * 2 + (c & 1)) * 128, da + o, db + o, idesc(1, 0), i > 0);
+            }
+            umma_commit(&sh.s_full[w][c & 1]);
+          }
+          if (ok) umma_commit(&sh.q_free[c & 1]);
+        }
+        if (ok) umma_commit(&sh.k_free[ic & 1]);
+        ++ic;
+      }
+      umma_commit(&sh.done);
+    }
+    // Nothing is in flight when the tensor memory is freed.
+    __syncwarp();
+    (void)paged_wait_warp(&sh.done, 0);
+  } else if (warp == 12) {
+    // ---- loads queries and the rows' sums ----
+    unsigned c = 0;
+    bool ok = true;
+    int j0, j1;
+    const int n_q = n_kv * G;
+    for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
+      steps(k, j0, j1);
+      const int row0 = sh.row0[k.seq];
+      const int64_t rows = (int64_t)sh.n_new[k.seq] * G;
+      const int skip = skip_of(k.seq, k.kt);
+      for (int j = j0; ok && j < j1; ++j, ++c) {
+        const int64_t r0 = (int64_t)(skip + j) * kMassRows;
+        float n[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t r = r0 + lane * 4 + e;
+          const float ls = r < rows ? a.lse[(row0 + (r >> g_log2)) * n_q + k.head * G + (int)(r & (G - 1))] : -INFINITY;
+          n[e] = ls == -INFINITY ? -INFINITY : -ls * kLog2e;
+        }
+        ok = c < 2 || __all_sync(FULL, wait(&sh.q_free[c & 1], ((c >> 1) - 1) & 1));
+        if (!ok) break;
+        *reinterpret_cast<float4*>(&sh.nlse[c & 7][lane * 4]) = make_float4(n[0], n[1], n[2], n[3]);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_expect_tx(&sh.q_full[c & 1], kMassTile);
+          const int tok = row0 + (int)(r0 >> g_log2);
+          const uint32_t to = sq + (c & 1) * kMassTile;
+          tma3(to, &qmap, 0, k.head * G, tok, &sh.q_full[c & 1]);
+          tma3(to + kMassTile / 2, &qmap, 64, k.head * G, tok, &sh.q_full[c & 1]);
+        }
+      }
+    }
+    // No copy is in flight when the kernel ends, also after a wait that ran out.
+    for (unsigned i = c < 2 ? 0 : c - 2; i < c; ++i) (void)paged_wait_warp(&sh.q_full[i & 1], (i >> 1) & 1);
+  } else if (warp >= 8) {
+    // ---- keys into shared memory ----
+    const int lt = tid - 256;
+    unsigned ic = 0;
+    bool ok = true;
+    int j0, j1;
+    auto page_at = [&](const MassCursor& k) {  // lane g < 16: the page of the item's 16-key group g, -1 where there is none
+      const int tok = k.kt * kMassKeys + lane * 16;
+      int p = -1;
+      if (lane < 16 && tok < sh.len[k.seq]) {
+        p = a.b.page_table[(int64_t)k.seq * a.b.table_stride + (tok >> L.p_log2)];
+        if (p < 0 || p >= L.n_pages) {
+          paged_error(L, ERR_PAGED_PAGE, k.seq, p);
+          p = -1;
+        }
+      }
+      return p;
+    };
+    if (E4M3) {
+      // 16 codes ck of rows r + 16 i, as the attention of several query tokens loads them.
+      const int ck = (lane & 3) | (lane >> 1 & 4), r = (lane >> 2 & 1) | (lane >> 3 & 2) | (warp & 3) << 2;
+      const uint32_t put = (ck >> 2) * (kMassTile / 2) + r * 128 + ((((2 * ck) & 7) ^ (r & 7)) << 4);
+      const int64_t page_stride = (int64_t)n_kv * L.P * D;
+      for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
+        steps(k, j0, j1);
+        if (j0 >= j1) continue;
+        const int pg = page_at(k);
+        uint4 x[16];
+        const uint8_t* from = L.k + (int64_t)k.head * L.P * D + ck * 16;
+        const int slot = k.kt * kMassKeys + r;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int p = __shfl_sync(FULL, pg, i);
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (p >= 0) x[i] = *reinterpret_cast<const uint4*>(from + p * page_stride + ((slot + 16 * i) & (L.P - 1)) * D);
+        }
+        float ks = 1.0f;
+        if (lt < 16 && pg >= 0) ks = L.k_scale[(int64_t)pg * n_kv + k.head];
+        ok = ic < 2 || __all_sync(FULL, wait_long(&sh.k_free[ic & 1], ((ic >> 1) - 1) & 1));
+        if (!ok) break;
+        if (lt < 16) {
+          sh.page[ic % kMeta][lt] = pg;
+          sh.ks[ic % kMeta][lt] = ks;
+        }
+        const uint32_t to = sk + (ic & 1) * 2 * kMassTile + put;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {  // exact: e4m3 has 4 significant bits
+            const uint32_t h = e4m3_h2(w[e >> 1] >> (16 * (e & 1)));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            o[e] = pack2<false>(f.x, f.y);
+          }
+          const uint32_t at = to + (i >> 3) * kMassTile + (i & 7) * 2048;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at ^ 16), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
+        }
+        fence_proxy_async();
+        mbar_arrive_warp(&sh.k_full[ic & 1], lane);
+        ++ic;
+      }
+    } else if (warp == 8) {
+      for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
+        steps(k, j0, j1);
+        if (j0 >= j1) continue;
+        const int pg = page_at(k);
+        ok = ic < 2 || __all_sync(FULL, wait_long(&sh.k_free[ic & 1], ((ic >> 1) - 1) & 1));
+        if (!ok) break;
+        if (lane < 16) sh.page[ic % kMeta][lane] = pg;
+        const unsigned groups = __ballot_sync(FULL, pg >= 0);
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(&sh.k_full[ic & 1], __popc(groups) * 16 * D * 2);
+        __syncwarp();
+        if (pg >= 0) {
+          const uint32_t to = sk + ((ic & 1) * 2 + (lane >> 3)) * kMassTile + (lane & 7) * 2048;
+          const int y = k.head * L.P + ((k.kt * kMassKeys + lane * 16) & (L.P - 1)), z = a.layer_page0 + pg;
+          tma3(to, &kmap, 0, y, z, &sh.k_full[ic & 1]);
+          tma3(to + kMassTile / 2, &kmap, 64, y, z, &sh.k_full[ic & 1]);
+        }
+        ++ic;
+      }
+      for (unsigned i = ic < 2 ? 0 : ic - 2; i < ic; ++i) (void)paged_wait_warp(&sh.k_full[i & 1], (i >> 1) & 1);
+    }
+  } else {
+    // ---- sums: one key a thread ----
+    const int w = warp >> 2, key = tid & 127;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + w * 256;
+    unsigned c = 0, ic = 0, meets = 0;
+    bool ok = true;
+    int j0, j1;
+    auto meet = [&]() {  // the four warps of this half
+      mbar_arrive_warp(&sh.met[w], lane);
+      const unsigned parity = meets++ & 1;
+      return __all_sync(FULL, wait(&sh.met[w], parity)) != 0;
+    };
+    for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
+      const int n = steps(k, j0, j1);
+      if (j0 >= j1) continue;
+      const int len = sh.len[k.seq], n_new = sh.n_new[k.seq], t = k.kt * kMassKeys + w * 128 + key;
+      const int64_t rows = (int64_t)n_new * G, r0 = (int64_t)(skip_of(k.seq, k.kt) + j0) * kMassRows;
+      // Rows left of the sequence from the step's first one on, and the first of them that sees the key.
+      int64_t left = rows - r0;
+      int64_t from = (a.causal ? max((int64_t)0, (int64_t)t - (len - n_new)) * G : 0) - r0;
+      float sum = 0.0f, low = 0.0f;
+      for (int j = j0; j < j1; ++j, ++c, left -= kMassRows, from -= kMassRows) {
+        ok = __all_sync(FULL, wait(&sh.s_full[w][c & 1], (c >> 1) & 1));
+        if (!ok) break;
+        tmem_fence_after_sync();
+        const float kf = E4M3 ? a.scale * sh.ks[ic % kMeta][w * 8 + (key >> 4)] : a.scale;
+        const uint64_t k2 = pair(kf, kf);
+        const int cols = (int)min(left, (int64_t)kMassRows), c0 = (int)min(max(from, (int64_t)0), (int64_t)kMassRows);
+        const bool cut = cols < kMassRows || __any_sync(FULL, c0 > 0);
+        const uint32_t tb = ts + (c & 1) * 128;
+        uint64_t add[2] = {0, 0};
+        uint32_t v[2][32];
+        tmem_ld32_async(tb, v[0]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          tmem_ld_wait(v[h & 1]);
+          if (h < 3) tmem_ld32_async(tb + (h + 1) * 32, v[(h + 1) & 1]);
+          if (h == 3) {  // all of S is in registers
+            tmem_fence_before_sync();
+            mbar_arrive_warp(&sh.s_free[w][c & 1], lane);
+          }
+          const uint32_t(&z)[32] = v[h & 1];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 nl = *reinterpret_cast<const float4*>(&sh.nlse[c & 7][32 * h + i]);
+            float x[4];
+            unpair(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), k2, pair(nl.x, nl.y)), x[0], x[1]);
+            unpair(fma2(pair(__uint_as_float(z[i + 2]), __uint_as_float(z[i + 3])), k2, pair(nl.z, nl.w)), x[2], x[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+            if (cut) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (32 * h + i + e < c0 || 32 * h + i + e >= cols) x[e] = 0.0f;
+            }
+            add[0] = add2(add[0], pair(x[0], x[1]));
+            add[1] = add2(add[1], pair(x[2], x[3]));
+          }
+        }
+        // Steps are added with the rounding's rest carried along: a key's rows may be millions.
+        float x[4];
+        unpair(add[0], x[0], x[1]);
+        unpair(add[1], x[2], x[3]);
+        const float y = ((x[0] + x[1]) + (x[2] + x[3])) - low, s = sum + y;
+        low = (s - sum) - y;
+        sum = s;
+      }
+      if (!ok) break;
+      const int page = sh.page[ic % kMeta][w * 8 + (key >> 4)];
+      ++ic;
+      auto put = [&](float x) {
+        if (page < 0 || t < a.first || t >= len) return;
+        float* to = a.mass + ((int64_t)page * n_kv + k.head) * L.P + (t & (L.P - 1));
+        *to = a.add && (!a.causal || t < len - n_new) ? *to + x : x;
+      };
+      if (j0 == 0 && j1 == n) {
+        put(sum);
+        continue;
+      }
+      // Several CTAs have steps of this item: the last to come adds the parts, in their order.
+      const int64_t place = sh.f0 + k.rel;
+      const int b_lo = (int)(place / sh.per), parts = (int)((place + n - 1) / sh.per) - b_lo + 1;
+      auto slot = [&](int i) { return a.part + (2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0)) * kMassKeys + w * 128 + key; };
+      *slot((int)blockIdx.x - b_lo) = sum;
+      __threadfence();
+      if (!(ok = meet())) break;
+      if (key == 0) {
+        int32_t* ctr = &a.counters[w * kPagedMaxCtas + b_lo];  // one item at most begins in b_lo and ends after it
+        const int old = atomicAdd(ctr, 1);
+        sh.last[w] = old == parts - 1;
+        if (sh.last[w]) *ctr = 0;
+      }
+      if (!(ok = meet())) break;
+      if (sh.last[w]) {
+        __threadfence();
+        float x = 0.0f;
+        for (int i = 0; i < parts; ++i) x += __ldcg(slot(i));
+        put(x);
+      }
+      ok = meet();  // sh.last is free again
+    }
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+  if (tid == 0 && sh.dead) paged_error(L, ERR_PAGED_WAIT, (int32_t)blockIdx.x, sh.dead - 1, (int32_t)MK_ETIMEOUT);
 }
 
 }  // namespace
@@ -135,12 +537,29 @@ cudaError_t launch_paged_mass_fold(const PagedLayer& L, const PagedScratch& w, c
                     (const float*)w.lse2, mass, first);
 }
 
-cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, bool causal,
-                                      const uint16_t* q, int64_t q_stride, float scale, const float* lse, float* mass,
-                                      int32_t first, bool add, cudaStream_t s) {
-  (void)w;
-  return launch_pdl(k_prefill_mass, dim3((unsigned)(b.n_seqs * L.n_kv), 256), dim3(kMassThreads), 0, s, 0, L, b,
-                    (int32_t)causal, q, q_stride, scale * kLog2e, lse, mass, first, (int32_t)add);
+cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                      const mk_paged_batch& b, bool causal, const uint16_t* q, int64_t q_stride,
+                                      float scale, const float* lse, float* mass, int32_t first, bool add,
+                                      cudaStream_t s) {
+  const void* fn = L.e4m3 ? (const void*)k_prefill_mass<true> : (const void*)k_prefill_mass<false>;
+  int sms = 0;
+  const cudaError_t e = kernel_smem_attr(fn, kMassSmem, kMassThreads, nullptr, &sms);
+  if (e != cudaSuccess) return e;
+  const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
+  // Queries as {channels, heads, tokens}; a box is 64 channels of the 128 rows
+  // (token, head of the group) of a step.
+  const TensorMapEncoder enc = tensor_map_encoder();
+  CUtensorMap qmap;
+  const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)L.n_kv * L.G, (cuuint64_t)b.n_tokens};
+  const cuuint64_t stride[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)L.G, (cuuint32_t)(kMassRows / L.G)}, one[3] = {1, 1, 1};
+  if (!enc || enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(q), dim, stride, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const MassArgs a{b, lse, mass, scale * kLog2e, causal ? 1 : 0, first, add ? 1 : 0, layer * L.n_pages, w.mass_part, w.prefill_counters};
+  return launch_pdl(L.e4m3 ? k_prefill_mass<true> : k_prefill_mass<false>, dim3(grid), dim3(kMassThreads), (size_t)kMassSmem, s, 0,
+                    L, a, maps.k, qmap);
 }
 
 }  // namespace mk
