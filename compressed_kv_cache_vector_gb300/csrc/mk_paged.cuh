@@ -42,6 +42,23 @@ using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint3
                                       const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                       CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 TensorMapEncoder tensor_map_encoder();
+// What a call's groups share, left by the kernel over the shared pages for the
+// one over the sequences' own tokens.
+struct PagedShared {
+  int64_t per;  // length of a CTA's run in the list of cells (group, 128 rows, kv head)
+  struct Seq {
+    int64_t place;  // in the list, of the first kv head's cell; the others follow, `cost` apart
+    int32_t len;    // shared tokens (0: none)
+    int32_t row;    // of the sequence's first query head in the cell
+    int32_t steps, cost;
+  } seq[MK_MAX_CALL_SEQS];
+};
+// A part of a row: 128 weighted values, their reference and the weights' sum.
+// The parts of a cell that lies in several CTAs' runs go by CTA: 128 rows, one
+// slot for a cell that begins in the run and one for a cell that does not.
+// Those of a whole cell go by sequence and head.
+constexpr int kPagedRowPart = MK_HEAD_DIM + 2;
+constexpr int kPagedPrefixPart = 128 * kPagedRowPart;
 // The workspace's parts that the attention kernels use.
 struct PagedScratch {
   float* part_acc;
@@ -50,6 +67,8 @@ struct PagedScratch {
   int32_t* prefill_counters;  // [2][kPagedMaxCtas], zero between calls
   float* prefill_part;        // paged_prefill_part_floats()
   float* mass_part;           // [2 kPagedMaxCtas][256]
+  PagedShared* shared;
+  float* row_part;            // [max_seqs][n_q_heads][kPagedRowPart]
   float* lse2;                // [max_seqs][n_q_heads]: a decode step's sums, as base-2 logarithms
 };
 // The workspace's parts that eviction uses.
@@ -172,6 +191,14 @@ cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, co
 cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
                                 float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s);
+// Shared prefixes: the parts of the rows over shared pages go to w.prefill_part,
+// what is shared to w.shared; then the sequences' own tokens, joined with them.
+cudaError_t launch_paged_prefix(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                const mk_paged_batch& b, const mk_paged_prefix& p, const uint16_t* q, int64_t q_stride,
+                                float scale, cudaStream_t s);
+cudaError_t launch_paged_decode_own(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                    const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
+                                    uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s);
 // With mass: the plain logits of layer pages go to scratch ([n_pages][n_kv][G]
 // [P] fp32) and the rows' sums to w.lse2; launch_paged_mass_fold adds their
 // weights to the mass.

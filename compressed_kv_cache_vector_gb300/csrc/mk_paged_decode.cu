@@ -58,6 +58,8 @@ struct DecodeArgs {
   float* part_acc;      // [2 grid][rows][128]
   float* part_ml;       // [2 grid][rows][2]
   int32_t* counters;    // [max_seqs][n_kv]
+  const PagedShared* shared;  // OWN
+  const float *shared_part, *row_part;
   float* logits;        // MASS: [n_pages][n_kv][G][P], the layer's plain logits in units of log 2
   float* lse2;          // MASS: [n_seqs][n_kv G], the rows' sums as base-2 logarithms
 };
@@ -108,16 +110,23 @@ struct DecodeSmem {
   static int bytes(int G) { return 1024 + ring + NW * rows(G) * D * 4; }
 };
 
-// MASS: the logits and the rows' sums are left for launch_paged_mass_fold.
-template <bool E4M3, int NW, int NS, int C, bool MASS>
+// kMass: the logits and the rows' sums are left for launch_paged_mass_fold.
+// kOwn: the tokens that a sequence shares with its group are left out; their
+// parts, from launch_paged_prefix, are joined with the result.
+enum DecodeMode { kPlain, kMass, kOwn };
+template <bool E4M3, int NW, int NS, int C, DecodeMode MODE>
 __global__ void __launch_bounds__(NW * 32, 1)
     k_paged_decode(PagedLayer L, DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
   constexpr int CH = DecodeSmem<E4M3, NW, NS, C>::CH, NT = CH / 8, NTHR = NW * 32;
   constexpr float kShift = E4M3 ? 14.0f : 0.0f;  // weights times 2^kShift before their rounding
+  constexpr bool MASS = MODE == kMass, OWN = MODE == kOwn;
+  static_assert(!OWN || C == 1, "one token a sequence");
   extern __shared__ unsigned char dyn[];
   __shared__ int64_t s_pre[MK_MAX_CALL_SEQS + 1];
   __shared__ int s_len[MK_MAX_CALL_SEQS], s_row[MK_MAX_CALL_SEQS], s_new[C == 1 ? 1 : MK_MAX_CALL_SEQS];
+  __shared__ int s_off[OWN ? MK_MAX_CALL_SEQS : 1];  // shared tokens
+  __shared__ float s_mul[OWN ? 8 : 1];
   __shared__ int64_t s_wsum[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NS];
   __shared__ __align__(16) float s_sc[NW][NS][4];  // k scale of box 0, 1; v scale of box 0, 1
@@ -145,10 +154,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
       const PagedSeq s = paged_seq(a.b, L.P, i, false);
       if (!s.ok) paged_error(L, ERR_PAGED_BATCH, i, s.len);
       const bool live = s.ok && (C == 1 ? s.n_new == 1 : s.n_new > 0);  // C = 2: n_new <= max_new <= 16 / G
-      s_len[i] = live ? s.len : 0;
+      const int off = OWN && live && s.len > 0 ? a.shared->seq[i].len : 0;  // at most s.len
+      s_len[i] = live ? s.len - off : 0;
       s_row[i] = live ? s.row0 : -1;
       if (C > 1) s_new[i] = live ? s.n_new : 0;
-      keys = live && s.len > 0;
+      if (OWN) s_off[i] = off;
+      keys = s_len[i] > 0;
     }
     units += __syncthreads_count(keys) * n_kv;
   }
@@ -183,9 +194,90 @@ __global__ void __launch_bounds__(NW * 32, 1)
   };
   int64_t total = list(1);
 
-  // Rows of empty sequences.
+  // OWN: the parts over the tokens that sequence seq shares.  `slot` is the
+  // i-th part's place among them, `row` the head's first row there.
+  struct SharedParts {
+    int b_lo, parts, row;
+    const float* whole;  // the rows' parts where there is one of each
+  };
+  auto shared_of = [&](int seq, int head) {
+    const PagedShared::Seq& s = a.shared->seq[seq];
+    const int64_t place = s.place + (int64_t)head * s.cost, per = a.shared->per;
+    const int b_lo = (int)(place / per);
+    return SharedParts{b_lo, (int)((place + s.steps - 1) / per) - b_lo + 1, s.row,
+                       a.row_part + ((int64_t)seq * n_kv + head) * G * kPagedRowPart};
+  };
+  auto shared_at = [&](const SharedParts& p, int i, int r) {  // part i of row r
+    return (p.parts == 1 ? p.whole
+                         : a.shared_part + (2 * (int64_t)(p.b_lo + i) + (i == 0 ? 1 : 0)) * kPagedPrefixPart + p.row * kPagedRowPart) +
+           r * kPagedRowPart;
+  };
+  // The rows' maxima and sums with the shared parts' (s_M, s_L), and what the
+  // rows' own values are multiplied by (s_mul).  The whole CTA, between barriers.
+  auto join_shared = [&](const SharedParts& p) {
+    for (int r = warp; r < G; r += NW) {
+      const float own = s_M[r] == -INFINITY ? -INFINITY : s_M[r] - kShift;
+      float M = own, S = 0.0f;
+      for (int i = lane; i < p.parts; i += 32) M = fmaxf(M, __ldcg(shared_at(p, i, r) + D));
+      M = warp_max(M);
+      for (int i = lane; i < p.parts; i += 32) {
+        const float* ml = shared_at(p, i, r) + D;
+        const float mi = __ldcg(ml);
+        S += __ldcg(ml + 1) * (mi == -INFINITY ? 1.0f : ex2(mi - M));
+      }
+      S = warp_sum(S);
+      if (lane == 0) {
+        const float f = own == -INFINITY ? 0.0f : ex2(own - M);
+        s_mul[r] = f;
+        s_L[r] = S + s_L[r] * (own == -INFINITY ? 1.0f : f);
+        s_M[r] = M + kShift;
+      }
+    }
+    __syncthreads();
+  };
+  auto add_shared = [&](const SharedParts& p, int e, float& x, float& y) {
+    const int r = e >> 6;
+    const float M = s_M[r] - kShift;
+    x *= s_mul[r];
+    y *= s_mul[r];
+#pragma unroll 8
+    for (int i = 0; i < p.parts; ++i) {
+      const float* part = shared_at(p, i, r);
+      const float mi = __ldcg(part + D);
+      const float f = mi == -INFINITY ? 0.0f : ex2(mi - M);
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(part + 2 * (e & 63)));
+      x = fmaf(v.x, f, x);
+      y = fmaf(v.y, f, y);
+    }
+  };
+
+  // Rows of sequences without tokens (of their own).
+  if (OWN)
+    for (int u = blockIdx.x; u < n_seqs * n_kv; u += gridDim.x) {
+      const int i = u / n_kv, head = u - i * n_kv;
+      if (s_row[i] < 0 || s_len[i] != 0 || s_off[i] == 0) continue;
+      const SharedParts p = shared_of(i, head);
+      if (tid < 8) {
+        s_M[tid] = -INFINITY;
+        s_L[tid] = 0.0f;
+      }
+      __syncthreads();
+      join_shared(p);
+      for (int e = tid; e < G * D / 2; e += NTHR) {
+        float x = 0.0f, y = 0.0f;
+        add_shared(p, e, x, y);
+        const int r = e >> 6;
+        const float f = s_L[r] > 0.0f || s_L[r] != s_L[r] ? 1.0f / s_L[r] : 0.0f;
+        *reinterpret_cast<uint32_t*>(a.out + (int64_t)s_row[i] * a.out_stride + (head * G + r) * D + 2 * (e & 63)) =
+            pack2<false>(x * f, y * f);
+      }
+      if (tid < G && a.lse)
+        a.lse[(int64_t)s_row[i] * n_kv * G + head * G + tid] =
+            s_L[tid] > 0.0f || s_L[tid] != s_L[tid] ? (log2f(s_L[tid]) + (s_M[tid] - kShift)) * 0.6931471805599453f : -INFINITY;
+      __syncthreads();
+    }
   for (int i = blockIdx.x; i < n_seqs; i += gridDim.x)
-    if (s_row[i] >= 0 && s_len[i] == 0) {
+    if (s_row[i] >= 0 && s_len[i] == 0 && (!OWN || s_off[i] == 0)) {
       for (int t = 0; t < (C == 1 ? 1 : s_new[i]); ++t) {
         for (int e = tid; e < n_kv * G * D / 8; e += NTHR)
           *reinterpret_cast<uint4*>(a.out + (int64_t)(s_row[i] + t) * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
@@ -250,7 +342,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   int pid = 0;
   auto fetch_pid = [&]() {
     if (issued < n_flat && lane < n_box) {
-      const int p = (ic.ch * CH + lane * box) >> L.p_log2;
+      const int p = (ic.ch * CH + lane * box + (OWN ? s_off[ic.seq] : 0)) >> L.p_log2;  // shared tokens fill whole pages
       if (ic.ch * CH + lane * box < s_len[ic.seq]) pid = a.b.page_table[(int64_t)ic.seq * a.b.table_stride + p];
     }
   };
@@ -609,6 +701,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
           s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + (s_M[r] - kShift)) * 0.6931471805599453f : -INFINITY;
     };
     const bool whole = u.ch == 0 && fe - fs == nch;
+    SharedParts sp{0, 0, 0, nullptr};
+    const bool joins = OWN && s_off[OWN ? u.seq : 0] > 0;
+    if (joins) {
+      sp = shared_of(u.seq, u.head);
+      if (whole) join_shared(sp);
+    }
     const int64_t part = 2 * (int64_t)blockIdx.x + (u.ch == 0 ? 1 : 0);
     for (int e = tid; e < R * D / 2; e += NTHR) {
       float x = 0.0f, y = 0.0f;
@@ -618,9 +716,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
         x += v.x;
         y += v.y;
       }
-      if (whole)
+      if (whole) {
+        if (joins) add_shared(sp, e, x, y);
         put(e, x, y);
-      else
+      } else
         *reinterpret_cast<float2*>(a.part_acc + part * R * D + 2 * e) = make_float2(x, y);
     }
     if (tid < R) {
@@ -662,9 +761,16 @@ __global__ void __launch_bounds__(NW * 32, 1)
           }
         }
         __syncthreads();
+        float own[8];  // the maxima before the shared parts'
+        if (OWN)
+          for (int h = 0; h < 8; ++h) own[h] = s_M[h];
+        if (joins) {
+          __syncthreads();
+          join_shared(sp);
+        }
         for (int e = tid; e < R * D / 2; e += NTHR) {
           const int h = e >> 6;
-          const float M = s_M[h];
+          const float M = OWN ? own[h] : s_M[h];
           float x = 0.0f, y = 0.0f;
 #pragma unroll 8
           for (int i = 0; i < parts; ++i) {
@@ -674,6 +780,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             x = fmaf(v.x, f, x);
             y = fmaf(v.y, f, y);
           }
+          if (joins) add_shared(sp, e, x, y);
           put(e, x, y);
         }
         if (tid < R) put_lse(tid);
@@ -690,14 +797,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
   }
 }
 
-template <bool E4M3, int NW, int NS, int C = 1, bool MASS = false>
+template <bool E4M3, int NW, int NS, int C = 1, DecodeMode MODE = kPlain>
 cudaError_t launch(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, cudaStream_t s) {
   const int bytes = DecodeSmem<E4M3, NW, NS, C>::bytes(L.G);
   int sms = 0;
-  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, NS, C, MASS>, bytes, NW * 32, nullptr, &sms);
+  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, NS, C, MODE>, bytes, NW * 32, nullptr, &sms);
   if (e != cudaSuccess) return e;
   const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
-  return launch_pdl(k_paged_decode<E4M3, NW, NS, C, MASS>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
+  return launch_pdl(k_paged_decode<E4M3, NW, NS, C, MODE>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
 }
 
 }  // namespace
@@ -706,7 +813,7 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
                                 const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
                                 float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s) {
   DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, causal ? 1 : 0,
-               w.part_acc, w.part_ml, w.counters, nullptr, nullptr};
+               w.part_acc, w.part_ml, w.counters, nullptr, nullptr, nullptr, nullptr, nullptr};
   // 16 rows: 64 accumulators more a lane, eight warps of 255 registers.
   if (several) return L.e4m3 ? launch<true, 8, 2, 2>(L, maps, a, s) : launch<false, 8, 2, 2>(L, maps, a, s);
   // 12 warps of two 8 KB stages: the conversion of a chunk takes a warp about
@@ -718,13 +825,22 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
   return L.e4m3 ? launch<true, 12, 2>(L, maps, a, s) : launch<false, 12, 2>(L, maps, a, s);
 }
 
+cudaError_t launch_paged_decode_own(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
+                                    const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
+                                    uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s) {
+  const DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 0,
+                     w.part_acc, w.part_ml, w.counters, w.shared, w.prefill_part, w.row_part, nullptr, nullptr};
+  if (L.G == 8) return L.e4m3 ? launch<true, 10, 2, 1, kOwn>(L, maps, a, s) : launch<false, 10, 2, 1, kOwn>(L, maps, a, s);
+  return L.e4m3 ? launch<true, 12, 2, 1, kOwn>(L, maps, a, s) : launch<false, 12, 2, 1, kOwn>(L, maps, a, s);
+}
+
 cudaError_t launch_paged_decode_mass(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                      const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
                                      uint16_t* out, int64_t out_stride, float* lse, float* logits, cudaStream_t s) {
   const DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 0,
-                     w.part_acc, w.part_ml, w.counters, logits, w.lse2};
-  if (L.G == 8) return L.e4m3 ? launch<true, 10, 2, 1, true>(L, maps, a, s) : launch<false, 10, 2, 1, true>(L, maps, a, s);
-  return L.e4m3 ? launch<true, 12, 2, 1, true>(L, maps, a, s) : launch<false, 12, 2, 1, true>(L, maps, a, s);
+                     w.part_acc, w.part_ml, w.counters, nullptr, nullptr, nullptr, logits, w.lse2};
+  if (L.G == 8) return L.e4m3 ? launch<true, 10, 2, 1, kMass>(L, maps, a, s) : launch<false, 10, 2, 1, kMass>(L, maps, a, s);
+  return L.e4m3 ? launch<true, 12, 2, 1, kMass>(L, maps, a, s) : launch<false, 12, 2, 1, kMass>(L, maps, a, s);
 }
 
 }  // namespace mk

@@ -603,8 +603,8 @@ typedef struct mk_paged_prefix {
  * each).  Shared values must be finite: a NaN or infinity among them reaches
  * every sequence of its group, also where its weight is 0.
  * MK_EDEVICE: as mk_paged_decode_attn, and cu_group not ascending or out of
- * range or a negative prefix_len (that group shares nothing; its rows are
- * right all the same). */
+ * range or a negative prefix_len (nothing is shared then; the rows are right
+ * all the same). */
 mk_status mk_paged_prefix_attn(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const mk_paged_prefix* prefix,
                                const void* q, int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
                                mk_stream stream);
