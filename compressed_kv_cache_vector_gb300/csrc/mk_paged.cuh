@@ -53,11 +53,12 @@ struct PagedShared {
     int32_t steps, cost;
   } seq[MK_MAX_CALL_SEQS];
 };
-// A part of a row: 128 weighted values, their reference and the weights' sum.
+// A part of a row: 128 weighted values, their reference and the weights' sum
+// (and two unused words: rows begin on 16 bytes).
 // The parts of a cell that lies in several CTAs' runs go by CTA: 128 rows, one
 // slot for a cell that begins in the run and one for a cell that does not.
 // Those of a whole cell go by sequence and head.
-constexpr int kPagedRowPart = MK_HEAD_DIM + 2;
+constexpr int kPagedRowPart = MK_HEAD_DIM + 4;
 constexpr int kPagedPrefixPart = 128 * kPagedRowPart;
 // The workspace's parts that the attention kernels use.
 struct PagedScratch {

@@ -38,6 +38,8 @@
 // 96% of the copy rate), 128K 56 us (4.7 TB/s: about 15 us are launch, ramp and
 // joining), 4K 12 us, 64 ragged sequences 206 us (5.3 TB/s), 4 x 32K bf16 93 us
 // (5.8 TB/s).  Reads its algorithmic bytes once (268.9 MB of DRAM reads at 128K).
+#include <algorithm>
+
 #include "mk_paged.cuh"
 
 namespace mk {
@@ -45,6 +47,7 @@ namespace mk {
 namespace {
 
 constexpr int kStageBytes = 8192;
+constexpr int kOwnWarps = 1;
 
 struct DecodeArgs {
   mk_paged_batch b;
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   __shared__ int64_t s_pre[MK_MAX_CALL_SEQS + 1];
   __shared__ int s_len[MK_MAX_CALL_SEQS], s_row[MK_MAX_CALL_SEQS], s_new[C == 1 ? 1 : MK_MAX_CALL_SEQS];
   __shared__ int s_off[OWN ? MK_MAX_CALL_SEQS : 1];  // shared tokens
-  __shared__ float s_mul[OWN ? 8 : 1];
+  __shared__ float s_mul[OWN ? 8 : 1], s_ref[OWN ? 8 : 1];
   __shared__ int64_t s_wsum[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NS];
   __shared__ __align__(16) float s_sc[NW][NS][4];  // k scale of box 0, 1; v scale of box 0, 1
@@ -145,6 +148,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
   pdl_wait();
   pdl_trigger();
   if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;  // one thread's reading for the CTA
+  // What a row's weights are taken from, by its maximum.  OWN: rounded up, so
+  // that no weight passes 2^kShift however large the logits are, and parts are
+  // joined by it.
+  auto less = [](float m) { return OWN ? __fsub_ru(m, kShift) : m - kShift; };
+  auto apart = [&](float m, float M) { return OWN ? less(m) - less(M) : m - M; };
 
   int units = 0;  // (sequence, kv head) pairs with keys
   for (int i0 = 0; i0 < n_seqs; i0 += NTHR) {
@@ -212,11 +220,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
                          : a.shared_part + (2 * (int64_t)(p.b_lo + i) + (i == 0 ? 1 : 0)) * kPagedPrefixPart + p.row * kPagedRowPart) +
            r * kPagedRowPart;
   };
-  // The rows' maxima and sums with the shared parts' (s_M, s_L), and what the
-  // rows' own values are multiplied by (s_mul).  The whole CTA, between barriers.
+  // The rows' references and sums with the shared parts' (s_ref, s_L), and what
+  // the rows' own values are multiplied by (s_mul).  The whole CTA, between barriers.
   auto join_shared = [&](const SharedParts& p) {
     for (int r = warp; r < G; r += NW) {
-      const float own = s_M[r] == -INFINITY ? -INFINITY : s_M[r] - kShift;
+      const float own = less(s_M[r]);
       float M = own, S = 0.0f;
       for (int i = lane; i < p.parts; i += 32) M = fmaxf(M, __ldcg(shared_at(p, i, r) + D));
       M = warp_max(M);
@@ -230,14 +238,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
         const float f = own == -INFINITY ? 0.0f : ex2(own - M);
         s_mul[r] = f;
         s_L[r] = S + s_L[r] * (own == -INFINITY ? 1.0f : f);
-        s_M[r] = M + kShift;
+        s_ref[r] = M;
       }
     }
     __syncthreads();
   };
   auto add_shared = [&](const SharedParts& p, int e, float& x, float& y) {
     const int r = e >> 6;
-    const float M = s_M[r] - kShift;
+    const float M = s_ref[r];
     x *= s_mul[r];
     y *= s_mul[r];
 #pragma unroll 8
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       }
       if (tid < G && a.lse)
         a.lse[(int64_t)s_row[i] * n_kv * G + head * G + tid] =
-            s_L[tid] > 0.0f || s_L[tid] != s_L[tid] ? (log2f(s_L[tid]) + (s_M[tid] - kShift)) * 0.6931471805599453f : -INFINITY;
+            s_L[tid] > 0.0f || s_L[tid] != s_L[tid] ? (log2f(s_L[tid]) + s_ref[tid]) * 0.6931471805599453f : -INFINITY;
       __syncthreads();
     }
   for (int i = blockIdx.x; i < n_seqs; i += gridDim.x)
@@ -568,7 +576,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
           mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
           if (__any_sync(FULL, mx > m[i])) {
             const float mn = fmaxf(m[i], mx);
-            const float cr = m[i] == -INFINITY ? 0.0f : ex2(m[i] - mn);
+            const float cr = m[i] == -INFINITY ? 0.0f : ex2(apart(m[i], mn));
             m[i] = mn;
             l[i] *= cr;
             const float c0f = __shfl_sync(FULL, cr, 8 * c), c1f = __shfl_sync(FULL, cr, 8 * c + 4);
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
               o[i][n][3] *= c1f;
             }
           }
-          const float ms = (m[i] == -INFINITY ? 0.0f : m[i]) - kShift;
+          const float ms = less(m[i] == -INFINITY ? 0.0f : m[i]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             z[i][nt][0] = ex2(z[i][nt][0] - ms);
@@ -658,7 +666,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       float M = -INFINITY, S = 0.0f;
       for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][tid][0]);
       // A part whose maximum is -infinity has no weights, or only NaN: its sum, 0 or NaN, counts as it is.
-      for (int w = 0; w < NW; ++w) S += s_ml[w][tid][1] * (s_ml[w][tid][0] == -INFINITY ? 1.0f : ex2(s_ml[w][tid][0] - M));
+      for (int w = 0; w < NW; ++w) S += s_ml[w][tid][1] * (s_ml[w][tid][0] == -INFINITY ? 1.0f : ex2(apart(s_ml[w][tid][0], M)));
       s_M[tid] = M;
       s_L[tid] = S;
     }
@@ -670,7 +678,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         if (h < R) {
           float M = -INFINITY;
           for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][h][0]);
-          const float f = s_ml[warp][h][0] == -INFINITY ? 0.0f : ex2(s_ml[warp][h][0] - M);
+          const float f = s_ml[warp][h][0] == -INFINITY ? 0.0f : ex2(apart(s_ml[warp][h][0], M));
           float* to = s_acc + (warp * R + h) * D;
 #pragma unroll
           for (int n = 0; n < 8; ++n) {
@@ -684,6 +692,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
       }
     __syncthreads();
+    const bool joins = OWN && s_off[OWN ? u.seq : 0] > 0;
     // Row x of the result (where it has one): its output, and its lse.
     auto put = [&](int e, float x, float y) {
       const int r = e >> 6;
@@ -698,11 +707,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
             s_L[r] > 0.0f || s_L[r] != s_L[r] ? log2f(s_L[r]) + (s_M[r] - kShift) : INFINITY;
       if (!a.lse || !live_row(r)) return;
       a.lse[(int64_t)(row + tok_of(r)) * n_kv * G + head_of(r)] =
-          s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + (s_M[r] - kShift)) * 0.6931471805599453f : -INFINITY;
+          s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + (joins ? s_ref[OWN ? r : 0] : less(s_M[r]))) * 0.6931471805599453f
+                                            : -INFINITY;
     };
     const bool whole = u.ch == 0 && fe - fs == nch;
     SharedParts sp{0, 0, 0, nullptr};
-    const bool joins = OWN && s_off[OWN ? u.seq : 0] > 0;
     if (joins) {
       sp = shared_of(u.seq, u.head);
       if (whole) join_shared(sp);
@@ -752,7 +761,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
           M = warp_max(M);
           for (int i = lane; i < parts; i += 32) {
             const float mi = __ldcg(a.part_ml + (slot(i) * R + h) * 2);
-            S += __ldcg(a.part_ml + (slot(i) * R + h) * 2 + 1) * (mi == -INFINITY ? 1.0f : ex2(mi - M));
+            S += __ldcg(a.part_ml + (slot(i) * R + h) * 2 + 1) * (mi == -INFINITY ? 1.0f : ex2(apart(mi, M)));
           }
           S = warp_sum(S);
           if (lane == 0) {
@@ -761,21 +770,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
           }
         }
         __syncthreads();
-        float own[8];  // the maxima before the shared parts'
-        if (OWN)
-          for (int h = 0; h < 8; ++h) own[h] = s_M[h];
-        if (joins) {
-          __syncthreads();
-          join_shared(sp);
-        }
+        if (joins) join_shared(sp);
         for (int e = tid; e < R * D / 2; e += NTHR) {
           const int h = e >> 6;
-          const float M = OWN ? own[h] : s_M[h];
+          const float M = s_M[h];
           float x = 0.0f, y = 0.0f;
 #pragma unroll 8
           for (int i = 0; i < parts; ++i) {
             const float mi = __ldcg(a.part_ml + (slot(i) * R + h) * 2);
-            const float f = mi == -INFINITY ? 0.0f : ex2(mi - M);
+            const float f = mi == -INFINITY ? 0.0f : ex2(apart(mi, M));
             const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_acc + slot(i) * R * D + 2 * e));
             x = fmaf(v.x, f, x);
             y = fmaf(v.y, f, y);
@@ -807,6 +810,22 @@ cudaError_t launch(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, cud
   return launch_pdl(k_paged_decode<E4M3, NW, NS, C, MODE>, dim3(grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
 }
 
+// The tokens that sequences do not share are few and in many units: CTAs of one
+// warp, as many as fit, each with a run of its own, so that nobody waits for
+// the joining of warps.
+template <bool E4M3>
+cudaError_t launch_own(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, int64_t part_floats, cudaStream_t s) {
+  constexpr int NW = kOwnWarps;
+  const int bytes = DecodeSmem<E4M3, NW, 2, 1>::bytes(L.G);
+  int occ = 0, sms = 0;
+  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, 2, 1, kOwn>, bytes, NW * 32, &occ, &sms);
+  if (e != cudaSuccess) return e;
+  const int64_t slot = (int64_t)L.G * (D + 2);
+  const int64_t grid = std::min<int64_t>((int64_t)(sms > 0 ? sms : 128) * occ, part_floats / (2 * slot));
+  a.part_ml = a.part_acc + 2 * grid * L.G * D;
+  return launch_pdl(k_paged_decode<E4M3, NW, 2, 1, kOwn>, dim3((unsigned)grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
@@ -828,10 +847,12 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
 cudaError_t launch_paged_decode_own(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                     const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
                                     uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s) {
+  // Behind the shared pages' parts.
+  const int64_t shared = (int64_t)2 * kPagedMaxCtas * kPagedPrefixPart;
   const DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 0,
-                     w.part_acc, w.part_ml, w.counters, w.shared, w.prefill_part, w.row_part, nullptr, nullptr};
-  if (L.G == 8) return L.e4m3 ? launch<true, 10, 2, 1, kOwn>(L, maps, a, s) : launch<false, 10, 2, 1, kOwn>(L, maps, a, s);
-  return L.e4m3 ? launch<true, 12, 2, 1, kOwn>(L, maps, a, s) : launch<false, 12, 2, 1, kOwn>(L, maps, a, s);
+                     w.prefill_part + shared, nullptr, w.counters, w.shared, w.prefill_part, w.row_part, nullptr, nullptr};
+  const int64_t left = paged_prefill_part_floats() - shared;
+  return L.e4m3 ? launch_own<true>(L, maps, a, left, s) : launch_own<false>(L, maps, a, left, s);
 }
 
 cudaError_t launch_paged_decode_mass(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,

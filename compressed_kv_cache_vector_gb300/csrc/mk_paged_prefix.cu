@@ -6,21 +6,21 @@
 // Mathematics as in mk_paged_decode.cu; every row of a group sees all keys.
 //
 // What bounds it: HBM up to about a hundred rows of a kv head (every page is
-// read once for 128 rows), the tensor cores and the exponentials beyond.  The
-// rows of a decode step are few and ragged, so the keys take the 128 rows of a
-// product and the query rows its columns: S^T = K Q^T and O^T = V^T P with 64
-// or 128 columns, no row of the tensor cores empty however few the queries.  A
-// thread has one key of a step and one half of the columns:
-//  * a row's running maximum is needed only as a bound.  A step first looks
-//    whether any logit passes its row's by 2^4 (fp16 weights) or 2^8 (bf16):
-//    one comparison a logit and one vote of four warps.  Only then are maxima
-//    formed over the threads and the accumulator rescaled.
-//  * a row's sum stays in the threads, one number a key and row, until the end.
-//  * the weights go to shared memory as the B operand, as they come.
-// One CTA per SM:
-//  * warps 0-3 and 4-7: softmax of the first and the second half of the columns;
-//  * warps 8-11 (e4m3): codes to bf16 (keys) and fp16 (values), both exact;
-//  * warp 12 issues the products, warp 13 the copies (a ring of four tiles).
+// read once for 128 rows), the tensor cores and shared memory's rate beyond.
+// 128 rows are one accumulator, so there is one row tile and not two in turn
+// (mk_paged_prefill.cu): two groups of four warps take the steps of 128 keys in
+// turn instead, each with logits, weights and an accumulator of its own in
+// tensor memory, so that one group's products run while the other forms its
+// weights; their halves are joined when the cell ends.  A thread has one row:
+// its maximum and sum need no exchange.  One CTA per SM:
+//  * warps 0-3 and 4-7: softmax of the even and the odd steps;
+//  * warps 8-11 (e4m3): value codes to fp16, exact, two tiles;
+//  * warp 12 issues the products, warp 13 the copies.
+//  * e4m3 keys are multiplied as they are: a query row, brought to [128, 256) by
+//    a power of two, is the sum of an e4m3 and an e5m2 number each, exact but
+//    for channels below 2^-15 of the row's largest, which are off by at most
+//    2^-20 of it.  That spares the keys' conversion, which shared memory's rate
+//    would pay for (16 KB read and 32 KB written a step).
 //  * Work split on the device: all (group, 128 rows, kv head) cells' steps of
 //    128 keys in a row, cut into equal runs, one a CTA.
 #include "mk_paged_tc.cuh"
@@ -33,15 +33,22 @@ constexpr int kRows = 128;                // rows of a cell
 constexpr int kKeys = 128;                // keys of a step
 constexpr int kTile = kKeys * D * 2;      // 32 KB: a 16-bit tile
 constexpr int kHalf = kTile / 2;          // its channels 0-63, then 64-127
-constexpr int kRaw = kKeys * D;           // 16 KB: a tile of codes
 constexpr int kThreads = 512;
 constexpr int kCellCost = 3;              // a cell's queries and result take as long as this many steps
 constexpr int kMinRun = 2;                // shortest run of a CTA, in steps
-constexpr int kSmem = 1024 + 6 * kTile;   // queries, weights, keys and values
+constexpr int kSmem = 1024 + 6 * kTile;   // queries, keys and values
+// Tiles on their way: of keys and of values (e4m3: codes, 16 KB each, besides
+// the two tiles of values in fp16).
+template <bool E4M3>
+struct Ring {
+  static constexpr int tile = E4M3 ? kTile / 2 : kTile, keys = E4M3 ? 3 : 2, values = 3;
+};
 // Registers of a thread of each four warps; the launch gives 128 each.
-constexpr int kSoftmaxRegs = 168, kLoadRegs = 112, kIssueRegs = 64;
-static_assert(2 * kSoftmaxRegs + kLoadRegs + kIssueRegs == 4 * 128, "register shares");
-constexpr float kNone = 1e30f;            // stands for a bound that no logit has set yet
+template <bool E4M3>
+struct Regs {
+  static constexpr int softmax = 168, load = 112, issue = 64;
+  static_assert(2 * softmax + load + issue == 4 * 128, "register shares");
+};
 
 struct PrefixArgs {
   mk_paged_batch b;
@@ -67,87 +74,72 @@ struct Shared {
   Cursor start;
   int64_t f0, per;
   int span, bad;
-  uint64_t q_full, s_full[2], s_free[2], p_full[2], pv_done[2], done;
-  uint64_t kv_full[4], kv_free[4];          // the ring of copies
-  uint64_t k_full, k_free, v_full, v_free;  // e4m3: the tiles formed from it
-  uint64_t met[2];
-  __align__(16) float nm[kRows];            // shift - bound of each row
-  float m[kRows], f[kRows], top[2][4][kRows / 2];
-  int vote[2][2][4];
-  // e4m3, per 16 keys of a step, ring of 4 steps: {k scale, log2 v scale}, 1 / v scale
-  __align__(16) float2 kb[4][8];
-  float inv[4][8];
+  uint64_t q_full, s_full[2], p_half[2], p_full[2], o_full, met, done;
+  uint64_t k_full[3], k_free[3], v_full[3], v_free[3];  // the copies' rings
+  uint64_t c_full[2], c_free[2];                        // e4m3: values in fp16
+  float ml[2][kRows][2];                                // the two groups' maxima and sums
+  // e4m3, per 16 keys of a step, ring of 8 steps: {k scale, log2 v scale}, 1 / v scale
+  __align__(16) float2 kb[8][8];
+  float inv[8][8];
   uint32_t tmem;
   volatile int dead;
 };
 
-// D (128 x N, fp32) of A and B of one 16-bit type, each along its rows' own
-// direction where the flag is set.
-__device__ __forceinline__ uint32_t idesc_of(int bf16, int a_mn, int b_mn, int n) {
-  return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&v)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
-                 "+r"(v[15])::"memory");
-}
-// Over the 32 lanes and 16 columns each: lane c < 16 (and 16 + c) gets the
-// result of column c.
-template <typename Op>
-__device__ __forceinline__ float across16(float (&x)[16], int lane, Op op) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    const bool up = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float give = up ? x[i] : x[i + o], keep = up ? x[i + o] : x[i];
-      x[i] = op(keep, __shfl_xor_sync(FULL, give, o));
+// A place in a ring of N tiles and the parity of its phase.
+template <int N>
+struct Place {
+  unsigned slot = 0, phase = 0;
+  __device__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1u;
     }
   }
-  return op(x[0], __shfl_xor_sync(FULL, x[0], 16));
+};
+
+// 8-bit products: A e4m3 (0) or e5m2 (1), B e4m3, 32 channels a step.
+__host__ __device__ constexpr uint32_t idesc8(int a_e5m2) {
+  return (1u << 4) | ((uint32_t)a_e5m2 << 7) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void umma8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
 }
 
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_prefix(PagedLayer L, PrefixArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   constexpr float kShift = E4M3 ? 10.0f : 0.0f;  // weights times 2^kShift before their rounding
-  constexpr float kLazy = E4M3 ? 4.0f : 8.0f;    // how far logits may pass a row's bound
+  constexpr float kLazy = E4M3 ? 4.0f : 8.0f;    // how far logits may pass the running maximum
+  constexpr int NK = Ring<E4M3>::keys, NV = Ring<E4M3>::values, kSlot = Ring<E4M3>::tile;
   extern __shared__ unsigned char dyn[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-  // bf16: a ring of four tiles (K, V, K, V).  e4m3: four tiles of codes, one of keys, one of values.
-  const uint32_t sq = base, sp = base + kTile, ring = base + 2 * kTile, sk = ring + 4 * kRaw, sv = sk + kTile;
-  constexpr int kSlot = E4M3 ? kRaw : kTile;
+  const uint32_t sq = base, sk = base + kTile, sv = sk + NK * kSlot, sc = sv + NV * kSlot;
+  static_assert(kTile + (NK + NV) * kSlot + (E4M3 ? 2 * kTile : 0) <= 6 * kTile, "shared memory");
   const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv, n_groups = a.p.n_groups, members = kRows / G;
 
   if (tid == 0) {
-    mbar_init(&sh.q_full, 8);
+    mbar_init(&sh.q_full, E4M3 ? 12 : 8);
+    mbar_init(&sh.o_full, 1);
+    mbar_init(&sh.met, 8);
+    mbar_init(&sh.done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_free[i], 8);
-      mbar_init(&sh.p_full[i], 8);
-      mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.met[i], 4);
+      mbar_init(&sh.p_half[i], 4);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.c_full[i], 4);
+      mbar_init(&sh.c_free[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh.kv_full[i], 1);
-      mbar_init(&sh.kv_free[i], E4M3 ? 4 : 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_free[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_free[i], E4M3 ? 4 : 1);
     }
-    mbar_init(&sh.k_full, 4);
-    mbar_init(&sh.v_full, 4);
-    mbar_init(&sh.k_free, 1);
-    mbar_init(&sh.v_free, 1);
-    mbar_init(&sh.done, 1);
     sh.dead = 0;
     sh.bad = 0;
   }
@@ -276,48 +268,72 @@ __global__ void __launch_bounds__(kThreads, 1)
   int j0, j1;
 
   if (warp >= 12) {
-    fewer_registers<kIssueRegs>();
+    fewer_registers<Regs<E4M3>::issue>();
     if (warp == 12) {
-      // ---- issues the products ----
+      // ---- issues the products: a step's logits before the values of the one before it ----
       if (elect_one()) {
-        unsigned c = 0, ic = 0;
+        unsigned c = 0, ic = 0;  // steps and cells so far
         bool ok = true;
-        const uint64_t dq = sw128_desc(sq, 16);
+        Place<NK> kp;
+        Place<NV> vp;
+        unsigned ph = 0;  // bit w: phase of p_half[w] and p_full[w]
+        const uint64_t dq = sw128_desc(sq, 16), dl = sw128_desc(sq + kHalf, 16);
         for (Cursor k = sh.start; ok && k.rel < sh.span; next(k)) {
           if (!steps(k, j0, j1)) continue;
-          const int n = rows_of(k) <= 64 ? 64 : 128, len = sh.len[k.group];
-          const uint32_t id_s = idesc_of(1, 0, 0, n), id_o = idesc_of(!E4M3, 1, 1, n);
+          const int len = sh.len[k.group];
           ok = wait(&sh.q_full, ic++ & 1);
           for (int j = j0 - 1; ok && j < j1; ++j) {
-            if (j + 1 < j1) {  // the next step's logits
-              const unsigned s = j < j0 ? c : c + 1, slot = (2 * s) & 3;
-              ok = wait(E4M3 ? &sh.k_full : &sh.kv_full[slot], E4M3 ? s & 1 : (s >> 1) & 1) &&
-                   (s < 2 || wait(&sh.s_free[s & 1], ((s >> 1) - 1) & 1));
+            if (j + 1 < j1) {
+              const unsigned w = (j < j0 ? c : c + 1) & 1;
+              ok = wait(&sh.k_full[kp.slot], kp.phase);
               if (!ok) break;
               tmem_fence_after_sync();
-              const uint64_t d = sw128_desc(E4M3 ? sk : ring + slot * kSlot, 16);
+              const uint64_t d = sw128_desc(sk + kp.slot * kSlot, 16);
+              if (E4M3) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
-                umma_ss(tmem + (s & 1) * 128, d + o, dq + o, id_s, i > 0);
+                for (int i = 0; i < 4; ++i) umma8(tmem + w * 128, dq + i * 2, d + i * 2, idesc8(0), i > 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) umma8(tmem + w * 128, dl + i * 2, d + i * 2, idesc8(1), 1);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+                  umma_ss(tmem + w * 128, dq + o, d + o, idesc(1, 0), i > 0);
+                }
               }
-              umma_commit(&sh.s_full[s & 1]);
-              umma_commit(E4M3 ? &sh.k_free : &sh.kv_free[slot]);
+              umma_commit(&sh.s_full[w]);
+              umma_commit(&sh.k_free[kp.slot]);
+              kp.next();
             }
             if (j < j0) continue;
-            const unsigned slot = (2 * c + 1) & 3;
-            ok = wait(E4M3 ? &sh.v_full : &sh.kv_full[slot], E4M3 ? c & 1 : (c >> 1) & 1) && wait(&sh.p_full[c & 1], (c >> 1) & 1);
+            const unsigned w = c & 1;
+            ok = (E4M3 ? wait(&sh.c_full[w], (c >> 1) & 1) : wait(&sh.v_full[vp.slot], vp.phase)) && wait(&sh.p_half[w], (ph >> w) & 1);
             if (!ok) break;
             tmem_fence_after_sync();
-            const uint64_t dv = sw128_desc(E4M3 ? sv : ring + slot * kSlot, kHalf);
-            const uint64_t dp = sw128_desc(sp + (n == 64 ? (c & 1) * kHalf : 0), kHalf);
-            const int blocks = min(8, (len - j * kKeys) / 16);  // whole pages: 16 keys each, none hidden
+            const uint64_t d = sw128_desc(E4M3 ? sc + w * kTile : sv + vp.slot * kSlot, kHalf);
+            const int blocks = (len - j * kKeys) / 16;  // whole pages: 16 keys each, none hidden
+            const uint32_t o = tmem + 256 + w * 128, p = tmem + w * 128;
+            const int more = j >= j0 + 2;  // the group has an accumulator
+            if (blocks >= 8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) umma_ts(o, p + i * 8, d + i * (2048 >> 4), idesc(!E4M3, 1), more || i > 0);
+              ok = wait(&sh.p_full[w], (ph >> w) & 1);
+              if (!ok) break;
+              tmem_fence_after_sync();
+#pragma unroll
+              for (int i = 4; i < 8; ++i) umma_ts(o, p + i * 8, d + i * (2048 >> 4), idesc(!E4M3, 1), 1);
+            } else {
+              ok = wait(&sh.p_full[w], (ph >> w) & 1);
+              if (!ok) break;
+              tmem_fence_after_sync();
 #pragma unroll 1
-            for (int i = 0; i < blocks; ++i)
-              umma_ss(tmem + 256, dv + i * (2048 >> 4), dp + i * (2048 >> 4), id_o, j > j0 || i > 0);
-            umma_commit(&sh.pv_done[c & 1]);
-            umma_commit(E4M3 ? &sh.v_free : &sh.kv_free[slot]);
+              for (int i = 0; i < blocks; ++i) umma_ts(o, p + i * 8, d + i * (2048 >> 4), idesc(!E4M3, 1), more || i > 0);
+            }
+            ph ^= 1u << w;
+            umma_commit(E4M3 ? &sh.c_free[w] : &sh.v_free[vp.slot]);
+            vp.next();
             ++c;
+            if (j == j1 - 1) umma_commit(&sh.o_full);
           }
         }
         umma_commit(&sh.done);
@@ -326,8 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       (void)paged_wait_warp(&sh.done, 0);
     } else if (warp == 13) {
-      // ---- issues the copies: keys, then values of each step ----
-      unsigned c = 0;  // tiles so far
+      // ---- issues the copies, in the order of the products ----
+      Place<NK> kp;
+      Place<NV> vp;
+      unsigned nk = 0, nv = 0;
       bool ok = true;
       const int box = !E4M3 || L.P < 32 ? 16 : 32, lanes = kKeys / box;
       for (Cursor k = sh.start; ok && k.rel < sh.span; next(k)) {
@@ -338,54 +356,70 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tok = j * kKeys + lane * box;
           return lane < lanes && j < j1 && tok < len ? table[tok >> L.p_log2] : -1;
         };
-        int pg_next = fetch(j0);
-        for (int j = j0; ok && j < j1; ++j) {
-          int pg = pg_next;
-          pg_next = fetch(j + 1);
+        auto copy = [&](const CUtensorMap* map, int j, int pg, uint64_t* full, uint64_t* free, bool first, unsigned phase, uint32_t to) {
+          ok = ok && (first || __all_sync(FULL, wait(free, phase ^ 1u)));
+          if (!ok) return;
           const bool in = lane < lanes && j * kKeys + lane * box < len;
-          if (in && (pg < 0 || pg >= L.n_pages)) {
-            paged_error(L, ERR_PAGED_PAGE, sh.table_row[k.group], pg);
-            pg = 0;
-          }
           const int boxes = __popc(__ballot_sync(FULL, in));
-          const int y = k.head * L.P + ((j * kKeys + lane * box) & (L.P - 1)), z = a.layer_page0 + pg;
-#pragma unroll
-          for (int t = 0; t < 2; ++t, ++c) {
-            ok = ok && (c < 4 || __all_sync(FULL, wait(&sh.kv_free[c & 3], ((c >> 2) - 1) & 1)));
-            if (!ok) break;
-            uint64_t* bar = &sh.kv_full[c & 3];
-            if (lane == 0) mbar_expect_tx(bar, boxes * box * D * (E4M3 ? 1 : 2));
-            __syncwarp();
-            if (in) {
-              const uint32_t to = ring + (c & 3) * kSlot + lane * box * 128;
-              const CUtensorMap* map = t ? &vmap : &kmap;
-              tma3(to, map, 0, y, z, bar);
-              if (!E4M3) tma3(to + kHalf, map, 64, y, z, bar);
-            }
+          if (lane == 0) mbar_expect_tx(full, boxes * box * D * (E4M3 ? 1 : 2));
+          __syncwarp();
+          if (in) {
+            const int y = k.head * L.P + ((j * kKeys + lane * box) & (L.P - 1)), z = a.layer_page0 + pg;
+            tma3(to + lane * box * 128, map, 0, y, z, full);
+            if (!E4M3) tma3(to + kHalf + lane * box * 128, map, 64, y, z, full);
           }
+        };
+        auto checked = [&](int j, int pg) {
+          if (lane < lanes && j < j1 && j * kKeys + lane * box < len && (pg < 0 || pg >= L.n_pages)) {
+            paged_error(L, ERR_PAGED_PAGE, sh.table_row[k.group], pg);
+            return 0;
+          }
+          return pg;
+        };
+        int pg = 0, pg_next = checked(j0, fetch(j0)), pg_after = fetch(j0 + 1);  // of steps j, j + 1, j + 2
+        for (int j = j0 - 1; ok && j < j1; ++j) {
+          if (j + 1 < j1) {
+            copy(&kmap, j + 1, pg_next, &sh.k_full[kp.slot], &sh.k_free[kp.slot], nk < NK, kp.phase, sk + kp.slot * kSlot);
+            if (ok) kp.next(), ++nk;
+          }
+          if (j >= j0) {
+            copy(&vmap, j, pg, &sh.v_full[vp.slot], &sh.v_free[vp.slot], nv < NV, vp.phase, sv + vp.slot * kSlot);
+            if (ok) vp.next(), ++nv;
+          }
+          pg = pg_next;
+          pg_next = checked(j + 2, pg_after);
+          pg_after = fetch(j + 3);
         }
       }
       // No copy is in flight when the kernel ends, also after a wait that ran out.
-      for (unsigned i = c < 4 ? 0 : c - 4; i < c; ++i) (void)paged_wait_warp(&sh.kv_full[i & 3], (i >> 2) & 1);
+      for (unsigned i = 0; i < NK && i < nk; ++i) {
+        const unsigned at = nk - 1 - i;
+        (void)paged_wait_warp(&sh.k_full[at % NK], (at / NK) & 1);
+      }
+      for (unsigned i = 0; i < NV && i < nv; ++i) {
+        const unsigned at = nv - 1 - i;
+        (void)paged_wait_warp(&sh.v_full[at % NV], (at / NV) & 1);
+      }
     }
   } else if (warp >= 8) {
-    fewer_registers<kLoadRegs>();
+    fewer_registers<Regs<E4M3>::load>();
     if (E4M3) {
-      // ---- codes to 16 bits ----
+      // ---- values to 16 bits ----
       // 16 codes ck of rows r + 16 i: eight neighbouring lanes are four chunks
       // of one half by two rows of different parity, whose stores meet in no bank.
       const int ck = (lane & 3) | (lane >> 1 & 4), r = (lane >> 2 & 1) | (lane >> 3 & 2) | (warp & 3) << 2, lt = tid - 256;
       const uint32_t put = (ck >> 2) * kHalf + r * 128 + ((((2 * ck) & 7) ^ (r & 7)) << 4);
       const uint32_t get = r * 128 + ((ck ^ (r & 7)) << 4);
-      unsigned c = 0;
+      unsigned c = 0, ic = 0;
       bool ok = true;
+      Place<NV> vp;
       for (Cursor k = sh.start; ok && k.rel < sh.span; next(k)) {
         if (!steps(k, j0, j1)) continue;
         const int len = sh.len[k.group];
         const int32_t* table = a.b.page_table + (int64_t)sh.table_row[k.group] * a.b.table_stride;
-        // Threads < 8: the scales of 16 keys of a step, fetched a step ahead.
+        // Threads < 8: the scales of 16 keys of a step.
         float ks = 1.0f, vs = 1.0f;
-        auto scales = [&](int j) {
+        auto fetch = [&](int j) {
           const int tok = j * kKeys + lt * 16;
           ks = vs = 1.0f;
           if (lt < 8 && j < j1 && tok < len) {
@@ -396,271 +430,313 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         };
-        scales(j0);
-        for (int j = j0; ok && j < j1; ++j, ++c) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const unsigned tile = 2 * c + t, slot = tile & 3;
-            ok = ok && __all_sync(FULL, wait(&sh.kv_full[slot], (tile >> 2) & 1)) &&
-                 (c == 0 || __all_sync(FULL, wait(t ? &sh.v_free : &sh.k_free, (c - 1) & 1)));
-            if (!ok) break;
-            const uint32_t from = ring + slot * kSlot + get, to = (t ? sv : sk) + put;
-            uint4 x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
-                           : "r"(from + i * 2048));
-            if (t == 0 && lt < 8) {
-              sh.kb[c & 3][lt] = make_float2(ks, __log2f(vs));
-              sh.inv[c & 3][lt] = __frcp_rn(vs);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-              uint32_t o[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                o[e] = e4m3_h2(w[e >> 1] >> (16 * (e & 1)));
-                if (t == 0) {
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[e]));
-                  o[e] = pack2<false>(f.x, f.y);
-                }
-              }
-              const uint32_t at = to + i * 2048;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at ^ 16), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
-            }
-            fence_proxy_async();
-            mbar_arrive_warp(&sh.kv_free[slot], lane);
-            if (lane == 0) mbar_arrive(t ? &sh.v_full : &sh.k_full);
-            if (t == 0) scales(j + 1);
+        auto leave = [&](unsigned step) {  // for the softmax of a step, before its logits can be there
+          if (lt < 8) {
+            sh.kb[step & 7][lt] = make_float2(ks, __log2f(vs));
+            sh.inv[step & 7][lt] = __frcp_rn(vs);
           }
+        };
+        fetch(j0);
+        leave(c);
+        fetch(j0 + 1);
+        leave(c + 1);
+        fetch(j0 + 2);
+        // The first two steps' scales are there: the products may begin, once
+        // those of the cell before have (its phase is complete).
+        ok = ic == 0 || __all_sync(FULL, wait(&sh.q_full, (ic - 1) & 1));
+        if (!ok) break;
+        ++ic;
+        mbar_arrive_warp(&sh.q_full, lane);
+        for (int j = j0; ok && j < j1; ++j, ++c) {
+          ok = __all_sync(FULL, wait(&sh.v_full[vp.slot], vp.phase)) &&
+               (c < 2 || __all_sync(FULL, wait(&sh.c_free[c & 1], ((c >> 1) - 1) & 1)));
+          if (!ok) break;
+          const uint32_t from = sv + vp.slot * kSlot + get, to = sc + (c & 1) * kTile + put;
+          uint4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                         : "r"(from + i * 2048));
+          leave(c + 2);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"((to + i * 2048) ^ (e * 16)), "r"(e4m3_h2(w[2 * e])),
+                           "r"(e4m3_h2(w[2 * e] >> 16)), "r"(e4m3_h2(w[2 * e + 1])), "r"(e4m3_h2(w[2 * e + 1] >> 16))
+                           : "memory");
+          }
+          fence_proxy_async();
+          mbar_arrive_warp(&sh.v_free[vp.slot], lane);
+          if (lane == 0) mbar_arrive(&sh.c_full[c & 1]);
+          vp.next();
+          fetch(j + 3);
         }
       }
     }
   } else {
-    // ---- softmax: one key a thread, half of the columns ----
-    more_registers<kSoftmaxRegs>();
-    const int w = warp >> 2, key = tid & 127;
-    const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    unsigned c = 0, meets = 0;
+    // ---- softmax: one row a thread, every other step ----
+    more_registers<Regs<E4M3>::softmax>();
+    const int w = warp >> 2, wrow = (warp & 3) * 32, row = wrow + lane;
+    const uint32_t trow = tmem + ((uint32_t)wrow << 16);
+    const uint32_t ts = trow + w * 128, to = trow + 256 + w * 128;
     bool ok = true;
-    auto meet = [&]() {  // the four warps of this half
-      mbar_arrive_warp(&sh.met[w], lane);
-      const unsigned parity = meets++ & 1;
-      return __all_sync(FULL, wait(&sh.met[w], parity)) != 0;
+    unsigned c = 0, ic = 0, ph = 0;  // steps and cells so far; bit 0: phase of s_full, bit 1: of met
+    // What the weights' exponents are taken from: rounded up, so that no weight
+    // passes 2^(kShift + kLazy) however large the logits.
+    auto less = [](float x) { return __fsub_ru(x, kShift); };
+    auto meet = [&]() {  // the eight softmax warps
+      mbar_arrive_warp(&sh.met, lane);
+      ph ^= 2u;
+      return __all_sync(FULL, wait(&sh.met, (~ph >> 1) & 1)) != 0;
     };
     for (Cursor k = sh.start; ok && k.rel < sh.span; next(k)) {
       if (!steps(k, j0, j1)) continue;
-      const int rows = rows_of(k), len = sh.len[k.group];
-      // Columns of each half, in groups of 16.
-      const int ng = rows <= 32 ? 1 : rows <= 64 ? 2 : 4, cw = ng * 16, col0 = w * cw;
-      const bool two = rows <= 64;  // two buffers of weights
-      // ---- the cell's queries: 16 lanes a row ----
+      const int rows = rows_of(k), len = sh.len[k.group], seq0 = sh.first[k.group] + k.block * members;
+      const bool live = wrow < rows;  // this warp has rows
+      float zf = fmaxf(a.scale, kTiny);
+      // ---- the cell's queries: 16 lanes a row, eight warps ----
       {
-        const int ck = tid & 15, seq0 = sh.first[k.group] + k.block * members;
-#pragma unroll
+        const int ck = lane & 15;
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-          const int row = 16 * i + (tid >> 4);
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (row < rows) {
-            const PagedSeq s = paged_seq(a.b, L.P, seq0 + (row >> g_log2), false);
+          const int x = 2 * i + (lane >> 4), r = (warp & 3) * 32 + w * 16 + x;  // this warp writes 16 of the rows
+          uint4 q = make_uint4(0, 0, 0, 0);
+          if (r < rows) {
+            const PagedSeq s = paged_seq(a.b, L.P, seq0 + (r >> g_log2), false);
             if (s.ok && s.n_new == 1 && s.len > 0)
-              x = *reinterpret_cast<const uint4*>(a.q + (int64_t)s.row0 * a.q_stride + (k.head * G + (row & (G - 1))) * D + ck * 8);
+              q = *reinterpret_cast<const uint4*>(a.q + (int64_t)s.row0 * a.q_stride + (k.head * G + (r & (G - 1))) * D + ck * 8);
           }
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(sq + (ck >> 3) * kHalf + row * 128 + (((ck & 7) ^ (row & 7)) << 4)),
-                       "r"(x.x ^ a.q_sign), "r"(x.y ^ a.q_sign), "r"(x.z ^ a.q_sign), "r"(x.w ^ a.q_sign)
-                       : "memory");
-        }
-        if (key < cw) {
-          sh.m[col0 + key] = -INFINITY;
-          sh.nm[col0 + key] = kNone;
+          const uint32_t h[4] = {q.x ^ a.q_sign, q.y ^ a.q_sign, q.z ^ a.q_sign, q.w ^ a.q_sign};
+          if (E4M3) {
+            float top = 0.0f, y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[2 * e] = __uint_as_float(h[e] << 16);
+              y[2 * e + 1] = __uint_as_float(h[e] & 0xffff0000u);
+              top = fmaxf(top, fmaxf(fabsf(y[2 * e]), fabsf(y[2 * e + 1])));
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+            if (top == INFINITY) {  // a row with an infinity has no logits: NaN there, 0 elsewhere
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] -= y[e];
+            }
+            int ex = (int)(__float_as_uint(top) >> 23) - 127 - 7;
+            ex = max(-100, min(ex, 120));
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t a2[2], b2[2];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float x0 = y[4 * e + 2 * u] * down, x1 = y[4 * e + 2 * u + 1] * down;
+                a2[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t back = e4m3_h2(a2[u]);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                b2[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0 - f.x, x1 - f.y), __NV_SATFINITE, __NV_E5M2);
+              }
+              hi[e] = a2[0] | a2[1] << 16;
+              lo[e] = b2[0] | b2[1] << 16;
+            }
+            const uint32_t at = sq + r * 128 + (((ck >> 1) ^ (r & 7)) << 4) + (ck & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + kHalf), "r"(lo[0]), "r"(lo[1]) : "memory");
+            if (ck == 0) sh.ml[0][r][0] = __uint_as_float((uint32_t)(127 + ex) << 23);
+          } else {
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(sq + (ck >> 3) * kHalf + r * 128 + (((ck & 7) ^ (r & 7)) << 4)),
+                         "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                         : "memory");
+          }
         }
         fence_proxy_async();
         mbar_arrive_warp(&sh.q_full, lane);
-        ok = meet();  // the rows' bounds are set
+        if (E4M3) {
+          if (!(ok = meet())) break;
+          zf *= sh.ml[0][row][0];
+          if (!(ok = meet())) break;  // sh.ml is free again
+        }
       }
-      uint64_t l[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) l[i] = 0;
-      for (int j = j0; ok && j < j1; ++j, ++c) {
-        const bool cut = len - j * kKeys < kKeys, in = j * kKeys + key < len;
-        ok = __all_sync(FULL, wait(&sh.s_full[c & 1], (c >> 1) & 1));
+      float m = -INFINITY, l = 0.0f;
+      bool begun = false;
+      const unsigned c_end = c + (unsigned)(j1 - j0);
+      for (int j = j0 + (int)((c ^ (unsigned)w) & 1u); j < j1; j += 2) {
+        const unsigned step = c + (unsigned)(j - j0);
+        ok = __all_sync(FULL, wait(&sh.s_full[w], ph & 1));
+        ph ^= 1u;
         if (!ok) break;
         tmem_fence_after_sync();
-        const uint32_t ts = tlane + (c & 1) * 128 + col0;
-        float kf = fmaxf(a.scale, kTiny), lv = 0.0f, inv = 1.0f;
-        if (E4M3) {
-          const float2 kb = sh.kb[c & 3][key >> 4];
-          kf = fmaxf(a.scale * kb.x, kTiny);
-          lv = kb.y;
-          inv = sh.inv[c & 3][key >> 4];
-        }
-        const uint64_t k2 = pair(kf, kf), lv2 = pair(lv, lv), inv2 = pair(inv, inv);
-        uint32_t v[2][16];
-        auto load = [&](int h) {  // columns 16 h .. are in v[h & 1], the next are asked for
-          tmem_ld_wait16(v[h & 1]);
-          if (h + 1 < ng) tmem_ld16_async(ts + (h + 1) * 16, v[(h + 1) & 1]);
-          if (cut) {
-            asm volatile("");  // a branch, not 16 selections in every step
-            if (!in) {
+        if (live) {
+          const int lim = len - j * kKeys;  // columns from here on are hidden
+          const bool cut = lim < kKeys;
+          // The logits are read twice from tensor memory, 32 columns at a time, the next ones on their way.
+          uint32_t v[2][32];
+          auto arrive = [&](int h, int hh) {
+            tmem_ld_wait(v[hh]);
+            if (h < 3) tmem_ld32_async(ts + (h + 1) * 32, v[hh ^ 1]);
+            if (cut) {
+              asm volatile("");  // a branch, not 32 selections in every step
 #pragma unroll
-              for (int i = 0; i < 16; ++i) v[h & 1][i] = 0xff800000u;
+              for (int i = 0; i < 32; ++i)
+                if (i >= lim - 32 * h) v[hh][i] = 0xff800000u;
             }
-          }
-        };
-        auto pair_at = [&](int h, int i) {
-          return pair(__uint_as_float(v[h & 1][i]), __uint_as_float(v[h & 1][i + 1]));
-        };
-        // Does a logit pass its row's bound?  The logit is rounded before the
-        // bound is taken off, here as in the maximum and the weights: one
-        // fused step would leave the largest of huge logits above its bound.
-        float top = -INFINITY;
-        tmem_ld16_async(ts, v[0]);
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (h < ng) {
-            load(h);
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float4 nm = *reinterpret_cast<const float4*>(&sh.nm[col0 + 16 * h + i]);
-              float x, y;
-              unpair(add2(fma2(pair_at(h, i), k2, lv2), pair(nm.x, nm.y)), x, y);
-              top = fmaxf(top, fmaxf(x, y));
-              unpair(add2(fma2(pair_at(h, i + 2), k2, lv2), pair(nm.z, nm.w)), x, y);
-              top = fmaxf(top, fmaxf(x, y));
-            }
-          }
-        const bool over = __any_sync(FULL, top > kShift + kLazy);
-        int* vote = sh.vote[w][meets & 1];
-        if (lane == 0) vote[warp & 3] = over;
-        if (!(ok = meet())) break;
-        if (vote[0] | vote[1] | vote[2] | vote[3]) {
-          // ---- the rows' maxima over the step's keys; bounds, sums and accumulator follow ----
-          tmem_ld16_async(ts, v[0]);
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            if (h < ng) {
-              load(h);
-              float x[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(v[h & 1][i]), kf, lv);
-              const float y = across16(x, lane, [](float p, float q) { return fmaxf(p, q); });
-              if (lane < 16) sh.top[w][warp & 3][16 * h + lane] = y;
-            }
-          if (!(ok = meet())) break;
-          if (key < cw) {
-            const float mx = fmaxf(fmaxf(sh.top[w][0][key], sh.top[w][1][key]), fmaxf(sh.top[w][2][key], sh.top[w][3][key]));
-            const float m = sh.m[col0 + key];
-            const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
-            sh.f[col0 + key] = !raise ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mx);
-            if (raise) {
-              sh.m[col0 + key] = mx;
-              sh.nm[col0 + key] = __fsub_rd(kShift, mx);  // never above it, however large
-            }
-          }
-          if (!(ok = meet())) break;
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (2 * i < cw) {
-              float x, y;
-              unpair(l[i], x, y);
-              l[i] = pair(x * sh.f[col0 + 2 * i], y * sh.f[col0 + 2 * i + 1]);
-            }
-          if (j > j0) {
-            ok = __all_sync(FULL, wait(&sh.pv_done[(c - 1) & 1], ((c - 1) >> 1) & 1));
-            if (!ok) break;
-            tmem_fence_after_sync();
+          };
+          tmem_ld32_async(ts, v[0]);
+          float mx = -INFINITY;
 #pragma unroll 1
-            for (int h = 0; h < ng; ++h) {
-              uint32_t o[16];
-              tmem_ld16(tlane + 256 + col0 + h * 16, o);
+          for (int h0 = 0; h0 < 4; h0 += 2)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.f[col0 + h * 16 + i]);
-              tmem_st16(tlane + 256 + col0 + h * 16, o);
-            }
-            tmem_wait_st();
-          }
-        }
-        // ---- the weights ----
-        const unsigned back = two ? 2 : 1;  // the step whose weights were in this buffer
-        if (c >= back) ok = __all_sync(FULL, wait(&sh.pv_done[(c - back) & 1], ((c - back) >> 1) & 1));
-        if (!ok) break;
-        const uint32_t to = sp + (two ? (c & 1) * kHalf : 0) + key * 128;
-        tmem_ld16_async(ts, v[0]);
+            for (int hh = 0; hh < 2; ++hh) {
+              const int h = h0 + hh;
+              arrive(h, hh);
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          if (h < ng) {
-            load(h);
-            if (h == ng - 1) {  // all of S is in registers
-              tmem_fence_before_sync();
-              mbar_arrive_warp(&sh.s_free[c & 1], lane);
-            }
-            uint32_t p[8];
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float4 nm = *reinterpret_cast<const float4*>(&sh.nm[col0 + 16 * h + i]);
-              float x[4];
-              unpair(add2(fma2(pair_at(h, i), k2, lv2), pair(nm.x, nm.y)), x[0], x[1]);
-              unpair(add2(fma2(pair_at(h, i + 2), k2, lv2), pair(nm.z, nm.w)), x[2], x[3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint64_t& s = l[8 * h + i / 2 + e];
-                s = E4M3 ? fma2(pair(x[2 * e], x[2 * e + 1]), inv2, s) : add2(s, pair(x[2 * e], x[2 * e + 1]));
-                p[i / 2 + e] = pack2<E4M3>(x[2 * e], x[2 * e + 1]);
+              for (int s = 0; s < 2; ++s) {  // 16 keys: one scale
+                const uint32_t* z = &v[hh][16 * s];
+                float x = max3(z[0], z[1], z[2]);
+                float y = max3(z[3], z[4], z[5]);
+                x = max3(__float_as_uint(x), z[6], z[7]);
+                y = max3(__float_as_uint(y), z[8], z[9]);
+                x = max3(__float_as_uint(x), z[10], z[11]);
+                y = max3(__float_as_uint(y), z[12], z[13]);
+                x = fmaxf(max3(__float_as_uint(x), z[14], z[15]), y);
+                if (E4M3) {
+                  const float2 kb = sh.kb[step & 7][2 * h + s];
+                  x = fmaf(x, fmaxf(zf * kb.x, kTiny), kb.y);
+                }
+                mx = fmaxf(mx, x);
               }
             }
+          tmem_ld32_async(ts, v[0]);
+          if (!E4M3) mx *= zf;
+          const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
+          if (__any_sync(FULL, raise)) {
+            const float mn = raise ? mx : m;
+            const float f = m == -INFINITY ? 0.0f : ex2(less(m) - less(mn));  // rows that stay: 2^0
+            l *= f;
+            m = mn;
+            if (begun) {
+#pragma unroll 2
+              for (int h = 0; h < 8; ++h) {
+                uint32_t x[16];
+                tmem_ld16(to + h * 16, x);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int chunk = (col0 + 16 * h) / 8 + e;  // 8 columns
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (chunk >> 3) * kHalf + (((chunk & 7) ^ (key & 7)) << 4)),
-                           "r"(p[4 * e]), "r"(p[4 * e + 1]), "r"(p[4 * e + 2]), "r"(p[4 * e + 3])
-                           : "memory");
+                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                tmem_st16(to + h * 16, x);
+              }
             }
           }
-        tmem_fence_before_sync();
-        fence_proxy_async();
-        mbar_arrive_warp(&sh.p_full[c & 1], lane);
+          const float ms = m == -INFINITY ? -kShift : less(m);
+#pragma unroll 1
+          for (int h0 = 0; h0 < 4; h0 += 2) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const int h = h0 + hh;
+              arrive(h, hh);
+              uint32_t p[16];
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                float kk = zf, bb = 0.0f;
+                if (E4M3) {
+                  const float2 kb = sh.kb[step & 7][2 * h + s];
+                  kk = fmaxf(zf * kb.x, kTiny);
+                  bb = kb.y;
+                }
+                const uint64_t k2 = pair(kk, kk), b2 = pair(bb, bb), m2 = pair(-ms, -ms);
+                uint64_t add = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t* z = &v[hh][16 * s + 2 * i];
+                  float x, y;
+                  // The logit is rounded before the maximum is taken off, as it was in the maximum:
+                  // one fused step would leave the largest of huge logits above it.
+                  unpair(add2(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), k2, b2), m2), x, y);
+                  x = ex2(x);
+                  y = ex2(y);
+                  add = add2(add, pair(x, y));
+                  p[8 * s + i] = pack2<E4M3>(x, y);
+                }
+                float x, y;
+                unpair(add, x, y);
+                l = E4M3 ? fmaf(x + y, sh.inv[step & 7][2 * h + s], l) : l + (x + y);
+              }
+              tmem_st16(ts + h * 16, p);
+            }
+            // Half of the weights are enough to begin the value product.
+            tmem_wait_st();
+            tmem_fence_before_sync();
+            mbar_arrive_warp(h0 == 0 ? &sh.p_half[w] : &sh.p_full[w], lane);
+          }
+        } else {  // no rows here: the weights may be anything
+          mbar_arrive_warp(&sh.p_half[w], lane);
+          mbar_arrive_warp(&sh.p_full[w], lane);
+        }
+        begun = true;
       }
       if (!ok) break;
-      // ---- the rows' results: a part ----
-      const bool whole = j1 - j0 == steps_of(k.group);
-      const int seq0 = sh.first[k.group] + k.block * members;
-      auto row_at = [&](int r) {
-        return whole ? a.row_part + ((int64_t)(seq0 + (r >> g_log2)) * n_kv * G + k.head * G + (r & (G - 1))) * kPagedRowPart
-                     : a.part + (2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0)) * kPagedPrefixPart + r * kPagedRowPart;
-      };
-#pragma unroll
-      for (int h = 0; h < 4; ++h)
-        if (h < ng) {
-          float x[16];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) unpair(l[8 * h + i], x[2 * i], x[2 * i + 1]);
-          const float y = across16(x, lane, [](float p, float q) { return p + q; });
-          if (lane < 16) sh.top[w][warp & 3][16 * h + lane] = y;
-        }
-      if (!(ok = meet())) break;
-      if (key < cw && col0 + key < rows) {
-        float* ml = row_at(col0 + key) + D;
-        ml[0] = sh.m[col0 + key] == -INFINITY ? -INFINITY : -sh.nm[col0 + key];
-        ml[1] = (sh.top[w][0][key] + sh.top[w][1][key]) + (sh.top[w][2][key] + sh.top[w][3][key]);
-      }
-      ok = __all_sync(FULL, wait(&sh.pv_done[(c - 1) & 1], ((c - 1) >> 1) & 1));
+      c = c_end;
+      ok = __all_sync(FULL, wait(&sh.o_full, ic++ & 1));
       if (!ok) break;
       tmem_fence_after_sync();
+      // ---- the rows' results, a part: the two groups' joined, half of the channels each ----
+      sh.ml[w][row][0] = m;
+      sh.ml[w][row][1] = l;
+      if (!(ok = meet())) break;
+      if (live) {
+        const float m0 = sh.ml[0][row][0], m1 = sh.ml[1][row][0], M = fmaxf(m0, m1);
+        // The references that the weights were formed with; a group without steps has none.
+        const float r0 = less(m0), r1 = less(m1), R = less(M);
+        const bool has0 = j1 - j0 > 1 || ((c_end - 1) & 1) == 0, has1 = j1 - j0 > 1 || ((c_end - 1) & 1) == 1;
+        const float f0 = r0 == -INFINITY ? 0.0f : ex2(r0 - R), f1 = r1 == -INFINITY ? 0.0f : ex2(r1 - R);
+        const bool whole = j1 - j0 == steps_of(k.group);
+        float* const part = whole ? a.row_part + ((int64_t)seq0 * n_kv + k.head) * G * kPagedRowPart
+                                  : a.part + (2 * (int64_t)blockIdx.x + (j0 == 0 ? 1 : 0)) * kPagedPrefixPart;
+        auto row_at = [&](int r) {
+          return part + (int64_t)(whole ? (r >> g_log2) * (n_kv * G) + (r & (G - 1)) : r) * kPagedRowPart;
+        };
+        if (w == 0 && row < rows) {
+          float* const at = row_at(row);
+          // A sum of NaN, or of a group whose every logit was one, counts as it is.
+          const float s0 = sh.ml[0][row][1], s1 = sh.ml[1][row][1];
+          at[D] = R;
+          at[D + 1] = s0 * (r0 == -INFINITY ? 1.0f : f0) + s1 * (r1 == -INFINITY ? 1.0f : f1);
+        }
+        // 32 channels at a time, through the warp's 4 KB of the query tile: rows
+        // leave 128 bytes at a time.
+        const uint32_t stage = sq + warp * 4096;
 #pragma unroll 1
-      for (int h = 0; h < ng; ++h) {
-        uint32_t o[16];
-        tmem_ld16(tlane + 256 + col0 + h * 16, o);
+        for (int b = 2 * w; b < 2 * w + 2; ++b) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (col0 + h * 16 + i < rows) row_at(col0 + h * 16 + i)[key] = __uint_as_float(o[i]);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[16], y[16];
+            tmem_ld16(trow + 256 + b * 32 + h * 16, x);
+            tmem_ld16(trow + 384 + b * 32 + h * 16, y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              x[i] = __float_as_uint((has0 ? __uint_as_float(x[i]) * f0 : 0.0f) + (has1 ? __uint_as_float(y[i]) * f1 : 0.0f));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stage + lane * 128 + (((4 * h + i) ^ (lane & 7)) << 4)), "r"(x[4 * i]),
+                           "r"(x[4 * i + 1]), "r"(x[4 * i + 2]), "r"(x[4 * i + 3])
+                           : "memory");
+          }
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < 8; ++i) {
+            const int x = 4 * i + (lane >> 3);
+            uint4 o;
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                         : "r"(stage + x * 128 + (((lane & 7) ^ (x & 7)) << 4)));
+            if (wrow + x < rows) *reinterpret_cast<uint4*>(row_at(wrow + x) + b * 32 + (lane & 7) * 4) = o;
+          }
+          __syncwarp();
+        }
       }
       tmem_fence_before_sync();
-      ok = meet();  // the bounds and sums may be set anew
+      ok = meet();  // sh.ml and the accumulators are free again
     }
   }
   tmem_fence_before_sync();
