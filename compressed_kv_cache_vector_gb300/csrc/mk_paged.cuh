@@ -69,7 +69,8 @@ struct PagedScratch {
   float* prefill_part;        // paged_prefill_part_floats()
   float* mass_part;           // [2 kPagedMaxCtas][256]
   PagedShared* shared;
-  float* row_part;            // [max_seqs][n_q_heads][kPagedRowPart]
+  float *row_part, *own_row;  // [max_seqs][n_q_heads][kPagedRowPart]: over shared tokens, over a sequence's own
+  int32_t* own;               // [max_seqs][n_kv][2]
   float* lse2;                // [max_seqs][n_q_heads]: a decode step's sums, as base-2 logarithms
 };
 // The workspace's parts that eviction uses.
@@ -192,14 +193,19 @@ cudaError_t launch_paged_append(const PagedLayer& L, const mk_paged_batch& b, co
 cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
                                 float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s);
-// Shared prefixes: the parts of the rows over shared pages go to w.prefill_part,
-// what is shared to w.shared; then the sequences' own tokens, joined with them.
+// The parts of units of own tokens in several runs lie behind those of cells.
+inline float* paged_own_parts(const PagedScratch& w) { return w.prefill_part + (int64_t)2 * kPagedMaxCtas * kPagedPrefixPart; }
+
+// Shared prefixes: the rows' parts over shared pages and what is shared; their
+// parts over the sequences' own tokens; both joined.
 cudaError_t launch_paged_prefix(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, const mk_paged_prefix& p, const uint16_t* q, int64_t q_stride,
                                 float scale, cudaStream_t s);
 cudaError_t launch_paged_decode_own(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                     const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
-                                    uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s);
+                                    cudaStream_t s);
+cudaError_t launch_paged_join(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, uint16_t* out,
+                              int64_t out_stride, float* lse, cudaStream_t s);
 // With mass: the plain logits of layer pages go to scratch ([n_pages][n_kv][G]
 // [P] fp32) and the rows' sums to w.lse2; launch_paged_mass_fold adds their
 // weights to the mass.

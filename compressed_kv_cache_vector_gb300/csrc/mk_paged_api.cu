@@ -78,6 +78,7 @@ inline int64_t shared_bytes() { return align_up(sizeof(mk::PagedShared)); }
 inline int64_t row_part_bytes(const mk_paged_config* c) {
   return align_up((int64_t)c->max_seqs * c->n_q_heads * mk::kPagedRowPart * 4);
 }
+inline int64_t own_bytes(const mk_paged_config* c) { return align_up((int64_t)c->max_seqs * c->n_kv_heads * 8); }
 inline int64_t lse2_bytes(const mk_paged_config* c) { return align_up((int64_t)c->max_seqs * c->n_q_heads * 4); }
 // Eviction: the counter (a line of its own) and the plan, then two words per page and head.
 inline int64_t plan_bytes(const mk_paged_config* c) { return align_up(kAlign + (int64_t)c->max_seqs * 8); }
@@ -177,7 +178,7 @@ mk_status mk_paged_sizes(const mk_paged_config* cfg, size_t* pool_bytes, size_t*
   if (scale_bytes) *scale_bytes = (size_t)(scale_layer_count(cfg) * cfg->n_layers * 4);
   if (workspace_bytes)
     *workspace_bytes = (size_t)(clear_bytes(cfg) + part_acc_bytes(cfg) + part_ml_bytes(cfg) + prefill_part_bytes() +
-                                shared_bytes() + row_part_bytes(cfg) + lse2_bytes(cfg) + plan_bytes(cfg) + 2 * group_words_bytes(cfg));
+                                shared_bytes() + 2 * row_part_bytes(cfg) + own_bytes(cfg) + lse2_bytes(cfg) + plan_bytes(cfg) + 2 * group_words_bytes(cfg));
   return MK_OK;
 }
 
@@ -218,6 +219,8 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
   h->scratch.mass_part = h->scratch.prefill_part;  // calls of a handle are ordered
   h->scratch.shared = reinterpret_cast<mk::PagedShared*>(take(shared_bytes()));
   h->scratch.row_part = reinterpret_cast<float*>(take(row_part_bytes(cfg)));
+  h->scratch.own_row = reinterpret_cast<float*>(take(row_part_bytes(cfg)));
+  h->scratch.own = reinterpret_cast<int32_t*>(take(own_bytes(cfg)));
   h->scratch.lse2 = reinterpret_cast<float*>(take(lse2_bytes(cfg)));
   char* plan = take(plan_bytes(cfg));
   h->evict.ticket = reinterpret_cast<int32_t*>(plan);
@@ -327,8 +330,9 @@ mk_status mk_paged_prefix_attn(mk_paged* h, int32_t layer, const mk_paged_batch*
   } else {
     e = mk::launch_paged_prefix(L, h->dec, h->scratch, layer, *batch, *prefix, qq, q_stride, scale, (cudaStream_t)stream);
     if (e == cudaSuccess)
-      e = mk::launch_paged_decode_own(L, h->dec, h->scratch, layer, *batch, qq, q_stride, scale, oo, out_stride, lse,
-                                      (cudaStream_t)stream);
+      e = mk::launch_paged_decode_own(L, h->dec, h->scratch, layer, *batch, qq, q_stride, scale, (cudaStream_t)stream);
+    if (e == cudaSuccess)
+      e = mk::launch_paged_join(L, h->scratch, *batch, oo, out_stride, lse, (cudaStream_t)stream);
   }
   return e == cudaSuccess ? MK_OK : MK_ECUDA;
 }

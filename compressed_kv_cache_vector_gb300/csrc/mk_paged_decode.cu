@@ -47,7 +47,6 @@ namespace mk {
 namespace {
 
 constexpr int kStageBytes = 8192;
-constexpr int kOwnWarps = 1;
 
 struct DecodeArgs {
   mk_paged_batch b;
@@ -62,7 +61,8 @@ struct DecodeArgs {
   float* part_ml;       // [2 grid][rows][2]
   int32_t* counters;    // [max_seqs][n_kv]
   const PagedShared* shared;  // OWN
-  const float *shared_part, *row_part;
+  float *own_part, *own_row;  // parts of units in several runs, and of whole ones
+  int2* own;                  // [n_seqs][n_kv]: first run and number of the parts
   float* logits;        // MASS: [n_pages][n_kv][G][P], the layer's plain logits in units of log 2
   float* lse2;          // MASS: [n_seqs][n_kv G], the rows' sums as base-2 logarithms
 };
@@ -114,8 +114,9 @@ struct DecodeSmem {
 };
 
 // kMass: the logits and the rows' sums are left for launch_paged_mass_fold.
-// kOwn: the tokens that a sequence shares with its group are left out; their
-// parts, from launch_paged_prefix, are joined with the result.
+// kOwn: the tokens that a sequence shares with its group are left out, and the
+// rows' results are parts, which launch_paged_join joins with those over the
+// shared ones.
 enum DecodeMode { kPlain, kMass, kOwn };
 template <bool E4M3, int NW, int NS, int C, DecodeMode MODE>
 __global__ void __launch_bounds__(NW * 32, 1)
@@ -129,7 +130,6 @@ __global__ void __launch_bounds__(NW * 32, 1)
   __shared__ int64_t s_pre[MK_MAX_CALL_SEQS + 1];
   __shared__ int s_len[MK_MAX_CALL_SEQS], s_row[MK_MAX_CALL_SEQS], s_new[C == 1 ? 1 : MK_MAX_CALL_SEQS];
   __shared__ int s_off[OWN ? MK_MAX_CALL_SEQS : 1];  // shared tokens
-  __shared__ float s_mul[OWN ? 8 : 1], s_ref[OWN ? 8 : 1];
   __shared__ int64_t s_wsum[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NS];
   __shared__ __align__(16) float s_sc[NW][NS][4];  // k scale of box 0, 1; v scale of box 0, 1
@@ -202,90 +202,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
   };
   int64_t total = list(1);
 
-  // OWN: the parts over the tokens that sequence seq shares.  `slot` is the
-  // i-th part's place among them, `row` the head's first row there.
-  struct SharedParts {
-    int b_lo, parts, row;
-    const float* whole;  // the rows' parts where there is one of each
-  };
-  auto shared_of = [&](int seq, int head) {
-    const PagedShared::Seq& s = a.shared->seq[seq];
-    const int64_t place = s.place + (int64_t)head * s.cost, per = a.shared->per;
-    const int b_lo = (int)(place / per);
-    return SharedParts{b_lo, (int)((place + s.steps - 1) / per) - b_lo + 1, s.row,
-                       a.row_part + ((int64_t)seq * n_kv + head) * G * kPagedRowPart};
-  };
-  auto shared_at = [&](const SharedParts& p, int i, int r) {  // part i of row r
-    return (p.parts == 1 ? p.whole
-                         : a.shared_part + (2 * (int64_t)(p.b_lo + i) + (i == 0 ? 1 : 0)) * kPagedPrefixPart + p.row * kPagedRowPart) +
-           r * kPagedRowPart;
-  };
-  // The rows' references and sums with the shared parts' (s_ref, s_L), and what
-  // the rows' own values are multiplied by (s_mul).  The whole CTA, between barriers.
-  auto join_shared = [&](const SharedParts& p) {
-    for (int r = warp; r < G; r += NW) {
-      const float own = less(s_M[r]);
-      float M = own, S = 0.0f;
-      for (int i = lane; i < p.parts; i += 32) M = fmaxf(M, __ldcg(shared_at(p, i, r) + D));
-      M = warp_max(M);
-      for (int i = lane; i < p.parts; i += 32) {
-        const float* ml = shared_at(p, i, r) + D;
-        const float mi = __ldcg(ml);
-        S += __ldcg(ml + 1) * (mi == -INFINITY ? 1.0f : ex2(mi - M));
-      }
-      S = warp_sum(S);
-      if (lane == 0) {
-        const float f = own == -INFINITY ? 0.0f : ex2(own - M);
-        s_mul[r] = f;
-        s_L[r] = S + s_L[r] * (own == -INFINITY ? 1.0f : f);
-        s_ref[r] = M;
-      }
-    }
-    __syncthreads();
-  };
-  auto add_shared = [&](const SharedParts& p, int e, float& x, float& y) {
-    const int r = e >> 6;
-    const float M = s_ref[r];
-    x *= s_mul[r];
-    y *= s_mul[r];
-#pragma unroll 8
-    for (int i = 0; i < p.parts; ++i) {
-      const float* part = shared_at(p, i, r);
-      const float mi = __ldcg(part + D);
-      const float f = mi == -INFINITY ? 0.0f : ex2(mi - M);
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(part + 2 * (e & 63)));
-      x = fmaf(v.x, f, x);
-      y = fmaf(v.y, f, y);
-    }
-  };
-
-  // Rows of sequences without tokens (of their own).
-  if (OWN)
-    for (int u = blockIdx.x; u < n_seqs * n_kv; u += gridDim.x) {
-      const int i = u / n_kv, head = u - i * n_kv;
-      if (s_row[i] < 0 || s_len[i] != 0 || s_off[i] == 0) continue;
-      const SharedParts p = shared_of(i, head);
-      if (tid < 8) {
-        s_M[tid] = -INFINITY;
-        s_L[tid] = 0.0f;
-      }
-      __syncthreads();
-      join_shared(p);
-      for (int e = tid; e < G * D / 2; e += NTHR) {
-        float x = 0.0f, y = 0.0f;
-        add_shared(p, e, x, y);
-        const int r = e >> 6;
-        const float f = s_L[r] > 0.0f || s_L[r] != s_L[r] ? 1.0f / s_L[r] : 0.0f;
-        *reinterpret_cast<uint32_t*>(a.out + (int64_t)s_row[i] * a.out_stride + (head * G + r) * D + 2 * (e & 63)) =
-            pack2<false>(x * f, y * f);
-      }
-      if (tid < G && a.lse)
-        a.lse[(int64_t)s_row[i] * n_kv * G + head * G + tid] =
-            s_L[tid] > 0.0f || s_L[tid] != s_L[tid] ? (log2f(s_L[tid]) + s_ref[tid]) * 0.6931471805599453f : -INFINITY;
-      __syncthreads();
-    }
+  // Rows of empty sequences.
+  if (!OWN)
   for (int i = blockIdx.x; i < n_seqs; i += gridDim.x)
-    if (s_row[i] >= 0 && s_len[i] == 0 && (!OWN || s_off[i] == 0)) {
+    if (s_row[i] >= 0 && s_len[i] == 0) {
       for (int t = 0; t < (C == 1 ? 1 : s_new[i]); ++t) {
         for (int e = tid; e < n_kv * G * D / 8; e += NTHR)
           *reinterpret_cast<uint4*>(a.out + (int64_t)(s_row[i] + t) * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
@@ -651,6 +571,31 @@ __global__ void __launch_bounds__(NW * 32, 1)
       }
     }
 
+    if constexpr (OWN) {  // one warp: its rows are a part as they are
+      static_assert(NW == 1, "one warp a CTA");
+      float sum = l[0] + __shfl_xor_sync(FULL, l[0], 1);
+      sum += __shfl_xor_sync(FULL, sum, 2);
+      const int64_t u0 = s_pre[u.seq] + (int64_t)u.head * places(u.seq, pad);
+      const int b_lo = (int)(u0 / per), parts = (int)((u0 + nch - 1) / per) - b_lo + 1;
+      float* const part = parts == 1 ? a.own_row + ((int64_t)u.seq * n_kv + u.head) * G * kPagedRowPart
+                                     : a.own_part + (2 * (int64_t)blockIdx.x + (u.ch == 0 ? 1 : 0)) * G * kPagedRowPart;
+      if (u.ch == 0 && lane == 0) a.own[u.seq * n_kv + u.head] = make_int2(b_lo, parts);
+      if (c == 0 && g < G) *reinterpret_cast<float2*>(part + g * kPagedRowPart + D) = make_float2(less(m[0]), sum);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (2 * c + e >= G) continue;
+        float* const to = part + (2 * c + e) * kPagedRowPart;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          if (E4M3) {
+            *reinterpret_cast<float2*>(to + 16 * g + 2 * n) = make_float2(o[0][n][e], o[0][n][2 + e]);
+          } else {
+            to[16 * n + g] = o[0][n][e];
+            to[16 * n + 8 + g] = o[0][n][2 + e];
+          }
+        }
+      }
+    } else {
     // ---- join the warps ----
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -692,7 +637,6 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
       }
     __syncthreads();
-    const bool joins = OWN && s_off[OWN ? u.seq : 0] > 0;
     // Row x of the result (where it has one): its output, and its lse.
     auto put = [&](int e, float x, float y) {
       const int r = e >> 6;
@@ -707,15 +651,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
             s_L[r] > 0.0f || s_L[r] != s_L[r] ? log2f(s_L[r]) + (s_M[r] - kShift) : INFINITY;
       if (!a.lse || !live_row(r)) return;
       a.lse[(int64_t)(row + tok_of(r)) * n_kv * G + head_of(r)] =
-          s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + (joins ? s_ref[OWN ? r : 0] : less(s_M[r]))) * 0.6931471805599453f
-                                            : -INFINITY;
+          s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + (s_M[r] - kShift)) * 0.6931471805599453f : -INFINITY;
     };
     const bool whole = u.ch == 0 && fe - fs == nch;
-    SharedParts sp{0, 0, 0, nullptr};
-    if (joins) {
-      sp = shared_of(u.seq, u.head);
-      if (whole) join_shared(sp);
-    }
     const int64_t part = 2 * (int64_t)blockIdx.x + (u.ch == 0 ? 1 : 0);
     for (int e = tid; e < R * D / 2; e += NTHR) {
       float x = 0.0f, y = 0.0f;
@@ -725,10 +663,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
         x += v.x;
         y += v.y;
       }
-      if (whole) {
-        if (joins) add_shared(sp, e, x, y);
+      if (whole)
         put(e, x, y);
-      } else
+      else
         *reinterpret_cast<float2*>(a.part_acc + part * R * D + 2 * e) = make_float2(x, y);
     }
     if (tid < R) {
@@ -770,7 +707,6 @@ __global__ void __launch_bounds__(NW * 32, 1)
           }
         }
         __syncthreads();
-        if (joins) join_shared(sp);
         for (int e = tid; e < R * D / 2; e += NTHR) {
           const int h = e >> 6;
           const float M = s_M[h];
@@ -783,13 +719,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
             x = fmaf(v.x, f, x);
             y = fmaf(v.y, f, y);
           }
-          if (joins) add_shared(sp, e, x, y);
           put(e, x, y);
         }
         if (tid < R) put_lse(tid);
       }
     }
     __syncthreads();  // s_ml, s_acc, s_M, s_L are free again
+    }
     fs = fe;
     u.ch = 0;
     if (++u.head == n_kv) {
@@ -811,19 +747,16 @@ cudaError_t launch(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, cud
 }
 
 // The tokens that sequences do not share are few and in many units: CTAs of one
-// warp, as many as fit, each with a run of its own, so that nobody waits for
-// the joining of warps.
+// warp, as many as fit, each with a run of its own, so that no warp waits for
+// another.
 template <bool E4M3>
-cudaError_t launch_own(const PagedLayer& L, const PagedMaps& maps, DecodeArgs a, int64_t part_floats, cudaStream_t s) {
-  constexpr int NW = kOwnWarps;
-  const int bytes = DecodeSmem<E4M3, NW, 2, 1>::bytes(L.G);
+cudaError_t launch_own(const PagedLayer& L, const PagedMaps& maps, const DecodeArgs& a, int64_t part_floats, cudaStream_t s) {
+  constexpr int bytes = 1024 + DecodeSmem<E4M3, 1, 2, 1>::ring;
   int occ = 0, sms = 0;
-  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, NW, 2, 1, kOwn>, bytes, NW * 32, &occ, &sms);
+  const cudaError_t e = kernel_smem_attr((const void*)k_paged_decode<E4M3, 1, 2, 1, kOwn>, bytes, 32, &occ, &sms);
   if (e != cudaSuccess) return e;
-  const int64_t slot = (int64_t)L.G * (D + 2);
-  const int64_t grid = std::min<int64_t>((int64_t)(sms > 0 ? sms : 128) * occ, part_floats / (2 * slot));
-  a.part_ml = a.part_acc + 2 * grid * L.G * D;
-  return launch_pdl(k_paged_decode<E4M3, NW, 2, 1, kOwn>, dim3((unsigned)grid), dim3(NW * 32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
+  const int64_t grid = std::min<int64_t>((int64_t)(sms > 0 ? sms : 128) * occ, part_floats / (2 * L.G * kPagedRowPart));
+  return launch_pdl(k_paged_decode<E4M3, 1, 2, 1, kOwn>, dim3((unsigned)grid), dim3(32), (size_t)bytes, s, 0, L, a, maps.k, maps.v);
 }
 
 }  // namespace
@@ -832,7 +765,7 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
                                 const mk_paged_batch& b, bool several, bool causal, const uint16_t* q, int64_t q_stride,
                                 float scale, uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s) {
   DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, causal ? 1 : 0,
-               w.part_acc, w.part_ml, w.counters, nullptr, nullptr, nullptr, nullptr, nullptr};
+               w.part_acc, w.part_ml, w.counters, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   // 16 rows: 64 accumulators more a lane, eight warps of 255 registers.
   if (several) return L.e4m3 ? launch<true, 8, 2, 2>(L, maps, a, s) : launch<false, 8, 2, 2>(L, maps, a, s);
   // 12 warps of two 8 KB stages: the conversion of a chunk takes a warp about
@@ -846,12 +779,10 @@ cudaError_t launch_paged_decode(const PagedLayer& L, const PagedMaps& maps, cons
 
 cudaError_t launch_paged_decode_own(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                     const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
-                                    uint16_t* out, int64_t out_stride, float* lse, cudaStream_t s) {
-  // Behind the shared pages' parts.
-  const int64_t shared = (int64_t)2 * kPagedMaxCtas * kPagedPrefixPart;
-  const DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 0,
-                     w.prefill_part + shared, nullptr, w.counters, w.shared, w.prefill_part, w.row_part, nullptr, nullptr};
-  const int64_t left = paged_prefill_part_floats() - shared;
+                                    cudaStream_t s) {
+  const DecodeArgs a{b, q, nullptr, nullptr, q_stride, 0, scale * kLog2e, layer * L.n_pages, 0,
+                     nullptr, nullptr, nullptr, w.shared, paged_own_parts(w), w.own_row, reinterpret_cast<int2*>(w.own), nullptr, nullptr};
+  const int64_t left = paged_prefill_part_floats() - (paged_own_parts(w) - w.prefill_part);
   return L.e4m3 ? launch_own<true>(L, maps, a, left, s) : launch_own<false>(L, maps, a, left, s);
 }
 
@@ -859,7 +790,7 @@ cudaError_t launch_paged_decode_mass(const PagedLayer& L, const PagedMaps& maps,
                                      const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
                                      uint16_t* out, int64_t out_stride, float* lse, float* logits, cudaStream_t s) {
   const DecodeArgs a{b, q, out, lse, q_stride, out_stride, scale * kLog2e, layer * L.n_pages, 0,
-                     w.part_acc, w.part_ml, w.counters, nullptr, nullptr, nullptr, logits, w.lse2};
+                     w.part_acc, w.part_ml, w.counters, nullptr, nullptr, nullptr, nullptr, logits, w.lse2};
   if (L.G == 8) return L.e4m3 ? launch<true, 10, 2, 1, kMass>(L, maps, a, s) : launch<false, 10, 2, 1, kMass>(L, maps, a, s);
   return L.e4m3 ? launch<true, 12, 2, 1, kMass>(L, maps, a, s) : launch<false, 12, 2, 1, kMass>(L, maps, a, s);
 }

@@ -746,7 +746,100 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && sh.dead) paged_error(L, ERR_PAGED_WAIT, (int32_t)blockIdx.x, sh.dead - 1, (int32_t)MK_ETIMEOUT);
 }
 
+// ---- joins a row's parts: over shared tokens and over its sequence's own ----
+// A warp a row, four channels a lane.
+constexpr int kJoinWarps = 4;
+
+struct JoinArgs {
+  mk_paged_batch b;
+  const PagedShared* shared;
+  const float *part, *row_part, *own_part, *own_row;
+  const int2* own;
+  uint16_t* out;
+  float* lse;
+  int64_t out_stride;
+};
+
+__global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(PagedLayer L, JoinArgs a) {
+  const int lane = threadIdx.x & 31, G = L.G, n_q = L.n_kv * G;
+  pdl_wait();
+  pdl_trigger();
+  if (__syncthreads_or(threadIdx.x == 0 && paged_stopped(L))) return;
+  const int64_t at = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  const int seq = (int)(at / n_q), h = (int)(at % n_q), head = h / G, r = h % G;
+  if (seq >= a.b.n_seqs) return;
+  const PagedSeq s = paged_seq(a.b, L.P, seq, false);
+  if (!s.ok || s.n_new != 1) return;
+  const float *sp = nullptr, *op = nullptr;  // the first part of each kind
+  int64_t s_rest = 0, o_rest = 0;            // from it to the second, and the distance of the others
+  int ns = 0, no = 0;
+  const int64_t s_slot = 2 * (int64_t)kPagedPrefixPart, o_slot = 2 * (int64_t)G * kPagedRowPart;
+  int off = 0;
+  if (s.len > 0) {
+    const PagedShared::Seq& c = a.shared->seq[seq];
+    off = c.len;
+    if (off > 0) {
+      const int64_t place = c.place + (int64_t)head * c.cost, per = a.shared->per, b_lo = place / per;
+      ns = (int)((place + c.steps - 1) / per - b_lo) + 1;
+      sp = ns == 1 ? a.row_part + ((int64_t)seq * n_q + h) * kPagedRowPart
+                   : a.part + (2 * b_lo + 1) * kPagedPrefixPart + (int64_t)(c.row + r) * kPagedRowPart;
+      s_rest = kPagedPrefixPart;
+    }
+    if (s.len > off) {
+      const int2 o = a.own[seq * L.n_kv + head];
+      no = o.y;
+      op = no == 1 ? a.own_row + ((int64_t)seq * n_q + h) * kPagedRowPart
+                   : a.own_part + ((2 * (int64_t)o.x + 1) * G + r) * kPagedRowPart;
+      o_rest = (int64_t)G * kPagedRowPart;
+    }
+  }
+  // A run that begins an item has its odd slot, one that goes on with it the even one.
+  auto part = [&](int i) {
+    if (i < ns) return i == 0 ? sp : sp - s_rest + i * s_slot;
+    i -= ns;
+    return i == 0 ? op : op - o_rest + i * o_slot;
+  };
+  const int n = ns + no;
+  float M = -INFINITY, S = 0.0f;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + D));
+  M = warp_max(M);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float mine = 0.0f;
+    if (i0 + lane < n) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part(i0 + lane) + D));
+      // A part whose reference is -infinity has no weights, or only NaN: its sum, 0 or NaN, counts as it is.
+      mine = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
+      S += ml.y * (ml.x == -INFINITY ? 1.0f : mine);
+    }
+    const int m = min(32, n - i0);
+#pragma unroll 8
+    for (int i = 0; i < m; ++i) {
+      const float f = __shfl_sync(FULL, mine, i);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part(i0 + i)) + lane);
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+  }
+  S = warp_sum(S);
+  const bool any = S > 0.0f || S != S;
+  const float f = any ? 1.0f / S : 0.0f;
+  const uint2 w = make_uint2(pack2<false>(o.x * f, o.y * f), pack2<false>(o.z * f, o.w * f));
+  *reinterpret_cast<uint2*>(a.out + (int64_t)s.row0 * a.out_stride + h * D + lane * 4) = w;
+  if (a.lse && lane == 0) a.lse[(int64_t)s.row0 * n_q + h] = any ? (log2f(S) + M) * kLn2 : -INFINITY;
+}
+
 }  // namespace
+
+cudaError_t launch_paged_join(const PagedLayer& L, const PagedScratch& w, const mk_paged_batch& b, uint16_t* out,
+                              int64_t out_stride, float* lse, cudaStream_t s) {
+  const JoinArgs a{b, w.shared, w.prefill_part, w.row_part, paged_own_parts(w), w.own_row, reinterpret_cast<const int2*>(w.own),
+                   out, lse, out_stride};
+  const int64_t rows = (int64_t)b.n_seqs * L.n_kv * L.G;
+  return launch_pdl(k_paged_join, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, 0, L, a);
+}
 
 cudaError_t launch_paged_prefix(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, const mk_paged_prefix& p, const uint16_t* q, int64_t q_stride,
