@@ -68,7 +68,7 @@ __device__ __forceinline__ int page_of(const PagedLayer& L, const mk_paged_batch
 template <int CL>
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, EvictArgs a) {
   extern __shared__ uint32_t cache[];  // [kCache]
-  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t hist[kBins], sums[CL > 1 ? kBins : 1];
   __shared__ int s_warp[kSelThreads / 32][2], s_tot[2], s_pick[2], s_scan[kSelThreads / 32];
   constexpr int kWarps = kSelThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -109,7 +109,25 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
     return p < 0 ? 0u : mass_key(a.mass[((int64_t)p * L.n_kv + head) * L.P + (t & (L.P - 1))]);
   };
   auto key_of = [&](int i) { return i < kCache ? cache[i] : load_key(i); };
-  for (int i = tid; i < min(n, kCache); i += kSelThreads) cache[i] = load_key(i);
+  for (int i0 = tid; i0 < min(n, kCache); i0 += 8 * kSelThreads) {  // eight tokens at a time: the loads' latency
+    int page[8];
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = i0 + e * kSelThreads;
+      page[e] = i < min(n, kCache) ? page_of(L, a.b, seq, t0 + i) : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = t0 + i0 + e * kSelThreads;
+      w[e] = page[e] < 0 ? __int_as_float(0x7fffffff) : a.mass[((int64_t)page[e] * L.n_kv + head) * L.P + (t & (L.P - 1))];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = i0 + e * kSelThreads;
+      if (i < min(n, kCache)) cache[i] = mass_key(w[e]);
+    }
+  }
 
   // The k-th largest key, digit by digit: those above `prefix` are kept, of
   // the ones that begin with it `left`.
@@ -126,21 +144,27 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
         if (pass == 0 || (key ^ prefix) >> (shift + bits) == 0) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
       }
       __syncthreads();
-      if (CL > 1) cg::this_cluster().sync();
+      if (CL > 1) {
+        // Each CTA adds up a share of the bins and hands the sums to all.
+        auto cluster = cg::this_cluster();
+        cluster.sync();
+        constexpr int kShare = kBins / CL;
+        for (int i = tid; i < kShare; i += kSelThreads) {
+          const int bin = rank * kShare + i;
+          uint32_t x = 0;
+#pragma unroll
+          for (int r = 0; r < CL; ++r) x += *cluster.map_shared_rank(&hist[bin], r);
+#pragma unroll
+          for (int r = 0; r < CL; ++r) *cluster.map_shared_rank(&sums[bin], r) = x;
+        }
+        cluster.sync();
+      }
       // From the top down, four bins a thread: b = bins - 1 - 4 tid - i.
       int c[4], mine = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int bin = bins - 1 - 4 * tid - i;
-        c[i] = 0;
-        if (bin >= 0) {
-          if (CL > 1) {
-#pragma unroll
-            for (int r = 0; r < CL; ++r) c[i] += (int)*cg::this_cluster().map_shared_rank(&hist[bin], r);
-          } else {
-            c[i] = (int)hist[bin];
-          }
-        }
+        c[i] = bin >= 0 ? (int)(CL > 1 ? sums[bin] : hist[bin]) : 0;
         mine += c[i];
       }
       const int ex = warp_excl_scan(mine, lane);
@@ -160,7 +184,7 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
       prefix |= (uint32_t)s_pick[0] << shift;
       left = s_pick[1];
       shift -= pass == 0 ? 11 : 10;
-      if (CL > 1) cg::this_cluster().sync();  // the histograms have been read
+      __syncthreads();
     }
   } else {
     __syncthreads();
@@ -236,7 +260,7 @@ __device__ __forceinline__ void codes_to(uint32_t lo, uint32_t hi, float s, floa
 }
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kMoveThreads) k_evict_move(PagedLayer L, EvictArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, EvictArgs a) {
   constexpr int kChunks = E4M3 ? 8 : 16;                       // 16 bytes of a row
   constexpr int kRowsPass = kMoveThreads / kChunks, kPass = kGroup / kRowsPass;
   __shared__ int64_t s_end[MK_MAX_CALL_SEQS];                  // items up to and with a sequence

@@ -1,5 +1,7 @@
 // Attention mass over the paged cache: what softmax weights each held token
 // got, summed over query tokens and over the query heads of its kv head.
+#include <type_traits>
+
 #include "mk_paged_tc.cuh"
 
 namespace mk {
@@ -9,7 +11,8 @@ namespace {
 // ---- a decode step's weights, from the logits that the attention left ----
 // A thread a token: the group's weights 2^(z - lse2) summed and added.  HBM
 // (mostly L2, where the logits still are): 4 G bytes read, 8 for the mass.
-constexpr int kFoldThreads = 256;
+constexpr int kFoldThreads = 256, kFoldTokens = 4;  // tokens of a thread, for the loads in flight
+constexpr int kFoldTile = kFoldThreads * kFoldTokens;
 
 __global__ void __launch_bounds__(kFoldThreads)
     k_mass_fold(PagedLayer L, mk_paged_batch b, const float* logits, const float* lse2, float* mass, int32_t first) {
@@ -25,7 +28,7 @@ __global__ void __launch_bounds__(kFoldThreads)
     int64_t x = 0;
     if (tid < b.n_seqs) {
       const PagedSeq s = paged_seq(b, L.P, tid, false);
-      if (s.ok && s.n_new == 1 && s.len > first) x = (int64_t)((s.len - first + kFoldThreads - 1) / kFoldThreads) * n_kv;
+      if (s.ok && s.n_new == 1 && s.len > first) x = (int64_t)((s.len - first + kFoldTile - 1) / kFoldTile) * n_kv;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -49,18 +52,31 @@ __global__ void __launch_bounds__(kFoldThreads)
     }
     const int64_t in = tile - (seq ? s_end[seq - 1] : 0);
     const int len = b.kv_len[seq], head = (int)(in % n_kv);
-    const int64_t t = first + in / n_kv * kFoldThreads + tid;
-    if (t >= len) continue;
-    const int page = b.page_table[(int64_t)seq * b.table_stride + (t >> L.p_log2)];
-    if (page < 0 || page >= L.n_pages) continue;  // recorded by the attention
-    const int64_t unit = (int64_t)page * n_kv + head;
-    const int slot = (int)t & (L.P - 1);
-    float* to = mass + unit * L.P + slot;
-    const float* z = logits + unit * G * L.P + slot;
+    const int64_t t0 = first + in / n_kv * kFoldTile + tid;
     const float* ls = lse2 + ((int64_t)seq * n_kv + head) * G;
-    float sum = 0.0f;
-    for (int g = 0; g < G; ++g) sum += ex2(z[g * L.P] - ls[g]);
-    *to = t == len - 1 ? sum : *to + sum;
+    int64_t unit[kFoldTokens];
+#pragma unroll
+    for (int e = 0; e < kFoldTokens; ++e) {
+      const int64_t t = t0 + e * kFoldThreads;
+      const int page = t < len ? b.page_table[(int64_t)seq * b.table_stride + (t >> L.p_log2)] : -1;
+      unit[e] = page < 0 || page >= L.n_pages ? -1 : (int64_t)page * n_kv + head;  // a bad one is recorded by the attention
+    }
+    float sum[kFoldTokens], old[kFoldTokens];
+#pragma unroll
+    for (int e = 0; e < kFoldTokens; ++e) {
+      const int64_t t = t0 + e * kFoldThreads;
+      sum[e] = old[e] = 0.0f;
+      if (unit[e] >= 0 && t < len - 1) old[e] = mass[unit[e] * L.P + (t & (L.P - 1))];
+    }
+    for (int g = 0; g < G; ++g) {
+      const float s = ls[g];
+#pragma unroll
+      for (int e = 0; e < kFoldTokens; ++e)
+        if (unit[e] >= 0) sum[e] += ex2(logits[(unit[e] * G + g) * L.P + ((t0 + e * kFoldThreads) & (L.P - 1))] - s);
+    }
+#pragma unroll
+    for (int e = 0; e < kFoldTokens; ++e)
+      if (unit[e] >= 0) mass[unit[e] * L.P + ((t0 + e * kFoldThreads) & (L.P - 1))] = old[e] + sum[e];
   }
 }
 
@@ -76,7 +92,8 @@ constexpr int kMassTile = 128 * D * 2;
 constexpr int kMassThreads = 448;  // 8 warps sum, 4 load keys, 1 loads queries, 1 issues
 constexpr int kMassItemCost = 1;   // an item's begin and end take as long as this many steps
 constexpr int kMassMinRun = 4;
-constexpr int kMassSmem = 1024 + 4 * kMassTile + 2 * kMassTile;
+constexpr int kMassSmem = 1024 + 6 * kMassTile;
+constexpr int kMassMany = 8;         // row tiles of a sequence from which an item has many steps
 constexpr int kMeta = 8;           // items whose pages are kept
 
 struct MassArgs {
@@ -101,7 +118,7 @@ struct MassShared {
   MassCursor start;
   int64_t f0, per;
   int span, patience;
-  uint64_t q_full[2], q_free[2], s_full[2][2], s_free[2][2], k_full[2], k_free[2], met[2], done;
+  uint64_t q_full[4], q_free[4], s_full[2][2], s_free[2][2], k_full[2], k_free[2], met[2], done;
   // -lse log2 e of a step's rows, -infinity where there is none.  A sum gives its
   // logits back before it has read the last of these, hence more than four.
   __align__(16) float nlse[8][kMassRows];
@@ -112,20 +129,26 @@ struct MassShared {
   volatile int dead;
 };
 
-template <bool E4M3>
+// NK: items whose keys are held.  Few steps an item want the next item's keys
+// early (2), many want queries early (1: four tiles of them, 6000-token prompt
+// X us against Y).
+template <bool E4M3, int NK>
 __global__ void __launch_bounds__(kMassThreads, 1)
     k_prefill_mass(PagedLayer L, MassArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ unsigned char dyn[];
   __shared__ MassShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-  const uint32_t sk = base, sq = base + 4 * kMassTile;
+  constexpr int NQ = 6 - 2 * NK;  // tiles of queries
+  const uint32_t sk = base, sq = base + 2 * NK * kMassTile;
   const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv, n_seqs = a.b.n_seqs;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_free[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       for (int j = 0; j < 2; ++j) {
         mbar_init(&sh.s_full[i][j], 1);
         mbar_init(&sh.s_free[i][j], 4);
@@ -272,14 +295,14 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
         steps(k, j0, j1);
         if (j0 >= j1) continue;
-        ok = wait(&sh.k_full[ic & 1], (ic >> 1) & 1);
+        ok = wait(&sh.k_full[ic % NK], (ic / NK) & 1);
         for (int j = j0; ok && j < j1; ++j, ++c) {
-          ok = wait(&sh.q_full[c & 1], (c >> 1) & 1);
+          ok = wait(&sh.q_full[c % NQ], (c / NQ) & 1);
           for (int w = 0; ok && w < 2; ++w) {
             ok = c < 2 || wait(&sh.s_free[w][c & 1], ((c >> 1) - 1) & 1);
             if (!ok) break;
             tmem_fence_after_sync();
-            const uint64_t da = dk + (uint64_t)((((ic & 1) * 2 + w) * kMassTile) >> 4), db = dq + (uint64_t)(((c & 1) * kMassTile) >> 4);
+            const uint64_t da = dk + (uint64_t)((((ic % NK) * 2 + w) * kMassTile) >> 4), db = dq + (uint64_t)(((c % NQ) * kMassTile) >> 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint32_t o = ((i >> 2) * (kMassTile / 2) + (i & 3) * 32) >> 4;
@@ -287,9 +310,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             }
             umma_commit(&sh.s_full[w][c & 1]);
           }
-          if (ok) umma_commit(&sh.q_free[c & 1]);
+          if (ok) umma_commit(&sh.q_free[c % NQ]);
         }
-        if (ok) umma_commit(&sh.k_free[ic & 1]);
+        if (ok) umma_commit(&sh.k_free[ic % NK]);
         ++ic;
       }
       umma_commit(&sh.done);
@@ -317,21 +340,21 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           const float ls = r < rows ? a.lse[(row0 + (r >> g_log2)) * n_q + k.head * G + (int)(r & (G - 1))] : -INFINITY;
           n[e] = ls == -INFINITY ? -INFINITY : -ls * kLog2e;
         }
-        ok = c < 2 || __all_sync(FULL, wait(&sh.q_free[c & 1], ((c >> 1) - 1) & 1));
+        ok = c < NQ || __all_sync(FULL, wait(&sh.q_free[c % NQ], (c / NQ - 1) & 1));
         if (!ok) break;
         *reinterpret_cast<float4*>(&sh.nlse[c & 7][lane * 4]) = make_float4(n[0], n[1], n[2], n[3]);
         __syncwarp();
         if (lane == 0) {
-          mbar_expect_tx(&sh.q_full[c & 1], kMassTile);
+          mbar_expect_tx(&sh.q_full[c % NQ], kMassTile);
           const int tok = row0 + (int)(r0 >> g_log2);
-          const uint32_t to = sq + (c & 1) * kMassTile;
-          tma3(to, &qmap, 0, k.head * G, tok, &sh.q_full[c & 1]);
-          tma3(to + kMassTile / 2, &qmap, 64, k.head * G, tok, &sh.q_full[c & 1]);
+          const uint32_t to = sq + (c % NQ) * kMassTile;
+          tma3(to, &qmap, 0, k.head * G, tok, &sh.q_full[c % NQ]);
+          tma3(to + kMassTile / 2, &qmap, 64, k.head * G, tok, &sh.q_full[c % NQ]);
         }
       }
     }
     // No copy is in flight when the kernel ends, also after a wait that ran out.
-    for (unsigned i = c < 2 ? 0 : c - 2; i < c; ++i) (void)paged_wait_warp(&sh.q_full[i & 1], (i >> 1) & 1);
+    for (unsigned i = c < NQ ? 0 : c - NQ; i < c; ++i) (void)paged_wait_warp(&sh.q_full[i % NQ], (i / NQ) & 1);
   } else if (warp >= 8) {
     // ---- keys into shared memory ----
     const int lt = tid - 256;
@@ -370,13 +393,13 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         }
         float ks = 1.0f;
         if (lt < 16 && pg >= 0) ks = L.k_scale[(int64_t)pg * n_kv + k.head];
-        ok = ic < 2 || __all_sync(FULL, wait_long(&sh.k_free[ic & 1], ((ic >> 1) - 1) & 1));
+        ok = ic < NK || __all_sync(FULL, wait_long(&sh.k_free[ic % NK], (ic / NK - 1) & 1));
         if (!ok) break;
         if (lt < 16) {
           sh.page[ic % kMeta][lt] = pg;
           sh.ks[ic % kMeta][lt] = ks;
         }
-        const uint32_t to = sk + (ic & 1) * 2 * kMassTile + put;
+        const uint32_t to = sk + (ic % NK) * 2 * kMassTile + put;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -392,7 +415,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at ^ 16), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]) : "memory");
         }
         fence_proxy_async();
-        mbar_arrive_warp(&sh.k_full[ic & 1], lane);
+        mbar_arrive_warp(&sh.k_full[ic % NK], lane);
         ++ic;
       }
     } else if (warp == 8) {
@@ -400,22 +423,22 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         steps(k, j0, j1);
         if (j0 >= j1) continue;
         const int pg = page_at(k);
-        ok = ic < 2 || __all_sync(FULL, wait_long(&sh.k_free[ic & 1], ((ic >> 1) - 1) & 1));
+        ok = ic < NK || __all_sync(FULL, wait_long(&sh.k_free[ic % NK], (ic / NK - 1) & 1));
         if (!ok) break;
         if (lane < 16) sh.page[ic % kMeta][lane] = pg;
         const unsigned groups = __ballot_sync(FULL, pg >= 0);
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(&sh.k_full[ic & 1], __popc(groups) * 16 * D * 2);
+        if (lane == 0) mbar_expect_tx(&sh.k_full[ic % NK], __popc(groups) * 16 * D * 2);
         __syncwarp();
         if (pg >= 0) {
-          const uint32_t to = sk + ((ic & 1) * 2 + (lane >> 3)) * kMassTile + (lane & 7) * 2048;
+          const uint32_t to = sk + ((ic % NK) * 2 + (lane >> 3)) * kMassTile + (lane & 7) * 2048;
           const int y = k.head * L.P + ((k.kt * kMassKeys + lane * 16) & (L.P - 1)), z = a.layer_page0 + pg;
-          tma3(to, &kmap, 0, y, z, &sh.k_full[ic & 1]);
-          tma3(to + kMassTile / 2, &kmap, 64, y, z, &sh.k_full[ic & 1]);
+          tma3(to, &kmap, 0, y, z, &sh.k_full[ic % NK]);
+          tma3(to + kMassTile / 2, &kmap, 64, y, z, &sh.k_full[ic % NK]);
         }
         ++ic;
       }
-      for (unsigned i = ic < 2 ? 0 : ic - 2; i < ic; ++i) (void)paged_wait_warp(&sh.k_full[i & 1], (i >> 1) & 1);
+      for (unsigned i = ic < NK ? 0 : ic - NK; i < ic; ++i) (void)paged_wait_warp(&sh.k_full[i % NK], (i / NK) & 1);
     }
   } else {
     // ---- sums: one key a thread ----
@@ -448,34 +471,42 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         const bool cut = cols < kMassRows || __any_sync(FULL, c0 > 0);
         const uint32_t tb = ts + (c & 1) * 128;
         uint64_t add[2] = {0, 0};
-        uint32_t v[2][32];
-        tmem_ld32_async(tb, v[0]);
+        auto sum_up = [&](auto masked) {
+          constexpr bool kCut = decltype(masked)::value;
+          uint32_t v[2][32];
+          tmem_ld32_async(tb, v[0]);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          tmem_ld_wait(v[h & 1]);
-          if (h < 3) tmem_ld32_async(tb + (h + 1) * 32, v[(h + 1) & 1]);
-          if (h == 3) {  // all of S is in registers
-            tmem_fence_before_sync();
-            mbar_arrive_warp(&sh.s_free[w][c & 1], lane);
-          }
-          const uint32_t(&z)[32] = v[h & 1];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 nl = *reinterpret_cast<const float4*>(&sh.nlse[c & 7][32 * h + i]);
-            float x[4];
-            unpair(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), k2, pair(nl.x, nl.y)), x[0], x[1]);
-            unpair(fma2(pair(__uint_as_float(z[i + 2]), __uint_as_float(z[i + 3])), k2, pair(nl.z, nl.w)), x[2], x[3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
-            if (cut) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (32 * h + i + e < c0 || 32 * h + i + e >= cols) x[e] = 0.0f;
+          for (int h = 0; h < 4; ++h) {
+            tmem_ld_wait(v[h & 1]);
+            if (h < 3) tmem_ld32_async(tb + (h + 1) * 32, v[(h + 1) & 1]);
+            if (h == 3) {  // all of S is in registers
+              tmem_fence_before_sync();
+              mbar_arrive_warp(&sh.s_free[w][c & 1], lane);
             }
-            add[0] = add2(add[0], pair(x[0], x[1]));
-            add[1] = add2(add[1], pair(x[2], x[3]));
+            if (kCut && 32 * h >= cols) continue;
+            const uint32_t(&z)[32] = v[h & 1];
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 nl = *reinterpret_cast<const float4*>(&sh.nlse[c & 7][32 * h + i]);
+              float x[4];
+              unpair(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), k2, pair(nl.x, nl.y)), x[0], x[1]);
+              unpair(fma2(pair(__uint_as_float(z[i + 2]), __uint_as_float(z[i + 3])), k2, pair(nl.z, nl.w)), x[2], x[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+              if (kCut) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (32 * h + i + e < c0 || 32 * h + i + e >= cols) x[e] = 0.0f;
+              }
+              add[0] = add2(add[0], pair(x[0], x[1]));
+              add[1] = add2(add[1], pair(x[2], x[3]));
+            }
           }
-        }
+        };
+        if (cut)
+          sum_up(std::true_type());
+        else
+          sum_up(std::false_type());
         // Steps are added with the rounding's rest carried along: a key's rows may be millions.
         float x[4];
         unpair(add[0], x[0], x[1]);
@@ -541,9 +572,11 @@ cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps
                                       const mk_paged_batch& b, bool causal, const uint16_t* q, int64_t q_stride,
                                       float scale, const float* lse, float* mass, int32_t first, bool add,
                                       cudaStream_t s) {
-  const void* fn = L.e4m3 ? (const void*)k_prefill_mass<true> : (const void*)k_prefill_mass<false>;
+  // Row tiles of a sequence, at most.
+  const bool many = ((int64_t)b.max_new * L.G + kMassRows - 1) / kMassRows >= kMassMany;
+  auto fn = L.e4m3 ? (many ? k_prefill_mass<true, 1> : k_prefill_mass<true, 2>) : (many ? k_prefill_mass<false, 1> : k_prefill_mass<false, 2>);
   int sms = 0;
-  const cudaError_t e = kernel_smem_attr(fn, kMassSmem, kMassThreads, nullptr, &sms);
+  const cudaError_t e = kernel_smem_attr((const void*)fn, kMassSmem, kMassThreads, nullptr, &sms);
   if (e != cudaSuccess) return e;
   const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
   // Queries as {channels, heads, tokens}; a box is 64 channels of the 128 rows
@@ -558,7 +591,7 @@ cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   const MassArgs a{b, lse, mass, scale * kLog2e, causal ? 1 : 0, first, add ? 1 : 0, layer * L.n_pages, w.mass_part, w.prefill_counters};
-  return launch_pdl(L.e4m3 ? k_prefill_mass<true> : k_prefill_mass<false>, dim3(grid), dim3(kMassThreads), (size_t)kMassSmem, s, 0,
+  return launch_pdl(fn, dim3(grid), dim3(kMassThreads), (size_t)kMassSmem, s, 0,
                     L, a, maps.k, qmap);
 }
 
