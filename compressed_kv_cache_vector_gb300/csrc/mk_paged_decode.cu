@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     const int spare = (int)gridDim.x - units;
     int64_t p = (total + spare - 1) / spare;  // sum of ceil(n / p) <= total / p + units <= CTAs
     if (p < kShortest) p = kShortest;
-    if (p <= kAligned) {
+    if (p <= kAligned && (!OWN || p <= kShortest || p <= 2 * per)) {  // OWN: no run much longer than the mean
       per = pad = (int)p;
       total = list(pad);
     }

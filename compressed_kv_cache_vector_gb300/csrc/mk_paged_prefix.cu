@@ -46,7 +46,7 @@ struct Ring {
 // Registers of a thread of each four warps; the launch gives 128 each.
 template <bool E4M3>
 struct Regs {
-  static constexpr int softmax = 168, load = 112, issue = 64;
+  static constexpr int softmax = 176, load = 96, issue = 64;
   static_assert(2 * softmax + load + issue == 4 * 128, "register shares");
 };
 
@@ -74,13 +74,13 @@ struct Shared {
   Cursor start;
   int64_t f0, per;
   int span, bad;
-  uint64_t q_full, s_full[2], p_half[2], p_full[2], o_full, met, done;
+  uint64_t q_full, s_full[2], p_full[2], o_full, met, done;
   uint64_t k_full[3], k_free[3], v_full[3], v_free[3];  // the copies' rings
   uint64_t c_full[2], c_free[2];                        // e4m3: values in fp16
   float ml[2][kRows][2];                                // the two groups' maxima and sums
   // e4m3, per 16 keys of a step, ring of 8 steps: {k scale, log2 v scale}, 1 / v scale
   __align__(16) float2 kb[8][8];
-  float inv[8][8];
+  __align__(16) float inv[8][8];
   uint32_t tmem;
   volatile int dead;
 };
@@ -111,8 +111,8 @@ __device__ __forceinline__ void umma8(uint32_t d, uint64_t a, uint64_t b, uint32
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_prefix(PagedLayer L, PrefixArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  constexpr float kShift = E4M3 ? 10.0f : 0.0f;  // weights times 2^kShift before their rounding
-  constexpr float kLazy = E4M3 ? 4.0f : 8.0f;    // how far logits may pass the running maximum
+  constexpr float kShift = E4M3 ? 7.0f : 0.0f;  // weights times 2^kShift before their rounding
+  constexpr float kLazy = 8.0f;                 // how far logits may pass the running maximum
   constexpr int NK = Ring<E4M3>::keys, NV = Ring<E4M3>::values, kSlot = Ring<E4M3>::tile;
   extern __shared__ unsigned char dyn[];
   __shared__ Shared sh;
@@ -129,7 +129,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_half[i], 4);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.c_full[i], 4);
       mbar_init(&sh.c_free[i], 1);
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         Place<NK> kp;
         Place<NV> vp;
-        unsigned ph = 0;  // bit w: phase of p_half[w] and p_full[w]
+        unsigned ph = 0;  // bit w: phase of p_full[w]
         const uint64_t dq = sw128_desc(sq, 16), dl = sw128_desc(sq + kHalf, 16);
         for (Cursor k = sh.start; ok && k.rel < sh.span; next(k)) {
           if (!steps(k, j0, j1)) continue;
@@ -307,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (j < j0) continue;
             const unsigned w = c & 1;
-            ok = (E4M3 ? wait(&sh.c_full[w], (c >> 1) & 1) : wait(&sh.v_full[vp.slot], vp.phase)) && wait(&sh.p_half[w], (ph >> w) & 1);
+            ok = (E4M3 ? wait(&sh.c_full[w], (c >> 1) & 1) : wait(&sh.v_full[vp.slot], vp.phase)) && wait(&sh.p_full[w], (ph >> w) & 1);
             if (!ok) break;
             tmem_fence_after_sync();
             const uint64_t d = sw128_desc(E4M3 ? sc + w * kTile : sv + vp.slot * kSlot, kHalf);
@@ -316,16 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int more = j >= j0 + 2;  // the group has an accumulator
             if (blocks >= 8) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) umma_ts(o, p + i * 8, d + i * (2048 >> 4), idesc(!E4M3, 1), more || i > 0);
-              ok = wait(&sh.p_full[w], (ph >> w) & 1);
-              if (!ok) break;
-              tmem_fence_after_sync();
-#pragma unroll
-              for (int i = 4; i < 8; ++i) umma_ts(o, p + i * 8, d + i * (2048 >> 4), idesc(!E4M3, 1), 1);
+              for (int i = 0; i < 8; ++i) umma_ts(o, p + i * 8, d + i * (2048 >> 4), idesc(!E4M3, 1), more || i > 0);
             } else {
-              ok = wait(&sh.p_full[w], (ph >> w) & 1);
-              if (!ok) break;
-              tmem_fence_after_sync();
 #pragma unroll 1
               for (int i = 0; i < blocks; ++i) umma_ts(o, p + i * 8, d + i * (2048 >> 4), idesc(!E4M3, 1), more || i > 0);
             }
@@ -572,105 +563,119 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (live) {
           const int lim = len - j * kKeys;  // columns from here on are hidden
           const bool cut = lim < kKeys;
-          // The logits are read twice from tensor memory, 32 columns at a time, the next ones on their way.
-          uint32_t v[2][32];
-          auto arrive = [&](int h, int hh) {
-            tmem_ld_wait(v[hh]);
-            if (h < 3) tmem_ld32_async(ts + (h + 1) * 32, v[hh ^ 1]);
+          // The scales, all at once: read one by one, each would be waited for.
+          float kk[E4M3 ? 8 : 1], kb[E4M3 ? 8 : 1], inv[E4M3 ? 8 : 1];
+          if (E4M3) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const float4 x = *reinterpret_cast<const float4*>(&sh.kb[step & 7][i]);
+              kk[i] = fmaxf(zf * x.x, kTiny);
+              kb[i] = x.y;
+              kk[i + 1] = fmaxf(zf * x.z, kTiny);
+              kb[i + 1] = x.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(&inv[i]) = *reinterpret_cast<const float4*>(&sh.inv[step & 7][i]);
+          }
+          uint32_t v[32];
+          auto logits = [&](int h) {  // columns 32 h ..
+            tmem_ld32_async(ts + h * 32, v);
+            tmem_ld_wait(v);
             if (cut) {
               asm volatile("");  // a branch, not 32 selections in every step
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (i >= lim - 32 * h) v[hh][i] = 0xff800000u;
+                if (i >= lim - 32 * h) v[i] = 0xff800000u;
             }
           };
-          tmem_ld32_async(ts, v[0]);
-          float mx = -INFINITY;
+          // Weights under the maximum so far, in one reading of the logits: the
+          // largest exponent tells whether all fit.  Where not, and in a row's
+          // first step, the maximum is raised first.  The weights replace the
+          // logits, so they stay in registers until they are right.
+          float sum;
+          uint32_t p[64];
+          bool raise = !begun;
+          for (;;) {
+            if (__any_sync(FULL, raise)) {
+              float mx = -INFINITY;
 #pragma unroll 1
-          for (int h0 = 0; h0 < 4; h0 += 2)
+              for (int h = 0; h < 4; ++h) {
+                logits(h);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const int h = h0 + hh;
-              arrive(h, hh);
-#pragma unroll
-              for (int s = 0; s < 2; ++s) {  // 16 keys: one scale
-                const uint32_t* z = &v[hh][16 * s];
-                float x = max3(z[0], z[1], z[2]);
-                float y = max3(z[3], z[4], z[5]);
-                x = max3(__float_as_uint(x), z[6], z[7]);
-                y = max3(__float_as_uint(y), z[8], z[9]);
-                x = max3(__float_as_uint(x), z[10], z[11]);
-                y = max3(__float_as_uint(y), z[12], z[13]);
-                x = fmaxf(max3(__float_as_uint(x), z[14], z[15]), y);
-                if (E4M3) {
-                  const float2 kb = sh.kb[step & 7][2 * h + s];
-                  x = fmaf(x, fmaxf(zf * kb.x, kTiny), kb.y);
+                for (int s = 0; s < 2; ++s) {
+                  const uint32_t* z = &v[16 * s];
+                  float x = max3(z[0], z[1], z[2]);
+                  float y = max3(z[3], z[4], z[5]);
+                  x = max3(__float_as_uint(x), z[6], z[7]);
+                  y = max3(__float_as_uint(y), z[8], z[9]);
+                  x = max3(__float_as_uint(x), z[10], z[11]);
+                  y = max3(__float_as_uint(y), z[12], z[13]);
+                  x = fmaxf(max3(__float_as_uint(x), z[14], z[15]), y);
+                  if (E4M3) {
+                    const float2 b = sh.kb[step & 7][2 * h + s];
+                    x = fmaf(x, fmaxf(zf * b.x, kTiny), b.y);
+                  } else {
+                    x *= zf;
+                  }
+                  mx = fmaxf(mx, x);
                 }
-                mx = fmaxf(mx, x);
               }
-            }
-          tmem_ld32_async(ts, v[0]);
-          if (!E4M3) mx *= zf;
-          const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
-          if (__any_sync(FULL, raise)) {
-            const float mn = raise ? mx : m;
-            const float f = m == -INFINITY ? 0.0f : ex2(less(m) - less(mn));  // rows that stay: 2^0
-            l *= f;
-            m = mn;
-            if (begun) {
+              const float mn = raise ? fmaxf(m, mx) : m;
+              const float f = m == -INFINITY ? 1.0f : ex2(less(m) - less(mn));  // no weights yet: nothing to bring along
+              l *= f;
+              m = mn;
+              if (begun) {
 #pragma unroll 2
-              for (int h = 0; h < 8; ++h) {
-                uint32_t x[16];
-                tmem_ld16(to + h * 16, x);
+                for (int h = 0; h < 8; ++h) {
+                  uint32_t x[16];
+                  tmem_ld16(to + h * 16, x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                tmem_st16(to + h * 16, x);
+                  for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                  tmem_st16(to + h * 16, x);
+                }
               }
             }
-          }
-          const float ms = m == -INFINITY ? -kShift : less(m);
-#pragma unroll 1
-          for (int h0 = 0; h0 < 4; h0 += 2) {
+            // A row whose logits were all -infinity so far: any other is above.
+            const float ms = m == -INFINITY ? -1e30f : less(m);
+            const uint64_t m2 = pair(-ms, -ms);
+            float top0 = -INFINITY, top1 = -INFINITY;
+            sum = 0.0f;
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const int h = h0 + hh;
-              arrive(h, hh);
-              uint32_t p[16];
+            for (int h = 0; h < 4; ++h) {
+              logits(h);
 #pragma unroll
               for (int s = 0; s < 2; ++s) {
-                float kk = zf, bb = 0.0f;
-                if (E4M3) {
-                  const float2 kb = sh.kb[step & 7][2 * h + s];
-                  kk = fmaxf(zf * kb.x, kTiny);
-                  bb = kb.y;
-                }
-                const uint64_t k2 = pair(kk, kk), b2 = pair(bb, bb), m2 = pair(-ms, -ms);
+                const float kf = E4M3 ? kk[2 * h + s] : zf, bb = E4M3 ? kb[2 * h + s] : 0.0f;
+                const uint64_t k2 = pair(kf, kf), b2 = pair(bb, bb);
                 uint64_t add = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  const uint32_t* z = &v[hh][16 * s + 2 * i];
+                  const uint32_t* z = &v[16 * s + 2 * i];
                   float x, y;
                   // The logit is rounded before the maximum is taken off, as it was in the maximum:
                   // one fused step would leave the largest of huge logits above it.
                   unpair(add2(fma2(pair(__uint_as_float(z[0]), __uint_as_float(z[1])), k2, b2), m2), x, y);
+                  (i & 1 ? top1 : top0) = max3(__float_as_uint(i & 1 ? top1 : top0), __float_as_uint(x), __float_as_uint(y));
                   x = ex2(x);
                   y = ex2(y);
                   add = add2(add, pair(x, y));
-                  p[8 * s + i] = pack2<E4M3>(x, y);
+                  p[16 * h + 8 * s + i] = pack2<E4M3>(x, y);
                 }
                 float x, y;
                 unpair(add, x, y);
-                l = E4M3 ? fmaf(x + y, sh.inv[step & 7][2 * h + s], l) : l + (x + y);
+                sum = E4M3 ? fmaf(x + y, inv[2 * h + s], sum) : sum + (x + y);
               }
-              tmem_st16(ts + h * 16, p);
             }
-            // Half of the weights are enough to begin the value product.
-            tmem_wait_st();
-            tmem_fence_before_sync();
-            mbar_arrive_warp(h0 == 0 ? &sh.p_half[w] : &sh.p_full[w], lane);
+            raise = fmaxf(top0, top1) > kShift + kLazy;
+            if (!__any_sync(FULL, raise)) break;  // so after a maximum was raised
           }
+          l += sum;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) tmem_st16(ts + h * 16, *reinterpret_cast<const uint32_t(*)[16]>(&p[16 * h]));
+          tmem_wait_st();
+          tmem_fence_before_sync();
+          mbar_arrive_warp(&sh.p_full[w], lane);
         } else {  // no rows here: the weights may be anything
-          mbar_arrive_warp(&sh.p_half[w], lane);
           mbar_arrive_warp(&sh.p_full[w], lane);
         }
         begun = true;
