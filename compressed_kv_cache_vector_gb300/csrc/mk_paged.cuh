@@ -200,7 +200,7 @@ inline float* paged_own_parts(const PagedScratch& w) { return w.prefill_part + (
 // parts over the sequences' own tokens; both joined.
 cudaError_t launch_paged_prefix(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, const mk_paged_prefix& p, const uint16_t* q, int64_t q_stride,
-                                float scale, cudaStream_t s);
+                                float scale, bool check_only, cudaStream_t s);
 cudaError_t launch_paged_decode_own(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                     const mk_paged_batch& b, const uint16_t* q, int64_t q_stride, float scale,
                                     cudaStream_t s);

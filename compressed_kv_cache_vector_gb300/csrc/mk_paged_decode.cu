@@ -155,6 +155,35 @@ __global__ void __launch_bounds__(NW * 32, 1)
   auto apart = [&](float m, float M) { return OWN ? less(m) - less(M) : m - M; };
 
   int units = 0;  // (sequence, kv head) pairs with keys
+  if constexpr (OWN) {  // one warp: several sequences a lane, their loads in flight together
+    constexpr int kEach = MK_MAX_CALL_SEQS / NTHR;
+    PagedSeq s[kEach];
+    int off[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = e * NTHR + tid;
+      s[e].ok = false;
+      off[e] = 0;
+      if (i < n_seqs) {
+        s[e] = paged_seq(a.b, L.P, i, false);
+        off[e] = a.shared->seq[i].len;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = e * NTHR + tid;
+      if (i < n_seqs) {
+        if (!s[e].ok) paged_error(L, ERR_PAGED_BATCH, i, s[e].len);
+        const bool live = s[e].ok && s[e].n_new == 1;
+        if (!live || s[e].len <= 0) off[e] = 0;  // otherwise at most its length
+        s_len[i] = live ? s[e].len - off[e] : 0;
+        s_row[i] = live ? s[e].row0 : -1;
+        s_off[i] = off[e];
+      }
+      units += __popc(__ballot_sync(FULL, i < n_seqs && s_len[i < n_seqs ? i : 0] > 0)) * n_kv;
+    }
+    __syncthreads();
+  } else
   for (int i0 = 0; i0 < n_seqs; i0 += NTHR) {
     const int i = i0 + tid;
     bool keys = false;
@@ -162,12 +191,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
       const PagedSeq s = paged_seq(a.b, L.P, i, false);
       if (!s.ok) paged_error(L, ERR_PAGED_BATCH, i, s.len);
       const bool live = s.ok && (C == 1 ? s.n_new == 1 : s.n_new > 0);  // C = 2: n_new <= max_new <= 16 / G
-      const int off = OWN && live && s.len > 0 ? a.shared->seq[i].len : 0;  // at most s.len
-      s_len[i] = live ? s.len - off : 0;
+      s_len[i] = live ? s.len : 0;
       s_row[i] = live ? s.row0 : -1;
       if (C > 1) s_new[i] = live ? s.n_new : 0;
-      if (OWN) s_off[i] = off;
-      keys = s_len[i] > 0;
+      keys = live && s.len > 0;
     }
     units += __syncthreads_count(keys) * n_kv;
   }

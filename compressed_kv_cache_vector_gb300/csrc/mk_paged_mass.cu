@@ -112,12 +112,42 @@ struct MassCursor {
   int seq, head, kt, rel;
 };
 
-struct MassShared {
+// The list of items, and a CTA's run of it.
+struct MassList {
   int64_t pre[MK_MAX_CALL_SEQS + 1];  // cost of the sequences before each
   int row0[MK_MAX_CALL_SEQS], n_new[MK_MAX_CALL_SEQS], len[MK_MAX_CALL_SEQS];
   MassCursor start;
   int64_t f0, per;
   int span, patience;
+  int G, n_kv, n_seqs, kt0, causal;
+
+  __device__ int tiles_of(int seq) const { return (int)(((int64_t)n_new[seq] * G + kMassRows - 1) / kMassRows); }
+  __device__ int ends_of(int seq) const { return (len[seq] + kMassKeys - 1) / kMassKeys; }
+  __device__ int skip_of(int seq, int kt) const {  // row tiles before the first that sees the item's first key
+    const int64_t t = (int64_t)kt * kMassKeys - (len[seq] - n_new[seq]);
+    return causal && t > 0 ? (int)(t * G / kMassRows) : 0;
+  }
+  __device__ int cost_of(int seq, int kt) const { return tiles_of(seq) - skip_of(seq, kt) + kMassItemCost; }
+  __device__ void next(MassCursor& k) const {
+    k.rel += cost_of(k.seq, k.kt);
+    if (++k.kt < ends_of(k.seq)) return;
+    k.kt = kt0;
+    if (++k.head < n_kv) return;
+    k.head = 0;
+    do ++k.seq;
+    while (k.seq < n_seqs && ends_of(k.seq) <= kt0);
+  }
+  // The item's steps in this run are the row tiles [j0, j1) behind the skipped ones.
+  __device__ int steps(const MassCursor& k, int& j0, int& j1) const {
+    const int n = cost_of(k.seq, k.kt) - kMassItemCost;
+    j0 = max(0, -k.rel);
+    j1 = min(n, span - k.rel);
+    return n;
+  }
+};
+
+struct MassShared {
+  MassList list;
   uint64_t q_full[4], q_free[4], s_full[2][2], s_free[2][2], k_full[2], k_free[2], met[2], done;
   // -lse log2 e of a step's rows, -infinity where there is none.  A sum gives its
   // logits back before it has read the last of these, hence more than four.
@@ -128,6 +158,136 @@ struct MassShared {
   int last[2];
   volatile int dead;
 };
+
+// Forms the list (an item's steps are the row tiles that see its first key; it
+// is as long as these and kMassItemCost) and the CTA's run: the list is cut
+// into equal runs, one a CTA.  False where nothing is left for this CTA.
+__device__ bool mass_list(const PagedLayer& L, const MassArgs& a, MassList& m) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_seqs = a.b.n_seqs, n_kv = L.n_kv, warps = blockDim.x / 32;
+  if (tid == 0) {
+    m.G = L.G;
+    m.n_kv = n_kv;
+    m.n_seqs = n_seqs;
+    m.kt0 = a.first / kMassKeys;
+    m.causal = a.causal;
+  }
+  __syncthreads();
+  const int kt0 = m.kt0;
+  for (int i = warp; i < n_seqs; i += warps) {
+    PagedSeq s = paged_seq(a.b, L.P, i, false);
+    if (!s.ok) {
+      if (lane == 0) paged_error(L, ERR_PAGED_BATCH, i, s.len);
+      s.n_new = 0;
+    }
+    if (s.n_new == 0) s.len = 0;
+    if (lane == 0) {
+      m.row0[i] = s.row0;
+      m.n_new[i] = s.n_new;
+      m.len[i] = s.len;
+    }
+    __syncwarp();
+    int64_t x = 0;
+    for (int kt = kt0 + lane, n = m.ends_of(i); kt < n; kt += 32) x += m.cost_of(i, kt);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+    if (lane == 0) m.pre[i] = x * n_kv;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t at = 0;
+    for (int i0 = 0; i0 < n_seqs; i0 += 32) {
+      const int i = i0 + lane;
+      const int64_t mine = i < n_seqs ? m.pre[i] : 0;
+      int64_t x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+      }
+      if (i < n_seqs) m.pre[i] = at + x - mine;
+      at += __shfl_sync(FULL, x, 31);
+    }
+    if (lane == 0) m.pre[n_seqs] = at;
+  }
+  __syncthreads();
+  const int64_t total = m.pre[n_seqs];
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < kMassMinRun) per = kMassMinRun;
+  const int64_t f0 = (int64_t)blockIdx.x * per;
+  if (f0 >= total) return false;
+  if (warp == 0) {
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {  // the last sequence that begins at or before f0
+      const int mid = (lo + hi + 1) >> 1;
+      if (m.pre[mid] <= f0) lo = mid; else hi = mid - 1;
+    }
+    const int64_t one = (m.pre[lo + 1] - m.pre[lo]) / n_kv;  // a kv head's items
+    const int head = (int)((f0 - m.pre[lo]) / one);
+    int64_t at = m.pre[lo] + head * one;
+    for (int k0 = kt0, n = m.ends_of(lo); k0 < n; k0 += 32) {
+      const int kt = k0 + lane;
+      const int64_t cost = kt < n ? m.cost_of(lo, kt) : 0;
+      int64_t x = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned past = __ballot_sync(FULL, at + x > f0);
+      if (past) {
+        if (lane == __ffs(past) - 1) m.start = MassCursor{lo, head, kt, (int)(at + x - cost - f0)};
+        break;
+      }
+      at += __shfl_sync(FULL, x, 31);
+    }
+    if (lane == 0) {
+      m.f0 = f0;
+      m.per = per;
+      m.span = (int)(total - f0 < per ? total - f0 : per);
+      m.patience = 100 + m.span / 1024;
+    }
+  }
+  __syncthreads();
+  return true;
+}
+
+// A key's sum over the item's steps [j0, j1) of n: into the mass, or a part
+// where several CTAs have steps of the item: the last to come adds the parts,
+// in their order.  128 threads (key) for each half w of the item's keys.
+template <typename Meet>
+__device__ __forceinline__ bool mass_leave(const PagedLayer& L, const MassArgs& a, const MassList& list, const MassCursor& k, int j0,
+                                           int j1, int n, int page, int w, int key, float sum, int* last, Meet meet) {
+  const int len = list.len[k.seq], n_new = list.n_new[k.seq], t = k.kt * kMassKeys + w * 128 + key;
+  auto put = [&](float x) {
+    if (page < 0 || t < a.first || t >= len) return;
+    float* to = a.mass + ((int64_t)page * L.n_kv + k.head) * L.P + (t & (L.P - 1));
+    *to = a.add && (!a.causal || t < len - n_new) ? *to + x : x;
+  };
+  if (j0 == 0 && j1 == n) {
+    put(sum);
+    return true;
+  }
+  const int64_t place = list.f0 + k.rel;
+  const int b_lo = (int)(place / list.per), parts = (int)((place + n - 1) / list.per) - b_lo + 1;
+  auto slot = [&](int i) { return a.part + (2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0)) * kMassKeys + w * 128 + key; };
+  *slot((int)blockIdx.x - b_lo) = sum;
+  __threadfence();
+  if (!meet()) return false;
+  if (key == 0) {
+    int32_t* ctr = &a.counters[w * kPagedMaxCtas + b_lo];  // one item at most begins in b_lo and ends after it
+    const int old = atomicAdd(ctr, 1);
+    *last = old == parts - 1;
+    if (*last) *ctr = 0;
+  }
+  if (!meet()) return false;
+  if (*last) {
+    __threadfence();
+    float x = 0.0f;
+    for (int i = 0; i < parts; ++i) x += __ldcg(slot(i));
+    put(x);
+  }
+  return meet();  // *last is free again
+}
 
 // NK: items whose keys are held.  Few steps an item want the next item's keys
 // early (2), many want queries early (1: four tiles of them, 6000-token prompt
@@ -141,7 +301,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
   constexpr int NQ = 6 - 2 * NK;  // tiles of queries
   const uint32_t sk = base, sq = base + 2 * NK * kMassTile;
-  const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv, n_seqs = a.b.n_seqs;
+  const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv;
 
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -165,92 +325,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   pdl_trigger();
   if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;
 
-  // ---- the CTA's run of the list of items ----
-  // An item's steps are the row tiles that see its first key; it is as long as
-  // these and kMassItemCost.  The list is cut into equal runs, one a CTA.
-  const int kt0 = a.first / kMassKeys;
-  auto tiles_of = [&](int seq) { return (int)(((int64_t)sh.n_new[seq] * G + kMassRows - 1) / kMassRows); };
-  auto ends_of = [&](int seq) { return (sh.len[seq] + kMassKeys - 1) / kMassKeys; };
-  auto skip_of = [&](int seq, int kt) {  // row tiles before the first that sees the item's first key
-    const int64_t t = (int64_t)kt * kMassKeys - (sh.len[seq] - sh.n_new[seq]);
-    return a.causal && t > 0 ? (int)(t * G / kMassRows) : 0;
-  };
-  auto cost_of = [&](int seq, int kt) { return tiles_of(seq) - skip_of(seq, kt) + kMassItemCost; };
-  for (int i = warp; i < n_seqs; i += kMassThreads / 32) {
-    PagedSeq s = paged_seq(a.b, L.P, i, false);
-    if (!s.ok) {
-      if (lane == 0) paged_error(L, ERR_PAGED_BATCH, i, s.len);
-      s.n_new = 0;
-    }
-    if (s.n_new == 0) s.len = 0;
-    if (lane == 0) {
-      sh.row0[i] = s.row0;
-      sh.n_new[i] = s.n_new;
-      sh.len[i] = s.len;
-    }
-    __syncwarp();
-    int64_t x = 0;
-    for (int kt = kt0 + lane, n = ends_of(i); kt < n; kt += 32) x += cost_of(i, kt);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
-    if (lane == 0) sh.pre[i] = x * n_kv;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int64_t at = 0;
-    for (int i0 = 0; i0 < n_seqs; i0 += 32) {
-      const int i = i0 + lane;
-      const int64_t mine = i < n_seqs ? sh.pre[i] : 0;
-      int64_t x = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(FULL, x, o);
-        if (lane >= o) x += y;
-      }
-      if (i < n_seqs) sh.pre[i] = at + x - mine;
-      at += __shfl_sync(FULL, x, 31);
-    }
-    if (lane == 0) sh.pre[n_seqs] = at;
-  }
-  __syncthreads();
-  const int64_t total = sh.pre[n_seqs];
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < kMassMinRun) per = kMassMinRun;
-  const int64_t f0 = (int64_t)blockIdx.x * per;
-  if (f0 >= total) return;
-  if (warp == 0) {
-    int lo = 0, hi = n_seqs - 1;
-    while (lo < hi) {  // the last sequence that begins at or before f0
-      const int mid = (lo + hi + 1) >> 1;
-      if (sh.pre[mid] <= f0) lo = mid; else hi = mid - 1;
-    }
-    const int64_t one = (sh.pre[lo + 1] - sh.pre[lo]) / n_kv;  // a kv head's items
-    const int head = (int)((f0 - sh.pre[lo]) / one);
-    int64_t at = sh.pre[lo] + head * one;
-    for (int k0 = kt0, n = ends_of(lo); k0 < n; k0 += 32) {
-      const int kt = k0 + lane;
-      const int64_t cost = kt < n ? cost_of(lo, kt) : 0;
-      int64_t x = cost;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(FULL, x, o);
-        if (lane >= o) x += y;
-      }
-      const unsigned past = __ballot_sync(FULL, at + x > f0);
-      if (past) {
-        if (lane == __ffs(past) - 1) sh.start = MassCursor{lo, head, kt, (int)(at + x - cost - f0)};
-        break;
-      }
-      at += __shfl_sync(FULL, x, 31);
-    }
-    if (lane == 0) {
-      sh.f0 = f0;
-      sh.per = per;
-      sh.span = (int)(total - f0 < per ? total - f0 : per);
-      sh.patience = 100 + sh.span / 1024;
-    }
-  }
-  __syncthreads();
+  if (!mass_list(L, a, sh.list)) return;
+  const MassList& list = sh.list;
   if (warp == 13) tmem_alloc(&sh.tmem, 512);
   tmem_fence_before_sync();
   __syncthreads();
@@ -267,24 +343,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
   };
   auto wait = [&](uint64_t* bar, unsigned parity) { return mbar_try_wait(bar, parity) || slow(bar, parity, 1); };
   // For a wait that an item's steps can lie between.
-  auto wait_long = [&](uint64_t* bar, unsigned parity) { return mbar_try_wait(bar, parity) || slow(bar, parity, sh.patience); };
-  auto next = [&](MassCursor& k) {
-    k.rel += cost_of(k.seq, k.kt);
-    if (++k.kt < ends_of(k.seq)) return;
-    k.kt = kt0;
-    if (++k.head < n_kv) return;
-    k.head = 0;
-    do ++k.seq;
-    while (k.seq < n_seqs && ends_of(k.seq) <= kt0);
-  };
-  // The item's steps in this run are the row tiles [j0, j1) behind the skipped ones.
-  auto steps = [&](const MassCursor& k, int& j0, int& j1) {
-    const int n = cost_of(k.seq, k.kt) - kMassItemCost;
-    j0 = max(0, -k.rel);
-    j1 = min(n, sh.span - k.rel);
-    return n;
-  };
-
+  auto wait_long = [&](uint64_t* bar, unsigned parity) { return mbar_try_wait(bar, parity) || slow(bar, parity, list.patience); };
   if (warp == 13) {
     // ---- issues the products ----
     if (elect_one()) {
@@ -292,8 +351,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       bool ok = true;
       const uint64_t dk = sw128_desc(sk, 16), dq = sw128_desc(sq, 16);
       int j0, j1;
-      for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
-        steps(k, j0, j1);
+      for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
+        list.steps(k, j0, j1);
         if (j0 >= j1) continue;
         ok = wait(&sh.k_full[ic % NK], (ic / NK) & 1);
         for (int j = j0; ok && j < j1; ++j, ++c) {
@@ -326,11 +385,11 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     bool ok = true;
     int j0, j1;
     const int n_q = n_kv * G;
-    for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
-      steps(k, j0, j1);
-      const int row0 = sh.row0[k.seq];
-      const int64_t rows = (int64_t)sh.n_new[k.seq] * G;
-      const int skip = skip_of(k.seq, k.kt);
+    for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
+      list.steps(k, j0, j1);
+      const int row0 = list.row0[k.seq];
+      const int64_t rows = (int64_t)list.n_new[k.seq] * G;
+      const int skip = list.skip_of(k.seq, k.kt);
       for (int j = j0; ok && j < j1; ++j, ++c) {
         const int64_t r0 = (int64_t)(skip + j) * kMassRows;
         float n[4];
@@ -364,7 +423,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     auto page_at = [&](const MassCursor& k) {  // lane g < 16: the page of the item's 16-key group g, -1 where there is none
       const int tok = k.kt * kMassKeys + lane * 16;
       int p = -1;
-      if (lane < 16 && tok < sh.len[k.seq]) {
+      if (lane < 16 && tok < list.len[k.seq]) {
         p = a.b.page_table[(int64_t)k.seq * a.b.table_stride + (tok >> L.p_log2)];
         if (p < 0 || p >= L.n_pages) {
           paged_error(L, ERR_PAGED_PAGE, k.seq, p);
@@ -378,8 +437,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const int ck = (lane & 3) | (lane >> 1 & 4), r = (lane >> 2 & 1) | (lane >> 3 & 2) | (warp & 3) << 2;
       const uint32_t put = (ck >> 2) * (kMassTile / 2) + r * 128 + ((((2 * ck) & 7) ^ (r & 7)) << 4);
       const int64_t page_stride = (int64_t)n_kv * L.P * D;
-      for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
-        steps(k, j0, j1);
+      for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
+        list.steps(k, j0, j1);
         if (j0 >= j1) continue;
         const int pg = page_at(k);
         uint4 x[16];
@@ -419,8 +478,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         ++ic;
       }
     } else if (warp == 8) {
-      for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
-        steps(k, j0, j1);
+      for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
+        list.steps(k, j0, j1);
         if (j0 >= j1) continue;
         const int pg = page_at(k);
         ok = ic < NK || __all_sync(FULL, wait_long(&sh.k_free[ic % NK], (ic / NK - 1) & 1));
@@ -452,11 +511,11 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const unsigned parity = meets++ & 1;
       return __all_sync(FULL, wait(&sh.met[w], parity)) != 0;
     };
-    for (MassCursor k = sh.start; ok && k.rel < sh.span; next(k)) {
-      const int n = steps(k, j0, j1);
+    for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
+      const int n = list.steps(k, j0, j1);
       if (j0 >= j1) continue;
-      const int len = sh.len[k.seq], n_new = sh.n_new[k.seq], t = k.kt * kMassKeys + w * 128 + key;
-      const int64_t rows = (int64_t)n_new * G, r0 = (int64_t)(skip_of(k.seq, k.kt) + j0) * kMassRows;
+      const int len = list.len[k.seq], n_new = list.n_new[k.seq], t = k.kt * kMassKeys + w * 128 + key;
+      const int64_t rows = (int64_t)n_new * G, r0 = (int64_t)(list.skip_of(k.seq, k.kt) + j0) * kMassRows;
       // Rows left of the sequence from the step's first one on, and the first of them that sees the key.
       int64_t left = rows - r0;
       int64_t from = (a.causal ? max((int64_t)0, (int64_t)t - (len - n_new)) * G : 0) - r0;
@@ -518,36 +577,335 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       if (!ok) break;
       const int page = sh.page[ic % kMeta][w * 8 + (key >> 4)];
       ++ic;
-      auto put = [&](float x) {
-        if (page < 0 || t < a.first || t >= len) return;
-        float* to = a.mass + ((int64_t)page * n_kv + k.head) * L.P + (t & (L.P - 1));
-        *to = a.add && (!a.causal || t < len - n_new) ? *to + x : x;
-      };
-      if (j0 == 0 && j1 == n) {
-        put(sum);
-        continue;
+      ok = mass_leave(L, a, list, k, j0, j1, n, page, w, key, sum, &sh.last[w], meet);
+    }
+  }
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 13) tmem_dealloc(tmem, 512);
+  if (tid == 0 && sh.dead) paged_error(L, ERR_PAGED_WAIT, (int32_t)blockIdx.x, sh.dead - 1, (int32_t)MK_ETIMEOUT);
+}
+
+// ---- the weights of a few queries: up to 256 rows a kv head ----
+// A window of a prompt's last queries, or drafted tokens, against long
+// contexts: every key is read for a step or two, so HBM bounds it.  The
+// queries of a (sequence, kv head) stay in shared memory, and keys go by in a
+// ring of copies.  e4m3 keys are multiplied as they are, a query row being the
+// sum of an e4m3 and an e5m2 number each after a power of two (exact but for
+// channels below 2^-15 of the row's largest, off by at most 2^-20 of it): no
+// conversion of keys that are used once.
+constexpr int kWindowRows = 256;
+
+// TILES: row tiles of a sequence, at most.  With one, the next (sequence, kv
+// head)'s queries are loaded while this one's are in use.
+template <bool E4M3, int TILES>
+struct WindowShared {
+  MassList list;
+  static constexpr int NU = 2 / TILES, NK = E4M3 ? 4 : 2;
+  uint64_t q_full[NU], q_free[NU], s_full[2][2], s_free[2][2], k_full[NK], k_free[NK], met[2], done;
+  __align__(16) float nlse[2][kMassRows], ze[2][kMassRows];  // by row tile of a unit, or by unit
+  int page[kMeta][kMassKeys / 16];
+  float ks[kMeta][kMassKeys / 16];
+  uint32_t tmem;
+  int last[2];
+  volatile int dead;
+};
+
+template <bool E4M3, int TILES>
+__global__ void __launch_bounds__(kMassThreads, 1)
+    k_window_mass(PagedLayer L, MassArgs a, const uint16_t* q, int64_t q_stride, const __grid_constant__ CUtensorMap kmap) {
+  using Sh = WindowShared<E4M3, TILES>;
+  constexpr int NU = Sh::NU, NK = Sh::NK, kItem = E4M3 ? kMassTile : 2 * kMassTile, kSide = kMassTile / 2;
+  extern __shared__ unsigned char dyn[];
+  __shared__ Sh sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
+  const uint32_t sq = base, sk = base + 2 * kMassTile;
+  const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv;
+
+  if (tid == 0) {
+    for (int i = 0; i < NU; ++i) {
+      mbar_init(&sh.q_full[i], 4);
+      mbar_init(&sh.q_free[i], 9);  // the products' end and the eight summing warps
+    }
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_free[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&sh.s_full[i][j], 1);
+        mbar_init(&sh.s_free[i][j], 4);
       }
-      // Several CTAs have steps of this item: the last to come adds the parts, in their order.
-      const int64_t place = sh.f0 + k.rel;
-      const int b_lo = (int)(place / sh.per), parts = (int)((place + n - 1) / sh.per) - b_lo + 1;
-      auto slot = [&](int i) { return a.part + (2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0)) * kMassKeys + w * 128 + key; };
-      *slot((int)blockIdx.x - b_lo) = sum;
-      __threadfence();
-      if (!(ok = meet())) break;
-      if (key == 0) {
-        int32_t* ctr = &a.counters[w * kPagedMaxCtas + b_lo];  // one item at most begins in b_lo and ends after it
-        const int old = atomicAdd(ctr, 1);
-        sh.last[w] = old == parts - 1;
-        if (sh.last[w]) *ctr = 0;
+      mbar_init(&sh.met[i], 4);
+    }
+    mbar_init(&sh.done, 1);
+    sh.dead = 0;
+  }
+  mbar_init_fence();
+  pdl_wait();
+  pdl_trigger();
+  if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;
+  if (!mass_list(L, a, sh.list)) return;
+  const MassList& list = sh.list;
+  if (warp == 13) tmem_alloc(&sh.tmem, 512);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tmem = sh.tmem;
+
+  auto slow = [&](uint64_t* bar, unsigned parity, int times) {
+    for (int i = 0; i < times; ++i) {
+      if (sh.dead) return false;
+      if (paged_wait(bar, parity)) return true;
+    }
+    sh.dead = 1 + warp;
+    return false;
+  };
+  auto wait = [&](uint64_t* bar, unsigned parity) { return mbar_try_wait(bar, parity) || slow(bar, parity, 1); };
+  // For a wait that a unit's items can lie between.
+  auto wait_long = [&](uint64_t* bar, unsigned parity) { return mbar_try_wait(bar, parity) || slow(bar, parity, list.patience); };
+  // Every role goes through the same items; `u` counts the units (sequence, kv
+  // head), -1 before the first.
+  auto enters = [](const MassCursor& k, int& seq, int& head) {
+    const bool is = k.seq != seq || k.head != head;
+    seq = k.seq;
+    head = k.head;
+    return is;
+  };
+  int j0, j1, seq = -1, head = -1, u = -1;
+
+  if (warp == 13) {
+    // ---- issues the products ----
+    if (elect_one()) {
+      unsigned c = 0, ic = 0;
+      bool ok = true;
+      for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
+        list.steps(k, j0, j1);
+        if (j0 >= j1) continue;
+        if (enters(k, seq, head)) {
+          if (u >= 0) umma_commit(&sh.q_free[u % NU]);
+          ++u;
+          ok = wait(&sh.q_full[u % NU], (u / NU) & 1);
+        }
+        const int skip = list.skip_of(k.seq, k.kt);
+        ok = ok && wait(&sh.k_full[ic % NK], (ic / NK) & 1);
+        const uint64_t dk = sw128_desc(sk + (ic % NK) * kItem, 16);
+        for (int j = j0; ok && j < j1; ++j, ++c) {
+          const uint64_t dq = sw128_desc(sq + (TILES == 2 ? skip + j : u % NU) * kMassTile, 16);
+          for (int w = 0; ok && w < 2; ++w) {
+            ok = c < 2 || wait(&sh.s_free[w][c & 1], ((c >> 1) - 1) & 1);
+            if (!ok) break;
+            tmem_fence_after_sync();
+            const uint32_t d = tmem + (w * 2 + (c & 1)) * 128;
+            const uint64_t da = dk + (uint64_t)((w * (kItem / 2)) >> 4);
+            if (E4M3) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) umma8(d, da + i * 2, dq + i * 2, idesc8(0, 0), i > 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) umma8(d, da + i * 2, dq + (kSide >> 4) + i * 2, idesc8(0, 1), 1);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t o = ((i >> 2) * kSide + (i & 3) * 32) >> 4;
+                umma_ss(d, da + o, dq + o, idesc(1, 0), i > 0);
+              }
+            }
+            umma_commit(&sh.s_full[w][c & 1]);
+          }
+        }
+        if (ok) umma_commit(&sh.k_free[ic % NK]);
+        ++ic;
       }
-      if (!(ok = meet())) break;
-      if (sh.last[w]) {
-        __threadfence();
-        float x = 0.0f;
-        for (int i = 0; i < parts; ++i) x += __ldcg(slot(i));
-        put(x);
+      umma_commit(&sh.done);
+    }
+    // Nothing is in flight when the tensor memory is freed.
+    __syncwarp();
+    (void)paged_wait_warp(&sh.done, 0);
+  } else if (warp == 12) {
+    // ---- keys: copies, their pages and scales a step ahead ----
+    unsigned ic = 0;
+    bool ok = true;
+    const int box = !E4M3 || L.P < 32 ? 16 : 32, boxes = kMassKeys / box;
+    // Lane g < 16: the page and scale of the item's 16-key group g; -1 where there is none.
+    int pg = -1;
+    float ks = 1.0f;
+    auto fetch = [&](const MassCursor& k) {
+      const int tok = k.kt * kMassKeys + lane * 16;
+      pg = -1;
+      ks = 1.0f;
+      if (k.rel < list.span && lane < 16 && tok < list.len[k.seq]) {
+        pg = a.b.page_table[(int64_t)k.seq * a.b.table_stride + (tok >> L.p_log2)];
+        if (pg < 0 || pg >= L.n_pages) {
+          paged_error(L, ERR_PAGED_PAGE, k.seq, pg);
+          pg = -1;
+        }
+        if (E4M3 && pg >= 0) ks = L.k_scale[(int64_t)pg * n_kv + k.head];
       }
-      ok = meet();  // sh.last is free again
+    };
+    MassCursor k = list.start;
+    auto skip_empty = [&]() {  // to the next item with steps in this run
+      for (; k.rel < list.span; list.next(k)) {
+        list.steps(k, j0, j1);
+        if (j0 < j1) return;
+      }
+    };
+    skip_empty();
+    fetch(k);
+    while (ok && k.rel < list.span) {
+      ok = ic < NK || __all_sync(FULL, wait_long(&sh.k_free[ic % NK], (ic / NK - 1) & 1));
+      if (!ok) break;
+      if (lane < 16) {
+        sh.page[ic % kMeta][lane] = pg;
+        sh.ks[ic % kMeta][lane] = ks;
+      }
+      // Lane b < boxes copies `box` keys.
+      const int first = __shfl_sync(FULL, pg, (lane * box / 16) & 15);
+      const bool in = lane < boxes && first >= 0;
+      const unsigned n = __popc(__ballot_sync(FULL, in));
+      uint64_t* bar = &sh.k_full[ic % NK];
+      if (lane == 0) mbar_expect_tx(bar, n * box * D * (E4M3 ? 1 : 2));
+      __syncwarp();
+      if (in) {
+        const int key = lane * box, y = k.head * L.P + ((k.kt * kMassKeys + key) & (L.P - 1)), z = a.layer_page0 + first;
+        const uint32_t to = sk + (ic % NK) * kItem + (key >> 7) * (kItem / 2) + (key & 127) * 128;
+        tma3(to, &kmap, 0, y, z, bar);
+        if (!E4M3) tma3(to + kSide, &kmap, 64, y, z, bar);
+      }
+      ++ic;
+      list.next(k);
+      skip_empty();
+      fetch(k);
+    }
+    for (unsigned i = ic < NK ? 0 : ic - NK; i < ic; ++i) (void)paged_wait_warp(&sh.k_full[i % NK], (i / NK) & 1);
+  } else if (warp >= 8) {
+    // ---- queries of a unit, 16 lanes a row ----
+    const int ck = lane & 15, n_q = n_kv * G;
+    bool ok = true;
+    for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
+      list.steps(k, j0, j1);
+      if (j0 >= j1 || !enters(k, seq, head)) continue;
+      ++u;
+      ok = u < NU || __all_sync(FULL, wait_long(&sh.q_free[u % NU], (u / NU - 1) & 1));
+      if (!ok) break;
+      const int64_t row0 = list.row0[k.seq];
+      const int rows = list.n_new[k.seq] * G, tiles = list.tiles_of(k.seq);
+      for (int t = 0; t < tiles; ++t) {
+        const int at = TILES == 2 ? t : u % NU;
+        const uint32_t to = sq + at * kMassTile;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int r = i * 8 + (warp & 3) * 2 + (lane >> 4), x = t * kMassRows + r;
+          const int64_t tok = row0 + (x >> g_log2);
+          const int h = k.head * G + (x & (G - 1));
+          uint4 v = make_uint4(0, 0, 0, 0);
+          float ls = -INFINITY;
+          if (x < rows) {
+            v = *reinterpret_cast<const uint4*>(q + tok * q_stride + h * D + ck * 8);
+            if (ck == 0) ls = a.lse[tok * n_q + h];
+          }
+          if (E4M3) {
+            uint32_t hi[2], lo[2];
+            const float scale = split8(v, lane, hi, lo);
+            const uint32_t o = to + r * 128 + (((ck >> 1) ^ (r & 7)) << 4) + (ck & 1) * 8;
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o), "r"(hi[0]), "r"(hi[1]) : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o + kSide), "r"(lo[0]), "r"(lo[1]) : "memory");
+            if (ck == 0) sh.ze[at][r] = scale;
+          } else {
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (ck >> 3) * kSide + r * 128 + (((ck & 7) ^ (r & 7)) << 4)), "r"(v.x),
+                         "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
+          if (ck == 0) sh.nlse[at][r] = ls == -INFINITY ? -INFINITY : -ls * kLog2e;
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive_warp(&sh.q_full[u % NU], lane);
+    }
+  } else {
+    // ---- sums: one key a thread ----
+    const int w = warp >> 2, key = tid & 127;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + w * 256;
+    unsigned c = 0, ic = 0, meets = 0;
+    bool ok = true;
+    auto meet = [&]() {  // the four warps of this half
+      mbar_arrive_warp(&sh.met[w], lane);
+      const unsigned parity = meets++ & 1;
+      return __all_sync(FULL, wait(&sh.met[w], parity)) != 0;
+    };
+    for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
+      const int n = list.steps(k, j0, j1);
+      if (j0 >= j1) continue;
+      if (enters(k, seq, head)) {
+        if (u >= 0) mbar_arrive_warp(&sh.q_free[u % NU], lane);
+        ++u;
+      }
+      const int len = list.len[k.seq], n_new = list.n_new[k.seq], t = k.kt * kMassKeys + w * 128 + key;
+      const int skip = list.skip_of(k.seq, k.kt), rows = n_new * G;
+      const int seen = a.causal ? (int)min((int64_t)max(0, t - (len - n_new)) * G, (int64_t)rows) : 0;  // the first row that sees the key
+      float sum = 0.0f;
+      for (int j = j0; j < j1; ++j, ++c) {
+        ok = __all_sync(FULL, wait(&sh.s_full[w][c & 1], (c >> 1) & 1));
+        if (!ok) break;
+        tmem_fence_after_sync();
+        const float kf = E4M3 ? a.scale * sh.ks[ic % kMeta][w * 8 + (key >> 4)] : a.scale;
+        const uint64_t k2 = pair(kf, kf);
+        const int r0 = (skip + j) * kMassRows, cols = min(rows - r0, kMassRows), c0 = min(max(seen - r0, 0), kMassRows);
+        const float *nl = sh.nlse[TILES == 2 ? skip + j : u % NU], *ze = sh.ze[TILES == 2 ? skip + j : u % NU];
+        const uint32_t tb = ts + (c & 1) * 128;
+        uint64_t add[2] = {0, 0};
+        auto sum_up = [&](auto masked) {
+          constexpr bool kCut = decltype(masked)::value;
+          uint32_t v[2][32];
+          tmem_ld32_async(tb, v[0]);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            tmem_ld_wait(v[h & 1]);
+            if (h < 3) tmem_ld32_async(tb + (h + 1) * 32, v[(h + 1) & 1]);
+            if (h == 3) {  // all of S is in registers
+              tmem_fence_before_sync();
+              mbar_arrive_warp(&sh.s_free[w][c & 1], lane);
+            }
+            if (kCut && 32 * h >= cols) continue;
+            const uint32_t(&z)[32] = v[h & 1];
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 n4 = *reinterpret_cast<const float4*>(&nl[32 * h + i]);
+              uint64_t f0 = k2, f1 = k2;
+              if (E4M3) {
+                const float4 z4 = *reinterpret_cast<const float4*>(&ze[32 * h + i]);
+                f0 = mul2(pair(z4.x, z4.y), k2);
+                f1 = mul2(pair(z4.z, z4.w), k2);
+              }
+              float x[4];
+              unpair(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), f0, pair(n4.x, n4.y)), x[0], x[1]);
+              unpair(fma2(pair(__uint_as_float(z[i + 2]), __uint_as_float(z[i + 3])), f1, pair(n4.z, n4.w)), x[2], x[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
+              if (kCut) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (32 * h + i + e < c0 || 32 * h + i + e >= cols) x[e] = 0.0f;
+              }
+              add[0] = add2(add[0], pair(x[0], x[1]));
+              add[1] = add2(add[1], pair(x[2], x[3]));
+            }
+          }
+        };
+        if (cols < kMassRows || __any_sync(FULL, c0 > 0))
+          sum_up(std::true_type());
+        else
+          sum_up(std::false_type());
+        float x[4];
+        unpair(add[0], x[0], x[1]);
+        unpair(add[1], x[2], x[3]);
+        sum += (x[0] + x[1]) + (x[2] + x[3]);
+      }
+      if (!ok) break;
+      const int page = sh.page[ic % kMeta][w * 8 + (key >> 4)];
+      ++ic;
+      ok = mass_leave(L, a, list, k, j0, j1, n, page, w, key, sum, &sh.last[w], meet);
     }
   }
   tmem_fence_before_sync();
@@ -572,8 +930,19 @@ cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps
                                       const mk_paged_batch& b, bool causal, const uint16_t* q, int64_t q_stride,
                                       float scale, const float* lse, float* mass, int32_t first, bool add,
                                       cudaStream_t s) {
+  const MassArgs a{b, lse, mass, scale * kLog2e, causal ? 1 : 0, first, add ? 1 : 0, layer * L.n_pages, w.mass_part, w.prefill_counters};
+  const int64_t rows = (int64_t)b.max_new * L.G;
+  if (rows <= kWindowRows) {
+    const bool two = rows > kMassRows;
+    auto fn = L.e4m3 ? (two ? k_window_mass<true, 2> : k_window_mass<true, 1>) : (two ? k_window_mass<false, 2> : k_window_mass<false, 1>);
+    int sms = 0;
+    const cudaError_t e = kernel_smem_attr((const void*)fn, kMassSmem, kMassThreads, nullptr, &sms);
+    if (e != cudaSuccess) return e;
+    const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
+    return launch_pdl(fn, dim3(grid), dim3(kMassThreads), (size_t)kMassSmem, s, 0, L, a, q, q_stride, maps.k);
+  }
   // Row tiles of a sequence, at most.
-  const bool many = ((int64_t)b.max_new * L.G + kMassRows - 1) / kMassRows >= kMassMany;
+  const bool many = (rows + kMassRows - 1) / kMassRows >= kMassMany;
   auto fn = L.e4m3 ? (many ? k_prefill_mass<true, 1> : k_prefill_mass<true, 2>) : (many ? k_prefill_mass<false, 1> : k_prefill_mass<false, 2>);
   int sms = 0;
   const cudaError_t e = kernel_smem_attr((const void*)fn, kMassSmem, kMassThreads, nullptr, &sms);
@@ -590,7 +959,6 @@ cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const MassArgs a{b, lse, mass, scale * kLog2e, causal ? 1 : 0, first, add ? 1 : 0, layer * L.n_pages, w.mass_part, w.prefill_counters};
   return launch_pdl(fn, dim3(grid), dim3(kMassThreads), (size_t)kMassSmem, s, 0,
                     L, a, maps.k, qmap);
 }

@@ -57,7 +57,7 @@ struct PrefixArgs {
   int64_t q_stride;
   float scale;       // |scale| log2 e
   uint32_t q_sign;   // 0x80008000 when the scale is negative
-  int32_t layer_page0;
+  int32_t layer_page0, check_only;
   float* part;       // [2 kPagedMaxCtas][128] row parts
   float* row_part;   // [n_seqs][n_kv G] row parts
   PagedShared* shared;
@@ -96,17 +96,6 @@ struct Place {
     }
   }
 };
-
-// 8-bit products: A e4m3 (0) or e5m2 (1), B e4m3, 32 channels a step.
-__host__ __device__ constexpr uint32_t idesc8(int a_e5m2) {
-  return (1u << 4) | ((uint32_t)a_e5m2 << 7) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-__device__ __forceinline__ void umma8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
-}
 
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -156,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
+  if (a.check_only) return;
   const int groups = sh.bad ? 0 : n_groups;  // nothing is shared when the list is wrong
   auto blocks_of = [&](int g) { return (sh.last[g] - sh.first[g] + members - 1) / members; };
   auto steps_of = [&](int g) { return (sh.len[g] + kKeys - 1) / kKeys; };
@@ -290,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t d = sw128_desc(sk + kp.slot * kSlot, 16);
               if (E4M3) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) umma8(tmem + w * 128, dq + i * 2, d + i * 2, idesc8(0), i > 0);
+                for (int i = 0; i < 4; ++i) umma8(tmem + w * 128, dq + i * 2, d + i * 2, idesc8(0, 0), i > 0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) umma8(tmem + w * 128, dl + i * 2, d + i * 2, idesc8(1), 1);
+                for (int i = 0; i < 4; ++i) umma8(tmem + w * 128, dl + i * 2, d + i * 2, idesc8(1, 0), 1);
               } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -502,41 +492,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t h[4] = {q.x ^ a.q_sign, q.y ^ a.q_sign, q.z ^ a.q_sign, q.w ^ a.q_sign};
           if (E4M3) {
-            float top = 0.0f, y[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[2 * e] = __uint_as_float(h[e] << 16);
-              y[2 * e + 1] = __uint_as_float(h[e] & 0xffff0000u);
-              top = fmaxf(top, fmaxf(fabsf(y[2 * e]), fabsf(y[2 * e + 1])));
-            }
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-            if (top == INFINITY) {  // a row with an infinity has no logits: NaN there, 0 elsewhere
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] -= y[e];
-            }
-            int ex = (int)(__float_as_uint(top) >> 23) - 127 - 7;
-            ex = max(-100, min(ex, 120));
-            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
             uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t a2[2], b2[2];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float x0 = y[4 * e + 2 * u] * down, x1 = y[4 * e + 2 * u + 1] * down;
-                a2[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-                const uint32_t back = e4m3_h2(a2[u]);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-                b2[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0 - f.x, x1 - f.y), __NV_SATFINITE, __NV_E5M2);
-              }
-              hi[e] = a2[0] | a2[1] << 16;
-              lo[e] = b2[0] | b2[1] << 16;
-            }
+            const float scale = split8(make_uint4(h[0], h[1], h[2], h[3]), lane, hi, lo);
             const uint32_t at = sq + r * 128 + (((ck >> 1) ^ (r & 7)) << 4) + (ck & 1) * 8;
             asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
             asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + kHalf), "r"(lo[0]), "r"(lo[1]) : "memory");
-            if (ck == 0) sh.ml[0][r][0] = __uint_as_float((uint32_t)(127 + ex) << 23);
+            if (ck == 0) sh.ml[0][r][0] = scale;
           } else {
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(sq + (ck >> 3) * kHalf + r * 128 + (((ck & 7) ^ (r & 7)) << 4)),
                          "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
@@ -848,7 +809,7 @@ cudaError_t launch_paged_join(const PagedLayer& L, const PagedScratch& w, const 
 
 cudaError_t launch_paged_prefix(const PagedLayer& L, const PagedMaps& maps, const PagedScratch& w, int layer,
                                 const mk_paged_batch& b, const mk_paged_prefix& p, const uint16_t* q, int64_t q_stride,
-                                float scale, cudaStream_t s) {
+                                float scale, bool check_only, cudaStream_t s) {
   static_assert(kRows * kPagedRowPart == kPagedPrefixPart, "a part's size");
   const void* fn = L.e4m3 ? (const void*)k_paged_prefix<true> : (const void*)k_paged_prefix<false>;
   int sms = 0;
@@ -856,8 +817,8 @@ cudaError_t launch_paged_prefix(const PagedLayer& L, const PagedMaps& maps, cons
   if (e != cudaSuccess) return e;
   const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
   const PrefixArgs a{b, p, q, q_stride, (scale < 0.0f ? -scale : scale) * kLog2e, scale < 0.0f ? 0x80008000u : 0u,
-                     layer * L.n_pages, w.prefill_part, w.row_part, w.shared};
-  return launch_pdl(L.e4m3 ? k_paged_prefix<true> : k_paged_prefix<false>, dim3(grid), dim3(kThreads), (size_t)kSmem, s, 0, L, a,
+                     layer * L.n_pages, check_only ? 1 : 0, w.prefill_part, w.row_part, w.shared};
+  return launch_pdl(L.e4m3 ? k_paged_prefix<true> : k_paged_prefix<false>, dim3(check_only ? 1 : grid), dim3(kThreads), (size_t)kSmem, s, 0, L, a,
                     maps.k, maps.v);
 }
 

@@ -92,6 +92,60 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 8-bit products of 128 x 128, 32 channels a step: A and B e4m3 (0) or e5m2 (1).
+__host__ __device__ constexpr uint32_t idesc8(int a_e5m2, int b_e5m2) {
+  return (1u << 4) | ((uint32_t)a_e5m2 << 7) | ((uint32_t)b_e5m2 << 10) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void umma8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+// A row's eight bf16 channels (16 lanes have a row) as sums of an e4m3 number
+// and an e5m2 one, after the power of two that brings the row's largest to
+// [128, 256); returns what undoes it.  Exact for channels from 2^-15 of the
+// largest on: 8 significant bits are 4 and the 3 that a rest of at most 8
+// units wants; smaller ones are off by 2^-20 of it at most.
+__device__ __forceinline__ float split8(const uint4& v, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+  const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+  float top = 0.0f, y[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[2 * e] = __uint_as_float(h[e] << 16);
+    y[2 * e + 1] = __uint_as_float(h[e] & 0xffff0000u);
+    top = fmaxf(top, fmaxf(fabsf(y[2 * e]), fabsf(y[2 * e + 1])));
+  }
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+  if (top == INFINITY) {  // a row with an infinity has no logits: NaN there, 0 elsewhere
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] -= y[e];
+  }
+  int ex = (int)(__float_as_uint(top) >> 23) - 127 - 7;
+  ex = max(-100, min(ex, 120));
+  const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t a[2], b[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float x0 = y[4 * e + 2 * u] * down, x1 = y[4 * e + 2 * u + 1] * down;
+      a[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t back = e4m3_h2(a[u]);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+      b[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0 - f.x, x1 - f.y), __NV_SATFINITE, __NV_E5M2);
+    }
+    hi[e] = a[0] | a[1] << 16;
+    lo[e] = b[0] | b[1] << 16;
+  }
+  return __uint_as_float((uint32_t)(127 + ex) << 23);
+}
 // One lane of a converged warp (the tensor-core instructions take their
 // operands from uniform registers: a branch that only the lane's number
 // decides would make each of them a loop over the lanes).

@@ -150,6 +150,34 @@ def test_prompt_mass_longer(kv, news, lens, G, scale):
     _check_mass(made, before, m.mass, q, cu, news, scale, True, True, 0, lse)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("causal,add", [(True, False), (False, True)])
+@pytest.mark.parametrize("P,n_kv,G,top", [(16, 2, 4, 64), (32, 3, 8, 32), (64, 1, 2, 64), (32, 16, 1, 100), (16, 2, 8, 16)])
+def test_window_mass(kv, causal, add, P, n_kv, G, top):
+    """Up to 256 rows a kv head: one row tile or two, keys that the first tile does not see, many sequences, long ones."""
+    lens = [0, 1, 40, 129, 5000, 256, 333, 12, 5, 700, 257, 9000] + [100 + 31 * i for i in range(20)]
+    news = [3, 1, 0, top, 7, 33, 16, 9, 2, top - 1, top // 2, 1] + [1 + i % 13 for i in range(20)]
+    news = [min(x, top) for x in news]
+    made = Made(kv, P, n_kv, G, lens, 50 + P + G, spread=6)
+    cu = [0]
+    for x in news:
+        cu.append(cu[-1] + x)
+    rows = cu[-1]
+    wide = (1.5 * torch.randn(rows + 2, (n_kv * G + 1) * 128, generator=_gen(G), device=DEV)).to(torch.bfloat16)
+    wide[rows:] = float("nan")                                                          # padding rows are no one's
+    q = wide[:, :n_kv * G * 128].view(rows + 2, n_kv * G, 128)
+    b = K.PagedBatch(made.kv_len, made.table, _i32(cu), top, rows + 2)
+    _, lse = made.c.prefill_attn(0, b, q, causal=causal, scale=0.11, lse=True)
+    m = _made_mass(made, 4)
+    before = m.mass.clone()
+    made.c.prefill_mass(0, b, q, lse, m, causal=causal, first=7, add=add, scale=0.11)
+    assert made.c.poll_error() == (0, 0)
+    _check_mass(made, before, m.mass, q, cu, news, 0.11, causal, add, 7, lse)
+    again = K.PagedMass(made.c, before.clone())
+    made.c.prefill_mass(0, b, q, lse, again, causal=causal, first=7, add=add, scale=0.11)
+    assert torch.equal(again.mass, m.mass)
+
+
 def test_mass_sums_to_the_queries_and_a_nan_key_is_alone():
     """Every query hands out a total weight of 1; a key of NaN has a mass of NaN and spoils no other's."""
     made = Made("bf16", 16, 2, 4, [700, 90], 3)

@@ -20,10 +20,13 @@ def _built():
     build()
 
 
-def _shared(kv, P, n_kv, G, groups, seed, **kw):
-    """A cache whose groups share pages.  groups: [(tokens that name the same pages, [lengths of the sequences])]."""
+def _shared(kv, P, n_kv, G, groups, seed, wide=True, **kw):
+    """A cache whose groups share pages.  groups: [(tokens that name the same pages, [lengths of the sequences])].
+    wide: a page table so wide that the call cannot know that its batch is small (96 MB at most, where every sequence
+    reads what it shares by itself)."""
     lens = [t for _, ts in groups for t in ts]
-    made = Made(kv, P, n_kv, G, lens, seed, **kw)
+    cols = (96 << 20) // (len(lens) * P * n_kv * 256) + 1 if wide else 2
+    made = Made(kv, P, n_kv, G, lens, seed, extra_cols=cols, **kw)
     at, cu = 0, [0]
     for n, ts in groups:
         longest = at + max(range(len(ts)), key=lambda i: ts[i]) if ts else at
@@ -50,13 +53,13 @@ def _run(made, prefix, scale=128 ** -0.5, seed=1, size=1.5, check=True):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-@pytest.mark.parametrize("P,n_kv,G", [(16, 2, 4), (32, 1, 8), (64, 3, 1), (16, 1, 2)])
-def test_groups_of_every_shape(kv, P, n_kv, G):
+@pytest.mark.parametrize("P,n_kv,G,wide", [(16, 2, 4, True), (32, 1, 8, True), (64, 3, 1, True), (16, 1, 2, True), (32, 2, 4, False)])
+def test_groups_of_every_shape(kv, P, n_kv, G, wide):
     """Prefixes within a page, of whole pages, beyond a sequence's length; sequences that end with the prefix, that hold
     nothing; groups of one and of none."""
     groups = [(300, [330, 301, 300, 700, 304]), (0, [40]), (128, [128, 128, 129]), (5, [20, 9]), (64, []), (200, [210]),
               (1000, [64, 0, 640, 90]), (259, [260 + 7 * i for i in range(20)])]
-    made, prefix = _shared(kv, P, n_kv, G, groups, 40 + P, spread=5)
+    made, prefix = _shared(kv, P, n_kv, G, groups, 40 + P, wide, spread=5)
     _run(made, prefix, 0.1)
 
 
@@ -160,8 +163,9 @@ def test_captured_with_groups_that_change(kv):
         _check_attention(made, q, out, lse, 128 ** -0.5, [1] * 7, True, ROUND[kv])
 
 
-def test_wrong_groups_share_nothing_and_are_told():
-    made, prefix = _shared("bf16", 16, 2, 2, [(160, [200, 300, 170]), (64, [100, 90])], 6)
+@pytest.mark.parametrize("wide", [True, False])
+def test_wrong_groups_share_nothing_and_are_told(wide):
+    made, prefix = _shared("bf16", 16, 2, 2, [(160, [200, 300, 170]), (64, [100, 90])], 6, wide)
     q = torch.randn(5, 4, 128, generator=_gen(2), device=DEV).to(torch.bfloat16)
     b = K.PagedBatch(made.kv_len, made.table)
     for cu, shared in (([0, 4, 3], [160, 64]), ([0, 3, 6], [160, 64]), ([-1, 3, 5], [160, 64]), ([0, 3, 5], [160, -1])):
