@@ -65,7 +65,7 @@ struct PagedScratch {
   float* part_acc;
   float* part_ml;
   int32_t* counters;          // [max_seqs][n_kv], zero between calls
-  int32_t* prefill_counters;  // [2][kPagedMaxCtas], zero between calls
+  int32_t* prefill_counters;  // [kPagedMaxCtas], zero between calls
   float* prefill_part;        // paged_prefill_part_floats()
   float* mass_part;           // [2 kPagedMaxCtas][256]
   PagedShared* shared;

@@ -64,7 +64,7 @@ inline int64_t mass_layer_count(const mk_paged_config* c) { return (int64_t)c->n
 inline int64_t logits_bytes(const mk_paged_config* c) { return (int64_t)c->n_pages * c->n_q_heads * c->page * 4; }
 // Workspace: [error word][counters, zero between calls][split-token parts].
 inline int64_t clear_bytes(const mk_paged_config* c) {
-  return align_up(kAlign + ((int64_t)c->max_seqs * c->n_kv_heads + 2 * mk::kPagedMaxCtas) * 4);
+  return align_up(kAlign + ((int64_t)c->max_seqs * c->n_kv_heads + mk::kPagedMaxCtas) * 4);
 }
 // Rows of a unit of the decode kernel: at most 16 (several tokens a sequence).
 inline int64_t part_acc_bytes(const mk_paged_config*) {

@@ -103,7 +103,7 @@ struct MassArgs {
   float scale;  // times log2 e
   int32_t causal, first, add, layer_page0;
   float* part;        // [2 kPagedMaxCtas][kMassKeys]
-  int32_t* counters;  // [2][kPagedMaxCtas]
+  int32_t* counters;  // [kPagedMaxCtas]
 };
 
 // A place in the list of items: 256 keys of a (sequence, kv head), and where
@@ -146,16 +146,25 @@ struct MassList {
   }
 };
 
+// What the two groups of four summing warps (each with 64 columns of a step)
+// share.  They take the items' ends in turn: one leaves its sums here, the
+// other adds them to its own.  Four items' room: a group is at most two steps
+// behind the other, since the logits' buffers want both.
+struct MassSums {
+  uint64_t full[4], met[2];
+  float other[4][2][128];
+  int last[2];
+};
 struct MassShared {
   MassList list;
-  uint64_t q_full[4], q_free[4], s_full[2][2], s_free[2][2], k_full[2], k_free[2], met[2], done;
+  uint64_t q_full[4], q_free[4], s_full[2], s_free[2], k_full[2], k_free[2], done;
   // -lse log2 e of a step's rows, -infinity where there is none.  A sum gives its
   // logits back before it has read the last of these, hence more than four.
   __align__(16) float nlse[8][kMassRows];
   int page[kMeta][kMassKeys / 16];         // pages of an item's keys, -1: none
   float ks[kMeta][kMassKeys / 16];         // their scales (e4m3)
+  MassSums sums;
   uint32_t tmem;
-  int last[2];
   volatile int dead;
 };
 
@@ -251,30 +260,82 @@ __device__ bool mass_list(const PagedLayer& L, const MassArgs& a, MassList& m) {
   return true;
 }
 
-// A key's sum over the item's steps [j0, j1) of n: into the mass, or a part
-// where several CTAs have steps of the item: the last to come adds the parts,
-// in their order.  128 threads (key) for each half w of the item's keys.
+// One step of a warp: 64 of its 128 columns (from `col` on) for two keys a
+// thread, whose factors are k[0] and k[1]: a row's numbers, read from shared
+// memory for all lanes at once (as many cycles as columns), serve both.
+// kCut: columns before c[e], which key e is not seen by, and from `cols` on
+// count nothing.  ZE: a row has a factor of its own.  free() is called when all
+// logits have been read.
+template <bool kCut, bool ZE, typename Free>
+__device__ __forceinline__ void mass_step(uint32_t taddr, int col, const float* nl, const float* ze, const float (&k)[2], const int (&c)[2],
+                                          int cols, uint64_t (&add)[2][2], Free free) {
+  const uint64_t k2[2] = {pair(k[0], k[0]), pair(k[1], k[1])};
+  uint32_t v[2][2][16];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) tmem_ld16_async(taddr + e * 256, v[0][e]);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    tmem_ld_wait16(v[g & 1][0]);
+    tmem_ld_wait16(v[g & 1][1]);
+    if (g < 3) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) tmem_ld16_async(taddr + e * 256 + 16 * (g + 1), v[(g + 1) & 1][e]);
+    } else {
+      free();
+    }
+    if (kCut && col + 16 * g >= cols) continue;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 n4 = *reinterpret_cast<const float4*>(&nl[col + 16 * g + i]);
+      float4 z4;
+      if (ZE) z4 = *reinterpret_cast<const float4*>(&ze[col + 16 * g + i]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t(&z)[16] = v[g & 1][e];
+        const uint64_t f0 = ZE ? mul2(pair(z4.x, z4.y), k2[e]) : k2[e], f1 = ZE ? mul2(pair(z4.z, z4.w), k2[e]) : k2[e];
+        float x[4];
+        unpair(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), f0, pair(n4.x, n4.y)), x[0], x[1]);
+        unpair(fma2(pair(__uint_as_float(z[i + 2]), __uint_as_float(z[i + 3])), f1, pair(n4.z, n4.w)), x[2], x[3]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          x[u] = ex2(x[u]);
+          if (kCut && (col + 16 * g + i + u < c[e] || col + 16 * g + i + u >= cols)) x[u] = 0.0f;
+        }
+        add[e][0] = add2(add[e][0], pair(x[0], x[1]));
+        add[e][1] = add2(add[e][1], pair(x[2], x[3]));
+      }
+    }
+  }
+}
+
+// Two keys' sums (key and key + 128 of the item) over the item's steps [j0, j1)
+// of n: into the mass, or a part where several CTAs have steps of the item: the
+// last to come adds the parts, in their order.  128 threads.
 template <typename Meet>
 __device__ __forceinline__ bool mass_leave(const PagedLayer& L, const MassArgs& a, const MassList& list, const MassCursor& k, int j0,
-                                           int j1, int n, int page, int w, int key, float sum, int* last, Meet meet) {
-  const int len = list.len[k.seq], n_new = list.n_new[k.seq], t = k.kt * kMassKeys + w * 128 + key;
-  auto put = [&](float x) {
+                                           int j1, int n, const int* pages, int key, const float (&sum)[2], int* last, Meet meet) {
+  const int len = list.len[k.seq], n_new = list.n_new[k.seq];
+  auto put = [&](int e, float x) {
+    const int at = e * 128 + key, t = k.kt * kMassKeys + at, page = pages[at >> 4];
     if (page < 0 || t < a.first || t >= len) return;
     float* to = a.mass + ((int64_t)page * L.n_kv + k.head) * L.P + (t & (L.P - 1));
     *to = a.add && (!a.causal || t < len - n_new) ? *to + x : x;
   };
   if (j0 == 0 && j1 == n) {
-    put(sum);
+    put(0, sum[0]);
+    put(1, sum[1]);
     return true;
   }
   const int64_t place = list.f0 + k.rel;
   const int b_lo = (int)(place / list.per), parts = (int)((place + n - 1) / list.per) - b_lo + 1;
-  auto slot = [&](int i) { return a.part + (2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0)) * kMassKeys + w * 128 + key; };
-  *slot((int)blockIdx.x - b_lo) = sum;
+  auto slot = [&](int i) { return a.part + (2 * (int64_t)(b_lo + i) + (i == 0 ? 1 : 0)) * kMassKeys + key; };
+  float* const mine = slot((int)blockIdx.x - b_lo);
+  mine[0] = sum[0];
+  mine[128] = sum[1];
   __threadfence();
   if (!meet()) return false;
   if (key == 0) {
-    int32_t* ctr = &a.counters[w * kPagedMaxCtas + b_lo];  // one item at most begins in b_lo and ends after it
+    int32_t* ctr = &a.counters[b_lo];  // one item at most begins in b_lo and ends after it
     const int old = atomicAdd(ctr, 1);
     *last = old == parts - 1;
     if (*last) *ctr = 0;
@@ -282,11 +343,20 @@ __device__ __forceinline__ bool mass_leave(const PagedLayer& L, const MassArgs& 
   if (!meet()) return false;
   if (*last) {
     __threadfence();
-    float x = 0.0f;
-    for (int i = 0; i < parts; ++i) x += __ldcg(slot(i));
-    put(x);
+    float x = 0.0f, y = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+      x += __ldcg(slot(i));
+      y += __ldcg(slot(i) + 128);
+    }
+    put(0, x);
+    put(1, y);
   }
   return meet();  // *last is free again
+}
+
+__device__ __forceinline__ void mass_sums_init(MassSums& m) {
+  for (int i = 0; i < 4; ++i) mbar_init(&m.full[i], 4);
+  for (int i = 0; i < 2; ++i) mbar_init(&m.met[i], 4);
 }
 
 // NK: items whose keys are held.  Few steps an item want the next item's keys
@@ -309,14 +379,12 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       mbar_init(&sh.q_free[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      for (int j = 0; j < 2; ++j) {
-        mbar_init(&sh.s_full[i][j], 1);
-        mbar_init(&sh.s_free[i][j], 4);
-      }
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], 8);
       mbar_init(&sh.k_full[i], E4M3 ? 4 : 1);
       mbar_init(&sh.k_free[i], 1);
-      mbar_init(&sh.met[i], 4);
     }
+    mass_sums_init(sh.sums);
     mbar_init(&sh.done, 1);
     sh.dead = 0;
   }
@@ -357,19 +425,20 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         ok = wait(&sh.k_full[ic % NK], (ic / NK) & 1);
         for (int j = j0; ok && j < j1; ++j, ++c) {
           ok = wait(&sh.q_full[c % NQ], (c / NQ) & 1);
-          for (int w = 0; ok && w < 2; ++w) {
-            ok = c < 2 || wait(&sh.s_free[w][c & 1], ((c >> 1) - 1) & 1);
-            if (!ok) break;
-            tmem_fence_after_sync();
+          ok = ok && (c < 2 || wait(&sh.s_free[c & 1], ((c >> 1) - 1) & 1));
+          if (!ok) break;
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
             const uint64_t da = dk + (uint64_t)((((ic % NK) * 2 + w) * kMassTile) >> 4), db = dq + (uint64_t)(((c % NQ) * kMassTile) >> 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint32_t o = ((i >> 2) * (kMassTile / 2) + (i & 3) * 32) >> 4;
-              umma_ss(tmem + (w * 2 + (c & 1)) * 128, da + o, db + o, idesc(1, 0), i > 0);
+              umma_ss(tmem + w * 256 + (c & 1) * 128, da + o, db + o, idesc(1, 0), i > 0);
             }
-            umma_commit(&sh.s_full[w][c & 1]);
           }
-          if (ok) umma_commit(&sh.q_free[c % NQ]);
+          umma_commit(&sh.s_full[c & 1]);
+          umma_commit(&sh.q_free[c % NQ]);
         }
         if (ok) umma_commit(&sh.k_free[ic % NK]);
         ++ic;
@@ -500,84 +569,68 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       for (unsigned i = ic < NK ? 0 : ic - NK; i < ic; ++i) (void)paged_wait_warp(&sh.k_full[i % NK], (i / NK) & 1);
     }
   } else {
-    // ---- sums: one key a thread ----
+    // ---- sums: two keys a thread, half of the columns ----
+    int j0, j1;
     const int w = warp >> 2, key = tid & 127;
-    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + w * 256;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + w * 64;
     unsigned c = 0, ic = 0, meets = 0;
     bool ok = true;
-    int j0, j1;
     auto meet = [&]() {  // the four warps of this half
-      mbar_arrive_warp(&sh.met[w], lane);
+      mbar_arrive_warp(&sh.sums.met[w], lane);
       const unsigned parity = meets++ & 1;
-      return __all_sync(FULL, wait(&sh.met[w], parity)) != 0;
+      return __all_sync(FULL, wait(&sh.sums.met[w], parity)) != 0;
     };
     for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
       const int n = list.steps(k, j0, j1);
       if (j0 >= j1) continue;
-      const int len = list.len[k.seq], n_new = list.n_new[k.seq], t = k.kt * kMassKeys + w * 128 + key;
-      const int64_t rows = (int64_t)n_new * G, r0 = (int64_t)(list.skip_of(k.seq, k.kt) + j0) * kMassRows;
-      // Rows left of the sequence from the step's first one on, and the first of them that sees the key.
-      int64_t left = rows - r0;
-      int64_t from = (a.causal ? max((int64_t)0, (int64_t)t - (len - n_new)) * G : 0) - r0;
-      float sum = 0.0f, low = 0.0f;
-      for (int j = j0; j < j1; ++j, ++c, left -= kMassRows, from -= kMassRows) {
-        ok = __all_sync(FULL, wait(&sh.s_full[w][c & 1], (c >> 1) & 1));
+      const int len = list.len[k.seq], n_new = list.n_new[k.seq], t = k.kt * kMassKeys + key, skip = list.skip_of(k.seq, k.kt);
+      // Rows left of the sequence from the step's first one on, and the first of them that sees each key.
+      int64_t left = (int64_t)n_new * G - (int64_t)(skip + j0) * kMassRows, from[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        from[e] = (a.causal ? max((int64_t)0, (int64_t)t + 128 * e - (len - n_new)) * G : 0) - (int64_t)(skip + j0) * kMassRows;
+      float sum[2] = {0.0f, 0.0f}, low[2] = {0.0f, 0.0f};
+      for (int j = j0; j < j1; ++j, ++c, left -= kMassRows, from[0] -= kMassRows, from[1] -= kMassRows) {
+        ok = __all_sync(FULL, wait(&sh.s_full[c & 1], (c >> 1) & 1));
         if (!ok) break;
         tmem_fence_after_sync();
-        const float kf = E4M3 ? a.scale * sh.ks[ic % kMeta][w * 8 + (key >> 4)] : a.scale;
-        const uint64_t k2 = pair(kf, kf);
-        const int cols = (int)min(left, (int64_t)kMassRows), c0 = (int)min(max(from, (int64_t)0), (int64_t)kMassRows);
-        const bool cut = cols < kMassRows || __any_sync(FULL, c0 > 0);
-        const uint32_t tb = ts + (c & 1) * 128;
-        uint64_t add[2] = {0, 0};
-        auto sum_up = [&](auto masked) {
-          constexpr bool kCut = decltype(masked)::value;
-          uint32_t v[2][32];
-          tmem_ld32_async(tb, v[0]);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            tmem_ld_wait(v[h & 1]);
-            if (h < 3) tmem_ld32_async(tb + (h + 1) * 32, v[(h + 1) & 1]);
-            if (h == 3) {  // all of S is in registers
-              tmem_fence_before_sync();
-              mbar_arrive_warp(&sh.s_free[w][c & 1], lane);
-            }
-            if (kCut && 32 * h >= cols) continue;
-            const uint32_t(&z)[32] = v[h & 1];
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 nl = *reinterpret_cast<const float4*>(&sh.nlse[c & 7][32 * h + i]);
-              float x[4];
-              unpair(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), k2, pair(nl.x, nl.y)), x[0], x[1]);
-              unpair(fma2(pair(__uint_as_float(z[i + 2]), __uint_as_float(z[i + 3])), k2, pair(nl.z, nl.w)), x[2], x[3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
-              if (kCut) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (32 * h + i + e < c0 || 32 * h + i + e >= cols) x[e] = 0.0f;
-              }
-              add[0] = add2(add[0], pair(x[0], x[1]));
-              add[1] = add2(add[1], pair(x[2], x[3]));
-            }
-          }
+        const float kf[2] = {E4M3 ? a.scale * sh.ks[ic % kMeta][key >> 4] : a.scale, E4M3 ? a.scale * sh.ks[ic % kMeta][8 + (key >> 4)] : a.scale};
+        const int cols = (int)min(left, (int64_t)kMassRows);
+        const int c0[2] = {(int)min(max(from[0], (int64_t)0), (int64_t)kMassRows), (int)min(max(from[1], (int64_t)0), (int64_t)kMassRows)};
+        uint64_t add[2][2] = {{0, 0}, {0, 0}};
+        auto free = [&]() {
+          tmem_fence_before_sync();
+          mbar_arrive_warp(&sh.s_free[c & 1], lane);
         };
-        if (cut)
-          sum_up(std::true_type());
+        if (cols < kMassRows || __any_sync(FULL, c0[1] > 0))
+          mass_step<true, false>(ts + (c & 1) * 128, w * 64, sh.nlse[c & 7], nullptr, kf, c0, cols, add, free);
         else
-          sum_up(std::false_type());
+          mass_step<false, false>(ts + (c & 1) * 128, w * 64, sh.nlse[c & 7], nullptr, kf, c0, cols, add, free);
         // Steps are added with the rounding's rest carried along: a key's rows may be millions.
-        float x[4];
-        unpair(add[0], x[0], x[1]);
-        unpair(add[1], x[2], x[3]);
-        const float y = ((x[0] + x[1]) + (x[2] + x[3])) - low, s = sum + y;
-        low = (s - sum) - y;
-        sum = s;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x[4];
+          unpair(add[e][0], x[0], x[1]);
+          unpair(add[e][1], x[2], x[3]);
+          const float y = ((x[0] + x[1]) + (x[2] + x[3])) - low[e], s = sum[e] + y;
+          low[e] = (s - sum[e]) - y;
+          sum[e] = s;
+        }
       }
       if (!ok) break;
-      const int page = sh.page[ic % kMeta][w * 8 + (key >> 4)];
+      float(&other)[2][128] = sh.sums.other[ic & 3];
+      if ((ic & 1) != (unsigned)w) {
+        other[0][key] = sum[0];
+        other[1][key] = sum[1];
+        mbar_arrive_warp(&sh.sums.full[ic & 3], lane);
+      } else {
+        ok = __all_sync(FULL, wait(&sh.sums.full[ic & 3], (ic >> 2) & 1));
+        if (!ok) break;
+        // The first half of the columns first: the order does not depend on who adds.
+        const float x[2] = {w ? other[0][key] + sum[0] : sum[0] + other[0][key], w ? other[1][key] + sum[1] : sum[1] + other[1][key]};
+        ok = mass_leave(L, a, list, k, j0, j1, n, sh.page[ic % kMeta], key, x, &sh.sums.last[w], meet);
+      }
       ++ic;
-      ok = mass_leave(L, a, list, k, j0, j1, n, page, w, key, sum, &sh.last[w], meet);
     }
   }
   tmem_fence_before_sync();
@@ -603,12 +656,12 @@ template <bool E4M3, int TILES>
 struct WindowShared {
   MassList list;
   static constexpr int NU = 2 / TILES, NK = E4M3 ? 4 : 2;
-  uint64_t q_full[NU], q_free[NU], s_full[2][2], s_free[2][2], k_full[NK], k_free[NK], met[2], done;
+  uint64_t q_full[NU], q_free[NU], s_full[2], s_free[2], k_full[NK], k_free[NK], done;
   __align__(16) float nlse[2][kMassRows], ze[2][kMassRows];  // by row tile of a unit, or by unit
   int page[kMeta][kMassKeys / 16];
   float ks[kMeta][kMassKeys / 16];
+  MassSums sums;
   uint32_t tmem;
-  int last[2];
   volatile int dead;
 };
 
@@ -634,12 +687,10 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       mbar_init(&sh.k_free[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      for (int j = 0; j < 2; ++j) {
-        mbar_init(&sh.s_full[i][j], 1);
-        mbar_init(&sh.s_free[i][j], 4);
-      }
-      mbar_init(&sh.met[i], 4);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], 8);
     }
+    mass_sums_init(sh.sums);
     mbar_init(&sh.done, 1);
     sh.dead = 0;
   }
@@ -694,11 +745,12 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         const uint64_t dk = sw128_desc(sk + (ic % NK) * kItem, 16);
         for (int j = j0; ok && j < j1; ++j, ++c) {
           const uint64_t dq = sw128_desc(sq + (TILES == 2 ? skip + j : u % NU) * kMassTile, 16);
-          for (int w = 0; ok && w < 2; ++w) {
-            ok = c < 2 || wait(&sh.s_free[w][c & 1], ((c >> 1) - 1) & 1);
-            if (!ok) break;
-            tmem_fence_after_sync();
-            const uint32_t d = tmem + (w * 2 + (c & 1)) * 128;
+          ok = c < 2 || wait(&sh.s_free[c & 1], ((c >> 1) - 1) & 1);
+          if (!ok) break;
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t d = tmem + w * 256 + (c & 1) * 128;
             const uint64_t da = dk + (uint64_t)((w * (kItem / 2)) >> 4);
             if (E4M3) {
 #pragma unroll
@@ -712,8 +764,8 @@ __global__ void __launch_bounds__(kMassThreads, 1)
                 umma_ss(d, da + o, dq + o, idesc(1, 0), i > 0);
               }
             }
-            umma_commit(&sh.s_full[w][c & 1]);
           }
+          umma_commit(&sh.s_full[c & 1]);
         }
         if (ok) umma_commit(&sh.k_free[ic % NK]);
         ++ic;
@@ -794,45 +846,55 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       for (int t = 0; t < tiles; ++t) {
         const int at = TILES == 2 ? t : u % NU;
         const uint32_t to = sq + at * kMassTile;
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          const int r = i * 8 + (warp & 3) * 2 + (lane >> 4), x = t * kMassRows + r;
-          const int64_t tok = row0 + (x >> g_log2);
-          const int h = k.head * G + (x & (G - 1));
-          uint4 v = make_uint4(0, 0, 0, 0);
-          float ls = -INFINITY;
-          if (x < rows) {
-            v = *reinterpret_cast<const uint4*>(q + tok * q_stride + h * D + ck * 8);
-            if (ck == 0) ls = a.lse[tok * n_q + h];
+#pragma unroll 1
+        for (int i0 = 0; i0 < 16; i0 += 8) {  // eight rows' loads in flight
+          uint4 v[8];
+          float ls[8];
+          auto row_of = [&](int i) { return (i0 + i) * 8 + (warp & 3) * 2 + (lane >> 4); };
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int x = t * kMassRows + row_of(i);
+            const int64_t tok = row0 + (x >> g_log2);
+            const int h = k.head * G + (x & (G - 1));
+            v[i] = make_uint4(0, 0, 0, 0);
+            ls[i] = -INFINITY;
+            if (x < rows) {
+              v[i] = *reinterpret_cast<const uint4*>(q + tok * q_stride + h * D + ck * 8);
+              if (ck == 0) ls[i] = a.lse[tok * n_q + h];
+            }
           }
-          if (E4M3) {
-            uint32_t hi[2], lo[2];
-            const float scale = split8(v, lane, hi, lo);
-            const uint32_t o = to + r * 128 + (((ck >> 1) ^ (r & 7)) << 4) + (ck & 1) * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o), "r"(hi[0]), "r"(hi[1]) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o + kSide), "r"(lo[0]), "r"(lo[1]) : "memory");
-            if (ck == 0) sh.ze[at][r] = scale;
-          } else {
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (ck >> 3) * kSide + r * 128 + (((ck & 7) ^ (r & 7)) << 4)), "r"(v.x),
-                         "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = row_of(i);
+            if (E4M3) {
+              uint32_t hi[2], lo[2];
+              const float scale = split8(v[i], lane, hi, lo);
+              const uint32_t o = to + r * 128 + (((ck >> 1) ^ (r & 7)) << 4) + (ck & 1) * 8;
+              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o), "r"(hi[0]), "r"(hi[1]) : "memory");
+              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o + kSide), "r"(lo[0]), "r"(lo[1]) : "memory");
+              if (ck == 0) sh.ze[at][r] = scale;
+            } else {
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (ck >> 3) * kSide + r * 128 + (((ck & 7) ^ (r & 7)) << 4)),
+                           "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                           : "memory");
+            }
+            if (ck == 0) sh.nlse[at][r] = ls[i] == -INFINITY ? -INFINITY : -ls[i] * kLog2e;
           }
-          if (ck == 0) sh.nlse[at][r] = ls == -INFINITY ? -INFINITY : -ls * kLog2e;
         }
       }
       fence_proxy_async();
       mbar_arrive_warp(&sh.q_full[u % NU], lane);
     }
   } else {
-    // ---- sums: one key a thread ----
+    // ---- sums: two keys a thread, half of the columns ----
     const int w = warp >> 2, key = tid & 127;
-    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + w * 256;
+    const uint32_t ts = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + w * 64;
     unsigned c = 0, ic = 0, meets = 0;
     bool ok = true;
     auto meet = [&]() {  // the four warps of this half
-      mbar_arrive_warp(&sh.met[w], lane);
+      mbar_arrive_warp(&sh.sums.met[w], lane);
       const unsigned parity = meets++ & 1;
-      return __all_sync(FULL, wait(&sh.met[w], parity)) != 0;
+      return __all_sync(FULL, wait(&sh.sums.met[w], parity)) != 0;
     };
     for (MassCursor k = list.start; ok && k.rel < list.span; list.next(k)) {
       const int n = list.steps(k, j0, j1);
@@ -841,71 +903,54 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         if (u >= 0) mbar_arrive_warp(&sh.q_free[u % NU], lane);
         ++u;
       }
-      const int len = list.len[k.seq], n_new = list.n_new[k.seq], t = k.kt * kMassKeys + w * 128 + key;
-      const int skip = list.skip_of(k.seq, k.kt), rows = n_new * G;
-      const int seen = a.causal ? (int)min((int64_t)max(0, t - (len - n_new)) * G, (int64_t)rows) : 0;  // the first row that sees the key
-      float sum = 0.0f;
-      for (int j = j0; j < j1; ++j, ++c) {
-        ok = __all_sync(FULL, wait(&sh.s_full[w][c & 1], (c >> 1) & 1));
+      const int len = list.len[k.seq], n_new = list.n_new[k.seq], t = k.kt * kMassKeys + key, skip = list.skip_of(k.seq, k.kt);
+      // Rows left of the sequence from the step's first one on, and the first of them that sees each key.
+      int64_t left = (int64_t)n_new * G - (int64_t)(skip + j0) * kMassRows, from[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        from[e] = (a.causal ? max((int64_t)0, (int64_t)t + 128 * e - (len - n_new)) * G : 0) - (int64_t)(skip + j0) * kMassRows;
+      float sum[2] = {0.0f, 0.0f}, low[2] = {0.0f, 0.0f};
+      for (int j = j0; j < j1; ++j, ++c, left -= kMassRows, from[0] -= kMassRows, from[1] -= kMassRows) {
+        ok = __all_sync(FULL, wait(&sh.s_full[c & 1], (c >> 1) & 1));
         if (!ok) break;
         tmem_fence_after_sync();
-        const float kf = E4M3 ? a.scale * sh.ks[ic % kMeta][w * 8 + (key >> 4)] : a.scale;
-        const uint64_t k2 = pair(kf, kf);
-        const int r0 = (skip + j) * kMassRows, cols = min(rows - r0, kMassRows), c0 = min(max(seen - r0, 0), kMassRows);
-        const float *nl = sh.nlse[TILES == 2 ? skip + j : u % NU], *ze = sh.ze[TILES == 2 ? skip + j : u % NU];
-        const uint32_t tb = ts + (c & 1) * 128;
-        uint64_t add[2] = {0, 0};
-        auto sum_up = [&](auto masked) {
-          constexpr bool kCut = decltype(masked)::value;
-          uint32_t v[2][32];
-          tmem_ld32_async(tb, v[0]);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            tmem_ld_wait(v[h & 1]);
-            if (h < 3) tmem_ld32_async(tb + (h + 1) * 32, v[(h + 1) & 1]);
-            if (h == 3) {  // all of S is in registers
-              tmem_fence_before_sync();
-              mbar_arrive_warp(&sh.s_free[w][c & 1], lane);
-            }
-            if (kCut && 32 * h >= cols) continue;
-            const uint32_t(&z)[32] = v[h & 1];
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 n4 = *reinterpret_cast<const float4*>(&nl[32 * h + i]);
-              uint64_t f0 = k2, f1 = k2;
-              if (E4M3) {
-                const float4 z4 = *reinterpret_cast<const float4*>(&ze[32 * h + i]);
-                f0 = mul2(pair(z4.x, z4.y), k2);
-                f1 = mul2(pair(z4.z, z4.w), k2);
-              }
-              float x[4];
-              unpair(fma2(pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), f0, pair(n4.x, n4.y)), x[0], x[1]);
-              unpair(fma2(pair(__uint_as_float(z[i + 2]), __uint_as_float(z[i + 3])), f1, pair(n4.z, n4.w)), x[2], x[3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = ex2(x[e]);
-              if (kCut) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (32 * h + i + e < c0 || 32 * h + i + e >= cols) x[e] = 0.0f;
-              }
-              add[0] = add2(add[0], pair(x[0], x[1]));
-              add[1] = add2(add[1], pair(x[2], x[3]));
-            }
-          }
+        const float kf[2] = {E4M3 ? a.scale * sh.ks[ic % kMeta][key >> 4] : a.scale, E4M3 ? a.scale * sh.ks[ic % kMeta][8 + (key >> 4)] : a.scale};
+        const int cols = (int)min(left, (int64_t)kMassRows);
+        const int c0[2] = {(int)min(max(from[0], (int64_t)0), (int64_t)kMassRows), (int)min(max(from[1], (int64_t)0), (int64_t)kMassRows)};
+        uint64_t add[2][2] = {{0, 0}, {0, 0}};
+        auto free = [&]() {
+          tmem_fence_before_sync();
+          mbar_arrive_warp(&sh.s_free[c & 1], lane);
         };
-        if (cols < kMassRows || __any_sync(FULL, c0 > 0))
-          sum_up(std::true_type());
+        if (cols < kMassRows || __any_sync(FULL, c0[1] > 0))
+          mass_step<true, E4M3>(ts + (c & 1) * 128, w * 64, sh.nlse[TILES == 2 ? skip + j : u % NU], sh.ze[TILES == 2 ? skip + j : u % NU], kf, c0, cols, add, free);
         else
-          sum_up(std::false_type());
-        float x[4];
-        unpair(add[0], x[0], x[1]);
-        unpair(add[1], x[2], x[3]);
-        sum += (x[0] + x[1]) + (x[2] + x[3]);
+          mass_step<false, E4M3>(ts + (c & 1) * 128, w * 64, sh.nlse[TILES == 2 ? skip + j : u % NU], sh.ze[TILES == 2 ? skip + j : u % NU], kf, c0, cols, add, free);
+        // Steps are added with the rounding's rest carried along: a key's rows may be millions.
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x[4];
+          unpair(add[e][0], x[0], x[1]);
+          unpair(add[e][1], x[2], x[3]);
+          const float y = ((x[0] + x[1]) + (x[2] + x[3])) - low[e], s = sum[e] + y;
+          low[e] = (s - sum[e]) - y;
+          sum[e] = s;
+        }
       }
       if (!ok) break;
-      const int page = sh.page[ic % kMeta][w * 8 + (key >> 4)];
+      float(&other)[2][128] = sh.sums.other[ic & 3];
+      if ((ic & 1) != (unsigned)w) {
+        other[0][key] = sum[0];
+        other[1][key] = sum[1];
+        mbar_arrive_warp(&sh.sums.full[ic & 3], lane);
+      } else {
+        ok = __all_sync(FULL, wait(&sh.sums.full[ic & 3], (ic >> 2) & 1));
+        if (!ok) break;
+        // The first half of the columns first: the order does not depend on who adds.
+        const float x[2] = {w ? other[0][key] + sum[0] : sum[0] + other[0][key], w ? other[1][key] + sum[1] : sum[1] + other[1][key]};
+        ok = mass_leave(L, a, list, k, j0, j1, n, sh.page[ic % kMeta], key, x, &sh.sums.last[w], meet);
+      }
       ++ic;
-      ok = mass_leave(L, a, list, k, j0, j1, n, page, w, key, sum, &sh.last[w], meet);
     }
   }
   tmem_fence_before_sync();
