@@ -728,34 +728,37 @@ struct JoinArgs {
 
 __global__ void __launch_bounds__(kJoinWarps * 32) k_paged_join(PagedLayer L, JoinArgs a) {
   const int lane = threadIdx.x & 31, G = L.G, n_q = L.n_kv * G;
-  pdl_wait();
-  pdl_trigger();
-  if (__syncthreads_or(threadIdx.x == 0 && paged_stopped(L))) return;
   const int64_t at = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
   const int seq = (int)(at / n_q), h = (int)(at % n_q), head = h / G, r = h % G;
+  pdl_wait();
+  pdl_trigger();
   if (seq >= a.b.n_seqs) return;
+  // Everything that depends on nothing is asked for at once: the kernel is a
+  // chain of such waits.
+  const bool stopped = paged_stopped(L);
   const PagedSeq s = paged_seq(a.b, L.P, seq, false);
-  if (!s.ok || s.n_new != 1) return;
+  const PagedShared::Seq c = a.shared->seq[seq];
+  const int64_t per = a.shared->per;
+  const int2 own = a.own[seq * L.n_kv + head];
+  if (stopped || !s.ok || s.n_new != 1) return;
   const float *sp = nullptr, *op = nullptr;  // the first part of each kind
   int64_t s_rest = 0, o_rest = 0;            // from it to the second, and the distance of the others
   int ns = 0, no = 0;
   const int64_t s_slot = 2 * (int64_t)kPagedPrefixPart, o_slot = 2 * (int64_t)G * kPagedRowPart;
   int off = 0;
   if (s.len > 0) {
-    const PagedShared::Seq& c = a.shared->seq[seq];
     off = c.len;
     if (off > 0) {
-      const int64_t place = c.place + (int64_t)head * c.cost, per = a.shared->per, b_lo = place / per;
+      const int64_t place = c.place + (int64_t)head * c.cost, b_lo = place / per;
       ns = (int)((place + c.steps - 1) / per - b_lo) + 1;
       sp = ns == 1 ? a.row_part + ((int64_t)seq * n_q + h) * kPagedRowPart
                    : a.part + (2 * b_lo + 1) * kPagedPrefixPart + (int64_t)(c.row + r) * kPagedRowPart;
       s_rest = kPagedPrefixPart;
     }
     if (s.len > off) {
-      const int2 o = a.own[seq * L.n_kv + head];
-      no = o.y;
+      no = own.y;
       op = no == 1 ? a.own_row + ((int64_t)seq * n_q + h) * kPagedRowPart
-                   : a.own_part + ((2 * (int64_t)o.x + 1) * G + r) * kPagedRowPart;
+                   : a.own_part + ((2 * (int64_t)own.x + 1) * G + r) * kPagedRowPart;
       o_rest = (int64_t)G * kPagedRowPart;
     }
   }
