@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
   __shared__ int64_t s_wsum[NW];
   __shared__ __align__(8) uint64_t s_bar[NW][NS];
   __shared__ __align__(16) float s_sc[NW][NS][4];  // k scale of box 0, 1; v scale of box 0, 1
-  __shared__ int s_pg[MASS ? NW : 1][NS][2];  // pages of box 0, 1
+  __shared__ int s_pg[MASS ? NW : 1][NS][2];  // pages of box 0, 1; -1: a bad one, read as page 0
   __shared__ float s_ml[NW][8 * C][2];
   __shared__ float s_M[8 * C], s_L[8 * C];
   __shared__ int s_last;
@@ -304,9 +304,11 @@ __global__ void __launch_bounds__(NW * 32, 1)
   auto issue = [&](int stage) {
     if (issued >= n_flat) return;
     const int valid = s_len[ic.seq] - ic.ch * CH;  // tokens from the chunk's start
+    bool bad = false;
     if (lane < n_box && lane * box < valid && (pid < 0 || pid >= L.n_pages)) {
       paged_error(L, ERR_PAGED_PAGE, ic.seq, pid);
       pid = 0;
+      bad = true;
     }
     const int boxes = valid >= CH ? n_box : (valid + box - 1) / box;
     unsigned char* st = ring + (warp * NS + stage) * kStageBytes;
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
       }
     }
-    if (MASS && lane < 2) s_pg[warp][stage][lane] = lane ? p1 : p0;
+    if (MASS && lane < 2) s_pg[warp][stage][lane] = bad ? -1 : pid;
     if (E4M3 && lane < 4) {
       float* to = &s_sc[warp][stage][lane];
       const int i = lane & 1;
@@ -491,9 +493,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const int tok = 8 * nt + 2 * c;  // of the chunk; a page begins at an even token
-              const int64_t at = (((int64_t)s_pg[warp][stage][two ? nt >> 1 : 0] * n_kv + u.head) * G + g) * L.P + ((tok0 + tok) & (L.P - 1));
+              const int page = s_pg[warp][stage][two ? nt >> 1 : 0];
+              const int64_t at = (((int64_t)page * n_kv + u.head) * G + g) * L.P + ((tok0 + tok) & (L.P - 1));
               const float k = nt < 2 ? k0 : k1;
-              if (tok < valid) *reinterpret_cast<float2*>(a.logits + at) = make_float2(z[i][nt][0] * k, z[i][nt][1] * k);
+              if (page >= 0 && tok < valid) *reinterpret_cast<float2*>(a.logits + at) = make_float2(z[i][nt][0] * k, z[i][nt][1] * k);
             }
           }
           if (E4M3) {

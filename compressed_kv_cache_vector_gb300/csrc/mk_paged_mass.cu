@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 // queries of a (sequence, kv head) stay in shared memory, and keys go by in a
 // ring of copies.  e4m3 keys are multiplied as they are, a query row being the
 // sum of an e4m3 and an e5m2 number each after a power of two (exact but for
-// channels below 2^-15 of the row's largest, off by at most 2^-20 of it): no
+// channels below 2^-13 of the row's largest, off by at most 2^-21 of it): no
 // conversion of keys that are used once.
 constexpr int kWindowRows = 256;
 

@@ -18,8 +18,8 @@
 //  * warp 12 issues the products, warp 13 the copies.
 //  * e4m3 keys are multiplied as they are: a query row, brought to [128, 256) by
 //    a power of two, is the sum of an e4m3 and an e5m2 number each, exact but
-//    for channels below 2^-15 of the row's largest, which are off by at most
-//    2^-20 of it.  That spares the keys' conversion, which shared memory's rate
+//    for channels below 2^-13 of the row's largest, which are off by at most
+//    2^-21 of it.  That spares the keys' conversion, which shared memory's rate
 //    would pay for (16 KB read and 32 KB written a step).
 //  * Work split on the device: all (group, 128 rows, kv head) cells' steps of
 //    128 keys in a row, cut into equal runs, one a CTA.

@@ -122,9 +122,10 @@ __device__ __forceinline__ void umma8(uint32_t d, uint64_t a, uint64_t b, uint32
 }
 // A row's eight bf16 channels (16 lanes have a row) as sums of an e4m3 number
 // and an e5m2 one, after the power of two that brings the row's largest to
-// [128, 256); returns what undoes it.  Exact for channels from 2^-15 of the
-// largest on: 8 significant bits are 4 and the 3 that a rest of at most 8
-// units wants; smaller ones are off by 2^-20 of it at most.
+// [128, 256); returns what undoes it.  Exact for channels from 2^-13 of the
+// largest on (2^-6 to 2^8 and more: 8 significant bits are 4 and the 3 that a
+// rest of at most 8 units wants); smaller ones are off by half of e5m2's step
+// at 2^-10, 2^-21 of the largest, at most.
 __device__ __forceinline__ float split8(const uint4& v, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
   const uint32_t h[4] = {v.x, v.y, v.z, v.w};
   float top = 0.0f, y[8];

@@ -601,7 +601,10 @@ typedef struct mk_paged_prefix {
  * The weights of shared tokens are rounded before they multiply the values: to
  * fp16 for an e4m3 cache (2^-11 of each) and to bf16 for a bf16 cache (2^-8 of
  * each).  Shared values must be finite: a NaN or infinity among them reaches
- * every sequence of its group, also where its weight is 0.
+ * every sequence of its group, also where its weight is 0.  With an e4m3 cache
+ * a query row counts as its largest channel and the others to 2^-21 of that.
+ * Batches that could read 96 MB at most (n_seqs * table_stride * page tokens),
+ * and n_groups = 0, are mk_paged_decode_attn's to the bit.
  * MK_EDEVICE: as mk_paged_decode_attn, and cu_group not ascending or out of
  * range or a negative prefix_len (nothing is shared then; the rows are right
  * all the same). */
@@ -626,7 +629,8 @@ mk_status mk_paged_mass_sizes(const mk_paged_config* cfg, size_t* mass_bytes, si
  * new one) to its weight.  out and lse are mk_paged_decode_attn's.  mass: the
  * array of all layers, 4-byte aligned; scratch: scratch_bytes of
  * mk_paged_mass_sizes, 16-byte aligned (MK_ENOMEM when smaller), free again
- * when the call's kernels are done. */
+ * when the call's kernels are done.  What a bad page id leaves undefined
+ * includes the mass of its sequence. */
 mk_status mk_paged_decode_attn_mass(mk_paged* h, int32_t layer, const mk_paged_batch* batch, const void* q,
                                     int64_t q_stride, float scale, void* out, int64_t out_stride, float* lse,
                                     float* mass, int32_t first, void* scratch, size_t scratch_bytes, mk_stream stream);
@@ -639,7 +643,8 @@ mk_status mk_paged_decode_attn_mass(mk_paged* h, int32_t layer, const mk_paged_b
  * tokens held before the call's new ones (the first kv_len - n_new; with
  * causal = 0 all of them), set for the others; add = 0: set for all.  A
  * sequence without new tokens is left alone.  Logits, exponentials and sums
- * are fp32; the order of the sums depends on the lengths alone. */
+ * are fp32; the order of the sums depends on the lengths alone.  A key of NaN
+ * has a mass of NaN and no influence on another's. */
 mk_status mk_paged_prefill_mass(mk_paged* h, int32_t layer, const mk_paged_batch* batch, int32_t causal, const void* q,
                                 int64_t q_stride, float scale, const float* lse, float* mass, int32_t first,
                                 int32_t add, mk_stream stream);

@@ -6,6 +6,7 @@ most d = 128 * 2^-24 * sum |q k| scale; its product with the scale factors and t
 d + 2^-18 more; the exponential by 2^-21.  So w (2^-16 big + 2^-17), with big = largest sum |q k| scale of the row plus
 |lse|.  Sums of n weights in 32 bits: n 2^-24 of the total, and as much of the mass held before.
 """
+import ctypes
 import math
 
 import pytest
@@ -435,3 +436,101 @@ def test_device_errors_leave_other_sequences_right():
     c.evict(0, good, m, _i32([100] * 5), kept=torch.full((5, 2, 100), -1, dtype=torch.int32, device=DEV))
     c.clear_error()
     assert bool((again == -1).all())
+
+
+def test_a_bad_page_does_not_reach_other_sequences_mass():
+    """A page id that is none is read as page 0, whose own sequence keeps its logits."""
+    made = Made("e4m3", 16, 2, 4, [300, 200], 5)
+    c = made.c
+    zero = int((made.table[1] == 0).any())                                              # the sequence that owns page 0
+    owner, other = (1, 0) if zero else (0, 1)
+    if not bool((made.table[owner] == 0).any()):                                        # page 0 is free: give it to one
+        j = 3
+        old = made.rows[owner][j]
+        for x in ("k", "v"):
+            getattr(c, x + "_pool").view(torch.uint8)[0, 0] = getattr(c, x + "_pool").view(torch.uint8)[0, old]
+            getattr(c, x + "_scale")[0, 0] = getattr(c, x + "_scale")[0, old]
+        made.rows[owner][j] = 0
+        made.table[owner, j] = 0
+    made.table[other, 5] = 12345
+    q = torch.randn(2, 8, 128, generator=_gen(1), device=DEV).to(torch.bfloat16)
+    m = _made_mass(made, 2)
+    before = m.mass.clone()
+    c.decode_attn_mass(0, K.PagedBatch(made.kv_len, made.table), q, m)
+    assert c.poll_error() == (5, 17)
+    for h in range(2):
+        k, _ = made.held(owner, h)
+        w = sum(O.mass(q[owner:owner + 1, h * 4 + g].double(), k, SCALE, torch.full((1,), made.lens[owner], device=DEV))[0] for g in range(4))
+        old = _of(made, before, owner, h).clone()
+        old[-1] = 0
+        assert float((_of(made, m.mass, owner, h) - old - w).abs().max()) < 1e-4
+
+
+def test_refusals():
+    """Every argument that a call can check before it launches anything."""
+    made = Made("e4m3", 16, 2, 4, [40, 40], 5)
+    c, b = made.c, K.PagedBatch(made.kv_len, made.table)
+    m = K.PagedMass(c)
+    lib, ref, g = c.lib, b.ref, 1 << 20
+    two = K.PagedBatch(made.kv_len, made.table, _i32([0, 2, 4]), 2, 4)
+
+    def dec(batch=ref, q=g, scale=0.1, out=g, mass=g, first=0, scratch=g, size=1 << 40, layer=0):
+        return lib.mk_paged_decode_attn_mass(c.h, layer, batch, q, 1024, scale, out, 1024, None, mass, first, scratch, size, None)
+
+    assert dec(batch=two.ref) == 1 and dec(q=g + 2) == 1 and dec(mass=0) == 1 and dec(mass=g + 2) == 1 and dec(first=-1) == 1
+    assert dec(scratch=0) == 1 and dec(scratch=g + 8) == 1 and dec(size=m.scratch_bytes - 1) == 2 and dec(layer=1) == 1
+    assert dec(scale=math.inf) == 1
+
+    def pre(q=g, lse=g, mass=g, first=0, add=1, causal=1, scale=0.1, stride=1024):
+        return lib.mk_paged_prefill_mass(c.h, 0, two.ref, causal, q, stride, scale, lse, mass, first, add, None)
+
+    assert pre(q=0) == 1 and pre(lse=0) == 1 and pre(lse=g + 1) == 1 and pre(mass=0) == 1 and pre(first=-1) == 1 and pre(add=2) == 1
+    assert pre(causal=2) == 1 and pre(scale=math.nan) == 1 and pre(stride=1020) == 1
+
+    def ev(mass=g, keep=g, first=0, recent=0, kept=g, stride=8, new=g, batch=ref):
+        return lib.mk_paged_evict(c.h, 0, batch, mass, keep, first, recent, kept, stride, new, None)
+
+    assert ev(mass=0) == 1 and ev(keep=0) == 1 and ev(first=-1) == 1 and ev(recent=-1) == 1 and ev(kept=0) == 1 and ev(stride=-1) == 1
+    assert ev(new=0) == 1 and ev(new=made.kv_len.data_ptr()) == 1 and ev(keep=g + 2) == 1
+    assert lib.mk_paged_prefix_attn(c.h, 0, ref, None, g, 1024, 0.1, g, 1024, None, None) == 1
+    for n, cu, ln in ((3, g, g), (-1, g, g), (1, 0, g), (1, g, 0), (1, g + 2, g)):
+        p = K.MkPagedPrefix(n, cu, ln)
+        assert lib.mk_paged_prefix_attn(c.h, 0, ref, ctypes.byref(p), g, 1024, 0.1, g, 1024, None, None) == 1
+    with pytest.raises(ValueError):
+        K.PagedMass(c, torch.zeros(1, 2, 3, 4, device=DEV))
+    other = Made("e4m3", 32, 2, 4, [40], 5)
+    for call in (lambda: c.decode_attn_mass(0, b, torch.zeros(2, 8, 128, dtype=torch.bfloat16, device=DEV), K.PagedMass(other.c)),
+                 lambda: c.evict(0, b, m, _i32([4])), lambda: c.evict(0, b, m, _i32([4, 4]), kept=_i32([1, 2])),
+                 lambda: c.prefill_mass(0, two, torch.zeros(4, 8, 128, dtype=torch.bfloat16, device=DEV), torch.zeros(3, 8, device=DEV), m),
+                 lambda: K.PagedPrefix(_i32([0, 1, 2]), _i32([1]))):
+        with pytest.raises(ValueError):
+            call()
+    # nothing to do
+    none = K.PagedBatch(made.kv_len[:0], made.table[:0])
+    assert lib.mk_paged_evict(c.h, 0, none.ref, g, g, 0, 0, g, 8, g, None) == 0
+    assert c.poll_error() == (0, 0)
+
+
+def test_two_handles_side_by_side():
+    """Eviction and mass through two handles over pools of their own, on two streams at once."""
+    a, b = Made("e4m3", 32, 2, 4, [20000], 5), Made("bf16", 32, 2, 4, [9000, 700], 6)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ms = []
+    torch.cuda.synchronize()
+    for made, s in zip((a, b), streams):
+        with torch.cuda.stream(s):
+            m = K.PagedMass(made.c)
+            m.mass.uniform_(generator=_gen(4))
+            ms.append((m, m.mass.clone(), [getattr(made.c, x + "_pool").view(torch.uint8).clone() for x in ("k", "v")],
+                       None if made.kv == "bf16" else [getattr(made.c, x + "_scale").clone() for x in ("k", "v")]))
+    torch.cuda.synchronize()
+    res = []
+    for made, s, (m, *_) in zip((a, b), streams, ms):
+        res.append(made.c.evict(0, K.PagedBatch(made.kv_len, made.table), m, _i32([x // 3 for x in made.lens]), first=2, recent=9, stream=s))
+    torch.cuda.synchronize()
+    for made, (m, was, pools, scales), (new_len, kept) in zip((a, b), ms, res):
+        assert made.c.poll_error() == (0, 0)
+        before = {"k": pools[0], "v": pools[1]}
+        if scales:
+            before.update(ks=scales[0], vs=scales[1])
+        _evict_check(made, before, was, m.mass, [x // 3 for x in made.lens], 2, 9, kept, new_len)
