@@ -11,6 +11,8 @@ namespace {
 // ---- a decode step's weights, from the logits that the attention left ----
 // A thread a token: the group's weights 2^(z - lse2) summed and added.  HBM
 // (mostly L2, where the logits still are): 4 G bytes read, 8 for the mass.
+// 48 sequences of mixed lengths, 8 kv heads: 19 us behind 134 of attention (the
+// call 155; with one token a thread 161); 3 sequences of 100K tokens 19 behind 207.
 constexpr int kFoldThreads = 256, kFoldTokens = 4;  // tokens of a thread, for the loads in flight
 constexpr int kFoldTile = kFoldThreads * kFoldTokens;
 
@@ -86,6 +88,9 @@ __global__ void __launch_bounds__(kFoldThreads)
 // key: its sum over the rows needs no exchange, a causal mask is a first
 // column, and its page's scale one factor.  A weight is 2^(S k + n) with the
 // key's factor k and the row's n = -lse log2 e from shared memory.
+// What bounds it: the summing warps' instructions, the exponentials (32 a clock
+// and SM: 62 us of a 6000-token prompt with 32 query heads) with the reading of
+// logits and rows' numbers beside them: 153 us where the products take 76.
 constexpr int kMassKeys = 256;   // keys of an item: two tiles of 128
 constexpr int kMassRows = 128;   // rows of a step
 constexpr int kMassTile = 128 * D * 2;
@@ -93,7 +98,6 @@ constexpr int kMassThreads = 448;  // 8 warps sum, 4 load keys, 1 loads queries,
 constexpr int kMassItemCost = 1;   // an item's begin and end take as long as this many steps
 constexpr int kMassMinRun = 4;
 constexpr int kMassSmem = 1024 + 6 * kMassTile;
-constexpr int kMassMany = 8;         // row tiles of a sequence from which an item has many steps
 constexpr int kMeta = 8;           // items whose pages are kept
 
 struct MassArgs {
@@ -157,7 +161,7 @@ struct MassSums {
 };
 struct MassShared {
   MassList list;
-  uint64_t q_full[4], q_free[4], s_full[2], s_free[2], k_full[2], k_free[2], done;
+  uint64_t q_full[2], q_free[2], s_full[2], s_free[2], k_full[2], k_free[2], done;
   // -lse log2 e of a step's rows, -infinity where there is none.  A sum gives its
   // logits back before it has read the last of these, hence more than four.
   __align__(16) float nlse[8][kMassRows];
@@ -359,26 +363,24 @@ __device__ __forceinline__ void mass_sums_init(MassSums& m) {
   for (int i = 0; i < 2; ++i) mbar_init(&m.met[i], 4);
 }
 
-// NK: items whose keys are held.  Few steps an item want the next item's keys
-// early (2), many want queries early (1: four tiles of them, 6000-token prompt
-// X us against Y).
-template <bool E4M3, int NK>
+// The keys of two items and two tiles of queries are held: the next item's keys
+// are there early.  One item and four tiles: 161 against 153 us (6000 tokens),
+// 78 against 76 (five ragged chunks).
+template <bool E4M3>
 __global__ void __launch_bounds__(kMassThreads, 1)
     k_prefill_mass(PagedLayer L, MassArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ unsigned char dyn[];
   __shared__ MassShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-  constexpr int NQ = 6 - 2 * NK;  // tiles of queries
+  constexpr int NK = 2, NQ = 2;  // items' keys, tiles of queries
   const uint32_t sk = base, sq = base + 2 * NK * kMassTile;
   const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv;
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_free[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], 8);
       mbar_init(&sh.k_full[i], E4M3 ? 4 : 1);
@@ -986,9 +988,7 @@ cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps
     const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
     return launch_pdl(fn, dim3(grid), dim3(kMassThreads), (size_t)kMassSmem, s, 0, L, a, q, q_stride, maps.k);
   }
-  // Row tiles of a sequence, at most.
-  const bool many = (rows + kMassRows - 1) / kMassRows >= kMassMany;
-  auto fn = L.e4m3 ? (many ? k_prefill_mass<true, 1> : k_prefill_mass<true, 2>) : (many ? k_prefill_mass<false, 1> : k_prefill_mass<false, 2>);
+  auto fn = L.e4m3 ? k_prefill_mass<true> : k_prefill_mass<false>;
   int sms = 0;
   const cudaError_t e = kernel_smem_attr((const void*)fn, kMassSmem, kMassThreads, nullptr, &sms);
   if (e != cudaSuccess) return e;
