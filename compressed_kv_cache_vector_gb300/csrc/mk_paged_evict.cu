@@ -18,11 +18,19 @@
 // handed out in order by a counter, so whoever is waited for has begun and
 // reads without waiting: every wait ends.
 //
-// What bounds it: HBM (the kept rows read and written once) for long
-// sequences, the latency of the passes for short ones.
+// What bounds it: HBM for many sequences (24 in bf16 48 us, its bytes 49 at the
+// rate of a plain copy), chains of dependent steps for one (64K tokens in e4m3
+// 44 us, its bytes 10).  About half of these is the selection: loads 7 us, three
+// passes of histogram and cluster barriers 3-4 each, the writing of the numbers
+// 4.  An item of the move waits for a ticket, its tokens' numbers, their pages,
+// the rows and whoever reads here, 9 us in all; everything that depends on
+// nothing is asked for together (one lookup after the other 52 and 56 us).  The
+// next ticket drawn an item ahead is slower (58 against 52): items that others
+// wait for begin later.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "mk_paged.cuh"
 
@@ -66,7 +74,7 @@ __device__ __forceinline__ int page_of(const PagedLayer& L, const mk_paged_batch
 }
 
 template <int CL>
-__global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads, 2) k_evict_select(PagedLayer L, EvictArgs a) {
   extern __shared__ uint32_t cache[];  // [kCache]
   __shared__ uint32_t hist[kBins], sums[CL > 1 ? kBins : 1];
   __shared__ int s_warp[kSelThreads / 32][2], s_tot[2], s_pick[2], s_scan[kSelThreads / 32];
@@ -109,23 +117,31 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
     return p < 0 ? 0u : mass_key(a.mass[((int64_t)p * L.n_kv + head) * L.P + (t & (L.P - 1))]);
   };
   auto key_of = [&](int i) { return i < kCache ? cache[i] : load_key(i); };
-  for (int i0 = tid; i0 < min(n, kCache); i0 += 8 * kSelThreads) {  // eight tokens at a time: the loads' latency
+  const int held = min(n, kCache);
+  const int32_t* const table = a.b.page_table + (int64_t)seq * a.b.table_stride;
+  for (int i0 = tid; i0 < held; i0 += 8 * kSelThreads) {  // eight tokens at a time: the loads' latency
     int page[8];
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int i = i0 + e * kSelThreads;
-      page[e] = i < min(n, kCache) ? page_of(L, a.b, seq, t0 + i) : -1;
+      page[e] = i < held ? table[(t0 + i) >> L.p_log2] : 0;
     }
+    bool bad = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int t = t0 + i0 + e * kSelThreads;
-      w[e] = page[e] < 0 ? __int_as_float(0x7fffffff) : a.mass[((int64_t)page[e] * L.n_kv + head) * L.P + (t & (L.P - 1))];
+      const bool there = page[e] >= 0 && page[e] < L.n_pages;
+      bad |= !there;
+      w[e] = there && i0 + e * kSelThreads < held ? a.mass[((int64_t)page[e] * L.n_kv + head) * L.P + (t & (L.P - 1))] : __int_as_float(0x7fffffff);
     }
+    if (bad)
+      for (int e = 0; e < 8; ++e)
+        if (i0 + e * kSelThreads < held) (void)page_of(L, a.b, seq, t0 + i0 + e * kSelThreads);  // records it
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int i = i0 + e * kSelThreads;
-      if (i < min(n, kCache)) cache[i] = mass_key(w[e]);
+      if (i < held) cache[i] = mass_key(w[e]);
     }
   }
 
@@ -139,11 +155,13 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
       const int bits = pass == 2 ? 10 : 11, bins = 1 << bits;
       for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t key = key_of(i);
+      auto count = [&](uint32_t key) {
         if (pass == 0 || (key ^ prefix) >> (shift + bits) == 0) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
-      }
-      __syncthreads();
+      };
+#pragma unroll 8
+      for (int i = tid; i < held; i += kSelThreads) count(cache[i]);
+      for (int i = tid + (held - tid + kSelThreads - 1) / kSelThreads * kSelThreads; held < n && i < n; i += kSelThreads) count(load_key(i));
+      if (CL == 1) __syncthreads();
       if (CL > 1) {
         // Each CTA adds up a share of the bins and hands the sums to all.
         auto cluster = cg::this_cluster();
@@ -195,10 +213,15 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
   // Kept tokens in order: warp w has run [w0, w1) of the slice.
   const int run = ((n + kWarps - 1) / kWarps + 31) & ~31, w0 = min(n, warp * run), w1 = min(n, w0 + run);
   int above = 0, equal = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t key = key_of(i);
-    above += key > bar;
-    equal += key == bar;
+  {
+    const int w2 = min(w1, held);
+    auto count = [&](uint32_t key) {
+      above += key > bar;
+      equal += key == bar;
+    };
+#pragma unroll 4
+    for (int i = w0 + lane; i < w2; i += 32) count(cache[i]);
+    for (int i = max(w0, w2) + lane; i < w1; i += 32) count(load_key(i));
   }
   above = __reduce_add_sync(FULL, above);
   equal = __reduce_add_sync(FULL, equal);
@@ -207,20 +230,22 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
     s_warp[warp][1] = equal;
   }
   __syncthreads();
-  if (tid < 2) {
-    int x = 0;
-    for (int w = 0; w < kWarps; ++w) x += s_warp[w][tid];
-    s_tot[tid] = x;
+  if (warp < 2) {
+    const int x = __reduce_add_sync(FULL, lane < kWarps ? s_warp[lane][warp] : 0);
+    if (lane == 0) s_tot[warp] = x;
   }
   __syncthreads();
   int a0 = 0, e0 = 0;  // above and equal before this warp's run
+  cg::cluster_group::arrival_token read;
   if (CL > 1) {
     cg::this_cluster().sync();
-    for (int r = 0; r < rank; ++r) {
-      a0 += *cg::this_cluster().map_shared_rank(&s_tot[0], r);
-      e0 += *cg::this_cluster().map_shared_rank(&s_tot[1], r);
+    if (lane < rank) {
+      a0 = *cg::this_cluster().map_shared_rank(&s_tot[0], lane);
+      e0 = *cg::this_cluster().map_shared_rank(&s_tot[1], lane);
     }
-    cg::this_cluster().sync();  // no CTA ends before its shared memory has been read
+    a0 = __reduce_add_sync(FULL, a0);
+    e0 = __reduce_add_sync(FULL, e0);
+    read = cg::this_cluster().barrier_arrive();
   }
   for (int w = 0; w < warp; ++w) {
     a0 += s_warp[w][0];
@@ -228,6 +253,16 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
   }
   const int stay_eq = k > 0 ? left : 0;
   int at = lo + a0 + min(e0, stay_eq);
+  // What lies before each group of slots: 32 groups at a time, a lane each, for
+  // their pages' latency.
+  int n_groups = 0, group_tok = 0, group_rank = 0;
+  auto leave = [&]() {
+    if (lane < n_groups && group_tok < keep) {
+      const int p = page_of(L, a.b, seq, group_tok);
+      if (p >= 0) a.rank0[(int64_t)p * L.n_kv + head] = group_rank;
+    }
+    n_groups = 0;
+  };
   for (int i0 = w0; i0 < w1; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t key = i < w1 ? key_of(i) : 0u;
@@ -236,16 +271,23 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(PagedLayer L, Evic
     const unsigned ins = __ballot_sync(FULL, in);
     const int r = at + __popc(ins & below), t = t0 + i;
     if (in) kept[r] = t;
-    if (i < w1 && (t & (kGroup - 1)) == 0 && t < keep) {
-      const int p = page_of(L, a.b, seq, t);
-      if (p >= 0) a.rank0[(int64_t)p * L.n_kv + head] = r;
+    const int x = -(t0 + i0) & (kGroup - 1);  // the lane with a group's first token
+    if (x < 32 && i0 + x < w1) {
+      const int v = __shfl_sync(FULL, r, x);
+      if (lane == n_groups) {
+        group_tok = t0 + i0 + x;
+        group_rank = v;
+      }
+      if (++n_groups == 32) leave();
     }
     at += __popc(ins);
     e0 += __popc(eq);
   }
+  leave();
   // The tokens that are kept anyway.
   for (int t = rank * kSelThreads + tid; t < lo; t += CL * kSelThreads) kept[t] = t;
   for (int i = rank * kSelThreads + tid; i < a.recent; i += CL * kSelThreads) kept[lo + k + i] = hi + i;
+  if (CL > 1) cg::this_cluster().barrier_wait(std::move(read));  // no CTA ends before its shared memory has been read
 }
 
 // Eight e4m3 codes as floats times s (a power of two or any scale).
@@ -265,7 +307,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
   constexpr int kRowsPass = kMoveThreads / kChunks, kPass = kGroup / kRowsPass;
   __shared__ int64_t s_end[MK_MAX_CALL_SEQS];                  // items up to and with a sequence
   __shared__ int64_t s_wsum[kMoveThreads / 32];
-  __shared__ int s_tok[kGroup], s_item;
+  __shared__ int64_t s_at[kGroup];                             // where a row comes from
+  __shared__ int s_tok[kGroup], s_page[kGroup / 16], s_item;   // and its token, the pages that rows go to
   __shared__ float s_scale[2][kGroup], s_max[2][kGroup / 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_kv = L.n_kv, n_seqs = a.b.n_seqs;
   pdl_wait();
@@ -308,6 +351,10 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
     const int r0 = j * kGroup, cnt = min(kGroup, keep - r0);
     const int32_t* kept = a.kept + ((int64_t)seq * n_kv + head) * a.kept_stride;
     if (tid < cnt) s_tok[tid] = kept[r0 + tid];
+    if (tid >= kMoveThreads - kGroup / 16) {
+      const int i = tid - (kMoveThreads - kGroup / 16), slot = r0 + i * L.P;
+      if (i * L.P < cnt) s_page[i] = a.b.page_table[(int64_t)seq * a.b.table_stride + (slot >> L.p_log2)];
+    }
     __syncthreads();
     if (s_tok[cnt - 1] == r0 + cnt - 1) continue;  // all stay: nothing else reads or writes here
     // ---- read ----
@@ -316,33 +363,41 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
       const int p = t >= 0 && t < len ? page_of(L, a.b, seq, t) : -1;
       return p < 0 ? (int64_t)-1 : ((int64_t)p * n_kv + head) * L.P + (t & (L.P - 1));
     };
-    float w = 0.0f;
+    auto page_to = [&](int x) {  // the page of the group that row x goes to, or -1
+      const int p = s_page[x >> L.p_log2];
+      if (p >= 0 && p < L.n_pages) return p;
+      paged_error(L, ERR_PAGED_PAGE, seq, p);
+      return -1;
+    };
+    if (tid < kGroup) s_at[tid] = tid < cnt ? held_at(tid) : -1;
+    __syncthreads();
+    float w = 0.0f, scale[2] = {1.0f, 1.0f};
     if (tid < cnt) {
-      const int64_t at = held_at(tid);
+      const int64_t at = s_at[tid];
       w = at < 0 ? 0.0f : a.mass[at];
-      if (E4M3) {
-        s_scale[0][tid] = at < 0 ? 1.0f : L.k_scale[at >> L.p_log2];
-        s_scale[1][tid] = at < 0 ? 1.0f : L.v_scale[at >> L.p_log2];
+      if (E4M3 && at >= 0) {
+        scale[0] = L.k_scale[at >> L.p_log2];
+        scale[1] = L.v_scale[at >> L.p_log2];
       }
     }
     uint4 x[2][kPass];
 #pragma unroll
     for (int i = 0; i < kPass; ++i) {
       const int row = i * kRowsPass + tid / kChunks;
-      const int64_t at = row < cnt ? held_at(row) : -1;
+      const int64_t at = s_at[row];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         x[t][i] = at < 0 ? make_uint4(0, 0, 0, 0)
                          : *reinterpret_cast<const uint4*>((t ? L.v : L.k) + at * (D * (E4M3 ? 1 : 2)) + (tid % kChunks) * 16);
     }
-    const int my_page = page_of(L, a.b, seq, r0);
-    const int64_t here = (int64_t)my_page * n_kv + head;
-    // ---- say so, and wait for those who read here ----
-    __threadfence();
-    __syncthreads();
-    if (tid == 0 && my_page >= 0) {
-      asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(a.flag + here) : "memory");
+    if (E4M3 && tid < cnt) {
+      s_scale[0][tid] = scale[0];
+      s_scale[1][tid] = scale[1];
     }
+    const int my_page = page_to(0);
+    const int64_t here = (int64_t)my_page * n_kv + head;
+    const int32_t* from = nullptr;  // the flag of an item that reads here
+    int g = 0;
     if (warp == 0) {
       // Ranks of the kept tokens that come from slots r0 .. r0 + 63.
       auto rank_of = [&](int t) {  // kept tokens before token t (a group's first)
@@ -355,18 +410,25 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
       const int b0 = rank_of(r0);
       int b1 = r0 + kGroup < keep ? rank_of(r0 + kGroup) : min(keep, b0 + kGroup);
       b1 = min(b1, b0 + kGroup);
-      const int g = b0 / kGroup + lane;  // at most two items, none later than this one
+      g = b0 / kGroup + lane;  // at most two items, none later than this one
       if (lane < 2 && b1 > b0 && g <= (b1 - 1) / kGroup && g < j) {
         const int p = page_of(L, a.b, seq, g * kGroup);
-        if (p >= 0) {
-          const long long t0 = clock64();
-          int32_t done = 0;
-          do {
-            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(done) : "l"(a.flag + (int64_t)p * n_kv + head) : "memory");
-          } while (!done && clock64() - t0 < 400000000ll);
-          if (!done) paged_error(L, ERR_PAGED_WAIT, seq, g, (int32_t)MK_ETIMEOUT);
-        }
+        if (p >= 0) from = a.flag + (int64_t)p * n_kv + head;
       }
+    }
+    // ---- say so, and wait for those who read here ----
+    __threadfence();
+    __syncthreads();
+    if (tid == 0 && my_page >= 0) {
+      asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(a.flag + here) : "memory");
+    }
+    if (from) {
+      const long long t0 = clock64();
+      int32_t done = 0;
+      do {
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(done) : "l"(from) : "memory");
+      } while (!done && clock64() - t0 < 400000000ll);
+      if (!done) paged_error(L, ERR_PAGED_WAIT, seq, g, (int32_t)MK_ETIMEOUT);
     }
     if (E4M3) {  // largest value of every four rows
 #pragma unroll
@@ -374,18 +436,16 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
 #pragma unroll
         for (int i = 0; i < kPass; ++i) {
           const int row = i * kRowsPass + tid / kChunks;
-          float top = 0.0f, y[8];
-          const float s = row < cnt ? s_scale[t][row] : 0.0f;
+          // The largest code, as fp16 (exact; NaN counts as nothing), times the scale.
+          __half2 most = __float2half2_rn(0.0f);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            codes_to(e ? x[t][i].z : x[t][i].x, e ? x[t][i].w : x[t][i].y, s, y);
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-              const float m = fabsf(y[v]);
-              if (m <= 3.402823466e38f) top = fmaxf(top, m);
-            }
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t w = e < 2 ? x[t][i].x : e < 4 ? x[t][i].y : e < 6 ? x[t][i].z : x[t][i].w;
+            const uint32_t h = e4m3_h2(w >> (16 * (e & 1)));
+            most = __hmax2(most, __habs2(*reinterpret_cast<const __half2*>(&h)));
           }
-          top = warp_max(top);
+          const float2 m = __half22float2(most);
+          const float top = warp_max(fminf(fmaxf(m.x, m.y) * (row < cnt ? s_scale[t][row] : 0.0f), 3.402823466e38f));
           if (lane == 0) s_max[t][(i * kRowsPass) / 4 + warp] = top;
         }
     }
@@ -396,7 +456,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
       const int row = i * kRowsPass + tid / kChunks;
       const int p0 = row & ~(L.P - 1), last = min(cnt, p0 + L.P) - 1;  // the row's page in the group
       if (row >= cnt || s_tok[last] == r0 + last) continue;            // a page whose tokens all stay
-      const int page = page_of(L, a.b, seq, r0 + row);
+      const int page = page_to(row);
       if (page < 0) continue;
       const int64_t at = ((int64_t)page * n_kv + head) * L.P + (row & (L.P - 1));
 #pragma unroll
@@ -405,16 +465,19 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
         if (E4M3) {
           float top = 0.0f;
           for (int g = p0 >> 2; g < (p0 + L.P) >> 2; ++g) top = fmaxf(top, s_max[t][g]);
-          const float scale = scale_of(top), inv = __frcp_rn(scale), s = s_scale[t][row];
-          float y[8];
-          codes_to(o.x, o.y, s, y);
-          uint2 c = pack_e4m3(y, inv);
-          o.x = c.x;
-          o.y = c.y;
-          codes_to(o.z, o.w, s, y);
-          c = pack_e4m3(y, inv);
-          o.z = c.x;
-          o.w = c.y;
+          const float scale = scale_of(top), s = s_scale[t][row];
+          if (s != scale) {  // the codes of the same scale stay
+            const float inv = __frcp_rn(scale);
+            float y[8];
+            codes_to(o.x, o.y, s, y);
+            uint2 c = pack_e4m3(y, inv);
+            o.x = c.x;
+            o.y = c.y;
+            codes_to(o.z, o.w, s, y);
+            c = pack_e4m3(y, inv);
+            o.z = c.x;
+            o.w = c.y;
+          }
           if (row == p0 && tid % kChunks == 0) (t ? L.v_scale : L.k_scale)[at >> L.p_log2] = scale;
         }
         *reinterpret_cast<uint4*>((t ? L.v : L.k) + at * (D * (E4M3 ? 1 : 2)) + (tid % kChunks) * 16) = o;
@@ -422,7 +485,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
     }
     if (tid < cnt) {
       const int last = min(cnt, (tid & ~(L.P - 1)) + L.P) - 1;
-      const int page = s_tok[last] != r0 + last ? page_of(L, a.b, seq, r0 + tid) : -1;
+      const int page = s_tok[last] != r0 + last ? page_to(tid) : -1;
       if (page >= 0) a.mass[((int64_t)page * n_kv + head) * L.P + (tid & (L.P - 1))] = w;
     }
   }
