@@ -183,20 +183,21 @@ __global__ void __launch_bounds__(NW * 32, 1)
       units += __popc(__ballot_sync(FULL, i < n_seqs && s_len[i < n_seqs ? i : 0] > 0)) * n_kv;
     }
     __syncthreads();
-  } else
-  for (int i0 = 0; i0 < n_seqs; i0 += NTHR) {
-    const int i = i0 + tid;
-    bool keys = false;
-    if (i < n_seqs) {
-      const PagedSeq s = paged_seq(a.b, L.P, i, false);
-      if (!s.ok) paged_error(L, ERR_PAGED_BATCH, i, s.len);
-      const bool live = s.ok && (C == 1 ? s.n_new == 1 : s.n_new > 0);  // C = 2: n_new <= max_new <= 16 / G
-      s_len[i] = live ? s.len : 0;
-      s_row[i] = live ? s.row0 : -1;
-      if (C > 1) s_new[i] = live ? s.n_new : 0;
-      keys = live && s.len > 0;
+  } else {
+    for (int i0 = 0; i0 < n_seqs; i0 += NTHR) {
+      const int i = i0 + tid;
+      bool keys = false;
+      if (i < n_seqs) {
+        const PagedSeq s = paged_seq(a.b, L.P, i, false);
+        if (!s.ok) paged_error(L, ERR_PAGED_BATCH, i, s.len);
+        const bool live = s.ok && (C == 1 ? s.n_new == 1 : s.n_new > 0);  // C = 2: n_new <= max_new <= 16 / G
+        s_len[i] = live ? s.len : 0;
+        s_row[i] = live ? s.row0 : -1;
+        if (C > 1) s_new[i] = live ? s.n_new : 0;
+        keys = live && s.len > 0;
+      }
+      units += __syncthreads_count(keys) * n_kv;
     }
-    units += __syncthreads_count(keys) * n_kv;
   }
   // The list of chunks: exclusive prefix over the sequences, each unit rounded
   // up to a multiple of `pad` places.
@@ -230,16 +231,17 @@ __global__ void __launch_bounds__(NW * 32, 1)
   int64_t total = list(1);
 
   // Rows of empty sequences.
-  if (!OWN)
-  for (int i = blockIdx.x; i < n_seqs; i += gridDim.x)
-    if (s_row[i] >= 0 && s_len[i] == 0) {
-      for (int t = 0; t < (C == 1 ? 1 : s_new[i]); ++t) {
-        for (int e = tid; e < n_kv * G * D / 8; e += NTHR)
-          *reinterpret_cast<uint4*>(a.out + (int64_t)(s_row[i] + t) * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
-        if (a.lse)
-          for (int e = tid; e < n_kv * G; e += NTHR) a.lse[(int64_t)(s_row[i] + t) * n_kv * G + e] = -INFINITY;
+  if (!OWN) {
+    for (int i = blockIdx.x; i < n_seqs; i += gridDim.x)
+      if (s_row[i] >= 0 && s_len[i] == 0) {
+        for (int t = 0; t < (C == 1 ? 1 : s_new[i]); ++t) {
+          for (int e = tid; e < n_kv * G * D / 8; e += NTHR)
+            *reinterpret_cast<uint4*>(a.out + (int64_t)(s_row[i] + t) * a.out_stride + e * 8) = make_uint4(0, 0, 0, 0);
+          if (a.lse)
+            for (int e = tid; e < n_kv * G; e += NTHR) a.lse[(int64_t)(s_row[i] + t) * n_kv * G + e] = -INFINITY;
+        }
       }
-    }
+  }
 
   int64_t per = (total + gridDim.x - 1) / gridDim.x;
   // A run that ends one unit and begins another joins twice, 5 us a time: where
