@@ -56,7 +56,10 @@ struct EvictArgs {
   int32_t* ticket;       // items handed out
   int2* plan;            // [max_seqs] length and tokens kept; x < 0: nothing to move
   int32_t* rank0;        // [n_pages][n_kv], at a group's first page: kept tokens before the group
-  int32_t* flag;         // [n_pages][n_kv], likewise: the item's rows are read
+  // [n_pages][n_kv]: an item's rows are read, at the page of the last slot that
+  // it fills.  Of an item that moves anything this page is written, so no other
+  // sequence has it; the first one may be of a shared prefix.
+  int32_t* flag;
 };
 
 // Larger key: larger mass.  -0 is 0; NaN is the least.
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_evict_select(PagedLayer L, E
     return;
   }
   for (int t = (rank * kSelThreads + tid) * kGroup; t < keep; t += CL * kSelThreads * kGroup) {
-    const int p = page_of(L, a.b, seq, t);
+    const int p = page_of(L, a.b, seq, min(t + kGroup, keep) - 1);
     if (p >= 0) a.flag[(int64_t)p * L.n_kv + head] = 0;
   }
   // Tokens lo .. hi - 1 are chosen from, k of them stay; this CTA has t0 .. t1 - 1.
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
       s_scale[0][tid] = scale[0];
       s_scale[1][tid] = scale[1];
     }
-    const int my_page = page_to(0);
+    const int my_page = page_to(cnt - 1);
     const int64_t here = (int64_t)my_page * n_kv + head;
     const int32_t* from = nullptr;  // the flag of an item that reads here
     int g = 0;
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
       b1 = min(b1, b0 + kGroup);
       g = b0 / kGroup + lane;  // at most two items, none later than this one
       if (lane < 2 && b1 > b0 && g <= (b1 - 1) / kGroup && g < j) {
-        const int p = page_of(L, a.b, seq, g * kGroup);
+        const int p = page_of(L, a.b, seq, g * kGroup + kGroup - 1);  // an earlier item is full
         if (p >= 0) from = a.flag + (int64_t)p * n_kv + head;
       }
     }

@@ -327,6 +327,17 @@ def test_evict_large_values_move_into_fine_pages():
     _evict_run(made, [9], 0, 0, 1, tweak)
 
 
+@pytest.mark.parametrize("kv,P,first", [("bf16", 16, 80), ("e4m3", 16, 16), ("e4m3", 32, 100)])
+def test_evict_behind_a_shared_prefix(kv, P, first):
+    """Sequences whose first pages are the same, in the middle of 64 slots: each waits for its own readers alone."""
+    lens = [12000 - 700 * i for i in range(14)]
+    made = Made(kv, P, 2, 1, lens, 41, spread=2)
+    for row in made.rows[1:]:
+        row[:first // P] = made.rows[0][:first // P]
+    made.table.copy_(_i32(made.rows))
+    _evict_run(made, [t - 64 - 100 * i for i, t in enumerate(lens)], first, 7, 5)
+
+
 def test_step_evict_step_and_captured():
     """A run of them as they are used: a prompt, its mass, eviction in both layers, then steps that append with positions
     of their own and count mass, eager and captured; against the oracle over what the pages hold."""
