@@ -452,12 +452,14 @@ class PagedMass:
         shape = (c.n_layers, c.n_pages, c.n_kv_heads, c.page)
         if mass is None:
             mass = torch.zeros(shape, dtype=torch.float32, device=cache.device)
+            torch.cuda.current_stream(cache.device).synchronize()  # any stream's calls may come next
         _need(tuple(mass.shape) == shape and mass.dtype == torch.float32 and mass.is_contiguous()
               and mass.device == cache.device, f"mass must be a contiguous fp32 tensor of shape {shape} on {cache.device}")
         need = c_size()
         _check("mk_paged_mass_sizes", cache.lib.mk_paged_mass_sizes(ctypes.byref(c), None, ctypes.byref(need)))
         self.mass, self.shape, self.device, self.scratch_bytes = mass, shape, mass.device, need.value
         self.scratch = torch.empty(need.value, dtype=torch.uint8, device=cache.device)
+        self.known = {_raw_stream(cache.device.index)}  # streams that need no (further) record of this memory
 
 
 class PagedKV:
@@ -616,15 +618,22 @@ class PagedKV:
             raise MosaicKVError("mk_paged_prefix_attn", st)
         return out if lse is None else (out, lse)
 
-    def _mass(self, mass):
+    def _mass(self, mass, stream):
         c = self.cfg
         _need(mass.shape == (c.n_layers, c.n_pages, c.n_kv_heads, c.page) and mass.device == self.device,
               "the mass is of another cache's shape or device")
+        here = _raw_stream(self.device.index)
+        raw = here if stream is None else stream.cuda_stream
+        known = mass.__dict__.setdefault("known", {here})
+        if raw not in known:
+            known.add(raw)
+            for t in (mass.mass, mass.scratch):
+                t.record_stream(stream if stream is not None else torch.cuda.current_stream(self.device))
 
     def decode_attn_mass(self, layer, batch, q, mass, first=0, scale=None, out=None, lse=None, stream=None):
         """decode_attn that also adds every weight to its token's mass (a PagedMass), from token number `first` on; the
         new token's mass is set."""
-        self._mass(mass)
+        self._mass(mass, stream)
         args, out, lse = self._attn(batch, q, scale, out, lse, stream, mass.mass, mass.scratch)
         st = self.lib.mk_paged_decode_attn_mass(self.h, layer, batch.ref, *args[:-1], mass.mass.data_ptr(), first,
                                                 mass.scratch.data_ptr(), mass.scratch_bytes, args[-1])
@@ -636,7 +645,7 @@ class PagedKV:
         """The mass that the batch's queries give, from prefill_attn's q and lse: added to that of the tokens held
         before the new ones (add=False: it begins anew), from token number `first` on."""
         _need(batch.device == self.device, "the batch is on another device")
-        self._mass(mass)
+        self._mass(mass, stream)
         qs = self._rows(q, "q", batch, self.cfg.n_q_heads)
         _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == self.device
               and lse.numel() >= batch.n_tokens * self.cfg.n_q_heads, "lse must be contiguous fp32 [n_tokens, n_q_heads]")
@@ -651,7 +660,7 @@ class PagedKV:
         between, moved to the front of its pages.  Returns (new_len int32 [n], kept int32 [n, n_kv_heads, columns]: the
         tokens' numbers from before).  kept is made with max_keep columns (default: what the page table holds)."""
         _need(batch.device == self.device, "the batch is on another device")
-        self._mass(mass)
+        self._mass(mass, stream)
         _dev_i32(keep, "keep", self.device)
         _need(keep.numel() >= batch.n_seqs, "keep must name a count for every sequence")
         heads = self.cfg.n_kv_heads

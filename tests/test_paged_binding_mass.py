@@ -45,3 +45,12 @@ def test_nothing_is_recorded_on_the_current_stream(kv):  # noqa: F811
     kv.decode_attn_mass(0, b, q, m, out=out)
     for t in (b.kv_len, q, out, m.mass, m.scratch, kv.workspace):
         assert not _kept(t)
+
+
+def test_the_mass_is_kept_for_a_stream_that_became_the_current_one(kv):  # noqa: F811
+    b, q, out, m = _batch(), _t(2, 4, 128), _t(2, 4, 128), _mass(kv)
+    kv.decode_attn_mass(0, b, q, m, out=out)
+    kv.set_current(OTHER)
+    kv.decode_attn_mass(0, b, q, m, out=out)
+    kv.decode_attn_mass(0, b, q, m, out=out, stream=kv.stream_of(OTHER))
+    assert m.mass.streams == m.scratch.streams == [OTHER] and not _kept(q)
