@@ -18,7 +18,7 @@
 // handed out in order by a counter, so whoever is waited for has begun and
 // reads without waiting: every wait ends.
 //
-// What bounds it: HBM for many sequences (24 in bf16 48 us, its bytes 49 at the
+// What bounds it: HBM for many sequences (24 in bf16 47 us, its bytes 49 at the
 // rate of a plain copy), chains of dependent steps for one (64K tokens in e4m3
 // 44 us, its bytes 10).  About half of these is the selection: loads 7 us, three
 // passes of histogram and cluster barriers 3-4 each, the writing of the numbers
@@ -403,18 +403,18 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
     int g = 0;
     if (warp == 0) {
       // Ranks of the kept tokens that come from slots r0 .. r0 + 63.
-      auto rank_of = [&](int t) {  // kept tokens before token t (a group's first)
+      auto rank_of = [&](int t) {  // kept tokens before token t (a group's first); -1: its page is bad, nothing is waited for
         if (t <= a.first) return t;
         if (t >= len) return keep;
         if (t >= len - a.recent) return keep - (len - t);
         const int p = page_of(L, a.b, seq, t);
-        return p < 0 ? 0 : a.rank0[(int64_t)p * n_kv + head];
+        return p < 0 ? -1 : a.rank0[(int64_t)p * n_kv + head];
       };
       const int b0 = rank_of(r0);
       int b1 = r0 + kGroup < keep ? rank_of(r0 + kGroup) : min(keep, b0 + kGroup);
       b1 = min(b1, b0 + kGroup);
       g = b0 / kGroup + lane;  // at most two items, none later than this one
-      if (lane < 2 && b1 > b0 && g <= (b1 - 1) / kGroup && g < j) {
+      if (lane < 2 && b0 >= 0 && b1 > b0 && g <= (b1 - 1) / kGroup && g < j) {
         const int p = page_of(L, a.b, seq, g * kGroup + kGroup - 1);  // an earlier item is full
         if (p >= 0) from = a.flag + (int64_t)p * n_kv + head;
       }

@@ -449,6 +449,26 @@ def test_device_errors_leave_other_sequences_right():
     assert bool((again == -1).all())
 
 
+def test_eviction_waits_for_nobody_over_a_bad_page():
+    """A page id that is none at the first of 64 slots: who reads there cannot be told, and is not waited for (a wait
+    that runs out takes 200 ms)."""
+    made = Made("e4m3", 16, 1, 1, [5000, 300], 5)
+    for j in (128, 160):
+        made.table[0, j] = 99999
+    c, m = made.c, K.PagedMass(made.c)
+    m.mass.uniform_(generator=_gen(1))
+    was, b, keep = m.mass.clone(), K.PagedBatch(made.kv_len, made.table), _i32([4000, 200])
+    c.evict(0, K.PagedBatch(_i32([0, 0]), made.table), m, keep)                           # loads the kernels
+    a, e = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    a.record()
+    new_len, kept = c.evict(0, b, m, keep, first=100, recent=4)
+    e.record()
+    e.synchronize()
+    assert a.elapsed_time(e) < 100 and c.poll_error() == (5, 17)
+    assert new_len.tolist() == [4000, 200] and kept[1, 0, :200].tolist() == O.evict_tokens(_of(made, was, 1, 0).tolist(), 200, 100, 4)
+
+
 def test_a_bad_page_does_not_reach_other_sequences_mass():
     """A page id that is none is read as page 0, whose own sequence keeps its logits."""
     made = Made("e4m3", 16, 2, 4, [300, 200], 5)
