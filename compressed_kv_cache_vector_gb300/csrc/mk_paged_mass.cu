@@ -647,9 +647,9 @@ __global__ void __launch_bounds__(kMassThreads, 1)
 // contexts: every key is read for a step or two, so HBM bounds it.  The
 // queries of a (sequence, kv head) stay in shared memory, and keys go by in a
 // ring of copies.  e4m3 keys are multiplied as they are, a query row being the
-// sum of an e4m3 and an e5m2 number each after a power of two (exact but for
-// channels below 2^-13 of the row's largest, off by at most 2^-21 of it): no
-// conversion of keys that are used once.
+// sum of three e5m2 numbers each after a power of two (exact but for channels
+// below 2^-23 of the row's largest, off by at most 2^-31 of it): no conversion
+// of keys that are used once.
 constexpr int kWindowRows = 256;
 
 // TILES: row tiles of a sequence, at most.  With one, the next (sequence, kv
@@ -657,7 +657,7 @@ constexpr int kWindowRows = 256;
 template <bool E4M3, int TILES>
 struct WindowShared {
   MassList list;
-  static constexpr int NU = 2 / TILES, NK = E4M3 ? 4 : 2;
+  static constexpr int NU = 2 / TILES, NK = E4M3 ? 3 : 2;
   uint64_t q_full[NU], q_free[NU], s_full[2], s_free[2], k_full[NK], k_free[NK], done;
   __align__(16) float nlse[2][kMassRows], ze[2][kMassRows];  // by row tile of a unit, or by unit
   int page[kMeta][kMassKeys / 16];
@@ -672,11 +672,13 @@ __global__ void __launch_bounds__(kMassThreads, 1)
     k_window_mass(PagedLayer L, MassArgs a, const uint16_t* q, int64_t q_stride, const __grid_constant__ CUtensorMap kmap) {
   using Sh = WindowShared<E4M3, TILES>;
   constexpr int NU = Sh::NU, NK = Sh::NK, kItem = E4M3 ? kMassTile : 2 * kMassTile, kSide = kMassTile / 2;
+  constexpr int kQTile = E4M3 ? 3 * kSide : kMassTile;  // queries of a row tile: three 8-bit parts, or two halves of the channels
+  static_assert(1024 + 2 * kQTile + NK * kItem <= kMassSmem, "shared memory");
   extern __shared__ unsigned char dyn[];
   __shared__ Sh sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-  const uint32_t sq = base, sk = base + 2 * kMassTile;
+  const uint32_t sq = base, sk = base + 2 * kQTile;
   const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv;
 
   if (tid == 0) {
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
         ok = ok && wait(&sh.k_full[ic % NK], (ic / NK) & 1);
         const uint64_t dk = sw128_desc(sk + (ic % NK) * kItem, 16);
         for (int j = j0; ok && j < j1; ++j, ++c) {
-          const uint64_t dq = sw128_desc(sq + (TILES == 2 ? skip + j : u % NU) * kMassTile, 16);
+          const uint64_t dq = sw128_desc(sq + (TILES == 2 ? skip + j : u % NU) * kQTile, 16);
           ok = c < 2 || wait(&sh.s_free[c & 1], ((c >> 1) - 1) & 1);
           if (!ok) break;
           tmem_fence_after_sync();
@@ -756,9 +758,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             const uint64_t da = dk + (uint64_t)((w * (kItem / 2)) >> 4);
             if (E4M3) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) umma8(d, da + i * 2, dq + i * 2, idesc8(0, 0), i > 0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) umma8(d, da + i * 2, dq + (kSide >> 4) + i * 2, idesc8(0, 1), 1);
+              for (int i = 0; i < 12; ++i) umma8(d, da + (i & 3) * 2, dq + (i >> 2) * (kSide >> 4) + (i & 3) * 2, idesc8(0, 1), i > 0);
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       const int rows = list.n_new[k.seq] * G, tiles = list.tiles_of(k.seq);
       for (int t = 0; t < tiles; ++t) {
         const int at = TILES == 2 ? t : u % NU;
-        const uint32_t to = sq + at * kMassTile;
+        const uint32_t to = sq + at * kQTile;
 #pragma unroll 1
         for (int i0 = 0; i0 < 16; i0 += 8) {  // eight rows' loads in flight
           uint4 v[8];
@@ -869,11 +869,12 @@ __global__ void __launch_bounds__(kMassThreads, 1)
           for (int i = 0; i < 8; ++i) {
             const int r = row_of(i);
             if (E4M3) {
-              uint32_t hi[2], lo[2];
-              const float scale = split8(v[i], lane, hi, lo);
+              uint32_t part[3][2];
+              const float scale = split8(v[i], lane, part);
               const uint32_t o = to + r * 128 + (((ck >> 1) ^ (r & 7)) << 4) + (ck & 1) * 8;
-              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o), "r"(hi[0]), "r"(hi[1]) : "memory");
-              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o + kSide), "r"(lo[0]), "r"(lo[1]) : "memory");
+#pragma unroll
+              for (int p = 0; p < 3; ++p)
+                asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(o + p * kSide), "r"(part[p][0]), "r"(part[p][1]) : "memory");
               if (ck == 0) sh.ze[at][r] = scale;
             } else {
               asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (ck >> 3) * kSide + r * 128 + (((ck & 7) ^ (r & 7)) << 4)),

@@ -21,11 +21,11 @@
 //  * warps 0-3 and 4-7: softmax of the even and the odd steps;
 //  * warps 8-11 (e4m3): value codes to fp16, exact, two tiles;
 //  * warp 12 issues the products, warp 13 the copies.
-//  * e4m3 keys are multiplied as they are: a query row, brought to [128, 256) by
-//    a power of two, is the sum of an e4m3 and an e5m2 number each, exact but
-//    for channels below 2^-13 of the row's largest, which are off by at most
-//    2^-21 of it.  That spares the keys' conversion, which shared memory's rate
-//    would pay for (16 KB read and 32 KB written a step).
+//  * e4m3 keys are multiplied as they are: a query row, after a power of two, is
+//    the sum of three e5m2 numbers each, exact but for channels below 2^-23 of
+//    the row's largest, which are off by at most 2^-31 of it.  That spares the
+//    keys' conversion, which shared memory's rate would pay for (16 KB read and
+//    32 KB written a step).
 //  * Work split on the device: all (group, 128 rows, kv head) cells' steps of
 //    128 keys in a row, cut into equal runs, one a CTA.
 // Keys as rows of the logits (a thread a key, weights through shared memory) was
@@ -51,12 +51,13 @@ constexpr int kHalf = kTile / 2;          // its channels 0-63, then 64-127
 constexpr int kThreads = 512;
 constexpr int kCellCost = 3;              // a cell's queries and result take as long as this many steps
 constexpr int kMinRun = 2;                // shortest run of a CTA, in steps
-constexpr int kSmem = 1024 + 6 * kTile;   // queries, keys and values
 // Tiles on their way: of keys and of values (e4m3: codes, 16 KB each, besides
 // the two tiles of values in fp16).
 template <bool E4M3>
 struct Ring {
   static constexpr int tile = E4M3 ? kTile / 2 : kTile, keys = E4M3 ? 3 : 2, values = 3;
+  static constexpr int queries = E4M3 ? 3 * kHalf : kTile;  // e4m3: three 8-bit parts
+  static constexpr int smem = 1024 + queries + (keys + values) * tile + (E4M3 ? 2 * kTile : 0);
 };
 // Registers of a thread of each four warps; the launch gives 128 each.
 template <bool E4M3>
@@ -122,8 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;
-  const uint32_t sq = base, sk = base + kTile, sv = sk + NK * kSlot, sc = sv + NV * kSlot;
-  static_assert(kTile + (NK + NV) * kSlot + (E4M3 ? 2 * kTile : 0) <= 6 * kTile, "shared memory");
+  const uint32_t sq = base, sk = base + Ring<E4M3>::queries, sv = sk + NK * kSlot, sc = sv + NV * kSlot;
   const int G = L.G, g_log2 = __ffs(G) - 1, n_kv = L.n_kv, n_groups = a.p.n_groups, members = kRows / G;
 
   if (tid == 0) {
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Place<NK> kp;
         Place<NV> vp;
         unsigned ph = 0;  // bit w: phase of p_full[w]
-        const uint64_t dq = sw128_desc(sq, 16), dl = sw128_desc(sq + kHalf, 16);
+        const uint64_t dq = sw128_desc(sq, 16);
         for (Cursor k = sh.start; ok && k.rel < sh.span; next(k)) {
           if (!steps(k, j0, j1)) continue;
           const int len = sh.len[k.group];
@@ -295,9 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t d = sw128_desc(sk + kp.slot * kSlot, 16);
               if (E4M3) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) umma8(tmem + w * 128, dq + i * 2, d + i * 2, idesc8(0, 0), i > 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) umma8(tmem + w * 128, dl + i * 2, d + i * 2, idesc8(1, 0), 1);
+                for (int i = 0; i < 12; ++i)
+                  umma8(tmem + w * 128, dq + (i >> 2) * (kHalf >> 4) + (i & 3) * 2, d + (i & 3) * 2, idesc8(1, 0), i > 0);
               } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -507,11 +506,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t h[4] = {q.x ^ a.q_sign, q.y ^ a.q_sign, q.z ^ a.q_sign, q.w ^ a.q_sign};
           if (E4M3) {
-            uint32_t hi[2], lo[2];
-            const float scale = split8(make_uint4(h[0], h[1], h[2], h[3]), lane, hi, lo);
+            uint32_t part[3][2];
+            const float scale = split8(make_uint4(h[0], h[1], h[2], h[3]), lane, part);
             const uint32_t at = sq + r * 128 + (((ck >> 1) ^ (r & 7)) << 4) + (ck & 1) * 8;
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-            asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + kHalf), "r"(lo[0]), "r"(lo[1]) : "memory");
+#pragma unroll
+            for (int p = 0; p < 3; ++p)
+              asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + p * kHalf), "r"(part[p][0]), "r"(part[p][1]) : "memory");
             if (ck == 0) sh.ml[0][r][0] = scale;
           } else {
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(sq + (ck >> 3) * kHalf + r * 128 + (((ck & 7) ^ (r & 7)) << 4)),
@@ -831,12 +831,13 @@ cudaError_t launch_paged_prefix(const PagedLayer& L, const PagedMaps& maps, cons
   static_assert(kRows * kPagedRowPart == kPagedPrefixPart, "a part's size");
   const void* fn = L.e4m3 ? (const void*)k_paged_prefix<true> : (const void*)k_paged_prefix<false>;
   int sms = 0;
-  const cudaError_t e = kernel_smem_attr(fn, kSmem, kThreads, nullptr, &sms);
+  const int smem = L.e4m3 ? Ring<true>::smem : Ring<false>::smem;
+  const cudaError_t e = kernel_smem_attr(fn, smem, kThreads, nullptr, &sms);
   if (e != cudaSuccess) return e;
   const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
   const PrefixArgs a{b, p, q, q_stride, (scale < 0.0f ? -scale : scale) * kLog2e, scale < 0.0f ? 0x80008000u : 0u,
                      layer * L.n_pages, check_only ? 1 : 0, w.prefill_part, w.row_part, w.shared};
-  return launch_pdl(L.e4m3 ? k_paged_prefix<true> : k_paged_prefix<false>, dim3(check_only ? 1 : grid), dim3(kThreads), (size_t)kSmem, s, 0, L, a,
+  return launch_pdl(L.e4m3 ? k_paged_prefix<true> : k_paged_prefix<false>, dim3(check_only ? 1 : grid), dim3(kThreads), (size_t)smem, s, 0, L, a,
                     maps.k, maps.v);
 }
 

@@ -120,13 +120,18 @@ __device__ __forceinline__ void umma8(uint32_t d, uint64_t a, uint64_t b, uint32
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-// A row's eight bf16 channels (16 lanes have a row) as sums of an e4m3 number
-// and an e5m2 one, after the power of two that brings the row's largest to
-// [128, 256); returns what undoes it.  Exact for channels from 2^-13 of the
-// largest on (2^-6 to 2^8 and more: 8 significant bits are 4 and the 3 that a
-// rest of at most 8 units wants); smaller ones are off by half of e5m2's step
-// at 2^-10, 2^-21 of the largest, at most.
-__device__ __forceinline__ float split8(const uint4& v, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+// Two e5m2 codes (low 16 bits) as floats: an e5m2 code is the upper byte of an fp16 one.
+__device__ __forceinline__ float2 e5m2_f2(uint32_t two) {
+  const uint32_t h = (two & 0xffu) << 8 | (two & 0xff00u) << 16;
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// A row's eight bf16 channels (16 lanes have a row) as sums of three e5m2
+// numbers, after the power of two that brings the row's largest to
+// [2^14, 2^15); returns what undoes it.  A part has 3 significant bits and
+// leaves at most half of its step, so three hold the 8 of a bf16 number, down to
+// e5m2's smallest step, 2^-16: exact for channels from 2^-23 of the largest on;
+// smaller ones are off by half of that step, 2^-31 of the largest, at most.
+__device__ __forceinline__ float split8(const uint4& v, int lane, uint32_t (&part)[3][2]) {
   const uint32_t h[4] = {v.x, v.y, v.z, v.w};
   float top = 0.0f, y[8];
 #pragma unroll
@@ -141,23 +146,26 @@ __device__ __forceinline__ float split8(const uint4& v, int lane, uint32_t (&hi)
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] -= y[e];
   }
-  int ex = (int)(__float_as_uint(top) >> 23) - 127 - 7;
+  int ex = (int)(__float_as_uint(top) >> 23) - 127 - 14;
   ex = max(-100, min(ex, 120));
   const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    uint32_t a[2], b[2];
+  for (int e = 0; e < 8; ++e) y[e] *= down;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float x0 = y[4 * e + 2 * u] * down, x1 = y[4 * e + 2 * u + 1] * down;
-      a[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t back = e4m3_h2(a[u]);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-      b[u] = __nv_cvt_float2_to_fp8x2(make_float2(x0 - f.x, x1 - f.y), __NV_SATFINITE, __NV_E5M2);
+  for (int p = 0; p < 3; ++p)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t two[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float* const x = &y[4 * e + 2 * u];
+        two[u] = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E5M2);
+        const float2 f = e5m2_f2(two[u]);
+        x[0] -= f.x;
+        x[1] -= f.y;
+      }
+      part[p][e] = two[0] | two[1] << 16;
     }
-    hi[e] = a[0] | a[1] << 16;
-    lo[e] = b[0] | b[1] << 16;
-  }
   return __uint_as_float((uint32_t)(127 + ex) << 23);
 }
 // One lane of a converged warp (the tensor-core instructions take their

@@ -602,7 +602,7 @@ typedef struct mk_paged_prefix {
  * fp16 for an e4m3 cache (2^-11 of each) and to bf16 for a bf16 cache (2^-8 of
  * each).  Shared values must be finite: a NaN or infinity among them reaches
  * every sequence of its group, also where its weight is 0.  With an e4m3 cache
- * a query row counts as its largest channel and the others to 2^-21 of that.
+ * a query row's channels count to 2^-31 of its largest (exactly from 2^-23 on).
  * Batches that could read 96 MB at most (n_seqs * table_stride * page tokens),
  * and n_groups = 0, are mk_paged_decode_attn's to the bit.
  * MK_EDEVICE: as mk_paged_decode_attn, and cu_group not ascending or out of
@@ -643,8 +643,10 @@ mk_status mk_paged_decode_attn_mass(mk_paged* h, int32_t layer, const mk_paged_b
  * tokens held before the call's new ones (the first kv_len - n_new; with
  * causal = 0 all of them), set for the others; add = 0: set for all.  A
  * sequence without new tokens is left alone.  Logits, exponentials and sums
- * are fp32; the order of the sums depends on the lengths alone.  A key of NaN
- * has a mass of NaN and no influence on another's. */
+ * are fp32; the order of the sums depends on the lengths alone.  With an e4m3
+ * cache and max_new x n_q_heads / n_kv_heads <= 256 a query row's channels count
+ * to 2^-31 of its largest (exactly from 2^-23 on).  A key of NaN has a mass of
+ * NaN and no influence on another's. */
 mk_status mk_paged_prefill_mass(mk_paged* h, int32_t layer, const mk_paged_batch* batch, int32_t causal, const void* q,
                                 int64_t q_stride, float scale, const float* lse, float* mass, int32_t first,
                                 int32_t add, mk_stream stream);
