@@ -102,6 +102,8 @@ constexpr int kMeta = 8;           // items whose pages are kept
 
 struct MassArgs {
   mk_paged_batch b;
+  const uint16_t* q;
+  int64_t q_stride;
   const float* lse;
   float* mass;
   float scale;  // times log2 e
@@ -464,20 +466,42 @@ __global__ void __launch_bounds__(kMassThreads, 1)
       for (int j = j0; ok && j < j1; ++j, ++c) {
         const int64_t r0 = (int64_t)(skip + j) * kMassRows;
         float n[4];
+        bool none = false;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int64_t r = r0 + lane * 4 + e;
           const float ls = r < rows ? a.lse[(row0 + (r >> g_log2)) * n_q + k.head * G + (int)(r & (G - 1))] : -INFINITY;
           n[e] = ls == -INFINITY ? -INFINITY : -ls * kLog2e;
+          none |= r < rows && ls == -INFINITY;
         }
+        none = __any_sync(FULL, none);
         ok = c < NQ || __all_sync(FULL, wait(&sh.q_free[c % NQ], (c / NQ - 1) & 1));
         if (!ok) break;
         *reinterpret_cast<float4*>(&sh.nlse[c & 7][lane * 4]) = make_float4(n[0], n[1], n[2], n[3]);
         __syncwarp();
-        if (lane == 0) {
+        const uint32_t to = sq + (c % NQ) * kMassTile;
+        if (none) {  // a row without a sum, whatever its query holds: the step's queries by hand, without it
+#pragma unroll 8
+          for (int i = lane; i < kMassRows * 16; i += 32) {
+            const int x = i >> 4, ck = i & 15;
+            const int64_t tok = row0 + ((r0 + x) >> g_log2);
+            const int h = k.head * G + (x & (G - 1));
+            uint4 v = make_uint4(0, 0, 0, 0);
+            float ls = -INFINITY;
+            if (r0 + x < rows) {
+              v = *reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + h * D + ck * 8);
+              ls = a.lse[tok * n_q + h];
+            }
+            if (ls == -INFINITY) v = make_uint4(0, 0, 0, 0);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(to + (ck >> 3) * (kMassTile / 2) + x * 128 + (((ck & 7) ^ (x & 7)) << 4)),
+                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
+          fence_proxy_async();
+          mbar_arrive_warp(&sh.q_full[c % NQ], lane);
+        } else if (lane == 0) {
           mbar_expect_tx(&sh.q_full[c % NQ], kMassTile);
           const int tok = row0 + (int)(r0 >> g_log2);
-          const uint32_t to = sq + (c % NQ) * kMassTile;
           tma3(to, &qmap, 0, k.head * G, tok, &sh.q_full[c % NQ]);
           tma3(to + kMassTile / 2, &qmap, 64, k.head * G, tok, &sh.q_full[c % NQ]);
         }
@@ -669,7 +693,7 @@ struct WindowShared {
 
 template <bool E4M3, int TILES>
 __global__ void __launch_bounds__(kMassThreads, 1)
-    k_window_mass(PagedLayer L, MassArgs a, const uint16_t* q, int64_t q_stride, const __grid_constant__ CUtensorMap kmap) {
+    k_window_mass(PagedLayer L, MassArgs a, const __grid_constant__ CUtensorMap kmap) {
   using Sh = WindowShared<E4M3, TILES>;
   constexpr int NU = Sh::NU, NK = Sh::NK, kItem = E4M3 ? kMassTile : 2 * kMassTile, kSide = kMassTile / 2;
   constexpr int kQTile = E4M3 ? 3 * kSide : kMassTile;  // queries of a row tile: three 8-bit parts, or two halves of the channels
@@ -861,13 +885,15 @@ __global__ void __launch_bounds__(kMassThreads, 1)
             v[i] = make_uint4(0, 0, 0, 0);
             ls[i] = -INFINITY;
             if (x < rows) {
-              v[i] = *reinterpret_cast<const uint4*>(q + tok * q_stride + h * D + ck * 8);
+              v[i] = *reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + h * D + ck * 8);
               if (ck == 0) ls[i] = a.lse[tok * n_q + h];
             }
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = row_of(i);
+            ls[i] = __shfl_sync(FULL, ls[i], lane & 16);
+            if (ls[i] == -INFINITY) v[i] = make_uint4(0, 0, 0, 0);  // a row without a sum, whatever it holds
             if (E4M3) {
               uint32_t part[3][2];
               const float scale = split8(v[i], lane, part);
@@ -978,7 +1004,7 @@ cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps
                                       const mk_paged_batch& b, bool causal, const uint16_t* q, int64_t q_stride,
                                       float scale, const float* lse, float* mass, int32_t first, bool add,
                                       cudaStream_t s) {
-  const MassArgs a{b, lse, mass, scale * kLog2e, causal ? 1 : 0, first, add ? 1 : 0, layer * L.n_pages, w.mass_part, w.prefill_counters};
+  const MassArgs a{b, q, q_stride, lse, mass, scale * kLog2e, causal ? 1 : 0, first, add ? 1 : 0, layer * L.n_pages, w.mass_part, w.prefill_counters};
   const int64_t rows = (int64_t)b.max_new * L.G;
   if (rows <= kWindowRows) {
     const bool two = rows > kMassRows;
@@ -987,7 +1013,7 @@ cudaError_t launch_paged_prefill_mass(const PagedLayer& L, const PagedMaps& maps
     const cudaError_t e = kernel_smem_attr((const void*)fn, kMassSmem, kMassThreads, nullptr, &sms);
     if (e != cudaSuccess) return e;
     const int grid = sms > 0 && sms <= kPagedMaxCtas ? sms : 128;
-    return launch_pdl(fn, dim3(grid), dim3(kMassThreads), (size_t)kMassSmem, s, 0, L, a, q, q_stride, maps.k);
+    return launch_pdl(fn, dim3(grid), dim3(kMassThreads), (size_t)kMassSmem, s, 0, L, a, maps.k);
   }
   auto fn = L.e4m3 ? k_prefill_mass<true> : k_prefill_mass<false>;
   int sms = 0;

@@ -639,7 +639,7 @@ mk_status mk_paged_decode_attn_mass(mk_paged* h, int32_t layer, const mk_paged_b
  * over its query tokens and heads of exp(scale q.k - lse), over the queries
  * that see it (causal as in mk_paged_prefill_attn).  lse: fp32
  * [n_tokens][n_q_heads] as mk_paged_prefill_attn wrote it for these queries (a
- * row with lse = -infinity gives nothing).  add = 1: added to the mass of the
+ * row with lse = -infinity gives nothing, whatever its query holds).  add = 1: added to the mass of the
  * tokens held before the call's new ones (the first kv_len - n_new; with
  * causal = 0 all of them), set for the others; add = 0: set for all.  A
  * sequence without new tokens is left alone.  Logits, exponentials and sums

@@ -49,3 +49,25 @@ def test_queries_with_one_channel_far_above_the_others(kv, new):
     made.c.prefill_mass(0, b, q, lse, m)
     assert made.c.poll_error() == (0, 0)
     _check_mass(made, before, m.mass, q, cu, news, SCALE, True, True, 0, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news,G", [([20, 5, 1], 4), ([40, 5, 1], 4), ([100, 9, 64], 2), ([300, 70, 600], 4)])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_rows_without_a_sum_give_nothing(kv, news, G, what):
+    """Rows whose lse is -infinity, single ones and whole tiles, with queries that are no numbers."""
+    made = Made(kv, 16, 2, G, [900, 300, 700], 3)
+    cu = _cu(news)
+    q = torch.randn(cu[-1], 2 * G, 128, generator=_gen(2), device=DEV).to(torch.bfloat16)
+    b = K.PagedBatch(made.kv_len, made.table, _i32(cu), max(news), cu[-1])
+    _, lse = made.c.prefill_attn(0, b, q, lse=True)
+    gone = torch.rand(lse.shape, generator=_gen(3), device=DEV) < 0.1
+    gone[: min(50, cu[-1] // 2)] = True
+    lse[gone] = -math.inf
+    bad = q.clone()
+    bad[gone] = what
+    m = _made_mass(made, 2)
+    before = m.mass.clone()
+    made.c.prefill_mass(0, b, bad, lse, m)
+    assert made.c.poll_error() == (0, 0)
+    _check_mass(made, before, m.mass, q, cu, news, SCALE, True, True, 0, lse)
