@@ -103,12 +103,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_evict_select(PagedLayer L, E
   }
   if (!ok) return;
   int32_t* kept = a.kept + ((int64_t)seq * L.n_kv + head) * a.kept_stride;
+  // Token numbers are below 2^31 - 256; a step past them need not be.
   if (!cut) {
-    for (int t = rank * kSelThreads + tid; t < len; t += CL * kSelThreads) kept[t] = t;
+    for (int64_t t = rank * kSelThreads + tid; t < len; t += CL * kSelThreads) kept[t] = (int)t;
     return;
   }
-  for (int t = (rank * kSelThreads + tid) * kGroup; t < keep; t += CL * kSelThreads * kGroup) {
-    const int p = page_of(L, a.b, seq, min(t + kGroup, keep) - 1);
+  for (int64_t t = (rank * kSelThreads + tid) * kGroup; t < keep; t += CL * kSelThreads * kGroup) {
+    const int p = page_of(L, a.b, seq, (int)min(t + kGroup, (int64_t)keep) - 1);
     if (p >= 0) a.flag[(int64_t)p * L.n_kv + head] = 0;
   }
   // Tokens lo .. hi - 1 are chosen from, k of them stay; this CTA has t0 .. t1 - 1.
@@ -288,8 +289,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) k_evict_select(PagedLayer L, E
   }
   leave();
   // The tokens that are kept anyway.
-  for (int t = rank * kSelThreads + tid; t < lo; t += CL * kSelThreads) kept[t] = t;
-  for (int i = rank * kSelThreads + tid; i < a.recent; i += CL * kSelThreads) kept[lo + k + i] = hi + i;
+  for (int64_t t = rank * kSelThreads + tid; t < lo; t += CL * kSelThreads) kept[t] = (int)t;
+  for (int64_t i = rank * kSelThreads + tid; i < a.recent; i += CL * kSelThreads) kept[lo + k + i] = (int)(hi + i);
   if (CL > 1) cg::this_cluster().barrier_wait(std::move(read));  // no CTA ends before its shared memory has been read
 }
 
