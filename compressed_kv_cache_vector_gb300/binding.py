@@ -445,20 +445,26 @@ class PagedPrefix:
 
 class PagedMass:
     """The attention mass of a cache's tokens (fp32 [n_layers, n_pages, n_kv_heads, page], zeros unless given) and the
-    scratch of decode_attn_mass (one layer's logits)."""
+    scratch of decode_attn_mass (one layer's logits).  Making one waits for the current stream, so not while it is being
+    captured; a given mass is ready on whatever stream the first call uses when its caller has seen to that."""
 
     def __init__(self, cache, mass=None):
         c = cache.cfg
         shape = (c.n_layers, c.n_pages, c.n_kv_heads, c.page)
-        if mass is None:
+        given = mass is not None
+        if not given:
             mass = torch.zeros(shape, dtype=torch.float32, device=cache.device)
-            torch.cuda.current_stream(cache.device).synchronize()  # any stream's calls may come next
         _need(tuple(mass.shape) == shape and mass.dtype == torch.float32 and mass.is_contiguous()
               and mass.device == cache.device, f"mass must be a contiguous fp32 tensor of shape {shape} on {cache.device}")
         need = c_size()
         _check("mk_paged_mass_sizes", cache.lib.mk_paged_mass_sizes(ctypes.byref(c), None, ctypes.byref(need)))
         self.mass, self.shape, self.device, self.scratch_bytes = mass, shape, mass.device, need.value
         self.scratch = torch.empty(need.value, dtype=torch.uint8, device=cache.device)
+        # Any stream's calls may come next: the zeros are there, and whoever had the scratch's memory before is done.
+        here = torch.cuda.current_stream(cache.device)
+        here.synchronize()
+        if given:  # it may be another stream's
+            mass.record_stream(here)
         self.known = {_raw_stream(cache.device.index)}  # streams that need no (further) record of this memory
 
 
