@@ -495,6 +495,9 @@ class PagedKV:
         self.v_scale = own(v_scale, "v_scale", torch.float32, shape[:3]) if e4m3 else None
         self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=self.device)
         self._remember_streams()
+        for t in (k_pool, v_pool, k_scale, v_scale):
+            if t is not None:  # given memory may be another stream's
+                t.record_stream(torch.cuda.current_stream(self.device))
         self.q_row, self.kv_row = cfg.n_q_heads * MK_HEAD_DIM, cfg.n_kv_heads * MK_HEAD_DIM
         self.h = None
         h = c_vp()
