@@ -339,7 +339,11 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
   static_assert(kMoveThreads >= MK_MAX_CALL_SEQS, "one thread a sequence");
   for (;;) {
     __syncthreads();  // the previous item's shared memory is free
-    if (tid == 0) s_item = atomicAdd(a.ticket, 1);
+    if (tid == 0) {
+      const int mine = atomicAdd(a.ticket, 1);
+      const int32_t status = *reinterpret_cast<volatile int32_t*>(L.err);
+      s_item = status == (int32_t)MK_ETIMEOUT ? 0x7fffffff : mine;  // after a wait that ran out nothing is left to do
+    }
     __syncthreads();
     const int64_t item = s_item;
     if (item >= total) return;
@@ -426,13 +430,15 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
     if (tid == 0 && my_page >= 0) {
       asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(a.flag + here) : "memory");
     }
+    bool late = false;
     if (from) {
       const long long t0 = clock64();
       int32_t done = 0;
       do {
         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(done) : "l"(from) : "memory");
       } while (!done && clock64() - t0 < 400000000ll);
-      if (!done) paged_error(L, ERR_PAGED_WAIT, seq, g, (int32_t)MK_ETIMEOUT);
+      late = !done;
+      if (late) paged_error(L, ERR_PAGED_WAIT, seq, g, (int32_t)MK_ETIMEOUT);
     }
     if (E4M3) {  // largest value of every four rows
 #pragma unroll
@@ -453,7 +459,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) k_evict_move(PagedLayer L, Ev
           if (lane == 0) s_max[t][(i * kRowsPass) / 4 + warp] = top;
         }
     }
-    __syncthreads();
+    if (__syncthreads_or(late)) return;  // whoever reads here may not have read yet: its rows stay
     // ---- write ----
 #pragma unroll
     for (int i = 0; i < kPass; ++i) {

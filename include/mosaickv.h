@@ -672,7 +672,11 @@ mk_status mk_paged_prefill_mass(mk_paged* h, int32_t layer, const mk_paged_batch
  * MK_EDEVICE: keep[i] negative, below first + recent where the sequence holds
  * more than keep[i], or min(kv_len, keep) above kept_stride; a bad length or
  * page id.  That sequence is left as it is, with new_len its kv_len (with a bad
- * page id, its contents are undefined). */
+ * page id, its contents are undefined).
+ * MK_ETIMEOUT (an item waited 0.2 s for an earlier one; no table that keeps the
+ * above can make it): the rest of the move is left undone, so the keys, values,
+ * scales and mass of the sequences that are cut are undefined; kept and new_len
+ * are right, and other sequences are as they were. */
 mk_status mk_paged_evict(mk_paged* h, int32_t layer, const mk_paged_batch* batch, float* mass, const int32_t* keep,
                          int32_t first, int32_t recent, int32_t* kept, int32_t kept_stride, int32_t* new_len,
                          mk_stream stream);
