@@ -570,8 +570,9 @@ mk_status mk_paged_decode_attn(mk_paged* h, int32_t layer, const mk_paged_batch*
  * out = 0, lse = -infinity); causal = 0: every query sees all kv_len keys.
  * Logits, softmax statistics and accumulators are fp32.  The weights that
  * multiply the values are rounded first: to fp16 for an e4m3 cache (2^-11 of
- * each), and for a bf16 cache to bf16 (2^-8 of each), except in
- * mk_paged_decode_attn and here for max_new x n_q_heads / n_kv_heads <= 16,
+ * each, or 2^-35 W / s where that is more, s being its page's V scale and W the
+ * row's largest weight times scale), and for a bf16 cache to bf16 (2^-8 of each),
+ * except in mk_paged_decode_attn and here for max_new x n_q_heads / n_kv_heads <= 16,
  * which keep 16 bits of them.
  * Keys that a query does not see have no influence on it whatever they hold;
  * values must be finite: 256 rows (256 / group query tokens) are worked on
@@ -599,11 +600,13 @@ typedef struct mk_paged_prefix {
  * of its sequences holds (those without a token in the call or with kv_len 0
  * do not count), is read for each sequence, as the rest of its tokens is.
  * The weights of shared tokens are rounded before they multiply the values: to
- * fp16 for an e4m3 cache (2^-11 of each) and to bf16 for a bf16 cache (2^-8 of
- * each).  Shared values must be finite: a NaN or infinity among them reaches
+ * fp16 for an e4m3 cache (2^-11 of each; one that is multiplied with its page's V
+ * scale s is off by up to 2^-32 W / s where that is more, W being the row's
+ * largest weight times scale: tails that far below vanish) and to bf16 for a
+ * bf16 cache (2^-8 of each).  Shared values must be finite: a NaN or infinity among them reaches
  * every sequence of its group, also where its weight is 0.  With an e4m3 cache
  * a query row's channels count to 2^-31 of its largest (exactly from 2^-23 on).
- * Batches that could read 96 MB at most (n_seqs * table_stride * page tokens),
+ * Batches that could read 144 MiB at most (n_seqs * table_stride * page tokens),
  * and n_groups = 0, are mk_paged_decode_attn's to the bit.
  * MK_EDEVICE: as mk_paged_decode_attn, and cu_group not ascending or out of
  * range or a negative prefix_len (nothing is shared then; the rows are right
