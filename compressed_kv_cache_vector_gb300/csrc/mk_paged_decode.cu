@@ -22,7 +22,8 @@
 //    128-byte swizzle (no barrier between warps while a unit lasts); page ids
 //    are read one chunk ahead of the copy that needs them.
 //  * e4m3 codes become fp16 (exact) and q, scaled by a power of two per head
-//    so that it fits, fp16 too; products on mma.sync m16n8k16.  Few rows: the
+//    that brings its largest channel to [2^14, 2^15), fp16 too (exact for channels
+//    from 2^-31 of the largest on, the others off by 2^-39 of it); products on mma.sync m16n8k16.  Few rows: the
 //    tensor cores idle either way, and this form needs no shared-memory
 //    round trip for the weights.  S = Q K^T puts a head's weights in the lanes
 //    that hold them as the B operand of O^T = V^T P.  V's transpose is taken
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
         }
         top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
         top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        int e = (int)(__float_as_uint(top) >> 23) - 127 - 14;  // the largest to [2^14, 2^15)
         e = max(-100, min(e, 120));
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
         zf[i] *= __uint_as_float((uint32_t)(127 + e) << 23);

@@ -614,14 +614,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_prefill(PagedLayer L, Pre
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               uint32_t h[4] = {w[i].x ^ a.q_sign, w[i].y ^ a.q_sign, w[i].z ^ a.q_sign, w[i].w ^ a.q_sign};
-              if (E4M3) {  // fp16, after a power of two that brings the row into its range
+              if (E4M3) {  // fp16, after a power of two that brings the row's largest to [2^14, 2^15): small ones stay exact
                 float top = 0.0f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                   top = fmaxf(top, fmaxf(fabsf(__uint_as_float(h[k] << 16)), fabsf(__uint_as_float(h[k] & 0xffff0000u))));
 #pragma unroll
                 for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-                int ex = (int)(__float_as_uint(top) >> 23) - 127;
+                int ex = (int)(__float_as_uint(top) >> 23) - 127 - 14;
                 ex = max(-100, min(ex, 120));
                 const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
