@@ -149,11 +149,13 @@ __global__ void __launch_bounds__(NW * 32, 1)
   pdl_wait();
   pdl_trigger();
   if (__syncthreads_or(tid == 0 && paged_stopped(L))) return;  // one thread's reading for the CTA
-  // What a row's weights are taken from, by its maximum.  OWN: rounded up, so
-  // that no weight passes 2^kShift however large the logits are, and parts are
-  // joined by it.
-  auto less = [](float m) { return OWN ? __fsub_ru(m, kShift) : m - kShift; };
-  auto apart = [&](float m, float M) { return OWN ? less(m) - less(M) : m - M; };
+  // What a row's weights are taken from, by its maximum, so that no weight passes
+  // 2^kShift however large the logits are.  OWN: rounded up, and parts are joined
+  // by it.  Otherwise logits of 2^23 and more, next to which the shift would be
+  // lost in rounding, have none.
+  auto shift = [](float m) { return fabsf(m) < 8388608.0f ? kShift : 0.0f; };
+  auto less = [&](float m) { return OWN ? __fsub_ru(m, kShift) : m - shift(m); };
+  auto apart = [&](float m, float M) { return OWN ? less(m) - less(M) : (m - M) + (shift(M) - shift(m)); };
 
   int units = 0;  // (sequence, kv head) pairs with keys
   if constexpr (OWN) {  // one warp: several sequences a lane, their loads in flight together
@@ -681,10 +683,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
     auto put_lse = [&](int r) {
       if (MASS && live_row(r))  // a row without weights: 2^(z - infinity) = 0
         a.lse2[(int64_t)u.seq * n_kv * G + head_of(r)] =
-            s_L[r] > 0.0f || s_L[r] != s_L[r] ? log2f(s_L[r]) + (s_M[r] - kShift) : INFINITY;
+            s_L[r] > 0.0f || s_L[r] != s_L[r] ? log2f(s_L[r]) + less(s_M[r]) : INFINITY;
       if (!a.lse || !live_row(r)) return;
       a.lse[(int64_t)(row + tok_of(r)) * n_kv * G + head_of(r)] =
-          s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + (s_M[r] - kShift)) * 0.6931471805599453f : -INFINITY;
+          s_L[r] > 0.0f || s_L[r] != s_L[r] ? (log2f(s_L[r]) + less(s_M[r])) * 0.6931471805599453f : -INFINITY;
     };
     const bool whole = u.ch == 0 && fe - fs == nch;
     const int64_t part = 2 * (int64_t)blockIdx.x + (u.ch == 0 ? 1 : 0);

@@ -574,6 +574,8 @@ mk_status mk_paged_decode_attn(mk_paged* h, int32_t layer, const mk_paged_batch*
  * row's largest weight times scale), and for a bf16 cache to bf16 (2^-8 of each),
  * except in mk_paged_decode_attn and here for max_new x n_q_heads / n_kv_heads <= 16,
  * which keep 16 bits of them.
+ * Logits must stay below 2^23 (the calls for single tokens, and this one up to
+ * those 16 rows, take any finite ones).
  * Keys that a query does not see have no influence on it whatever they hold;
  * values must be finite: 256 rows (256 / group query tokens) are worked on
  * together, and a NaN or infinity among the values that the last of them sees

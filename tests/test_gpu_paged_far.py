@@ -55,3 +55,38 @@ def test_queries_with_one_channel_far_above_the_others(kv, small):
     out, lse = made.c.prefill_attn(0, K.PagedBatch(made.kv_len, made.table, cu, 64, 136), q, lse=True)
     assert made.c.poll_error() == (0, 0)
     _check_attention(made, q, out, lse, SCALE, news, True, 2.0 ** -8 if kv == "bf16" else 2.0 ** -11)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("up", [23, 25, 27, 29, 31, 40, 60])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_logits_too_large_for_a_shift(kv, up, sign):
+    """Keys of 2^up: next to the maximum a shift of its own size is lost in rounding.  Where one token is above the others
+    by more than the logits' error, its value is the result, and its logit the sum's logarithm."""
+    lens = [950, 901, 33, 1200, 5000]
+    made = Made(kv, 16, 2, 4, lens, 8)
+    for row in made.rows[1:]:
+        row[0] = made.rows[0][0]                                                        # for the prefix
+    made.table.copy_(_i32(made.rows))
+    if kv == "e4m3":
+        made.c.k_scale.mul_(2.0 ** up)
+    else:
+        made.c.k_pool.mul_(2.0 ** up)
+    q = torch.randn(5, 8, 128, generator=_gen(2), device=DEV).to(torch.bfloat16)
+    scale, seen = sign * SCALE, 0
+    for name, out, lse in _calls(made, q, scale, lens, 16):
+        assert made.c.poll_error() == (0, 0), name
+        assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all()), name
+        for i in range(5):
+            for h in range(8):
+                k, v = made.held(i, h // 4)
+                z = k @ q[i, h].double() * scale
+                d = 2.0 ** -17 * float((k.abs() @ q[i, h].double().abs()).max()) * abs(scale)
+                two = torch.topk(z, 2)
+                if float(two.values[0] - two.values[1]) < 4 * d + 60:
+                    continue
+                seen += 1
+                want = v[two.indices[0]]
+                assert bool(((out[i, h].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * want.abs()).all()), (name, i, h)
+                assert abs(float(lse[i, h]) - float(two.values[0])) <= d + 2.0 ** -22 * abs(float(two.values[0])), (name, i, h)
+    assert seen > 100
