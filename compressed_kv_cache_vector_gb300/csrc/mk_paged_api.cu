@@ -103,11 +103,14 @@ bool pool_map(mk::TensorMapEncoder enc, const mk_paged_config* c, void* pool, in
 }
 
 // Bytes of keys and values of a decode step up to which its sequences read what
-// they share each by themselves (the groups are checked all the same): two
-// kernels fewer to wait for.  32 query heads over 8, us a call, sharing against
-// not: 8 sequences on 2K 33.6 and 19.6 (37 MB), 32 on 1K 33.9 and 28.0 (84 MB),
-// 16 on 4K 41.4 and 34.1 (138 MB, still in L2), 64 on 1K 38.1 and 44.4 (168 MB).
-constexpr int64_t kSmallShared = 96 << 20;
+// they share each by themselves (the groups are checked all the same): one
+// kernel fewer to wait for, and no parts to join.  32 query heads over 8, us a
+// call of many in a row (and with cold caches), sharing against not with the
+// check (2 to 4 us): 24 sequences on 2K 35.9 (49.8) and 33.7 (41.6), 111 MiB; 16
+// on 4K 41.1 (57) and 36.3 (43.7), 138 MiB; 32 on 2K 36.7 (50) and 39.7 (46), 148
+// MiB; 64 on 1K 38.0 (52) and 46.3 (54), 168 MiB; in bf16 8 on 4K 32.9 (44) and
+// 26.5 (35.5), 138 MiB, 32 on 1K 29 (38) and 29 (38), 168 MiB.
+constexpr int64_t kSmallShared = 144 << 20;
 
 // Makes the handle's device current for the call and restores the caller's.
 struct DeviceGuard {

@@ -609,7 +609,8 @@ typedef struct mk_paged_prefix {
  * every sequence of its group, also where its weight is 0.  With an e4m3 cache
  * a query row's channels count to 2^-31 of its largest (exactly from 2^-23 on).
  * Batches that could read 144 MiB at most (n_seqs * table_stride * page tokens),
- * and n_groups = 0, are mk_paged_decode_attn's to the bit.
+ * and n_groups = 0, are mk_paged_decode_attn's to the bit.  Where the sequences'
+ * own tokens are many times what is shared once, mk_paged_decode_attn is faster.
  * MK_EDEVICE: as mk_paged_decode_attn, and cu_group not ascending or out of
  * range or a negative prefix_len (nothing is shared then; the rows are right
  * all the same). */
