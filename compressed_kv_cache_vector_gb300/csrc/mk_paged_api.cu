@@ -2,6 +2,7 @@
 // argument checks, the workspace layout, and the launches.  No device memory
 // is allocated here, and no call throws: nothing in it allocates but the
 // handle itself (nothrow).
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -83,6 +84,11 @@ inline int64_t lse2_bytes(const mk_paged_config* c) { return align_up((int64_t)c
 // Eviction: the counter (a line of its own) and the plan, then two words per page and head.
 inline int64_t plan_bytes(const mk_paged_config* c) { return align_up(kAlign + (int64_t)c->max_seqs * 8); }
 inline int64_t group_words_bytes(const mk_paged_config* c) { return align_up((int64_t)c->n_pages * c->n_kv_heads * 4); }
+// Shared prefixes, a step's mass and eviction take the same bytes: a handle's
+// calls are ordered, and nothing of one is left for the next.
+inline int64_t turns_bytes(const mk_paged_config* c) {
+  return std::max(std::max(shared_bytes() + 2 * row_part_bytes(c) + own_bytes(c), lse2_bytes(c)), plan_bytes(c) + 2 * group_words_bytes(c));
+}
 inline int64_t prefill_part_bytes() { return align_up(mk::paged_prefill_part_floats() * 4); }
 
 // Rows (query token, query head) of a kv head up to which several query tokens
@@ -187,8 +193,8 @@ mk_status mk_paged_sizes(const mk_paged_config* cfg, size_t* pool_bytes, size_t*
   if (pool_bytes) *pool_bytes = (size_t)(pool_layer_bytes(cfg) * cfg->n_layers);
   if (scale_bytes) *scale_bytes = (size_t)(scale_layer_count(cfg) * cfg->n_layers * 4);
   if (workspace_bytes)
-    *workspace_bytes = (size_t)(clear_bytes(cfg) + part_acc_bytes(cfg) + part_ml_bytes(cfg) + prefill_part_bytes() +
-                                shared_bytes() + 2 * row_part_bytes(cfg) + own_bytes(cfg) + lse2_bytes(cfg) + plan_bytes(cfg) + 2 * group_words_bytes(cfg));
+    *workspace_bytes =
+        (size_t)(clear_bytes(cfg) + part_acc_bytes(cfg) + part_ml_bytes(cfg) + prefill_part_bytes() + turns_bytes(cfg));
   return MK_OK;
 }
 
@@ -227,11 +233,13 @@ mk_status mk_paged_create(const mk_paged_config* cfg, void* k_pool, void* v_pool
   h->scratch.part_ml = reinterpret_cast<float*>(take(part_ml_bytes(cfg)));
   h->scratch.prefill_part = reinterpret_cast<float*>(take(prefill_part_bytes()));
   h->scratch.mass_part = h->scratch.prefill_part;  // calls of a handle are ordered
+  char* const turns = at;
   h->scratch.shared = reinterpret_cast<mk::PagedShared*>(take(shared_bytes()));
   h->scratch.row_part = reinterpret_cast<float*>(take(row_part_bytes(cfg)));
   h->scratch.own_row = reinterpret_cast<float*>(take(row_part_bytes(cfg)));
   h->scratch.own = reinterpret_cast<int32_t*>(take(own_bytes(cfg)));
-  h->scratch.lse2 = reinterpret_cast<float*>(take(lse2_bytes(cfg)));
+  h->scratch.lse2 = reinterpret_cast<float*>(turns);
+  at = turns;
   char* plan = take(plan_bytes(cfg));
   h->evict.ticket = reinterpret_cast<int32_t*>(plan);
   h->evict.plan = reinterpret_cast<int32_t*>(plan + kAlign);
