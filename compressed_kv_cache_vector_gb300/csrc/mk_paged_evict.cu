@@ -520,19 +520,19 @@ cudaError_t launch_paged_evict(const PagedLayer& L, const PagedEvictScratch& w, 
   // a sequence may be long enough to be worth cutting.
   const int64_t longest = (int64_t)b.table_stride * L.P;
   const int64_t want = longest <= 2048 ? 1 : longest <= 8192 ? 4 : 8;
-  cudaError_t e;
-  if (want >= 8 && units * 8 <= 304)
+  int occ = 0, sms = 0;
+  const void* fn = L.e4m3 ? (const void*)k_evict_move<true> : (const void*)k_evict_move<false>;
+  cudaError_t e = kernel_smem_attr(fn, 0, kMoveThreads, &occ, &sms);
+  if (e != cudaSuccess) return e;
+  const int64_t room = 2 * (int64_t)(sms > 0 ? sms : 128);
+  if (want >= 8 && units * 8 <= room)
     e = launch_select<8>(L, a, s);
-  else if (want >= 4 && units * 4 <= 304)
+  else if (want >= 4 && units * 4 <= room)
     e = launch_select<4>(L, a, s);
-  else if (want >= 2 && units * 2 <= 304)
+  else if (want >= 2 && units * 2 <= room)
     e = launch_select<2>(L, a, s);
   else
     e = launch_select<1>(L, a, s);
-  if (e != cudaSuccess) return e;
-  int occ = 0, sms = 0;
-  const void* fn = L.e4m3 ? (const void*)k_evict_move<true> : (const void*)k_evict_move<false>;
-  e = kernel_smem_attr(fn, 0, kMoveThreads, &occ, &sms);
   if (e != cudaSuccess) return e;
   int64_t grid = (int64_t)(sms > 0 ? sms : 128) * (occ > 0 ? occ : 1);
   const int64_t items = units * ((std::min<int64_t>(kept_stride, longest) + kGroup - 1) / kGroup);
