@@ -18,8 +18,8 @@
 // handed out in order by a counter, so whoever is waited for has begun and
 // reads without waiting: every wait ends.
 //
-// What bounds it: HBM for many sequences (24 in bf16 47 us, its bytes 49 at the
-// rate of a plain copy), chains of dependent steps for one (64K tokens in e4m3
+// What bounds it: HBM for many sequences (24 in bf16 47 to 51 us from box to box,
+// its bytes 49 at the rate of a plain copy, some of them from L2), chains of dependent steps for one (64K tokens in e4m3
 // 44 us, its bytes 10).  About half of these is the selection: loads 7 us, three
 // passes of histogram and cluster barriers 3-4 each, the writing of the numbers
 // 4.  An item of the move waits for a ticket, its tokens' numbers, their pages,

@@ -28,16 +28,25 @@
 //    32 KB written a step).
 //  * Work split on the device: all (group, 128 rows, kv head) cells' steps of
 //    128 keys in a row, cut into equal runs, one a CTA.
-// Keys as rows of the logits (a thread a key, weights through shared memory) was
-// the first form: 135 us for the shared part of 192 sequences of 32 query heads
-// on 32K tokens of 8 kv heads in e4m3, bound by shared memory; rows as rows 117.
-// Both groups at a half of every step: 171 us against 165 for the whole call
-// (96 sequences in 7 groups, with short cells, 97 against 100).
+//  * Weights are rounded once: to fp16 (e4m3), or to one bf16 number.  Two bf16
+//    parts, as the decode kernel has them, would double the value products and
+//    want 64 registers more while a step's weights wait for their maximum; one
+//    part puts 32 sequences on 64K at 0.0020 of 64 bits where the output's own
+//    rounding is 0.0017, as in the attention of several query tokens.
+//  * fp16 weights have room for 2^15: 2^7 for the reference and 2^8 for logits
+//    that pass it.  2^11 and 2^4 keep more of far tails, but raise the maximum
+//    so much more often that 192 sequences on 32K took 207 us in place of 171.
+// With queries of two 8-bit parts, not three: keys as rows of the logits (a
+// thread a key, weights through shared memory) was the first form, 135 us for
+// the shared part of 192 sequences of 32 query heads on 32K tokens of 8 kv heads
+// in e4m3, bound by shared memory, against 117; both groups at a half of every
+// step 171 us for the whole call against 165 (96 sequences in 7 groups, with
+// short cells, 97 against 100).  The third part costs 5 us of the 171 and 3 of
+// the 104 that these take now.
 //
 // The whole call in three kernels (shared, own, joined; alone, cold): 192
-// sequences on 32K 117, 37 and 11 us; 96 in 7 groups 50, 30 and 13; 32 on 64K in
-// bf16 62, 12 and 22, its shared pages (269 MB, 40 us at the measured 6.79 TB/s)
-// read once.
+// sequences on 32K 122, 39 and 13 us; 32 on 64K in bf16 62, 12 and 22, its shared
+// pages (269 MB, 40 us at the measured 6.79 TB/s) read once.
 #include "mk_paged_tc.cuh"
 
 namespace mk {
